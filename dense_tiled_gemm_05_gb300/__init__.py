@@ -34,6 +34,7 @@ OPTIONS = {"wait_timeout_us": 0, "force_path": 1, "group_m": 2, "max_ctas": 3,
            "fault_stall_producer": 4, "force_staging": 5, "cta_pair": 6,
            "block_n": 7, "exact_chunk": 8, "stream_k": 9, "host_panel": 10, "acc_chunk": 11, "stage_k": 12,
            "tile_rows": 13, "tf32_transpose": 14}
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
 PATHS = {0: "none", 1: "zero_fill", 2: "tcgen05", 3: "fma", 4: "tcgen05_3xtf32",
          5: "tcgen05_f16acc"}
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -45,7 +46,9 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_ex", "gemm_get_s
            "gemm_strerror", "gemm_set_option", "gemm_get_launch_count", "gemm_plan",
            "gemm_version", "gemm_run_noalloc", "gemm_schedule_segments", "gemm_run_host",
            "gemm_run_strided", "gemm_plan_strided", "gemm_tune", "gemm_tune_clear",
-           "gemm_softmax_rows", "gemm_set_kernel_events")
+           "gemm_softmax_rows", "gemm_set_kernel_events", "gemm_run_epilogue",
+           "gemm_run_epilogue_backward", "gemm_run_gated", "gemm_run_gated_backward",
+           "gemm_layer_norm", "gemm_layer_norm_backward")
 
 
 class GemmError(RuntimeError):
@@ -64,6 +67,13 @@ class TuneResult(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("pre", ctypes.c_void_p),
+                ("ld_pre", ctypes.c_int64), ("bias_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
 
 
 class StridedInfo(ctypes.Structure):
@@ -128,6 +138,22 @@ def lib():
                 L.gemm_tune.restype = i32
                 L.gemm_softmax_rows.argtypes = [vp, i64, i64, vp, i64, vp, i64, i32, i32, vp]
                 L.gemm_softmax_rows.restype = i32
+                L.gemm_run_epilogue.argtypes = run_args + [i32, i32, ctypes.POINTER(Epilogue), vp]
+                L.gemm_run_epilogue.restype = i32
+                L.gemm_run_epilogue_backward.argtypes = (
+                    [vp] + [i64] * 3 + [vp, i64] * 6 + [vp] + [i32] * 7 + [vp])
+                L.gemm_run_epilogue_backward.restype = i32
+                L.gemm_run_gated.argtypes = [vp] + [i64] * 3 + [vp, i64] * 6 + [i32] * 4 + [vp]
+                L.gemm_run_gated.restype = i32
+                L.gemm_run_gated_backward.argtypes = (
+                    [vp] + [i64] * 3 + [vp, i64] * 9 + [i32] * 4 + [vp])
+                L.gemm_run_gated_backward.restype = i32
+                L.gemm_layer_norm.argtypes = [vp, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp,
+                                              ctypes.c_float, i32, i32, i32, vp]
+                L.gemm_layer_norm.restype = i32
+                L.gemm_layer_norm_backward.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp,
+                                                       vp, i64, vp, vp, i32, i32, i32, vp]
+                L.gemm_layer_norm_backward.restype = i32
                 L.gemm_tune_clear.argtypes = [vp]
                 L.gemm_tune_clear.restype = i32
                 L.gemm_get_status.argtypes = [vp, vp]
@@ -178,6 +204,44 @@ def operand_layout(x):
     if s0 == 1 and (s1 >= max(r, 1) or c <= 1):
         return COL, max(s1, r, 1)
     raise ValueError("operand must be row- or column-major, got stride %s" % (x.stride(),))
+
+
+def _row_ld(x, shape, what, device=None):
+    """Leading dimension of a CUDA matrix with contiguous rows and the given shape."""
+    if x.dim() != 2 or tuple(x.shape) != shape:
+        raise ValueError("%s must be a %d x %d tensor, got %s" % ((what,) + shape + (tuple(x.shape),)))
+    if not x.is_cuda or (device is not None and x.device != device):
+        raise ValueError("%s must be a CUDA tensor on the operands' device" % what)
+    rows, cols = shape
+    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
+        raise ValueError("rows of %s must be contiguous" % what)
+    return x.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _vector(x, n, what, device):
+    """Data pointer of a contiguous vector of n values (0 for None)."""
+    if x is None:
+        return 0
+    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector of %d values" % (what, n))
+    if x.device != device:
+        raise ValueError("%s must be on the operands' device" % what)
+    return x.data_ptr()
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError("unknown activation %r (one of %s)"
+                         % (name, ", ".join(str(k) for k in ACTIVATIONS)))
+    return ACTIVATIONS[name]
+
+
+def _like(x):
+    """An empty tensor of x's shape in x's layout (row- or column-major), tight."""
+    r, c = x.shape
+    if operand_layout(x)[0] == ROW:
+        return torch.empty((r, c), dtype=x.dtype, device=x.device)
+    return torch.empty((c, r), dtype=x.dtype, device=x.device).t()
 
 
 def _dtype_code(d):
@@ -333,6 +397,217 @@ class Gemm:
         _check(code, "gemm_softmax_rows")
         return out
 
+    # ------------------------------------------------------- feed-forward operators
+
+    def _stream(self, x, stream):
+        return (torch.cuda.current_stream(x.device) if stream is None else stream).cuda_stream
+
+    def _two(self, a, b):
+        """Checked extents of a product's operands."""
+        if a.dtype != b.dtype:
+            raise TypeError("operands must share a dtype")
+        if not (a.is_cuda and b.is_cuda) or a.device != b.device:
+            raise ValueError("operands must be CUDA tensors on one device")
+        if a.dim() != 2 or b.dim() != 2:
+            raise ValueError("operands must be 2-D")
+        if a.shape[1] != b.shape[0]:
+            raise ValueError("inner dimensions differ: %d vs %d" % (a.shape[1], b.shape[0]))
+        return a.shape[0], b.shape[1], a.shape[1]
+
+    def matmul_epilogue(self, a, b, bias=None, activation=None, residual=None, out=None,
+                        out_dtype=None, precision="default", save=False, stream=None):
+        """act(a @ b + bias) + residual: a is M x K, b is K x N (row- or column-major views;
+        a weight stored as [N, K] is passed as ``w.t()``), bias has N values, residual is
+        M x N of the output's dtype (``out=residual`` updates it in place). activation: None,
+        "relu", "gelu", "gelu_tanh", "silu" or "sigmoid". ``save=True`` returns (out, pre)
+        with pre = a @ b + bias for :meth:`matmul_epilogue_backward`."""
+        M, N, K = self._two(a, b)
+        dev = a.device
+        if out is None:
+            od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else a.dtype
+            out = torch.empty((M, N), dtype=od, device=dev)
+        ep = Epilogue()
+        ep.activation = _activation(activation)
+        if bias is not None:
+            ep.bias = _vector(bias, N, "bias", dev)
+            ep.bias_dtype = _dtype_code(bias.dtype)
+        if residual is not None:
+            if residual.dtype != out.dtype:
+                raise TypeError("residual must have the output's dtype")
+            ep.ld_residual = _row_ld(residual, (M, N), "residual", dev)
+            ep.residual = residual.data_ptr()
+        pre = None
+        if save:
+            pre = torch.empty((M, N), dtype=out.dtype, device=dev)
+            ep.pre, ep.ld_pre = pre.data_ptr(), max(N, 1)
+        al, lda = operand_layout(a)
+        bl, ldb = operand_layout(b)
+        code = lib().gemm_run_epilogue(self._h, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb,
+                                       out.data_ptr(), _row_ld(out, (M, N), "out", dev),
+                                       _dtype_code(a.dtype), _dtype_code(out.dtype),
+                                       PREC[precision], al, bl, ctypes.byref(ep),
+                                       self._stream(a, stream))
+        _check(code, "gemm_run_epilogue")
+        return (out, pre) if save else out
+
+    def matmul_epilogue_backward(self, grad, a, b, pre=None, activation=None,
+                                 need=(True, True, True), bias_dtype=None, precision="default",
+                                 stream=None):
+        """Gradients of :meth:`matmul_epilogue` from grad (M x N, the output's dtype) and the
+        saved pre (needed unless there is no activation): (da, db, dbias), each None where
+        ``need`` says so; da and db in the layouts of a and b, dbias in ``bias_dtype``
+        (default: a's). The residual's gradient is grad itself."""
+        M, N, K = self._two(a, b)
+        dev = a.device
+        act = _activation(activation)
+        lddy = _row_ld(grad, (M, N), "grad", dev)
+        ldz = 0
+        if act:
+            if pre is None:
+                raise ValueError("the backward pass of an activation needs the saved pre")
+            if pre.dtype != grad.dtype:
+                raise TypeError("pre must have grad's dtype")
+            ldz = _row_ld(pre, (M, N), "pre", dev)
+        da = _like(a) if need[0] else None
+        db = _like(b) if need[1] else None
+        dbias = None
+        if need[2]:
+            bd = _TORCH_OF[_dtype_code(bias_dtype)] if bias_dtype is not None else a.dtype
+            dbias = torch.empty(N, dtype=bd, device=dev)
+        al, lda = operand_layout(a)
+        bl, ldb = operand_layout(b)
+        ptr = lambda t: 0 if t is None else t.data_ptr()
+        code = lib().gemm_run_epilogue_backward(
+            self._h, M, N, K, grad.data_ptr(), lddy, pre.data_ptr() if act else 0, ldz,
+            a.data_ptr(), lda, b.data_ptr(), ldb, ptr(da), operand_layout(da)[1] if need[0] else 0,
+            ptr(db), operand_layout(db)[1] if need[1] else 0, ptr(dbias),
+            _dtype_code(dbias.dtype) if need[2] else 0, _dtype_code(a.dtype),
+            _dtype_code(grad.dtype), PREC[precision], al, bl, act, self._stream(a, stream))
+        _check(code, "gemm_run_epilogue_backward")
+        return da, db, dbias
+
+    def _gated_args(self, x, w_gate, w_up):
+        M, F, K = self._two(x, w_gate)
+        if self._two(x, w_up) != (M, F, K):
+            raise ValueError("w_gate and w_up must have one shape")
+        ldx = _row_ld(x, (M, K), "x")
+        wl, ldg = operand_layout(w_gate)
+        wl2, ldu = operand_layout(w_up)
+        if wl != wl2:
+            raise ValueError("w_gate and w_up must have one layout")
+        return M, F, K, ldx, wl, ldg, ldu
+
+    def gated(self, x, w_gate, w_up, activation="silu", out=None, precision="default",
+              save=False, stream=None):
+        """act(x @ w_gate) * (x @ w_up), the gated half of a feed-forward block: x is M x K
+        with contiguous rows, both weights K x F in one layout (stored as [F, K]: pass
+        ``w.t()``). ``save=True`` returns (out, gate, up) with the two products for
+        :meth:`gated_backward` (column ranges of one M x 2F buffer)."""
+        M, F, K, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
+        dev = x.device
+        if out is None:
+            out = torch.empty((M, F), dtype=x.dtype, device=dev)
+        if out.dtype != x.dtype:
+            raise TypeError("out must have x's dtype")
+        gate = up = None
+        if save:
+            both = torch.empty((M, 2 * F), dtype=x.dtype, device=dev)
+            gate, up = both[:, :F], both[:, F:]
+        code = lib().gemm_run_gated(
+            self._h, M, F, K, x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
+            out.data_ptr(), _row_ld(out, (M, F), "out", dev), gate.data_ptr() if save else 0, 2 * F,
+            up.data_ptr() if save else 0, 2 * F, _dtype_code(x.dtype), PREC[precision], wl,
+            _activation(activation), self._stream(x, stream))
+        _check(code, "gemm_run_gated")
+        return (out, gate, up) if save else out
+
+    def gated_backward(self, grad, x, w_gate, w_up, gate, up, activation="silu",
+                       need=(True, True, True), precision="default", stream=None):
+        """Gradients of :meth:`gated` from grad (M x F) and the saved gate and up: (dx, dw_gate,
+        dw_up), each None where ``need`` says so, the weights' in the weights' layout."""
+        M, F, K, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
+        dev = x.device
+        for t in (grad, gate, up):
+            if t.dtype != x.dtype:
+                raise TypeError("grad, gate and up must have x's dtype")
+        lds = [_row_ld(t, (M, F), n, dev) for t, n in ((grad, "grad"), (gate, "gate"), (up, "up"))]
+        dx = torch.empty((M, K), dtype=x.dtype, device=dev) if need[0] else None
+        dwg = dwu = None
+        if need[1] and need[2] and wl == COL:
+            both = torch.empty((2 * F, K), dtype=x.dtype, device=dev)
+            dwg, dwu = both[:F].t(), both[F:].t()
+        else:
+            dwg = _like(w_gate) if need[1] else None
+            dwu = _like(w_up) if need[2] else None
+        ptr = lambda t: 0 if t is None else t.data_ptr()
+        ldw = max(K if wl == COL else F, 1)
+        code = lib().gemm_run_gated_backward(
+            self._h, M, F, K, grad.data_ptr(), lds[0], gate.data_ptr(), lds[1], up.data_ptr(),
+            lds[2], x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, ptr(dx),
+            max(K, 1), ptr(dwg), ldw, ptr(dwu), ldw, _dtype_code(x.dtype), PREC[precision], wl,
+            _activation(activation), self._stream(x, stream))
+        _check(code, "gemm_run_gated_backward")
+        return dx, dwg, dwu
+
+    def layer_norm(self, x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None,
+                   save=False, stream=None):
+        """Layer norm of each row of a CUDA matrix with contiguous rows; weight and bias (None:
+        1 and 0) share a dtype of their own. ``out=x`` runs in place. ``save=True`` returns
+        (out, mean, rstd) with the rows' fp32 statistics for :meth:`layer_norm_backward`."""
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D")
+        M, N = x.shape
+        dev = x.device
+        ldx = _row_ld(x, (M, N), "x")
+        if weight is not None and bias is not None and weight.dtype != bias.dtype:
+            raise TypeError("weight and bias must share a dtype")
+        params = weight if weight is not None else bias
+        if out is None:
+            od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else x.dtype
+            out = torch.empty((M, N), dtype=od, device=dev)
+        mean = rstd = None
+        if save:
+            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=dev)
+        code = lib().gemm_layer_norm(
+            self._h, M, N, x.data_ptr(), ldx, _vector(weight, N, "weight", dev),
+            _vector(bias, N, "bias", dev), out.data_ptr(), _row_ld(out, (M, N), "out", dev),
+            mean.data_ptr() if save else 0, rstd.data_ptr() if save else 0, eps,
+            _dtype_code(x.dtype), F32 if params is None else _dtype_code(params.dtype),
+            _dtype_code(out.dtype), self._stream(x, stream))
+        _check(code, "gemm_layer_norm")
+        return (out, mean, rstd) if save else out
+
+    def layer_norm_backward(self, grad, x, weight, mean, rstd, need=(True, True, True),
+                            param_dtype=None, stream=None):
+        """Gradients of :meth:`layer_norm` from grad (the output's dtype), x, weight (or None)
+        and the saved statistics: (dx, dweight, dbias), each None where ``need`` says so; the
+        last two in ``param_dtype`` (default: weight's, or float32)."""
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D")
+        M, N = x.shape
+        dev = x.device
+        ldx = _row_ld(x, (M, N), "x")
+        lddy = _row_ld(grad, (M, N), "grad", dev)
+        for t, n in ((mean, "mean"), (rstd, "rstd")):
+            if t.dtype != torch.float32:
+                raise TypeError("%s must be float32" % n)
+        pd = weight.dtype if weight is not None else torch.float32
+        if param_dtype is not None:
+            pd = _TORCH_OF[_dtype_code(param_dtype)]
+            if weight is not None and weight.dtype != pd:
+                raise TypeError("param_dtype must be weight's dtype")
+        dx = torch.empty((M, N), dtype=x.dtype, device=dev) if need[0] else None
+        dw = torch.empty(N, dtype=pd, device=dev) if need[1] else None
+        db = torch.empty(N, dtype=pd, device=dev) if need[2] else None
+        ptr = lambda t: 0 if t is None else t.data_ptr()
+        code = lib().gemm_layer_norm_backward(
+            self._h, M, N, grad.data_ptr(), lddy, x.data_ptr(), ldx,
+            _vector(weight, N, "weight", dev), _vector(mean, M, "mean", dev),
+            _vector(rstd, M, "rstd", dev), ptr(dx), max(N, 1), ptr(dw), ptr(db),
+            _dtype_code(x.dtype), _dtype_code(pd), _dtype_code(grad.dtype), self._stream(x, stream))
+        _check(code, "gemm_layer_norm_backward")
+        return dx, dw, db
+
     def tune_clear(self):
         _check(lib().gemm_tune_clear(self._h), "gemm_tune_clear")
 
@@ -450,6 +725,36 @@ def matmul(a, b, out=None, out_dtype=None, precision="default"):
 def softmax_rows(x, out=None, out_dtype=None):
     """Row softmax with the default handle of x's device; see :meth:`Gemm.softmax_rows`."""
     return handle(x.device.index).softmax_rows(x, out=out, out_dtype=out_dtype)
+
+
+def matmul_epilogue(a, b, **kw):
+    """act(a @ b + bias) + residual; see :meth:`Gemm.matmul_epilogue`."""
+    return handle(a.device.index).matmul_epilogue(a, b, **kw)
+
+
+def matmul_epilogue_backward(grad, a, b, **kw):
+    """Gradients of :func:`matmul_epilogue`; see :meth:`Gemm.matmul_epilogue_backward`."""
+    return handle(a.device.index).matmul_epilogue_backward(grad, a, b, **kw)
+
+
+def gated(x, w_gate, w_up, **kw):
+    """act(x @ w_gate) * (x @ w_up); see :meth:`Gemm.gated`."""
+    return handle(x.device.index).gated(x, w_gate, w_up, **kw)
+
+
+def gated_backward(grad, x, w_gate, w_up, gate, up, **kw):
+    """Gradients of :func:`gated`; see :meth:`Gemm.gated_backward`."""
+    return handle(x.device.index).gated_backward(grad, x, w_gate, w_up, gate, up, **kw)
+
+
+def layer_norm(x, weight=None, bias=None, **kw):
+    """Layer norm of the rows of x; see :meth:`Gemm.layer_norm`."""
+    return handle(x.device.index).layer_norm(x, weight, bias, **kw)
+
+
+def layer_norm_backward(grad, x, weight, mean, rstd, **kw):
+    """Gradients of :func:`layer_norm`; see :meth:`Gemm.layer_norm_backward`."""
+    return handle(x.device.index).layer_norm_backward(grad, x, weight, mean, rstd, **kw)
 
 
 def matmul_host(a, b, out=None, out_dtype=None, precision="default", device=None):

@@ -1,0 +1,183 @@
+// activation.cuh -- element types, 16-byte row pieces and activation functions shared by the
+// feed-forward operators' kernels (products with an epilogue, the gated pair, layer norm).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "gemm.h"
+
+// Runs a statement with T naming the element type of a gemm_dtype_t.
+#define FF_TYPED(dt, T, ...)                                  \
+  switch (dt) {                                               \
+    case GEMM_F32: { using T = float; __VA_ARGS__; break; }   \
+    case GEMM_F16: { using T = __half; __VA_ARGS__; break; }  \
+    default: { using T = __nv_bfloat16; __VA_ARGS__; break; } \
+  }
+
+namespace gemm_gb300 {
+namespace ff {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Element i of a vector whose type is known at run time (biases and norm weights, which are
+// read once a column and may be wider than the rows they apply to).
+__device__ __forceinline__ float load_any(const void *p, int dtype, int64_t i) {
+  if (dtype == GEMM_F32) return static_cast<const float *>(p)[i];
+  if (dtype == GEMM_F16) return __half2float(static_cast<const __half *>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, int dtype, int64_t i, float v) {
+  if (dtype == GEMM_F32) static_cast<float *>(p)[i] = v;
+  else if (dtype == GEMM_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// VEC consecutive values of a row from column j0, as fp32; columns past n read as 0. With
+// VECTOR (the row starts on a multiple of the piece's size, up to 16 bytes) a whole piece is
+// read in 16-byte loads (8 for a piece of four 16-bit values).
+template <typename T, int VEC, bool VECTOR>
+__device__ __forceinline__ void load_piece(const T *row, int64_t j0, int64_t n, float (&v)[VEC]) {
+  if (VECTOR && j0 + VEC <= n) {
+    constexpr int BYTES = VEC * static_cast<int>(sizeof(T));
+    static_assert(BYTES % 16 == 0 || BYTES == 8, "piece size");
+    alignas(16) T e[VEC];
+    if (BYTES == 8) {
+      *reinterpret_cast<uint2 *>(e) = *reinterpret_cast<const uint2 *>(row + j0);
+    } else {
+#pragma unroll
+      for (int w = 0; w < BYTES / 16; ++w)
+        reinterpret_cast<uint4 *>(e)[w] = reinterpret_cast<const uint4 *>(row + j0)[w];
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = j0 + i < n ? to_f32(row[j0 + i]) : 0.0f;
+  }
+}
+
+template <typename T, int VEC, bool VECTOR>
+__device__ __forceinline__ void store_piece(T *row, int64_t j0, int64_t n, const float (&v)[VEC]) {
+  if (VECTOR && j0 + VEC <= n) {
+    constexpr int BYTES = VEC * static_cast<int>(sizeof(T));
+    static_assert(BYTES % 16 == 0 || BYTES == 8, "piece size");
+    alignas(16) T e[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) e[i] = from_f32<T>(v[i]);
+    if (BYTES == 8) {
+      *reinterpret_cast<uint2 *>(row + j0) = *reinterpret_cast<const uint2 *>(e);
+    } else {
+#pragma unroll
+      for (int w = 0; w < BYTES / 16; ++w)
+        reinterpret_cast<uint4 *>(row + j0)[w] = reinterpret_cast<const uint4 *>(e)[w];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (j0 + i < n) row[j0 + i] = from_f32<T>(v[i]);
+  }
+}
+
+// 1 / (1 + exp(-z)). FAST (kernels whose inputs are 16-bit, so that z already carries errors
+// of 2^-9): the hardware exponential and division, a few fp32 ulps for |z| of ordinary size.
+// Both saturate to exactly 0 and 1.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float z) {
+  return FAST ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
+}
+
+constexpr float kSqrtHalf = 0.70710678118654752440f;
+constexpr float kSqrt2OverPi = 0.79788456080286535588f;   // sqrt(2 / pi)
+constexpr float kInvSqrt2Pi = 0.39894228040143267794f;    // 1 / sqrt(2 pi)
+constexpr float kGeluCubic = 0.044715f;                   // of the tanh form of gelu
+
+// The standard normal distribution function: (1 + erf(z / sqrt 2)) / 2, by erfc of the
+// negated argument where the lower tail is to keep its relative accuracy.
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float z) {
+  return FAST ? fmaf(0.5f, erff(z * kSqrtHalf), 0.5f) : 0.5f * erfcf(-z * kSqrtHalf);
+}
+
+// Argument of the logistic form of tanh-gelu: (1 + tanh t) / 2 = sigmoid(2 t).
+__device__ __forceinline__ float gelu_tanh_arg(float z) {
+  return 2.0f * kSqrt2OverPi * z * fmaf(kGeluCubic * z, z, 1.0f);
+}
+
+template <bool FAST>
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case GEMM_ACT_RELU: return z > 0.0f ? z : z != z ? z : 0.0f;  // NaN stays NaN
+    case GEMM_ACT_GELU: return z * normal_cdf<FAST>(z);
+    case GEMM_ACT_GELU_TANH: return z * sigmoid<FAST>(gelu_tanh_arg(z));
+    case GEMM_ACT_SILU: return z * sigmoid<FAST>(z);
+    case GEMM_ACT_SIGMOID: return sigmoid<FAST>(z);
+    default: return z;
+  }
+}
+
+// act(z) and act'(z) together (they share their exponential). Where the sigmoid has
+// saturated, s (1 - s) is 0 and the second term of the slope is left out: its other factor
+// may be infinite there.
+template <bool FAST>
+__device__ __forceinline__ void activate_slope(float z, int act, float &a, float &d) {
+  switch (act) {
+    case GEMM_ACT_RELU:
+      a = z > 0.0f ? z : z != z ? z : 0.0f;
+      d = z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+      return;
+    case GEMM_ACT_GELU: {
+      const float p = normal_cdf<FAST>(z);
+      const float e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
+      a = z * p;
+      d = p + (e > 0.0f ? z * kInvSqrt2Pi * e : 0.0f);
+      return;
+    }
+    case GEMM_ACT_GELU_TANH: {
+      const float s = sigmoid<FAST>(gelu_tanh_arg(z));
+      const float t = s * (1.0f - s);
+      a = z * s;
+      d = s + (t > 0.0f ? z * t * (2.0f * kSqrt2OverPi) * fmaf(3.0f * kGeluCubic * z, z, 1.0f) : 0.0f);
+      return;
+    }
+    case GEMM_ACT_SILU: {
+      const float s = sigmoid<FAST>(z);
+      const float t = s * (1.0f - s);
+      a = z * s;
+      d = s + (t > 0.0f ? z * t : 0.0f);
+      return;
+    }
+    case GEMM_ACT_SIGMOID:
+      a = sigmoid<FAST>(z);
+      d = a * (1.0f - a);
+      return;
+    default:
+      a = z;
+      d = 1.0f;
+      return;
+  }
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

@@ -53,6 +53,9 @@ struct gemm_handle_s {
   void *st_buf = nullptr;
   size_t st_bytes = 0;
   size_t hp_bytes = 0;
+  // feed-forward operators: products kept in fp32, slopes, partial column sums
+  void *ff_buf = nullptr;
+  size_t ff_bytes = 0;
   cudaStream_t hp_stream[3] = {nullptr, nullptr, nullptr};  // H2D, compute, D2H
   cudaEvent_t hp_event[2 + 4 * kMaxPanels] = {};
   bool hp_ready = false;

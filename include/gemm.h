@@ -287,6 +287,119 @@ GEMM_API gemm_status_t gemm_softmax_rows(gemm_handle_t h, int64_t M, int64_t N, 
                                          int64_t ldx, void *Y, int64_t ldy, gemm_dtype_t in_dtype,
                                          gemm_dtype_t out_dtype, void *cuda_stream);
 
+/* --------------------------------------------------- feed-forward operators
+ *
+ * The operators around a transformer's feed-forward block, on row-major matrices whose rows
+ * are tokens: a product with what follows it in its epilogue, the gated pair of projections,
+ * layer norm, and the backward pass of each. Common rules: M == 0 writes no row (sums over
+ * rows are then written as zeros); element sizes, alignment, precision modes, streams and
+ * errors are those of gemm_run_ex (any alignment to the element size is accepted); an output
+ * may not overlap an input or another output except where an entry says so; NaN and infinite
+ * inputs give what the formulas give. Sums, statistics and activations are computed in fp32. */
+
+typedef enum {
+  GEMM_ACT_NONE = 0,
+  GEMM_ACT_RELU = 1,      /* max(z, 0) */
+  GEMM_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  GEMM_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  GEMM_ACT_SILU = 4,      /* z / (1 + exp(-z)) */
+  GEMM_ACT_SIGMOID = 5    /* 1 / (1 + exp(-z)) */
+} gemm_activation_t;
+
+typedef struct {
+  const void *bias;       /* N values of bias_dtype added to every row, or NULL */
+  const void *residual;   /* M x N row-major, out_dtype, added after the activation, or NULL */
+  int64_t ld_residual;    /* >= N */
+  void *pre;              /* M x N row-major, out_dtype: receives z, or NULL */
+  int64_t ld_pre;         /* >= N */
+  int32_t bias_dtype;     /* gemm_dtype_t */
+  int32_t activation;     /* gemm_activation_t */
+} gemm_epilogue_t;
+
+/* z = A @ B + bias, C = act(z) + residual; z is also stored to `pre` when that is given (the
+ * backward pass reads it). Products, layouts, precision modes and checks are gemm_run_ex's;
+ * z, act(z) and the sum are fp32 and rounded once each where they are stored. C may be the
+ * residual itself (same address and leading dimension). `epilogue` NULL or empty is
+ * gemm_run_ex. 16-bit inputs run in one kernel: with few rows the outputs' features are the
+ * rows of the tensor-core tile and K is split over a cluster; with many, 256 x 256 tiles. fp32
+ * inputs run the product of their precision mode and then a kernel for what follows it.
+ * Errors: those of gemm_run_ex; INVALID_ARG for an unknown activation or bias type, a leading
+ * dimension below N, or overlapping buffers; ALIGNMENT for a bias, residual or pre pointer
+ * that is not aligned to its element size. */
+GEMM_API gemm_status_t gemm_run_epilogue(gemm_handle_t h, int64_t M, int64_t N, int64_t K,
+                                         const void *A, int64_t lda, const void *B, int64_t ldb,
+                                         void *C, int64_t ldc, gemm_dtype_t in_dtype,
+                                         gemm_dtype_t out_dtype, gemm_precision_t precision_mode,
+                                         gemm_layout_t a_layout, gemm_layout_t b_layout,
+                                         const gemm_epilogue_t *epilogue, void *cuda_stream);
+
+/* Backward pass of gemm_run_epilogue: from dY (M x N, out_dtype) and the stored pre-activation
+ * `pre` (out_dtype; needed unless the activation is NONE),
+ *     dz = dY * act'(pre),  dA = dz @ B^T,  dB = A^T @ dz,  dbias_j = sum_i dz_ij;
+ * the residual's gradient is dY itself. A, B, dA and dB have in_dtype; dA and dB are stored in
+ * the layouts of A and B. Any of dA, dB, dbias may be NULL. dbias sums dz in fp32; for the two
+ * products dz is rounded to in_dtype, the type the tensor cores take (GEMM_PREC_F16_ACC is
+ * UNSUPPORTED). relu's slope at 0 is 0. */
+GEMM_API gemm_status_t gemm_run_epilogue_backward(
+    gemm_handle_t h, int64_t M, int64_t N, int64_t K, const void *dY, int64_t lddy,
+    const void *pre, int64_t ld_pre, const void *A, int64_t lda, const void *B, int64_t ldb,
+    void *dA, int64_t ldda, void *dB, int64_t lddb, void *dbias, gemm_dtype_t bias_dtype,
+    gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, gemm_precision_t precision_mode,
+    gemm_layout_t a_layout, gemm_layout_t b_layout, gemm_activation_t activation,
+    void *cuda_stream);
+
+/* The gated pair of projections of a feed-forward block: with g = X @ Wg and u = X @ Wu
+ * (X: M x K row-major; Wg, Wu: K x F in w_layout),
+ *     H = act(g) * u,
+ * all of one dtype, row-major outputs. `gate` and `up` (both or neither NULL) receive g and u
+ * for the backward pass. 16-bit types run in one kernel that reads X once for both products.
+ * GEMM_PREC_F16_ACC is UNSUPPORTED. */
+GEMM_API gemm_status_t gemm_run_gated(gemm_handle_t h, int64_t M, int64_t F, int64_t K,
+                                      const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
+                                      const void *Wu, int64_t ldwu, void *H, int64_t ldh,
+                                      void *gate, int64_t ld_gate, void *up, int64_t ld_up,
+                                      gemm_dtype_t dtype, gemm_precision_t precision_mode,
+                                      gemm_layout_t w_layout, gemm_activation_t activation,
+                                      void *cuda_stream);
+
+/* Backward pass of gemm_run_gated from dH and the stored g and u (all M x F row-major):
+ *     dg = dH * u * act'(g),  du = dH * act(g),
+ *     dX = dg @ Wg^T + du @ Wu^T,  dWg = X^T @ dg,  dWu = X^T @ du,
+ * dWg and dWu in w_layout. Any of dX, dWg, dWu may be NULL. dg and du are rounded to the
+ * dtype, the type the tensor cores take; the two products of dX are one fp32 sum. */
+GEMM_API gemm_status_t gemm_run_gated_backward(
+    gemm_handle_t h, int64_t M, int64_t F, int64_t K, const void *dH, int64_t lddh,
+    const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, const void *X, int64_t ldx,
+    const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu, void *dX, int64_t lddx, void *dWg,
+    int64_t lddwg, void *dWu, int64_t lddwu, gemm_dtype_t dtype, gemm_precision_t precision_mode,
+    gemm_layout_t w_layout, gemm_activation_t activation, void *cuda_stream);
+
+/* Layer norm of each of the M rows of X (M x N row-major, in_dtype):
+ *     mean = sum_j x_j / N,  rstd = 1 / sqrt(sum_j (x_j - mean)^2 / N + eps),
+ *     Y_j = (x_j - mean) * rstd * weight_j + bias_j.
+ * weight and bias: N values of param_dtype, or NULL (1 and 0). mean and rstd: M fp32 values
+ * each for the backward pass, or NULL. In place (Y == X, same leading dimension and dtype) is
+ * allowed. eps must be finite and >= 0. M == 0 or N == 0 is a no-op. */
+GEMM_API gemm_status_t gemm_layer_norm(gemm_handle_t h, int64_t M, int64_t N, const void *X,
+                                       int64_t ldx, const void *weight, const void *bias, void *Y,
+                                       int64_t ldy, float *mean, float *rstd, float eps,
+                                       gemm_dtype_t in_dtype, gemm_dtype_t param_dtype,
+                                       gemm_dtype_t out_dtype, void *cuda_stream);
+
+/* Backward pass of gemm_layer_norm from dY (out_dtype), X and the stored mean and rstd: with
+ * xh = (x - mean) * rstd and v = dY * weight,
+ *     dX_j = rstd * (v_j - sum_k v_k / N - xh_j * sum_k v_k xh_k / N)   (in_dtype),
+ *     dweight_j = sum_i dY_ij xh_ij,  dbias_j = sum_i dY_ij             (param_dtype).
+ * Any of dX, dweight, dbias may be NULL. The sums over rows run in a fixed order: the same
+ * call gives the same bits. */
+GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int64_t N,
+                                                const void *dY, int64_t lddy, const void *X,
+                                                int64_t ldx, const void *weight,
+                                                const float *mean, const float *rstd, void *dX,
+                                                int64_t lddx, void *dweight, void *dbias,
+                                                gemm_dtype_t in_dtype, gemm_dtype_t param_dtype,
+                                                gemm_dtype_t out_dtype, void *cuda_stream);
+
 /* ------------------------------------------------------------------- tuning */
 
 typedef struct {
