@@ -178,6 +178,13 @@ cudaError_t stage_operand(const OperandPlan &o, void *dst, int es, cudaStream_t 
 gemm_status_t launch_tc(const Problem &P, const Plan &pl, const void *a_ptr, int64_t a_ld,
                         const void *b_ptr, int64_t b_ld, int *status, uint64_t timeout_ns,
                         int group_m, int debug_flags, SplitK sk, cudaStream_t s);
+// tcgen05 instruction descriptor of 16-bit or tf32 operands with an fp32 accumulator.
+uint32_t make_idesc(int in_dtype, bool a_mn, bool b_mn, int n, int m);
+// The handle's split-K workspace for `slots` workers and block_n-wide partial tiles.
+gemm_status_t split_workspace(gemm_handle_t h, int64_t slots, int block_n, int **epoch_word,
+                              int **flags, float **partials, CUtensorMap *tmP, cudaStream_t s);
+// GEMM_OPT_FAULT_STALL_PRODUCER value -> kernel debug flags.
+int stall_flags(int v);
 // record_events: record the handle's gemm_set_kernel_events pair around the main kernel
 // (the calls gemm_set_kernel_events documents; not the host pipeline or the tuner).
 gemm_status_t execute(gemm_handle_t h, const Problem &P, const Plan &pl, cudaStream_t s,

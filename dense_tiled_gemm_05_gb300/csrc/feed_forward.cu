@@ -5,10 +5,11 @@
 #include <cmath>
 
 #include "api_internal.h"
-#include "ff_internal.h"
+#include "ff_launch.h"
 
 using namespace gemm_gb300;
 using namespace gemm_gb300::api;
+using ff::Carve;
 
 namespace {
 
@@ -59,16 +60,6 @@ bool bad_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int layou
   if (rows == 0 || cols == 0) return false;
   return !p || ld < (layout == GEMM_ROW_MAJOR ? cols : rows);
 }
-
-// The handle's feed-forward buffer, cut into 256-byte aligned pieces.
-struct Carve {
-  size_t bytes = 0;
-  size_t take(int64_t n, int es) {
-    const size_t off = bytes;
-    bytes += static_cast<size_t>(round_up(n * es, 256));
-    return off;
-  }
-};
 
 gemm_status_t ensure_ff(gemm_handle_t h, size_t bytes) {
   if (bytes <= h->ff_bytes) return GEMM_OK;
@@ -129,6 +120,15 @@ gemm_status_t operand_gradients(gemm_handle_t h, int64_t M, int64_t N, int64_t K
   return st;
 }
 
+// Runs a product on the fused kernels when they take it.
+gemm_status_t fused(gemm_handle_t h, ff::FusedProduct &q, bool *taken, cudaStream_t s) {
+  Carve carve;
+  *taken = ff::plan_fused(h, &q, &carve);
+  if (!*taken) return GEMM_OK;
+  const gemm_status_t st = ensure_ff(h, carve.bytes);
+  return st == GEMM_OK ? ff::run_fused(h, q, static_cast<char *>(h->ff_buf), s) : st;
+}
+
 gemm_status_t check_epilogue(const Problem &P, const gemm_epilogue_t &E) {
   if (!valid_act(E.activation)) return GEMM_ERR_INVALID_ARG;
   if (E.bias && !valid_dtype(E.bias_dtype)) return GEMM_ERR_INVALID_ARG;
@@ -183,6 +183,18 @@ GEMM_API gemm_status_t gemm_run_epilogue(gemm_handle_t h, int64_t M, int64_t N, 
   if (!g.ok) return GEMM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (ep.empty()) return product(h, P, s);
+  if (precision_mode == GEMM_PREC_DEFAULT) {
+    ff::FusedProduct q;
+    q.M = M, q.N = N, q.K = K;
+    q.X.ptr = A, q.X.ld = lda, q.X.layout = a_layout;
+    q.W.ptr = B, q.W.ld = ldb, q.W.layout = b_layout;
+    q.in_dtype = in_dtype, q.out_dtype = out_dtype;
+    q.C = C, q.ldc = ldc;
+    q.ep = ep;
+    bool taken = false;
+    st = fused(h, q, &taken, s);
+    if (taken) return st;
+  }
   // The product in fp32 first: into C itself when C is fp32 and not the residual, else into
   // the handle's buffer.
   Problem Q = P;
@@ -296,6 +308,20 @@ GEMM_API gemm_status_t gemm_run_gated(gemm_handle_t h, int64_t M, int64_t F, int
   DeviceGuard guard(h->device);
   if (!guard.ok) return GEMM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  ff::FusedProduct q;
+  q.gated = true;
+  q.M = M, q.N = F, q.K = K;
+  q.X.ptr = X, q.X.ld = ldx;
+  q.W.ptr = Wg, q.W.ld = ldwg, q.W.layout = w_layout;
+  q.W2.ptr = Wu, q.W2.ld = ldwu, q.W2.layout = w_layout;
+  q.in_dtype = q.out_dtype = dtype;
+  q.C = H, q.ldc = ldh;
+  q.ep.act = activation;
+  q.ep.pre = gate, q.ep.ld_pre = ld_gate;
+  q.pre2 = up, q.ld_pre2 = ld_up;
+  bool taken = false;
+  st = fused(h, q, &taken, s);
+  if (taken) return st;
   // Both products in fp32 (into gate and up themselves when those are fp32), then h.
   const bool keep32 = gate && dtype == GEMM_F32;
   Problem PG = G, PU = U;
@@ -371,9 +397,20 @@ GEMM_API gemm_status_t gemm_run_gated_backward(
   // dg | du side by side, so that one product can take both
   const int64_t Fp = round_up(F, 16 / es), ldd = 2 * Fp;
   const int64_t ld32 = round_up(K, 4);
+  const bool make_dx = dX && M > 0 && K > 0;
   Carve carve;
   const size_t d_off = carve.take(M * ldd, es);
-  const size_t x_off = dX ? carve.take(M * ld32, 4) : 0, x2_off = dX ? carve.take(M * ld32, 4) : 0;
+  ff::FusedProduct q;  // dX = dg Wg^T + du Wu^T in one accumulator
+  q.M = M, q.N = K, q.K = q.K2 = F;
+  q.X.ld = q.X2.ld = ldd;
+  // (addresses in the handle's buffer once it is sized; 256-byte aligned, so never staged)
+  q.W.ptr = Wg, q.W.ld = ldwg, q.W2.ptr = Wu, q.W2.ld = ldwu;
+  q.W.layout = q.W2.layout = flip(w_layout);
+  q.in_dtype = q.out_dtype = dtype;
+  q.C = dX, q.ldc = lddx;
+  const bool taken = make_dx && ff::plan_fused(h, &q, &carve);
+  const size_t x_off = make_dx && !taken ? carve.take(M * ld32, 4) : 0;
+  const size_t x2_off = make_dx && !taken ? carve.take(M * ld32, 4) : 0;
   gemm_status_t st = ensure_ff(h, carve.bytes);
   if (st != GEMM_OK) return st;
   char *buf = static_cast<char *>(h->ff_buf);
@@ -384,7 +421,11 @@ GEMM_API gemm_status_t gemm_run_gated_backward(
                   "gated backward launch");
     if (st != GEMM_OK) return st;
   }
-  if (dX && M > 0 && K > 0) {
+  if (taken) {
+    q.X.ptr = dg, q.X2.ptr = du;
+    st = ff::run_fused(h, q, buf, s);
+    if (st != GEMM_OK) return st;
+  } else if (make_dx) {
     // two products in fp32, added and rounded once
     float *x32 = reinterpret_cast<float *>(buf + x_off), *x2 = reinterpret_cast<float *>(buf + x2_off);
     st = product(h, Problem{M, K, F, dg, ldd, Wg, ldwg, x32, ld32, dtype, GEMM_F32, precision_mode,
@@ -396,6 +437,11 @@ GEMM_API gemm_status_t gemm_run_gated_backward(
       st = launched(h, ff::add_rows_launch(x32, ld32, x2, ld32, dX, lddx, dtype, M, K, s), "sum of products");
     if (st != GEMM_OK) return st;
   }
+  // Gradients that adjoin in memory are one product with both halves of dg | du.
+  if (dWg && dWu && Fp == F && w_layout == GEMM_COL_MAJOR && lddwg == lddwu &&
+      static_cast<char *>(dWu) - static_cast<char *>(dWg) == F * lddwg * es)
+    return operand_gradients(h, M, 2 * F, K, dg, ldd, X, ldx, GEMM_ROW_MAJOR, nullptr, 0, w_layout,
+                             nullptr, 0, dWg, lddwg, dtype, precision_mode, s);
   for (int i = 0; i < 2 && st == GEMM_OK; ++i) {
     void *dW = i ? dWu : dWg;
     if (!dW) continue;

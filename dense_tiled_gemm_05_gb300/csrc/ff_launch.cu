@@ -1,0 +1,200 @@
+// ff_launch.cu -- host side of the fused products (ff_few_kernel.cu, ff_pair_kernel.cu): which
+// kernel and tile a product takes, copies of operands TMA cannot address, tensor maps, launch.
+#include <cstring>
+
+#include "ff_launch.h"
+
+using namespace gemm_gb300::api;
+
+namespace gemm_gb300 {
+namespace ff {
+
+namespace {
+
+bool tma_legal(const void *p, int64_t ld, int64_t lines, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (lines <= 1 || (ld * es) % 16 == 0);
+}
+
+// rows x cols operand with the K extent along columns (X) or rows (W).
+void plan_x(FusedOperand *o, int64_t M, int64_t K, Carve *carve) {
+  o->transpose = o->layout == GEMM_COL_MAJOR;
+  o->staged = o->transpose || !tma_legal(o->ptr, o->ld, M, 2);
+  if (!o->staged) return;
+  o->staged_ld = round_up(K, 8);
+  o->offset = carve->take(M * o->staged_ld, 2);
+}
+void plan_w(FusedOperand *o, int64_t K, int64_t N, Carve *carve) {
+  const int64_t lines = o->layout == GEMM_ROW_MAJOR ? K : N, len = o->layout == GEMM_ROW_MAJOR ? N : K;
+  o->staged = !tma_legal(o->ptr, o->ld, lines, 2);
+  if (!o->staged) return;
+  o->staged_ld = round_up(len, 8);
+  o->offset = carve->take(lines * o->staged_ld, 2);
+}
+
+// Tiles and cluster split of the few-token kernel.
+void plan_few(FusedProduct *q, int64_t k_blocks, int sm_count) {
+  FewParams &p = q->few_params;
+  const int most = q->gated ? 128 : 256;
+  p.tile_t = static_cast<int>(q->M >= most ? most : round_up(q->M, 16));
+  p.tiles_t = static_cast<int>((q->M + p.tile_t - 1) / p.tile_t);
+  p.tiles_f = static_cast<int>((q->N + kFewFeatures - 1) / kFewFeatures);
+  const int64_t tiles = static_cast<int64_t>(p.tiles_t) * p.tiles_f;
+  // Two CTAs share an SM while their rings leave each several stages; a token tile wide
+  // enough to fill the SM's shared memory runs alone.
+  const size_t stage = few_stage_bytes(q->gated, p.tile_t);
+  const bool two = few_smem_bytes(q->gated, p.tile_t, 3) <= 113 * 1024;
+  const int64_t slots = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * (two ? 2 : 1);
+  // The widest split that still fits one round of slots, with at least four K-blocks each.
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= slots && k_blocks >= 8 * p.splits) p.splits *= 2;
+  int64_t stages = static_cast<int64_t>(((two ? 113 : 226) * 1024 - kFewFixedBytes) / stage);
+  const int64_t per_cta = (k_blocks + p.splits - 1) / p.splits;
+  if (stages > per_cta) stages = per_cta;
+  if (stages > 16) stages = 16;
+  p.stages = static_cast<int>(stages < 1 ? 1 : stages);
+}
+
+cudaError_t stage(const FusedOperand &o, int64_t lines, int64_t len, char *buf, cudaStream_t s) {
+  if (o.transpose) return transpose_launch(o.ptr, o.ld, buf + o.offset, o.staged_ld, lines, len, 2, s);
+  return repack_launch(o.ptr, o.ld, buf + o.offset, o.staged_ld, lines, len, 2, s);
+}
+
+bool aligned(const void *p, int64_t ld, int es, int elems) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (es * elems) == 0 && ld % elems == 0);
+}
+
+}  // namespace
+
+bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
+  if (q->in_dtype == GEMM_F32 || q->M < 1 || q->N < 1 || q->K < 1) return false;
+  if (h->force_path == 2) return false;  // the FMA kernel was asked for
+  if (q->gated && q->out_dtype != q->in_dtype) return false;
+  const int64_t k_blocks = (q->K + 63) / 64 + (q->K2 + 63) / 64;
+  const int64_t tile_n = q->gated ? 128 : 256;
+  q->tiles_m = (q->M + 255) / 256;
+  q->tiles_n = (q->N + tile_n - 1) / tile_n;
+  const int64_t clusters = h->sm_count > 1 ? h->sm_count / 2 : 1;
+  if (q->tiles_m * q->tiles_n > INT32_MAX / 8 || k_blocks > INT32_MAX) return false;
+  // Few tiles of 256 rows, or rows that would fill less than half of one: the few-token
+  // kernel, whose tiles are smaller and share their K-loops over clusters.
+  q->few = q->M <= 128 || 2 * q->tiles_m * q->tiles_n <= clusters;
+  if (h->cta_pair) q->few = h->cta_pair == 1;  // GEMM_OPT_CTA_PAIR
+  if (q->few) plan_few(q, k_blocks, h->sm_count);
+  plan_x(&q->X, q->M, q->K, carve);
+  plan_w(&q->W, q->K, q->N, carve);
+  if (q->gated) {
+    plan_w(&q->W2, q->K, q->N, carve);
+  } else if (q->K2 > 0) {
+    plan_x(&q->X2, q->M, q->K2, carve);
+    plan_w(&q->W2, q->K2, q->N, carve);
+  }
+  return true;
+}
+
+gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const bool two_x = !q.gated && q.K2 > 0, two_w = q.gated || q.K2 > 0;
+  struct Use {
+    const FusedOperand *o;
+    bool used, w;
+    int64_t K;
+  };
+  const Use uses[4] = {{&q.X, true, false, q.K}, {&q.W, true, true, q.K}, {&q.X2, two_x, false, q.K2},
+                       {&q.W2, two_w, true, q.gated ? q.K : q.K2}};
+  // Operand boxes are one 128-byte row of K (or, for row-major weights, of N) wide.
+  const uint32_t x_rows = q.few ? static_cast<uint32_t>(q.few_params.tile_t) : 128u;
+  CUtensorMap maps[4];
+  for (int i = 0; i < 4; ++i) {
+    if (!uses[i].used) {
+      maps[i] = maps[i & 1];  // never read
+      continue;
+    }
+    const FusedOperand &o = *uses[i].o;
+    const bool w = uses[i].w, row = o.layout == GEMM_ROW_MAJOR;
+    // as stored: `lines` lines of `len` contiguous elements
+    int64_t lines = w ? (row ? uses[i].K : q.N) : (row ? q.M : uses[i].K);
+    int64_t len = w ? (row ? q.N : uses[i].K) : (row ? uses[i].K : q.M);
+    const void *ptr = o.ptr;
+    int64_t ld = o.ld;
+    if (o.staged) {
+      e = stage(o, lines, len, buf, s);
+      if (e != cudaSuccess) return cuda_fail(e, "stage operand");
+      h->launches += 1;
+      ptr = buf + o.offset;
+      ld = o.staged_ld;
+      if (o.transpose) {
+        const int64_t t = lines;
+        lines = len, len = t;
+      }
+    }
+    const uint32_t rows = w ? (row ? 64u : 128u) : x_rows;
+    if (!encode_2d(&maps[i], q.in_dtype, ptr, len, lines, ld, 64, rows)) return GEMM_ERR_CUDA;
+  }
+  FusedParams f{};
+  f.M = static_cast<int32_t>(q.M), f.N = static_cast<int32_t>(q.N);
+  f.kb_first = static_cast<int32_t>((q.K + 63) / 64);
+  f.k_blocks = f.kb_first + static_cast<int32_t>(two_x ? (q.K2 + 63) / 64 : 0);
+  f.out_dtype = q.out_dtype;
+  f.act = q.ep.act;
+  f.bias = q.ep.bias, f.bias_dtype = q.ep.bias_dtype;
+  f.residual = q.ep.residual, f.ld_residual = q.ep.ld_residual;
+  f.C = q.C, f.ldc = q.ldc;
+  f.pre = q.ep.pre, f.ld_pre = q.ep.ld_pre;
+  f.pre2 = q.pre2, f.ld_pre2 = q.ld_pre2;
+  f.status = h->status;
+  f.timeout_ns = h->timeout_us * 1000ull;
+  f.debug_flags = stall_flags(h->stall_producer);
+  const bool w_mn = q.W.layout == GEMM_ROW_MAJOR;
+  const int os = esize_of(q.out_dtype);
+  if (q.few) {
+    FewParams p = q.few_params;
+    p.f = f;
+    p.f.idesc = make_idesc(q.in_dtype, w_mn, false, p.tile_t, 128);
+    p.vec = aligned(q.C, q.ldc, os, 4) && aligned(f.pre, f.ld_pre, os, 4) &&
+            aligned(f.pre2, f.ld_pre2, os, 4) && aligned(f.residual, f.ld_residual, os, 4);
+    e = few_launch(q.gated, w_mn, maps[0], maps[1], maps[2], maps[3], p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "few-token kernel launch");
+    h->launches += 1;
+    return GEMM_OK;
+  }
+  PairMaps pm;
+  std::memset(&pm, 0, sizeof pm);
+  pm.X = maps[0], pm.W = maps[1], pm.X2 = maps[2], pm.W2 = maps[3];
+  PairParams p{};
+  p.f = f;
+  p.f.idesc = make_idesc(q.in_dtype, false, w_mn, 256, 256);
+  p.tiles_m = static_cast<int32_t>(q.tiles_m), p.tiles_n = static_cast<int32_t>(q.tiles_n);
+  p.group_m = h->group_m < p.tiles_m ? h->group_m : p.tiles_m;
+  // TMA stores only where rows end on 16-byte boundaries (see the planner)
+  p.tma_out = (q.N * os) % 16 == 0;
+  const void *outs[4] = {q.C, f.pre, f.pre2, f.residual};
+  const int64_t lds[4] = {q.ldc, f.ld_pre, f.ld_pre2, f.ld_residual};
+  CUtensorMap *out_maps[4] = {&pm.C, &pm.Z, &pm.Z2, &pm.R};
+  for (int i = 0; i < 4; ++i)
+    p.tma_out = p.tma_out && (!outs[i] || tma_legal(outs[i], lds[i], 2, os));
+  for (int i = 0; i < 4 && p.tma_out; ++i)
+    if (outs[i] && !encode_2d(out_maps[i], q.out_dtype, outs[i], q.N, q.M, lds[i],
+                              static_cast<uint32_t>(128 / os), 32))
+      return GEMM_ERR_CUDA;
+  const int64_t fit = tc2_max_active_clusters();
+  if (fit <= 0) return GEMM_ERR_CUDA;
+  const int64_t tiles = q.tiles_m * q.tiles_n;
+  int64_t slots = h->sm_count > 1 ? h->sm_count / 2 : 1;
+  if (slots > fit) slots = fit;
+  const int32_t t32 = static_cast<int32_t>(tiles), s32 = static_cast<int32_t>(slots);
+  p.sk_dp_tiles = sk_dp_tiles(t32, p.f.k_blocks, s32, use_split_k(h->stream_k, tiles, p.f.k_blocks, slots));
+  if (p.sk_dp_tiles < t32) {
+    const gemm_status_t st = split_workspace(h, slots, 256, &p.sk_epoch_word, &p.sk_flags,
+                                             &p.sk_partials, &pm.P, s);
+    if (st != GEMM_OK) return st;
+  } else if (slots > tiles) {
+    slots = tiles;
+  }
+  e = pair_launch(q.gated, w_mn, pm, p, static_cast<int>(2 * slots), s);
+  if (e != cudaSuccess) return cuda_fail(e, "fused product launch");
+  h->launches += 1;
+  return GEMM_OK;
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

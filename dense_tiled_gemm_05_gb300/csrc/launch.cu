@@ -107,7 +107,7 @@ bool encode_3d_panels(CUtensorMap *m, int dtype, const void *base, int64_t mn, i
   return r == CUDA_SUCCESS;
 }
 
-static uint32_t make_idesc(int in_dtype, bool a_mn, bool b_mn, int n, int m) {
+uint32_t make_idesc(int in_dtype, bool a_mn, bool b_mn, int n, int m) {
   const uint32_t fmt = in_dtype == GEMM_F16 ? 0u : in_dtype == GEMM_BF16 ? 1u : 2u;
   uint32_t d = 0;
   d |= 1u << 4;                               // accumulator: f32
@@ -168,6 +168,27 @@ static gemm_status_t ensure_sk_workspace(gemm_handle_t h, size_t bytes, size_t f
   h->sk_ws = p;
   h->sk_ws_bytes = bytes;
   return GEMM_OK;
+}
+
+// The split-K workspace of `slots` workers and its tensor map.
+// Layout: [epoch word, arrival count | one flag per epilogue warp of each CTA of the largest
+// grid (8 per CTA) | partial tiles]. The flag region has a fixed size, so a grown workspace
+// never finds partial data where flags are expected.
+gemm_status_t split_workspace(gemm_handle_t h, int64_t slots, int block_n, int **epoch_word,
+                              int **flags, float **partials, CUtensorMap *tmP, cudaStream_t s) {
+  const int64_t ctas_max = h->sm_count > 2 * slots ? h->sm_count : 2 * slots;
+  const size_t flag_region =
+      static_cast<size_t>(round_up(static_cast<int64_t>((2 + 8 * ctas_max) * sizeof(int)), 256));
+  const size_t part_bytes = static_cast<size_t>(slots) * 2 * kTcBlockM * block_n * sizeof(float);
+  const gemm_status_t st = ensure_sk_workspace(h, flag_region + part_bytes, flag_region, s);
+  if (st != GEMM_OK) return st;
+  *epoch_word = static_cast<int *>(h->sk_ws);
+  *flags = *epoch_word + 2;
+  *partials = reinterpret_cast<float *>(static_cast<char *>(h->sk_ws) + flag_region);
+  // partial tiles: rows [worker][cta rank][128], block_n fp32 columns; 32 x 32 boxes
+  return encode_2d(tmP, GEMM_F32, *partials, block_n, slots * 2 * kTcBlockM, block_n, 32, 32)
+             ? GEMM_OK
+             : GEMM_ERR_CUDA;
 }
 
 // Tensor maps, kernel parameters and launch of the tensor-core kernel for operands that
@@ -268,23 +289,9 @@ gemm_status_t launch_tc(const Problem &P, const Plan &pl, const void *a_ptr, int
     tp.sk_dp_tiles = sk_dp_tiles(tiles, tp.k_blocks, slots,
                                  use_split_k(sk.mode, tiles, tp.k_blocks, slots));
     if (tp.sk_dp_tiles < tiles) {
-      // Workspace: [epoch word, arrival count | one flag per epilogue warp of each CTA of
-      // the largest grid (8 per CTA) | partial tiles]. The flag region has a fixed size, so
-      // a grown workspace never finds partial data where flags are expected.
-      const int64_t ctas_max = sk.h->sm_count > grid ? sk.h->sm_count : grid;
-      const size_t flag_region =
-          static_cast<size_t>(round_up(static_cast<int64_t>((2 + 8 * ctas_max) * sizeof(int)), 256));
-      const size_t part_bytes =
-          static_cast<size_t>(slots) * 2 * kTcBlockM * pl.variant.block_n * sizeof(float);
-      gemm_status_t st = ensure_sk_workspace(sk.h, flag_region + part_bytes, flag_region, s);
+      const gemm_status_t st = split_workspace(sk.h, slots, pl.variant.block_n, &tp.sk_epoch_word,
+                                               &tp.sk_flags, &tp.sk_partials, &tmP, s);
       if (st != GEMM_OK) return st;
-      tp.sk_epoch_word = static_cast<int *>(sk.h->sk_ws);
-      tp.sk_flags = tp.sk_epoch_word + 2;
-      tp.sk_partials = reinterpret_cast<float *>(static_cast<char *>(sk.h->sk_ws) + flag_region);
-      // partial tiles: rows [worker][cta rank][128], block_n fp32 columns; 32 x 32 boxes
-      if (!encode_2d(&tmP, GEMM_F32, tp.sk_partials, pl.variant.block_n,
-                     static_cast<int64_t>(slots) * 2 * kTcBlockM, pl.variant.block_n, 32, 32))
-        return GEMM_ERR_CUDA;
     }
   }
   const cudaError_t e = tc_launch(pl.variant, tmA, tmB, tmC, tmP, tp, static_cast<int>(grid), s);
@@ -293,7 +300,7 @@ gemm_status_t launch_tc(const Problem &P, const Plan &pl, const void *a_ptr, int
 
 // GEMM_OPT_FAULT_STALL_PRODUCER value -> kernel debug flags: 1, no loads at all; v >= 2,
 // the loader of CTA rank (v & 1) stops after v >> 1 stage fills.
-static int stall_flags(int v) {
+int stall_flags(int v) {
   if (v == 1) return kDebugStallProducer;
   if (v >= 2) return ((v >> 1) << kDebugStallAfterShift) | ((v & 1) ? kDebugStallRank1 : 0);
   return 0;
