@@ -206,27 +206,59 @@ def operand_layout(x):
     raise ValueError("operand must be row- or column-major, got stride %s" % (x.stride(),))
 
 
-def _row_ld(x, shape, what, device=None):
-    """Leading dimension of a CUDA matrix with contiguous rows and the given shape."""
-    if x.dim() != 2 or tuple(x.shape) != shape:
-        raise ValueError("%s must be a %d x %d tensor, got %s" % ((what,) + shape + (tuple(x.shape),)))
-    if not x.is_cuda or (device is not None and x.device != device):
-        raise ValueError("%s must be a CUDA tensor on the operands' device" % what)
-    rows, cols = shape
-    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
+# The feed-forward operators' calls are short enough that a generation loop waits for the
+# host: these helpers ask a tensor for each thing once, in the cheapest form (device indices
+# instead of device objects, the raw stream handle instead of a torch.cuda.Stream).
+
+def _rows(x, what):
+    """(rows, columns, leading dimension) of a CUDA matrix with contiguous rows."""
+    if x.dim() != 2:
+        raise ValueError("%s must be 2-D" % what)
+    rows, cols = x.shape
+    s0, s1 = x.stride()
+    if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
         raise ValueError("rows of %s must be contiguous" % what)
-    return x.stride(0) if rows > 1 else max(cols, 1)
+    return rows, cols, s0 if rows > 1 else cols or 1
 
 
-def _vector(x, n, what, device):
+def _row_ld(x, rows, cols, what, dev):
+    """Leading dimension of a rows x cols matrix on device `dev`."""
+    r, c, ld = _rows(x, what)
+    if r != rows or c != cols:
+        raise ValueError("%s must be a %d x %d tensor, got %d x %d" % (what, rows, cols, r, c))
+    if x.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the operands' device" % what)
+    return ld
+
+
+def _vector(x, n, what, dev):
     """Data pointer of a contiguous vector of n values (0 for None)."""
     if x is None:
         return 0
-    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+    if x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
         raise ValueError("%s must be a contiguous vector of %d values" % (what, n))
-    if x.device != device:
-        raise ValueError("%s must be on the operands' device" % what)
+    if x.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the operands' device" % what)
     return x.data_ptr()
+
+
+def _code(dtype):
+    """gemm_dtype_t of a torch dtype."""
+    code = _DT.get(dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % dtype)
+    return code
+
+
+def _cuda_index(x, what):
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    return dev
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _activation(name):
@@ -399,20 +431,20 @@ class Gemm:
 
     # ------------------------------------------------------- feed-forward operators
 
-    def _stream(self, x, stream):
-        return (torch.cuda.current_stream(x.device) if stream is None else stream).cuda_stream
-
     def _two(self, a, b):
-        """Checked extents of a product's operands."""
+        """Checked extents and device of a product's operands."""
+        dev = a.get_device()
+        if dev < 0 or b.get_device() != dev:
+            raise ValueError("operands must be CUDA tensors on one device")
         if a.dtype != b.dtype:
             raise TypeError("operands must share a dtype")
-        if not (a.is_cuda and b.is_cuda) or a.device != b.device:
-            raise ValueError("operands must be CUDA tensors on one device")
         if a.dim() != 2 or b.dim() != 2:
             raise ValueError("operands must be 2-D")
-        if a.shape[1] != b.shape[0]:
-            raise ValueError("inner dimensions differ: %d vs %d" % (a.shape[1], b.shape[0]))
-        return a.shape[0], b.shape[1], a.shape[1]
+        M, K = a.shape
+        K2, N = b.shape
+        if K != K2:
+            raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
+        return M, N, K, dev
 
     def matmul_epilogue(self, a, b, bias=None, activation=None, residual=None, out=None,
                         out_dtype=None, precision="default", save=False, stream=None):
@@ -421,33 +453,33 @@ class Gemm:
         M x N of the output's dtype (``out=residual`` updates it in place). activation: None,
         "relu", "gelu", "gelu_tanh", "silu" or "sigmoid". ``save=True`` returns (out, pre)
         with pre = a @ b + bias for :meth:`matmul_epilogue_backward`."""
-        M, N, K = self._two(a, b)
-        dev = a.device
-        if out is None:
-            od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else a.dtype
-            out = torch.empty((M, N), dtype=od, device=dev)
-        ep = Epilogue()
-        ep.activation = _activation(activation)
-        if bias is not None:
-            ep.bias = _vector(bias, N, "bias", dev)
-            ep.bias_dtype = _dtype_code(bias.dtype)
+        M, N, K, dev = self._two(a, b)
+        dtype = a.dtype
+        in_code = _code(dtype)
+        if out is not None:
+            dtype, ldc = out.dtype, _row_ld(out, M, N, "out", dev)
+        else:
+            if out_dtype is not None:
+                dtype = _TORCH_OF[_dtype_code(out_dtype)]
+            out, ldc = torch.empty((M, N), dtype=dtype, device=a.device), N or 1
+        ld_residual = residual_ptr = 0
         if residual is not None:
-            if residual.dtype != out.dtype:
+            if residual.dtype != dtype:
                 raise TypeError("residual must have the output's dtype")
-            ep.ld_residual = _row_ld(residual, (M, N), "residual", dev)
-            ep.residual = residual.data_ptr()
-        pre = None
-        if save:
-            pre = torch.empty((M, N), dtype=out.dtype, device=dev)
-            ep.pre, ep.ld_pre = pre.data_ptr(), max(N, 1)
+            ld_residual = _row_ld(residual, M, N, "residual", dev)
+            residual_ptr = residual.data_ptr()
+        pre = torch.empty((M, N), dtype=dtype, device=a.device) if save else None
+        ep = Epilogue(_vector(bias, N, "bias", dev), residual_ptr, ld_residual,
+                      pre.data_ptr() if save else 0, N or 1,
+                      0 if bias is None else _code(bias.dtype), _activation(activation))
         al, lda = operand_layout(a)
         bl, ldb = operand_layout(b)
-        code = lib().gemm_run_epilogue(self._h, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb,
-                                       out.data_ptr(), _row_ld(out, (M, N), "out", dev),
-                                       _dtype_code(a.dtype), _dtype_code(out.dtype),
-                                       PREC[precision], al, bl, ctypes.byref(ep),
-                                       self._stream(a, stream))
-        _check(code, "gemm_run_epilogue")
+        code = (_lib or lib()).gemm_run_epilogue(
+            self._h, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldc, in_code,
+            _code(dtype), PREC[precision], al, bl, ep,
+            _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            raise GemmError(code, "gemm_run_epilogue")
         return (out, pre) if save else out
 
     def matmul_epilogue_backward(self, grad, a, b, pre=None, activation=None,
@@ -457,45 +489,50 @@ class Gemm:
         saved pre (needed unless there is no activation): (da, db, dbias), each None where
         ``need`` says so; da and db in the layouts of a and b, dbias in ``bias_dtype``
         (default: a's). The residual's gradient is grad itself."""
-        M, N, K = self._two(a, b)
-        dev = a.device
+        M, N, K, dev = self._two(a, b)
         act = _activation(activation)
-        lddy = _row_ld(grad, (M, N), "grad", dev)
+        lddy = _row_ld(grad, M, N, "grad", dev)
         ldz = 0
         if act:
             if pre is None:
                 raise ValueError("the backward pass of an activation needs the saved pre")
             if pre.dtype != grad.dtype:
                 raise TypeError("pre must have grad's dtype")
-            ldz = _row_ld(pre, (M, N), "pre", dev)
+            ldz = _row_ld(pre, M, N, "pre", dev)
         da = _like(a) if need[0] else None
         db = _like(b) if need[1] else None
         dbias = None
         if need[2]:
             bd = _TORCH_OF[_dtype_code(bias_dtype)] if bias_dtype is not None else a.dtype
-            dbias = torch.empty(N, dtype=bd, device=dev)
+            dbias = torch.empty(N, dtype=bd, device=a.device)
         al, lda = operand_layout(a)
         bl, ldb = operand_layout(b)
-        ptr = lambda t: 0 if t is None else t.data_ptr()
-        code = lib().gemm_run_epilogue_backward(
+        code = (_lib or lib()).gemm_run_epilogue_backward(
             self._h, M, N, K, grad.data_ptr(), lddy, pre.data_ptr() if act else 0, ldz,
-            a.data_ptr(), lda, b.data_ptr(), ldb, ptr(da), operand_layout(da)[1] if need[0] else 0,
-            ptr(db), operand_layout(db)[1] if need[1] else 0, ptr(dbias),
-            _dtype_code(dbias.dtype) if need[2] else 0, _dtype_code(a.dtype),
-            _dtype_code(grad.dtype), PREC[precision], al, bl, act, self._stream(a, stream))
-        _check(code, "gemm_run_epilogue_backward")
+            a.data_ptr(), lda, b.data_ptr(), ldb,
+            da.data_ptr() if need[0] else 0, operand_layout(da)[1] if need[0] else 0,
+            db.data_ptr() if need[1] else 0, operand_layout(db)[1] if need[1] else 0,
+            dbias.data_ptr() if need[2] else 0, _code(dbias.dtype) if need[2] else 0,
+            _code(a.dtype), _code(grad.dtype), PREC[precision], al, bl, act,
+            _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            raise GemmError(code, "gemm_run_epilogue_backward")
         return da, db, dbias
 
     def _gated_args(self, x, w_gate, w_up):
-        M, F, K = self._two(x, w_gate)
-        if self._two(x, w_up) != (M, F, K):
+        M, F, K, dev = self._two(x, w_gate)
+        if w_up.shape != w_gate.shape:
             raise ValueError("w_gate and w_up must have one shape")
-        ldx = _row_ld(x, (M, K), "x")
+        if w_up.dtype != x.dtype:
+            raise TypeError("operands must share a dtype")
+        if w_up.get_device() != dev:
+            raise ValueError("operands must be CUDA tensors on one device")
+        ldx = _rows(x, "x")[2]
         wl, ldg = operand_layout(w_gate)
         wl2, ldu = operand_layout(w_up)
         if wl != wl2:
             raise ValueError("w_gate and w_up must have one layout")
-        return M, F, K, ldx, wl, ldg, ldu
+        return M, F, K, dev, ldx, wl, ldg, ldu
 
     def gated(self, x, w_gate, w_up, activation="silu", out=None, precision="default",
               save=False, stream=None):
@@ -503,50 +540,54 @@ class Gemm:
         with contiguous rows, both weights K x F in one layout (stored as [F, K]: pass
         ``w.t()``). ``save=True`` returns (out, gate, up) with the two products for
         :meth:`gated_backward` (column ranges of one M x 2F buffer)."""
-        M, F, K, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
-        dev = x.device
+        M, F, K, dev, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
+        dtype = x.dtype
         if out is None:
-            out = torch.empty((M, F), dtype=x.dtype, device=dev)
-        if out.dtype != x.dtype:
-            raise TypeError("out must have x's dtype")
+            out, ldh = torch.empty((M, F), dtype=dtype, device=x.device), F or 1
+        else:
+            if out.dtype != dtype:
+                raise TypeError("out must have x's dtype")
+            ldh = _row_ld(out, M, F, "out", dev)
         gate = up = None
         if save:
-            both = torch.empty((M, 2 * F), dtype=x.dtype, device=dev)
+            both = torch.empty((M, 2 * F), dtype=dtype, device=x.device)
             gate, up = both[:, :F], both[:, F:]
-        code = lib().gemm_run_gated(
+        code = (_lib or lib()).gemm_run_gated(
             self._h, M, F, K, x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
-            out.data_ptr(), _row_ld(out, (M, F), "out", dev), gate.data_ptr() if save else 0, 2 * F,
-            up.data_ptr() if save else 0, 2 * F, _dtype_code(x.dtype), PREC[precision], wl,
-            _activation(activation), self._stream(x, stream))
-        _check(code, "gemm_run_gated")
+            out.data_ptr(), ldh, gate.data_ptr() if save else 0, 2 * F,
+            up.data_ptr() if save else 0, 2 * F, _code(dtype), PREC[precision], wl,
+            _activation(activation), _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            raise GemmError(code, "gemm_run_gated")
         return (out, gate, up) if save else out
 
     def gated_backward(self, grad, x, w_gate, w_up, gate, up, activation="silu",
                        need=(True, True, True), precision="default", stream=None):
         """Gradients of :meth:`gated` from grad (M x F) and the saved gate and up: (dx, dw_gate,
         dw_up), each None where ``need`` says so, the weights' in the weights' layout."""
-        M, F, K, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
-        dev = x.device
+        M, F, K, dev, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
+        dtype = x.dtype
         for t in (grad, gate, up):
-            if t.dtype != x.dtype:
+            if t.dtype != dtype:
                 raise TypeError("grad, gate and up must have x's dtype")
-        lds = [_row_ld(t, (M, F), n, dev) for t, n in ((grad, "grad"), (gate, "gate"), (up, "up"))]
-        dx = torch.empty((M, K), dtype=x.dtype, device=dev) if need[0] else None
+        lds = [_row_ld(t, M, F, n, dev) for t, n in ((grad, "grad"), (gate, "gate"), (up, "up"))]
+        dx = torch.empty((M, K), dtype=dtype, device=x.device) if need[0] else None
         dwg = dwu = None
         if need[1] and need[2] and wl == COL:
-            both = torch.empty((2 * F, K), dtype=x.dtype, device=dev)
+            both = torch.empty((2 * F, K), dtype=dtype, device=x.device)
             dwg, dwu = both[:F].t(), both[F:].t()
         else:
             dwg = _like(w_gate) if need[1] else None
             dwu = _like(w_up) if need[2] else None
-        ptr = lambda t: 0 if t is None else t.data_ptr()
         ldw = max(K if wl == COL else F, 1)
-        code = lib().gemm_run_gated_backward(
+        code = (_lib or lib()).gemm_run_gated_backward(
             self._h, M, F, K, grad.data_ptr(), lds[0], gate.data_ptr(), lds[1], up.data_ptr(),
-            lds[2], x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, ptr(dx),
-            max(K, 1), ptr(dwg), ldw, ptr(dwu), ldw, _dtype_code(x.dtype), PREC[precision], wl,
-            _activation(activation), self._stream(x, stream))
-        _check(code, "gemm_run_gated_backward")
+            lds[2], x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
+            dx.data_ptr() if need[0] else 0, max(K, 1), dwg.data_ptr() if need[1] else 0, ldw,
+            dwu.data_ptr() if need[2] else 0, ldw, _code(dtype), PREC[precision], wl,
+            _activation(activation), _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            raise GemmError(code, "gemm_run_gated_backward")
         return dx, dwg, dwu
 
     def layer_norm(self, x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None,
@@ -554,27 +595,34 @@ class Gemm:
         """Layer norm of each row of a CUDA matrix with contiguous rows; weight and bias (None:
         1 and 0) share a dtype of their own. ``out=x`` runs in place. ``save=True`` returns
         (out, mean, rstd) with the rows' fp32 statistics for :meth:`layer_norm_backward`."""
-        if x.dim() != 2:
-            raise ValueError("x must be 2-D")
-        M, N = x.shape
-        dev = x.device
-        ldx = _row_ld(x, (M, N), "x")
-        if weight is not None and bias is not None and weight.dtype != bias.dtype:
-            raise TypeError("weight and bias must share a dtype")
-        params = weight if weight is not None else bias
-        if out is None:
-            od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else x.dtype
-            out = torch.empty((M, N), dtype=od, device=dev)
+        dev = _cuda_index(x, "x")
+        M, N, ldx = _rows(x, "x")
+        dtype = x.dtype
+        in_code = out_code = _code(dtype)
+        params = F32
+        if weight is not None:
+            params = _code(weight.dtype)
+            if bias is not None and bias.dtype != weight.dtype:
+                raise TypeError("weight and bias must share a dtype")
+        elif bias is not None:
+            params = _code(bias.dtype)
+        if out is not None:
+            out_code, ldy = _code(out.dtype), _row_ld(out, M, N, "out", dev)
+        else:
+            if out_dtype is not None:
+                out_code = _dtype_code(out_dtype)
+                dtype = _TORCH_OF[out_code]
+            out, ldy = torch.empty((M, N), dtype=dtype, device=x.device), N or 1
         mean = rstd = None
         if save:
-            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=dev)
-        code = lib().gemm_layer_norm(
+            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        code = (_lib or lib()).gemm_layer_norm(
             self._h, M, N, x.data_ptr(), ldx, _vector(weight, N, "weight", dev),
-            _vector(bias, N, "bias", dev), out.data_ptr(), _row_ld(out, (M, N), "out", dev),
-            mean.data_ptr() if save else 0, rstd.data_ptr() if save else 0, eps,
-            _dtype_code(x.dtype), F32 if params is None else _dtype_code(params.dtype),
-            _dtype_code(out.dtype), self._stream(x, stream))
-        _check(code, "gemm_layer_norm")
+            _vector(bias, N, "bias", dev), out.data_ptr(), ldy, mean.data_ptr() if save else 0,
+            rstd.data_ptr() if save else 0, eps, in_code, params, out_code,
+            _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            raise GemmError(code, "gemm_layer_norm")
         return (out, mean, rstd) if save else out
 
     def layer_norm_backward(self, grad, x, weight, mean, rstd, need=(True, True, True),
@@ -582,30 +630,27 @@ class Gemm:
         """Gradients of :meth:`layer_norm` from grad (the output's dtype), x, weight (or None)
         and the saved statistics: (dx, dweight, dbias), each None where ``need`` says so; the
         last two in ``param_dtype`` (default: weight's, or float32)."""
-        if x.dim() != 2:
-            raise ValueError("x must be 2-D")
-        M, N = x.shape
-        dev = x.device
-        ldx = _row_ld(x, (M, N), "x")
-        lddy = _row_ld(grad, (M, N), "grad", dev)
-        for t, n in ((mean, "mean"), (rstd, "rstd")):
-            if t.dtype != torch.float32:
-                raise TypeError("%s must be float32" % n)
+        dev = _cuda_index(x, "x")
+        M, N, ldx = _rows(x, "x")
+        lddy = _row_ld(grad, M, N, "grad", dev)
+        if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+            raise TypeError("mean and rstd must be float32")
         pd = weight.dtype if weight is not None else torch.float32
         if param_dtype is not None:
             pd = _TORCH_OF[_dtype_code(param_dtype)]
             if weight is not None and weight.dtype != pd:
                 raise TypeError("param_dtype must be weight's dtype")
-        dx = torch.empty((M, N), dtype=x.dtype, device=dev) if need[0] else None
-        dw = torch.empty(N, dtype=pd, device=dev) if need[1] else None
-        db = torch.empty(N, dtype=pd, device=dev) if need[2] else None
-        ptr = lambda t: 0 if t is None else t.data_ptr()
-        code = lib().gemm_layer_norm_backward(
+        dx = torch.empty((M, N), dtype=x.dtype, device=x.device) if need[0] else None
+        dw = torch.empty(N, dtype=pd, device=x.device) if need[1] else None
+        db = torch.empty(N, dtype=pd, device=x.device) if need[2] else None
+        code = (_lib or lib()).gemm_layer_norm_backward(
             self._h, M, N, grad.data_ptr(), lddy, x.data_ptr(), ldx,
             _vector(weight, N, "weight", dev), _vector(mean, M, "mean", dev),
-            _vector(rstd, M, "rstd", dev), ptr(dx), max(N, 1), ptr(dw), ptr(db),
-            _dtype_code(x.dtype), _dtype_code(pd), _dtype_code(grad.dtype), self._stream(x, stream))
-        _check(code, "gemm_layer_norm_backward")
+            _vector(rstd, M, "rstd", dev), dx.data_ptr() if need[0] else 0, N or 1,
+            dw.data_ptr() if need[1] else 0, db.data_ptr() if need[2] else 0, _code(x.dtype),
+            _code(pd), _code(grad.dtype), _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            raise GemmError(code, "gemm_layer_norm_backward")
         return dx, dw, db
 
     def tune_clear(self):
@@ -724,37 +769,37 @@ def matmul(a, b, out=None, out_dtype=None, precision="default"):
 
 def softmax_rows(x, out=None, out_dtype=None):
     """Row softmax with the default handle of x's device; see :meth:`Gemm.softmax_rows`."""
-    return handle(x.device.index).softmax_rows(x, out=out, out_dtype=out_dtype)
+    return handle(x.get_device()).softmax_rows(x, out=out, out_dtype=out_dtype)
 
 
 def matmul_epilogue(a, b, **kw):
     """act(a @ b + bias) + residual; see :meth:`Gemm.matmul_epilogue`."""
-    return handle(a.device.index).matmul_epilogue(a, b, **kw)
+    return handle(a.get_device()).matmul_epilogue(a, b, **kw)
 
 
 def matmul_epilogue_backward(grad, a, b, **kw):
     """Gradients of :func:`matmul_epilogue`; see :meth:`Gemm.matmul_epilogue_backward`."""
-    return handle(a.device.index).matmul_epilogue_backward(grad, a, b, **kw)
+    return handle(a.get_device()).matmul_epilogue_backward(grad, a, b, **kw)
 
 
 def gated(x, w_gate, w_up, **kw):
     """act(x @ w_gate) * (x @ w_up); see :meth:`Gemm.gated`."""
-    return handle(x.device.index).gated(x, w_gate, w_up, **kw)
+    return handle(x.get_device()).gated(x, w_gate, w_up, **kw)
 
 
 def gated_backward(grad, x, w_gate, w_up, gate, up, **kw):
     """Gradients of :func:`gated`; see :meth:`Gemm.gated_backward`."""
-    return handle(x.device.index).gated_backward(grad, x, w_gate, w_up, gate, up, **kw)
+    return handle(x.get_device()).gated_backward(grad, x, w_gate, w_up, gate, up, **kw)
 
 
 def layer_norm(x, weight=None, bias=None, **kw):
     """Layer norm of the rows of x; see :meth:`Gemm.layer_norm`."""
-    return handle(x.device.index).layer_norm(x, weight, bias, **kw)
+    return handle(x.get_device()).layer_norm(x, weight, bias, **kw)
 
 
 def layer_norm_backward(grad, x, weight, mean, rstd, **kw):
     """Gradients of :func:`layer_norm`; see :meth:`Gemm.layer_norm_backward`."""
-    return handle(x.device.index).layer_norm_backward(grad, x, weight, mean, rstd, **kw)
+    return handle(x.get_device()).layer_norm_backward(grad, x, weight, mean, rstd, **kw)
 
 
 def matmul_host(a, b, out=None, out_dtype=None, precision="default", device=None):

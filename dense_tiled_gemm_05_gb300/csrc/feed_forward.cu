@@ -510,7 +510,7 @@ GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int6
   if (!dX && !dweight && !dbias) return GEMM_OK;
   DeviceGuard g(h->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  gemm_status_t st = ensure_ff(h, ff::layer_norm_backward_bytes(M, N, h->sm_count));
+  gemm_status_t st = ensure_ff(h, ff::layer_norm_backward_bytes(M, N, in_dtype == out_dtype, h->sm_count));
   if (st != GEMM_OK) return st;
   int launches = 0;
   const cudaError_t e = ff::layer_norm_backward_launch(

@@ -65,7 +65,8 @@ cudaError_t layer_norm_launch(const void *x, int64_t ldx, int in_dtype, const vo
                               int out_dtype, float *mean, float *rstd, float eps, int64_t M,
                               int64_t N, int sm_count, cudaStream_t s);
 
-size_t layer_norm_backward_bytes(int64_t M, int64_t N, int sm_count);
+// Workspace of the backward pass (one_type: dy has x's type).
+size_t layer_norm_backward_bytes(int64_t M, int64_t N, bool one_type, int sm_count);
 cudaError_t layer_norm_backward_launch(const void *dy, int64_t lddy, int grad_dtype, const void *x,
                                        int64_t ldx, int in_dtype, const void *weight,
                                        int param_dtype, const float *mean, const float *rstd,

@@ -36,69 +36,150 @@ __device__ __forceinline__ void group_sync(int g) {
   asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(T) : "memory");
 }
 
-// Sum over the T threads of a group; every thread gets it. `red`: T / 32 floats of the group's
-// own; consecutive calls alternate between two such arrays, so that one barrier a call is
-// enough (a thread writes an array again only after the barrier of the call in between).
+// Sums of one or two values over the T threads of a group; every thread gets them. `red`: K
+// times T / 32 floats of the group's own; consecutive calls alternate between two such
+// arrays, so that one barrier a call is enough (a thread writes an array again only after the
+// barrier of the call in between).
+template <int T, int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], float *red, int g) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+  if (T == 32) return;
+  constexpr int WARPS = T / 32;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) red[k * WARPS + (threadIdx.x % T) / 32] = v[k];
+  }
+  group_sync<T>(g);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[k] = red[k * WARPS + lane % WARPS];
+#pragma unroll
+    for (int o = WARPS / 2; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  }
+}
 template <int T>
 __device__ __forceinline__ float group_sum(float v, float *red, int g) {
-  v = warp_sum(v);
-  if (T == 32) return v;
-  const int warp = (threadIdx.x % T) / 32;
-  if (threadIdx.x % 32 == 0) red[warp] = v;
-  group_sync<T>(g);
-  float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < T / 32; ++w) s += red[w];
-  return s;
+  float a[1] = {v};
+  group_sum<T, 1>(a, red, g);
+  return a[0];
 }
 
-// Two sums at once (`red`: 2 T / 32 floats).
+// Threads of a CTA: one group of T, or as many groups of T as make up 256 threads; and the
+// CTAs an SM is to hold of it (1024 threads at 64 registers).
 template <int T>
-__device__ __forceinline__ void group_sum2(float &a, float &b, float *red, int g) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (T == 32) return;
-  const int warp = (threadIdx.x % T) / 32;
-  if (threadIdx.x % 32 == 0) {
-    red[2 * warp] = a;
-    red[2 * warp + 1] = b;
-  }
-  group_sync<T>(g);
-  a = b = 0.0f;
-#pragma unroll
-  for (int w = 0; w < T / 32; ++w) {
-    a += red[2 * w];
-    b += red[2 * w + 1];
-  }
-}
+struct Cta {
+  static constexpr int THREADS = T < 256 ? 256 : T;
+  static constexpr int GROUPS = THREADS / T;
+  static constexpr int PER_SM = 1024 / THREADS;
+};
+constexpr int VEC = 8;  // columns a thread holds of a row (twice that in the widest form)
 
-// Threads of a CTA: one group of T, or as many groups of T as make up 128 threads.
-template <int T>
-constexpr int kCtaThreads = T < 128 ? 128 : T;
+// A thread's eight columns among the 8 T from `first` on. VECTOR (rows start on 16-byte
+// boundaries, and so do N and the parameters): eight consecutive ones, in 16-byte accesses.
+// Otherwise every T-th one, so that the lanes of a warp read neighbours.
+template <int T, bool VECTOR>
+struct Columns {
+  int64_t first, n;
+  int t;
+  __device__ __forceinline__ int64_t at(int i) const {
+    return VECTOR ? first + t * VEC + i : first + i * T + t;
+  }
+  __device__ __forceinline__ bool in(int i) const { return at(VECTOR ? 0 : i) < n; }
+
+  template <typename E>
+  __device__ __forceinline__ void load(const E *row, E (&e)[VEC]) const {
+    if (VECTOR) {
+      constexpr int W = VEC * sizeof(E) / 16;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        reinterpret_cast<uint4 *>(e)[w] =
+            in(0) ? reinterpret_cast<const uint4 *>(row + at(0))[w] : uint4{0, 0, 0, 0};
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = in(i) ? row[at(i)] : from_f32<E>(0.0f);
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ void store(E *row, const float (&v)[VEC]) const {
+    if (VECTOR) {
+      constexpr int W = VEC * sizeof(E) / 16;
+      alignas(16) E e[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
+      if (in(0)) {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          reinterpret_cast<uint4 *>(row + at(0))[w] = reinterpret_cast<const uint4 *>(e)[w];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (in(i)) row[at(i)] = from_f32<E>(v[i]);
+    }
+  }
+  __device__ __forceinline__ void store(void *base, int dtype, int64_t offset,
+                                        const float (&v)[VEC]) const {
+    FF_TYPED(dtype, E, { store(static_cast<E *>(base) + offset, v); })
+  }
+  // A parameter vector (1 or 0 for every column where there is none).
+  __device__ __forceinline__ void params(const void *p, int dtype, float missing,
+                                         float (&v)[VEC]) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = missing;
+      return;
+    }
+    FF_TYPED(dtype, E, {
+      alignas(16) E e[VEC];
+      load(static_cast<const E *>(p), e);
+      _Pragma("unroll") for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
+    })
+  }
+};
 
 // ------------------------------------------------------------------------- forward
 
-// A group of T threads a row; a thread holds CH chunks of VEC consecutive columns, chunk c of
-// thread t being columns (c T + t) VEC ... .
-template <typename TI, typename TO, int T, int CH, bool VECTOR>
-__global__ void __launch_bounds__(kCtaThreads<T>)
+// A group of T threads a row; piece c of thread t is columns (c T + t) 8 ... . The CTAs stay
+// and walk the rows: with one piece a thread, weight and bias are read once into registers
+// (read for every row they are four times the bytes of a bf16 row with fp32 parameters, from
+// L2: 16384 x 4096 took 152 us that way), and the next row's loads are issued before the
+// current row's reductions. Two pieces a thread leave no registers for the parameters.
+template <typename TI, int T, int CH, bool VECTOR>
+__global__ void __launch_bounds__(Cta<T>::THREADS, Cta<T>::PER_SM)
     norm_rows_kernel(const TI *x, int64_t ldx, const void *weight, const void *bias,
-                     int param_dtype, TO *y, int64_t ldy, float *mean_out, float *rstd_out,
-                     float eps, int64_t M, int64_t N) {
-  constexpr int VEC = 16 / sizeof(TI);
-  constexpr int G = kCtaThreads<T> / T;
+                     int param_dtype, void *y, int64_t ldy, int out_dtype, float *mean_out,
+                     float *rstd_out, float eps, int64_t M, int64_t N) {
+  constexpr int G = Cta<T>::GROUPS;
   __shared__ float red[G][2][T / 32];
   const int g = threadIdx.x / T, t = threadIdx.x % T;
   const float n = static_cast<float>(N);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * G + g; row < M;
-       row += static_cast<int64_t>(gridDim.x) * G) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
+  if (row >= M) return;
+  auto columns = [&](int c) { return Columns<T, VECTOR>{static_cast<int64_t>(c) * T * VEC, N, t}; };
+  alignas(16) TI next[CH][VEC];
+  float w[VEC], b[VEC];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) columns(c).load(x + row * ldx, next[c]);
+  if (CH == 1) {
+    columns(0).params(weight, param_dtype, 1.0f, w);
+    columns(0).params(bias, param_dtype, 0.0f, b);
+  }
+  for (; row < M; row += step) {
     float v[CH][VEC];
     float s = 0.0f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      load_piece<TI, VEC, VECTOR>(x + row * ldx, (static_cast<int64_t>(c) * T + t) * VEC, N, v[c]);
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s += v[c][i];
+      for (int i = 0; i < VEC; ++i) {
+        v[c][i] = to_f32(next[c][i]);
+        s += v[c][i];
+      }
+    if (row + step < M) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) columns(c).load(x + (row + step) * ldx, next[c]);
     }
     const float mean = group_sum<T>(s, red[g][0], g) / n;
     float q = 0.0f;
@@ -107,20 +188,18 @@ __global__ void __launch_bounds__(kCtaThreads<T>)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         v[c][i] -= mean;
-        if ((static_cast<int64_t>(c) * T + t) * VEC + i < N) q = fmaf(v[c][i], v[c][i], q);
+        if (columns(c).in(i)) q = fmaf(v[c][i], v[c][i], q);
       }
     const float rstd = rsqrtf(group_sum<T>(q, red[g][1], g) / n + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t j0 = (static_cast<int64_t>(c) * T + t) * VEC;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const bool in = j0 + i < N;
-        const float w = weight && in ? load_any(weight, param_dtype, j0 + i) : 1.0f;
-        const float b = bias && in ? load_any(bias, param_dtype, j0 + i) : 0.0f;
-        v[c][i] = fmaf(v[c][i] * rstd, w, b);
+      if (CH > 1) {
+        columns(c).params(weight, param_dtype, 1.0f, w);
+        columns(c).params(bias, param_dtype, 0.0f, b);
       }
-      store_piece<TO, VEC, VECTOR>(y + row * ldy, j0, N, v[c]);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(v[c][i] * rstd, w[i], b[i]);
+      columns(c).store(y, out_dtype, row * ldy, v[c]);
     }
     if (t == 0) {
       if (mean_out) mean_out[row] = mean;
@@ -131,41 +210,43 @@ __global__ void __launch_bounds__(kCtaThreads<T>)
 
 // Rows too long for a CTA's registers: three passes over the row, the later two mostly from
 // L2 (the rows in flight fit in it).
-template <typename TI, typename TO, bool VECTOR>
+template <typename TI, bool VECTOR>
 __global__ void __launch_bounds__(512)
     norm_long_rows_kernel(const TI *x, int64_t ldx, const void *weight, const void *bias,
-                          int param_dtype, TO *y, int64_t ldy, float *mean_out, float *rstd_out,
-                          float eps, int64_t M, int64_t N) {
-  constexpr int T = 512, VEC = 16 / sizeof(TI);
+                          int param_dtype, void *y, int64_t ldy, int out_dtype, float *mean_out,
+                          float *rstd_out, float eps, int64_t M, int64_t N) {
+  constexpr int T = 512;
   __shared__ float red[2][T / 32];
   const float n = static_cast<float>(N);
+  Columns<T, VECTOR> cols{0, N, static_cast<int>(threadIdx.x)};
+  alignas(16) TI e[VEC];
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
     const TI *xr = x + row * ldx;
-    float v[VEC], s = 0.0f;
-    for (int64_t j0 = threadIdx.x * VEC; j0 < N; j0 += T * VEC) {
-      load_piece<TI, VEC, VECTOR>(xr, j0, N, v);
+    float s = 0.0f;
+    for (cols.first = 0; cols.first < N; cols.first += T * VEC) {
+      cols.load(xr, e);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s += v[i];
+      for (int i = 0; i < VEC; ++i) s += to_f32(e[i]);
     }
     const float mean = group_sum<T>(s, red[0], 0) / n;
     float q = 0.0f;
-    for (int64_t j0 = threadIdx.x * VEC; j0 < N; j0 += T * VEC) {
-      load_piece<TI, VEC, VECTOR>(xr, j0, N, v);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (j0 + i < N) q = fmaf(v[i] - mean, v[i] - mean, q);
-    }
-    const float rstd = rsqrtf(group_sum<T>(q, red[1], 0) / n + eps);
-    for (int64_t j0 = threadIdx.x * VEC; j0 < N; j0 += T * VEC) {
-      load_piece<TI, VEC, VECTOR>(xr, j0, N, v);
+    for (cols.first = 0; cols.first < N; cols.first += T * VEC) {
+      cols.load(xr, e);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const bool in = j0 + i < N;
-        const float w = weight && in ? load_any(weight, param_dtype, j0 + i) : 1.0f;
-        const float b = bias && in ? load_any(bias, param_dtype, j0 + i) : 0.0f;
-        v[i] = fmaf((v[i] - mean) * rstd, w, b);
+        const float d = to_f32(e[i]) - mean;
+        if (cols.in(i)) q = fmaf(d, d, q);
       }
-      store_piece<TO, VEC, VECTOR>(y + row * ldy, j0, N, v);
+    }
+    const float rstd = rsqrtf(group_sum<T>(q, red[1], 0) / n + eps);
+    for (cols.first = 0; cols.first < N; cols.first += T * VEC) {
+      float v[VEC], w[VEC], b[VEC];
+      cols.load(xr, e);
+      cols.params(weight, param_dtype, 1.0f, w);
+      cols.params(bias, param_dtype, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = fmaf((to_f32(e[i]) - mean) * rstd, w[i], b[i]);
+      cols.store(y, out_dtype, row * ldy, v);
     }
     if (threadIdx.x == 0) {
       if (mean_out) mean_out[row] = mean;
@@ -176,6 +257,106 @@ __global__ void __launch_bounds__(512)
 
 // ------------------------------------------------------------------------ backward
 
+// One pass for rows a CTA's registers hold (8 columns a thread): a group of T threads a row,
+// x and dy read once, with the next row's loads in flight during the current row's
+// reduction, dx written, and the columns' sums of dy xh and dy kept in registers over all of
+// the group's rows. The groups of a CTA join theirs at the end; column_finish adds the CTAs.
+template <typename TI, int T, bool VECTOR>
+__global__ void __launch_bounds__(Cta<T>::THREADS, Cta<T>::PER_SM)
+    norm_backward_kernel(const TI *__restrict__ dy, int64_t lddy, const TI *__restrict__ x,
+                         int64_t ldx, const void *weight, int param_dtype,
+                         const float *__restrict__ mean, const float *__restrict__ rstd,
+                         TI *__restrict__ dx, int64_t lddx, float *__restrict__ partials,
+                         int32_t M, int64_t N) {
+  constexpr int G = Cta<T>::GROUPS;
+  __shared__ float red[G][2][2 * (T / 32)];
+  __shared__ float join[G > 1 ? 2 : 1][G > 1 ? T * VEC : 1];
+  __shared__ float4 ws[2][T];  // the weight: registers go to the columns' sums
+  const int g = threadIdx.x / T, t = threadIdx.x % T;
+  const Columns<T, VECTOR> cols{0, N, t};
+  const int step = static_cast<int>(gridDim.x) * G;
+  int row = static_cast<int>(blockIdx.x) * G + g;
+  float dw[VEC], db[VEC];
+  alignas(16) TI nx[VEC];
+  alignas(16) TI nd[VEC];
+  float nmu = 0.0f, nr = 0.0f;
+  auto fetch = [&](int i) {
+    cols.load(x + i * ldx, nx);
+    cols.load(dy + i * lddy, nd);
+    nmu = mean[i];
+    nr = rstd[i];
+  };
+  if (row < M) fetch(row);
+  if (g == 0) {
+    cols.params(weight, param_dtype, 1.0f, dw);
+    ws[0][t] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+    ws[1][t] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) dw[i] = db[i] = 0.0f;
+  int buf = 0;
+  while (row < M) {
+    const int next = M - row > step ? row + step : M;
+    const float r = nr;
+    float xh[VEC], d[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      xh[i] = (to_f32(nx[i]) - nmu) * r;
+      d[i] = to_f32(nd[i]);
+    }
+    if (next < M) fetch(next);
+    const float4 w0 = ws[0][t], w1 = ws[1][t];
+    const float w[VEC] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {  // (dy reads as 0 past the row's end)
+      dw[i] = fmaf(d[i], xh[i], dw[i]);
+      db[i] += d[i];
+      d[i] *= w[i];
+      s[0] += d[i];
+      s[1] = fmaf(d[i], xh[i], s[1]);
+    }
+    group_sum<T, 2>(s, red[g][buf], g);
+    buf ^= 1;
+    if (dx) {
+      const float n = static_cast<float>(N);
+      const float a = s[0] / n, b = s[1] / n;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) d[i] = r * (d[i] - a - xh[i] * b);
+      cols.store(dx + row * lddx, d);
+    }
+    row = next;
+  }
+  if (!partials) return;
+  if (G > 1) {  // in the groups' order
+    for (int k = 0; k < G; ++k) {
+      if (g == k) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          join[0][i * T + t] = k ? join[0][i * T + t] + dw[i] : dw[i];
+          join[1][i * T + t] = k ? join[1][i * T + t] + db[i] : db[i];
+        }
+      }
+      __syncthreads();
+    }
+    if (g != 0) return;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      dw[i] = join[0][i * T + t];
+      db[i] = join[1][i * T + t];
+    }
+  }
+  float *out = partials + static_cast<int64_t>(blockIdx.x) * 2 * N;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+    if (cols.in(i)) {
+      out[cols.at(i)] = dw[i];
+      out[N + cols.at(i)] = db[i];
+    }
+}
+
+// Longer rows, and a dy of another type than x: the rows' means first, then columns.
 // mean_j(v) and mean_j(v xh) of each row, by a warp a row.
 template <typename TG, typename TI, bool VECTOR>
 __global__ void __launch_bounds__(256)
@@ -183,7 +364,6 @@ __global__ void __launch_bounds__(256)
                           int64_t ldx, const void *weight, int param_dtype,
                           const float *__restrict__ mean, const float *__restrict__ rstd,
                           float2 *__restrict__ means, int64_t M, int64_t N) {
-  constexpr int VEC = 8;
   const float n = static_cast<float>(N);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; row < M;
        row += static_cast<int64_t>(gridDim.x) * 8) {
@@ -207,6 +387,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+//
 // dx and the sums of dy xh and dy over a band of rows, from the rows' means: a warp covers
 // 256 columns, a CTA's eight warps eight rows at a time.
 template <typename TG, typename TI, bool VECTOR>
@@ -216,7 +397,6 @@ __global__ void __launch_bounds__(256)
                         const float *__restrict__ mean, const float *__restrict__ rstd,
                         const float2 *__restrict__ means, TI *__restrict__ dx, int64_t lddx,
                         float *__restrict__ partials, int64_t M, int64_t N, int64_t band) {
-  constexpr int VEC = 8;
   __shared__ float red[2][8][32 * VEC];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * VEC;
@@ -275,6 +455,7 @@ struct NormArgs {
   int param_dtype;
   void *y;
   int64_t ldy;
+  int out_dtype;
   float *mean, *rstd;
   float eps;
   int64_t M, N;
@@ -283,36 +464,46 @@ struct NormArgs {
   cudaStream_t s;
 };
 
-template <typename TI, typename TO, int T, int CH>
-void launch_rows(const NormArgs &a) {
-  constexpr int G = kCtaThreads<T> / T;
-  const int64_t ctas = (a.M + G - 1) / G;
-  const int64_t cap = static_cast<int64_t>(a.sm_count > 0 ? a.sm_count : 1) * 64;
-  const int grid = static_cast<int>(ctas < cap ? ctas : cap);
-  auto kernel = a.vec ? norm_rows_kernel<TI, TO, T, CH, true> : norm_rows_kernel<TI, TO, T, CH, false>;
-  kernel<<<grid, kCtaThreads<T>, 0, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias,
-                                             a.param_dtype, static_cast<TO *>(a.y), a.ldy, a.mean,
-                                             a.rstd, a.eps, a.M, a.N);
+int grid_of(int64_t ctas, int sm_count, int per_sm) {
+  const int64_t cap = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * per_sm;
+  return static_cast<int>(ctas < 1 ? 1 : ctas < cap ? ctas : cap);
 }
 
-// Threads a row: the fewest (32 .. 1024) that hold it at 16 values a thread, then 1024 at 32.
-template <typename TI, typename TO>
+template <typename TI, int T, int CH>
+void launch_rows(const NormArgs &a) {
+  const int grid = grid_of((a.M + Cta<T>::GROUPS - 1) / Cta<T>::GROUPS, a.sm_count, Cta<T>::PER_SM);
+  auto kernel = a.vec ? norm_rows_kernel<TI, T, CH, true> : norm_rows_kernel<TI, T, CH, false>;
+  kernel<<<grid, Cta<T>::THREADS, 0, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias,
+                                            a.param_dtype, a.y, a.ldy, a.out_dtype, a.mean, a.rstd,
+                                            a.eps, a.M, a.N);
+}
+
+// Threads that hold a row of N columns, eight each: 32 .. 1024.
+int row_threads(int64_t N) {
+  int t = 32;
+  while (t < 1024 && t * VEC < N) t *= 2;
+  return t;
+}
+constexpr int64_t kOnePassColumns = 1024 * VEC;
+
+template <typename TI>
 void dispatch_rows(const NormArgs &a) {
-  constexpr int VEC = 16 / sizeof(TI), C16 = 16 / VEC, C32 = 32 / VEC;
-  const int64_t pieces = (a.N + VEC - 1) / VEC;
-  if (pieces <= 32 * C16) return launch_rows<TI, TO, 32, C16>(a);
-  if (pieces <= 64 * C16) return launch_rows<TI, TO, 64, C16>(a);
-  if (pieces <= 128 * C16) return launch_rows<TI, TO, 128, C16>(a);
-  if (pieces <= 256 * C16) return launch_rows<TI, TO, 256, C16>(a);
-  if (pieces <= 512 * C16) return launch_rows<TI, TO, 512, C16>(a);
-  if (pieces <= 1024 * C16) return launch_rows<TI, TO, 1024, C16>(a);
-  if (pieces <= 1024 * C32) return launch_rows<TI, TO, 1024, C32>(a);
-  const int64_t cap = static_cast<int64_t>(a.sm_count > 0 ? a.sm_count : 1) * 64;
-  const int grid = static_cast<int>(a.M < cap ? a.M : cap);
-  auto kernel = a.vec ? norm_long_rows_kernel<TI, TO, true> : norm_long_rows_kernel<TI, TO, false>;
-  kernel<<<grid, 512, 0, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias,
-                                a.param_dtype, static_cast<TO *>(a.y), a.ldy, a.mean, a.rstd, a.eps,
-                                a.M, a.N);
+  if (a.N > 2 * kOnePassColumns) {
+    auto kernel = a.vec ? norm_long_rows_kernel<TI, true> : norm_long_rows_kernel<TI, false>;
+    kernel<<<grid_of(a.M, a.sm_count, 64), 512, 0, a.s>>>(
+        static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias, a.param_dtype, a.y, a.ldy,
+        a.out_dtype, a.mean, a.rstd, a.eps, a.M, a.N);
+    return;
+  }
+  if (a.N > kOnePassColumns) return launch_rows<TI, 1024, 2>(a);
+  switch (row_threads(a.N)) {
+    case 32: return launch_rows<TI, 32, 1>(a);
+    case 64: return launch_rows<TI, 64, 1>(a);
+    case 128: return launch_rows<TI, 128, 1>(a);
+    case 256: return launch_rows<TI, 256, 1>(a);
+    case 512: return launch_rows<TI, 512, 1>(a);
+    default: return launch_rows<TI, 1024, 1>(a);
+  }
 }
 
 }  // namespace
@@ -321,13 +512,54 @@ cudaError_t layer_norm_launch(const void *x, int64_t ldx, int in_dtype, const vo
                               const void *bias, int param_dtype, void *y, int64_t ldy,
                               int out_dtype, float *mean, float *rstd, float eps, int64_t M,
                               int64_t N, int sm_count, cudaStream_t s) {
-  const bool vec = aligned16(x, ldx, esize(in_dtype)) && aligned16(y, ldy, esize(out_dtype));
-  const NormArgs a{x, ldx, weight, bias, param_dtype, y, ldy, mean, rstd, eps, M, N, vec, sm_count, s};
-  FF_TYPED(in_dtype, TI, { FF_TYPED(out_dtype, TO, { dispatch_rows<TI, TO>(a); }) })
+  const bool vec = aligned16(x, ldx, esize(in_dtype)) && aligned16(y, ldy, esize(out_dtype)) &&
+                   aligned16(weight, 0, 4) && aligned16(bias, 0, 4) && N % VEC == 0;
+  const NormArgs a{x, ldx, weight, bias, param_dtype, y, ldy, out_dtype, mean, rstd, eps, M, N,
+                   vec, sm_count, s};
+  FF_TYPED(in_dtype, TI, { dispatch_rows<TI>(a); })
   return cudaGetLastError();
 }
 
-size_t layer_norm_backward_bytes(int64_t M, int64_t N, int sm_count) {
+namespace {
+
+struct NormBackwardArgs {
+  const void *dy;
+  int64_t lddy;
+  const void *x;
+  int64_t ldx;
+  const void *weight;
+  int param_dtype;
+  const float *mean, *rstd;
+  void *dx;
+  int64_t lddx;
+  float *partials;
+  int64_t M, N;
+  bool vec;
+  int grid;
+  cudaStream_t s;
+};
+
+template <typename TI, int T>
+void launch_backward(const NormBackwardArgs &a) {
+  auto kernel = a.vec ? norm_backward_kernel<TI, T, true> : norm_backward_kernel<TI, T, false>;
+  kernel<<<a.grid, Cta<T>::THREADS, 0, a.s>>>(
+      static_cast<const TI *>(a.dy), a.lddy, static_cast<const TI *>(a.x), a.ldx, a.weight,
+      a.param_dtype, a.mean, a.rstd, static_cast<TI *>(a.dx), a.lddx, a.partials,
+      static_cast<int32_t>(a.M), a.N);
+}
+
+// Grid of the one-pass kernel: as many CTAs as stay on the SMs, or as have rows.
+int backward_grid(int64_t M, int64_t N, int sm_count) {
+  const int t = row_threads(N);
+  const int64_t groups = t < 256 ? 256 / t : 1;
+  return grid_of((M + groups - 1) / groups, sm_count, t < 256 ? 4 : 1024 / t);
+}
+
+}  // namespace
+
+size_t layer_norm_backward_bytes(int64_t M, int64_t N, bool one_type, int sm_count) {
+  if (N <= kOnePassColumns && one_type)
+    return static_cast<size_t>(backward_grid(M, N, sm_count)) * 2 * N * sizeof(float);
   return static_cast<size_t>((M * sizeof(float2) + 255) / 256 * 256) +
          column_partials_bytes(M, N, 2, sm_count);
 }
@@ -341,6 +573,29 @@ cudaError_t layer_norm_backward_launch(const void *dy, int64_t lddy, int grad_dt
   const int is = esize(in_dtype);
   const bool vec = aligned16(dy, lddy, esize(grad_dtype)) && aligned16(x, ldx, is) &&
                    aligned16(dx, lddx, is);
+  if (N <= kOnePassColumns && grad_dtype == in_dtype) {
+    float *sums = static_cast<float *>(workspace);
+    const int grid = backward_grid(M, N, sm_count);
+    const NormBackwardArgs a{dy, lddy, x, ldx, weight, param_dtype, mean, rstd, dx, lddx,
+                             dweight || dbias ? sums : nullptr, M, N,
+                             vec && aligned16(weight, 0, 4) && N % VEC == 0, grid, s};
+    FF_TYPED(in_dtype, TI, {
+      switch (row_threads(N)) {
+        case 32: launch_backward<TI, 32>(a); break;
+        case 64: launch_backward<TI, 64>(a); break;
+        case 128: launch_backward<TI, 128>(a); break;
+        case 256: launch_backward<TI, 256>(a); break;
+        case 512: launch_backward<TI, 512>(a); break;
+        default: launch_backward<TI, 1024>(a); break;
+      }
+    })
+    ++*launches;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.partials) return e;
+    ++*launches;
+    if (dweight) return column_finish_launch(sums, grid, 2, dweight, dbias, param_dtype, N, s);
+    return column_finish_launch(sums + N, grid, 2, dbias, nullptr, param_dtype, N, s);
+  }
   float2 *means = static_cast<float2 *>(workspace);
   float *partials = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                               (M * sizeof(float2) + 255) / 256 * 256);
