@@ -100,6 +100,74 @@ __device__ __forceinline__ void store_piece(T *row, int64_t j0, int64_t n, const
   }
 }
 
+constexpr int VEC = 8;  // columns a thread takes of a row
+
+// A thread's eight columns among the 8 T from `first` on. VECTOR (rows start on 16-byte
+// boundaries, and so do N and the parameters): eight consecutive ones, in 16-byte accesses.
+// Otherwise every T-th one, so that the lanes of a warp read neighbours.
+template <int T, bool VECTOR>
+struct Columns {
+  int64_t first, n;
+  int t;
+  __device__ __forceinline__ int64_t at(int i) const {
+    return VECTOR ? first + t * VEC + i : first + i * T + t;
+  }
+  __device__ __forceinline__ bool in(int i) const { return at(VECTOR ? 0 : i) < n; }
+
+  template <typename E>
+  __device__ __forceinline__ void load(const E *row, E (&e)[VEC]) const {
+    if (VECTOR) {
+      constexpr int W = VEC * sizeof(E) / 16;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        reinterpret_cast<uint4 *>(e)[w] =
+            in(0) ? reinterpret_cast<const uint4 *>(row + at(0))[w] : uint4{0, 0, 0, 0};
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = in(i) ? row[at(i)] : from_f32<E>(0.0f);
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ void store(E *row, const float (&v)[VEC]) const {
+    if (VECTOR) {
+      constexpr int W = VEC * sizeof(E) / 16;
+      alignas(16) E e[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
+      if (in(0)) {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          reinterpret_cast<uint4 *>(row + at(0))[w] = reinterpret_cast<const uint4 *>(e)[w];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (in(i)) row[at(i)] = from_f32<E>(v[i]);
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ void load_f32(const E *row, float (&v)[VEC]) const {
+    alignas(16) E e[VEC];
+    load(row, e);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
+  }
+  __device__ __forceinline__ void store(void *base, int dtype, int64_t offset,
+                                        const float (&v)[VEC]) const {
+    FF_TYPED(dtype, E, { store(static_cast<E *>(base) + offset, v); })
+  }
+  // A parameter vector (1 or 0 for every column where there is none).
+  __device__ __forceinline__ void params(const void *p, int dtype, float missing,
+                                         float (&v)[VEC]) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = missing;
+      return;
+    }
+    FF_TYPED(dtype, E, { load_f32(static_cast<const E *>(p), v); })
+  }
+};
+
 // 1 / (1 + exp(-z)). FAST (kernels whose inputs are 16-bit, so that z already carries errors
 // of 2^-9): the hardware exponential and division, a few fp32 ulps for |z| of ordinary size.
 // Both saturate to exactly 0 and 1.
@@ -178,6 +246,49 @@ __device__ __forceinline__ void activate_slope(float z, int act, float &a, float
       return;
   }
 }
+
+// A piece at a time, with one branch on the activation for all of it (a branch per element
+// would keep the elements' exponentials from overlapping).
+#define FF_EACH_ACT(X)      \
+  X(GEMM_ACT_RELU)          \
+  X(GEMM_ACT_GELU)          \
+  X(GEMM_ACT_GELU_TANH)     \
+  X(GEMM_ACT_SILU)          \
+  X(GEMM_ACT_SIGMOID)
+
+template <bool FAST, int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+  switch (act) {
+#define FF_ONE(A)                                                                   \
+  case A: {                                                                         \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = activate<FAST>(v[i], A);   \
+    return;                                                                         \
+  }
+    FF_EACH_ACT(FF_ONE)
+#undef FF_ONE
+    default: return;
+  }
+}
+
+template <bool FAST, int N>
+__device__ __forceinline__ void activate_slope_all(const float (&z)[N], int act, float (&a)[N],
+                                                   float (&d)[N]) {
+  switch (act) {
+#define FF_ONE(A)                                                                              \
+  case A: {                                                                                    \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) activate_slope<FAST>(z[i], A, a[i], d[i]);   \
+    return;                                                                                    \
+  }
+    FF_EACH_ACT(FF_ONE)
+#undef FF_ONE
+    default: {
+#pragma unroll
+      for (int i = 0; i < N; ++i) a[i] = z[i], d[i] = 1.0f;
+      return;
+    }
+  }
+}
+#undef FF_EACH_ACT
 
 }  // namespace ff
 }  // namespace gemm_gb300

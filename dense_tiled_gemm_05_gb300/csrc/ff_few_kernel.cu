@@ -79,8 +79,9 @@ __device__ __forceinline__ void finish4(const FusedParams &p, bool vec, int64_t 
       store4(static_cast<TO *>(p.pre) + m * p.ld_pre, n, p.N, vec, a);
       store4(static_cast<TO *>(p.pre2) + m * p.ld_pre2, n, p.N, vec, b);
     }
+    activate_all<true>(a, p.act);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = activate<true>(a[i], p.act) * b[i];
+    for (int i = 0; i < 4; ++i) a[i] *= b[i];
   } else {
     if (p.bias) {
 #pragma unroll
@@ -88,8 +89,7 @@ __device__ __forceinline__ void finish4(const FusedParams &p, bool vec, int64_t 
         if (n + i < p.N) a[i] += load_any(p.bias, p.bias_dtype, n + i);
     }
     if (p.pre) store4(static_cast<TO *>(p.pre) + m * p.ld_pre, n, p.N, vec, a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = activate<true>(a[i], p.act);
+    activate_all<true>(a, p.act);
     if (p.residual) {
       const TO *r = static_cast<const TO *>(p.residual) + m * p.ld_residual;
       if (vec)
@@ -278,29 +278,45 @@ __global__ void __launch_bounds__(kThreads)
   else
     __syncthreads();
   const uint32_t base = smem_u32(smem);
-  const int items = tokens * (kFewFeatures / 4);
-  for (int i = rank * kThreads + threadIdx.x; i < items; i += p.splits * kThreads) {
-    const int t = i / (kFewFeatures / 4), f = i % (kFewFeatures / 4) * 4;
-    if (f0 + f >= p.f.N) continue;
-    const uint32_t off = base + static_cast<uint32_t>(t * kFewFeatures + f) * 4;
-    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+  // A thread's items are BATCH at a time: all their partials are on the way before the first
+  // sum, or each would wait for the other SMs' shared memory in turn.
+  constexpr int BATCH = GATED ? 2 : 4;
+  const int items = tokens * (kFewFeatures / 4), stride = p.splits * kThreads;
+  for (int i0 = rank * kThreads + threadIdx.x; i0 < items; i0 += BATCH * stride) {
+    float a[BATCH][4], b[BATCH][4];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[j][i] = b[j][i] = 0.0f;
+#pragma unroll 2
     for (int q = 0; q < p.splits; ++q) {
-      const uint32_t at = p.splits > 1 ? mapa_shared(off, static_cast<uint32_t>(q)) : off;
-      const float4 v = ld_cluster_f4(at);
-      a[0] += v.x, a[1] += v.y, a[2] += v.z, a[3] += v.w;
-      if (GATED) {
-        const float4 w = ld_cluster_f4(at + plane * static_cast<uint32_t>(sizeof(float)));
-        b[0] += w.x, b[1] += w.y, b[2] += w.z, b[3] += w.w;
+      float4 v[BATCH], w[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int i = min(i0 + j * stride, items - 1);
+        const uint32_t off = base + static_cast<uint32_t>(i) * 16;
+        const uint32_t at = p.splits > 1 ? mapa_shared(off, static_cast<uint32_t>(q)) : off;
+        v[j] = ld_cluster_f4(at);
+        if (GATED) w[j] = ld_cluster_f4(at + plane * static_cast<uint32_t>(sizeof(float)));
+      }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        a[j][0] += v[j].x, a[j][1] += v[j].y, a[j][2] += v[j].z, a[j][3] += v[j].w;
+        if (GATED) b[j][0] += w[j].x, b[j][1] += w[j].y, b[j][2] += w[j].z, b[j][3] += w[j].w;
       }
     }
-    const int64_t m = t0 + t, n = f0 + f;
-    if (p.f.out_dtype == GEMM_BF16)
-      finish4<__nv_bfloat16, GATED>(p.f, p.vec, m, n, a, b);
-    else if (p.f.out_dtype == GEMM_F16)
-      finish4<__half, GATED>(p.f, p.vec, m, n, a, b);
-    else
-      finish4<float, GATED>(p.f, p.vec, m, n, a, b);
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int i = i0 + j * stride, f = i % (kFewFeatures / 4) * 4;
+      if (i >= items || f0 + f >= p.f.N) continue;
+      const int64_t m = t0 + i / (kFewFeatures / 4), n = f0 + f;
+      if (p.f.out_dtype == GEMM_BF16)
+        finish4<__nv_bfloat16, GATED>(p.f, p.vec, m, n, a[j], b[j]);
+      else if (p.f.out_dtype == GEMM_F16)
+        finish4<__half, GATED>(p.f, p.vec, m, n, a[j], b[j]);
+      else
+        finish4<float, GATED>(p.f, p.vec, m, n, a[j], b[j]);
+    }
   }
   if (threadIdx.x == 0 && *abort_flag) {
     // After an abort, let every copy already issued land: the last fill of stage s is fill

@@ -50,24 +50,6 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(kEpiWarps * OWNER_SLICE <= STAGES * STAGE_BYTES && PART_BYTES <= OWNER_SLICE,
               "owner slices fit the stages");
 
-template <int N>
-__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
-  switch (act) {  // one branch for the whole piece
-    case GEMM_ACT_NONE: return;
-#define FF_ACT(A)                                                      \
-  case A: {                                                            \
-    _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], A); \
-    return;                                                            \
-  }
-      FF_ACT(GEMM_ACT_RELU)
-      FF_ACT(GEMM_ACT_GELU)
-      FF_ACT(GEMM_ACT_GELU_TANH)
-      FF_ACT(GEMM_ACT_SILU)
-      FF_ACT(GEMM_ACT_SIGMOID)
-#undef FF_ACT
-  }
-}
-
 // COLS consecutive accumulator columns of this lane's row, as fp32.
 template <int COLS>
 __device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[COLS]) {
@@ -213,7 +195,7 @@ __device__ __forceinline__ bool plain_boxes(const PairMaps &maps, const PairPara
       write_box_row<OUT>(bx.row(b), lane, v);
       bx.store(b, &maps.Z, col, row0);
     }
-    activate_all(v, p.f.act);
+    activate_all<true>(v, p.f.act);
     if (res_box) {
       const int b = c & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&bx.bars[b], (bx.phases >> b) & 1u, wd))) return false;
@@ -263,7 +245,7 @@ __device__ __forceinline__ void gated_boxes(const PairMaps &maps, const PairPara
       write_box_row<OUT>(bx.row(b), lane, u);
       bx.store(b, &maps.Z2, col, row0);
     }
-    activate_all(g, p.f.act);
+    activate_all<true>(g, p.f.act);
 #pragma unroll
     for (int i = 0; i < COLS; ++i) g[i] *= u[i];
     const int b = bx.take();
@@ -301,7 +283,7 @@ __device__ __forceinline__ void direct_rows(const PairParams &p, uint32_t t_row,
           if (j < n) z2[j] = from_f32<T>(u[j]);
       }
     }
-    activate_all(v, p.f.act);
+    activate_all<true>(v, p.f.act);
     if (GATED) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= u[j];

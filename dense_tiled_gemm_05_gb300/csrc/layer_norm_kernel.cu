@@ -66,141 +66,201 @@ __device__ __forceinline__ float group_sum(float v, float *red, int g) {
   return a[0];
 }
 
-// Threads of a CTA: one group of T, or as many groups of T as make up 256 threads; and the
-// CTAs an SM is to hold of it (1024 threads at 64 registers).
-template <int T>
+// Threads of a CTA: one group of T threads, or as many as make up `AT_LEAST`.
+template <int T, int AT_LEAST>
 struct Cta {
-  static constexpr int THREADS = T < 256 ? 256 : T;
+  static constexpr int THREADS = T < AT_LEAST ? AT_LEAST : T;
   static constexpr int GROUPS = THREADS / T;
-  static constexpr int PER_SM = 1024 / THREADS;
 };
-constexpr int VEC = 8;  // columns a thread holds of a row (twice that in the widest form)
 
-// A thread's eight columns among the 8 T from `first` on. VECTOR (rows start on 16-byte
-// boundaries, and so do N and the parameters): eight consecutive ones, in 16-byte accesses.
-// Otherwise every T-th one, so that the lanes of a warp read neighbours.
-template <int T, bool VECTOR>
-struct Columns {
-  int64_t first, n;
-  int t;
-  __device__ __forceinline__ int64_t at(int i) const {
-    return VECTOR ? first + t * VEC + i : first + i * T + t;
-  }
-  __device__ __forceinline__ bool in(int i) const { return at(VECTOR ? 0 : i) < n; }
+// s / n, correctly rounded but for the last bit, without a division's instructions: the
+// quotient's residual corrects it (a row of equal values has exactly their mean).
+__device__ __forceinline__ float mean_of(float s, float n, float inv_n) {
+  const float q = s * inv_n, c = fmaf(-q, n, s);
+  return c == c ? fmaf(c, inv_n, q) : q;  // (an infinite sum's mean is infinite)
+}
 
-  template <typename E>
-  __device__ __forceinline__ void load(const E *row, E (&e)[VEC]) const {
-    if (VECTOR) {
-      constexpr int W = VEC * sizeof(E) / 16;
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-        reinterpret_cast<uint4 *>(e)[w] =
-            in(0) ? reinterpret_cast<const uint4 *>(row + at(0))[w] : uint4{0, 0, 0, 0};
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = in(i) ? row[at(i)] : from_f32<E>(0.0f);
-    }
+// The rows ahead of the one a thread works on, in its own slots of shared memory: cp.async
+// takes no registers, and a thread that reads only its own slots needs no barrier.
+template <int WORDS, int STAGES, int THREADS>
+struct RowRing {
+  static constexpr int BYTES = WORDS * STAGES * THREADS * 16;
+  uint4 *mem;
+  __device__ __forceinline__ uint4 *slot(int stage, int w) const {
+    return mem + (stage * WORDS + w) * THREADS + threadIdx.x;
   }
-  template <typename E>
-  __device__ __forceinline__ void store(E *row, const float (&v)[VEC]) const {
-    if (VECTOR) {
-      constexpr int W = VEC * sizeof(E) / 16;
-      alignas(16) E e[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
-      if (in(0)) {
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-          reinterpret_cast<uint4 *>(row + at(0))[w] = reinterpret_cast<const uint4 *>(e)[w];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (in(i)) row[at(i)] = from_f32<E>(v[i]);
-    }
+  __device__ __forceinline__ void copy(int stage, int w, const void *src) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(slot(stage, w)))),
+                 "l"(src)
+                 : "memory");
   }
-  __device__ __forceinline__ void store(void *base, int dtype, int64_t offset,
-                                        const float (&v)[VEC]) const {
-    FF_TYPED(dtype, E, { store(static_cast<E *>(base) + offset, v); })
-  }
-  // A parameter vector (1 or 0 for every column where there is none).
-  __device__ __forceinline__ void params(const void *p, int dtype, float missing,
-                                         float (&v)[VEC]) const {
-    if (!p) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = missing;
-      return;
-    }
-    FF_TYPED(dtype, E, {
-      alignas(16) E e[VEC];
-      load(static_cast<const E *>(p), e);
-      _Pragma("unroll") for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
-    })
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The oldest of STAGES groups in flight has arrived.
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
   }
 };
 
 // ------------------------------------------------------------------------- forward
 
-// A group of T threads a row; piece c of thread t is columns (c T + t) 8 ... . The CTAs stay
-// and walk the rows: with one piece a thread, weight and bias are read once into registers
-// (read for every row they are four times the bytes of a bf16 row with fp32 parameters, from
-// L2: 16384 x 4096 took 152 us that way), and the next row's loads are issued before the
-// current row's reductions. Two pieces a thread leave no registers for the parameters.
-template <typename TI, int T, int CH, bool VECTOR>
-__global__ void __launch_bounds__(Cta<T>::THREADS, Cta<T>::PER_SM)
+// Few rows (or rows that 16-byte accesses cannot read): T threads a row, eight columns each,
+// so that a row's time is short; weight and bias in registers, the next row loaded during the
+// current row's reductions.
+template <typename TI, int T, bool VECTOR>
+__global__ void __launch_bounds__(Cta<T, 256>::THREADS, 1024 / Cta<T, 256>::THREADS)
     norm_rows_kernel(const TI *x, int64_t ldx, const void *weight, const void *bias,
                      int param_dtype, void *y, int64_t ldy, int out_dtype, float *mean_out,
                      float *rstd_out, float eps, int64_t M, int64_t N) {
-  constexpr int G = Cta<T>::GROUPS;
+  constexpr int G = Cta<T, 256>::GROUPS;
   __shared__ float red[G][2][T / 32];
   const int g = threadIdx.x / T, t = threadIdx.x % T;
-  const float n = static_cast<float>(N);
+  const float n = static_cast<float>(N), inv_n = 1.0f / n;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
   if (row >= M) return;
-  auto columns = [&](int c) { return Columns<T, VECTOR>{static_cast<int64_t>(c) * T * VEC, N, t}; };
-  alignas(16) TI next[CH][VEC];
+  const Columns<T, VECTOR> cols{0, N, t};
+  alignas(16) TI next[VEC];
   float w[VEC], b[VEC];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) columns(c).load(x + row * ldx, next[c]);
-  if (CH == 1) {
-    columns(0).params(weight, param_dtype, 1.0f, w);
-    columns(0).params(bias, param_dtype, 0.0f, b);
-  }
+  cols.load(x + row * ldx, next);
+  cols.params(weight, param_dtype, 1.0f, w);
+  cols.params(bias, param_dtype, 0.0f, b);
   for (; row < M; row += step) {
-    float v[CH][VEC];
+    float v[VEC];
     float s = 0.0f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        v[c][i] = to_f32(next[c][i]);
-        s += v[c][i];
-      }
-    if (row + step < M) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) columns(c).load(x + (row + step) * ldx, next[c]);
+    for (int i = 0; i < VEC; ++i) {
+      v[i] = to_f32(next[i]);
+      s += v[i];
     }
-    const float mean = group_sum<T>(s, red[g][0], g) / n;
+    if (row + step < M) cols.load(x + (row + step) * ldx, next);
+    const float mean = mean_of(group_sum<T>(s, red[g][0], g), n, inv_n);
     float q = 0.0f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int i = 0; i < VEC; ++i) {
+      v[i] -= mean;
+      if (cols.in(i)) q = fmaf(v[i], v[i], q);
+    }
+    const float rstd = rsqrtf(mean_of(group_sum<T>(q, red[g][1], g), n, inv_n) + eps);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i] * rstd, w[i], b[i]);
+    cols.store(y, out_dtype, row * ldy, v);
+    if (t == 0) {
+      if (mean_out) mean_out[row] = mean;
+      if (rstd_out) rstd_out[row] = rstd;
+    }
+  }
+}
+
+// Many rows: 32 columns a thread, four pieces of eight, (c T + t) 8 ... for piece c. The
+// reductions' instructions are per thread, so wide threads make the kernel wait for memory
+// and not for issue slots (8 columns a thread issued 0.7 instructions a cycle and scheduler
+// and moved 4.5 TB/s on 16384 x 4096 bf16). The CTAs stay and walk the rows: weight and bias
+// wait in shared memory in fp32 (from L2 they are four times the bytes of a bf16 row), the
+// next row in the ring.
+constexpr int kWidePieces = 4;
+template <typename TI, int T>
+struct WideNorm {
+  using C = Cta<T, 512>;
+  static constexpr int WORDS = kWidePieces * VEC * static_cast<int>(sizeof(TI)) / 16;
+  static constexpr int STAGES = WORDS > 4 ? 1 : 2;
+  using Ring = RowRing<WORDS, STAGES, C::THREADS>;
+  static constexpr int COLUMNS = T * kWidePieces * VEC;
+  static constexpr int SMEM = Ring::BYTES + 2 * COLUMNS * 4;
+  static constexpr int PER_SM = C::THREADS > 512 || SMEM > 113 * 1024 ? 1 : 2;
+};
+template <typename TI, int T>
+__global__ void __launch_bounds__(WideNorm<TI, T>::C::THREADS, 1024 / WideNorm<TI, T>::C::THREADS)
+    norm_wide_rows_kernel(const TI *x, int64_t ldx, const void *weight, const void *bias,
+                          int param_dtype, void *y, int64_t ldy, int out_dtype, float *mean_out,
+                          float *rstd_out, float eps, int64_t M, int64_t N) {
+  using K = WideNorm<TI, T>;
+  constexpr int G = K::C::GROUPS, PIECE_WORDS = K::WORDS / kWidePieces;
+  __shared__ float red[G][2][T / 32];
+  extern __shared__ uint4 dyn[];
+  const typename K::Ring ring{dyn};
+  // weight, bias: [which][piece][half of the piece][t] of four columns
+  float4 *params = reinterpret_cast<float4 *>(dyn + K::Ring::BYTES / 16);
+  const int g = threadIdx.x / T, t = threadIdx.x % T;
+  const float n = static_cast<float>(N), inv_n = 1.0f / n;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
+  auto columns = [&](int c) { return Columns<T, true>{static_cast<int64_t>(c) * T * VEC, N, t}; };
+  auto fetch = [&](int64_t i, int stage) {
+    if (i < M) {
+#pragma unroll
+      for (int c = 0; c < kWidePieces; ++c)
+        if (columns(c).in(0)) {
+#pragma unroll
+          for (int k = 0; k < PIECE_WORDS; ++k)
+            ring.copy(stage, c * PIECE_WORDS + k,
+                      reinterpret_cast<const uint4 *>(x + i * ldx + columns(c).at(0)) + k);
+        }
+    }
+    ring.commit();
+  };
+#pragma unroll
+  for (int k = 0; k < K::STAGES; ++k) fetch(row + k * step, k);
+  if (g == 0) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+      for (int c = 0; c < kWidePieces; ++c) {
+        float p[VEC];
+        if (columns(c).in(0)) {
+          columns(c).params(which ? bias : weight, param_dtype, which ? 0.0f : 1.0f, p);
+          params[((which * kWidePieces + c) * 2) * T + t] = make_float4(p[0], p[1], p[2], p[3]);
+          params[((which * kWidePieces + c) * 2 + 1) * T + t] = make_float4(p[4], p[5], p[6], p[7]);
+        }
+      }
+  }
+  __syncthreads();
+  for (int stage = 0; row < M; row += step) {
+    float v[kWidePieces][VEC];
+    float s = 0.0f;
+    ring.wait();
+#pragma unroll
+    for (int c = 0; c < kWidePieces; ++c) {
+      alignas(16) TI e[VEC];
+#pragma unroll
+      for (int k = 0; k < PIECE_WORDS; ++k)
+        reinterpret_cast<uint4 *>(e)[k] =
+            columns(c).in(0) ? *ring.slot(stage, c * PIECE_WORDS + k) : uint4{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        v[c][i] -= mean;
-        if (columns(c).in(i)) q = fmaf(v[c][i], v[c][i], q);
+        v[c][i] = to_f32(e[i]);
+        s += v[c][i];
       }
-    const float rstd = rsqrtf(group_sum<T>(q, red[g][1], g) / n + eps);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (CH > 1) {
-        columns(c).params(weight, param_dtype, 1.0f, w);
-        columns(c).params(bias, param_dtype, 0.0f, b);
-      }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(v[c][i] * rstd, w[i], b[i]);
-      columns(c).store(y, out_dtype, row * ldy, v[c]);
     }
+    fetch(row + K::STAGES * step, stage);  // into the slots just read
+    stage = stage + 1 < K::STAGES ? stage + 1 : 0;
+    const float mean = mean_of(group_sum<T>(s, red[g][0], g), n, inv_n);
+    float q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kWidePieces; ++c)
+      if (columns(c).in(0)) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          v[c][i] -= mean;
+          q = fmaf(v[c][i], v[c][i], q);
+        }
+      }
+    const float rstd = rsqrtf(mean_of(group_sum<T>(q, red[g][1], g), n, inv_n) + eps);
+#pragma unroll
+    for (int c = 0; c < kWidePieces; ++c)
+      if (columns(c).in(0)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 w = params[(c * 2 + h) * T + t];
+          const float4 b = params[((kWidePieces + c) * 2 + h) * T + t];
+          float *o = &v[c][4 * h];
+          o[0] = fmaf(o[0] * rstd, w.x, b.x);
+          o[1] = fmaf(o[1] * rstd, w.y, b.y);
+          o[2] = fmaf(o[2] * rstd, w.z, b.z);
+          o[3] = fmaf(o[3] * rstd, w.w, b.w);
+        }
+        columns(c).store(y, out_dtype, row * ldy, v[c]);
+      }
     if (t == 0) {
       if (mean_out) mean_out[row] = mean;
       if (rstd_out) rstd_out[row] = rstd;
@@ -257,103 +317,157 @@ __global__ void __launch_bounds__(512)
 
 // ------------------------------------------------------------------------ backward
 
-// One pass for rows a CTA's registers hold (8 columns a thread): a group of T threads a row,
-// x and dy read once, with the next row's loads in flight during the current row's
-// reduction, dx written, and the columns' sums of dy xh and dy kept in registers over all of
-// the group's rows. The groups of a CTA join theirs at the end; column_finish adds the CTAs.
+// One pass for rows a CTA's registers hold: a group of T threads a row, 16 columns a thread in
+// two pieces, x and dy read once (the next rows on their way in the ring where rows are 16-byte
+// aligned), dx written, and the columns' sums of dy xh and dy kept in registers over all of the
+// group's rows. The groups of a CTA join theirs at the end; column_finish adds the CTAs.
+constexpr int kBackPieces = 2;
 template <typename TI, int T, bool VECTOR>
-__global__ void __launch_bounds__(Cta<T>::THREADS, Cta<T>::PER_SM)
+struct NormBackward {
+  using C = Cta<T, 256>;
+  static constexpr int PIECE_WORDS = VEC * static_cast<int>(sizeof(TI)) / 16;
+  static constexpr int WORDS = 2 * kBackPieces * PIECE_WORDS;  // x and dy
+  static constexpr int STAGES = 2;
+  using Ring = RowRing<WORDS, STAGES, C::THREADS>;
+  static constexpr int COLUMNS = T * kBackPieces * VEC;
+  // weight, or at the end the groups' sums: two fp32 values a column
+  static constexpr int SMEM = (VECTOR ? Ring::BYTES : 0) + 2 * COLUMNS * 4;
+  static constexpr int PER_SM = 512 / C::THREADS;  // 128 registers a thread
+};
+template <typename TI, int T, bool VECTOR>
+__global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREADS)
     norm_backward_kernel(const TI *__restrict__ dy, int64_t lddy, const TI *__restrict__ x,
                          int64_t ldx, const void *weight, int param_dtype,
                          const float *__restrict__ mean, const float *__restrict__ rstd,
                          TI *__restrict__ dx, int64_t lddx, float *__restrict__ partials,
                          int32_t M, int64_t N) {
-  constexpr int G = Cta<T>::GROUPS;
+  using K = NormBackward<TI, T, VECTOR>;
+  constexpr int G = K::C::GROUPS, PW = K::PIECE_WORDS;
   __shared__ float red[G][2][2 * (T / 32)];
-  __shared__ float join[G > 1 ? 2 : 1][G > 1 ? T * VEC : 1];
-  __shared__ float4 ws[2][T];  // the weight: registers go to the columns' sums
+  extern __shared__ uint4 dyn[];
+  const typename K::Ring ring{dyn};
+  float4 *ws = reinterpret_cast<float4 *>(dyn + (VECTOR ? K::Ring::BYTES / 16 : 0));
   const int g = threadIdx.x / T, t = threadIdx.x % T;
-  const Columns<T, VECTOR> cols{0, N, t};
+  const float n = static_cast<float>(N), inv_n = 1.0f / n;
   const int step = static_cast<int>(gridDim.x) * G;
   int row = static_cast<int>(blockIdx.x) * G + g;
-  float dw[VEC], db[VEC];
-  alignas(16) TI nx[VEC];
-  alignas(16) TI nd[VEC];
-  float nmu = 0.0f, nr = 0.0f;
-  auto fetch = [&](int i) {
-    cols.load(x + i * ldx, nx);
-    cols.load(dy + i * lddy, nd);
-    nmu = mean[i];
-    nr = rstd[i];
+  auto columns = [&](int c) { return Columns<T, VECTOR>{static_cast<int64_t>(c) * T * VEC, N, t}; };
+  auto after = [&](int i, int k) { return (M - 1 - i) / step >= k ? i + k * step : M; };
+  auto fetch = [&](int i, int stage) {
+    if (i < M) {
+#pragma unroll
+      for (int c = 0; c < kBackPieces; ++c)
+        if (columns(c).in(0)) {
+#pragma unroll
+          for (int k = 0; k < PW; ++k) {
+            ring.copy(stage, 2 * c * PW + k, reinterpret_cast<const uint4 *>(x + i * ldx + columns(c).at(0)) + k);
+            ring.copy(stage, (2 * c + 1) * PW + k,
+                      reinterpret_cast<const uint4 *>(dy + i * lddy + columns(c).at(0)) + k);
+          }
+        }
+    }
+    ring.commit();
   };
-  if (row < M) fetch(row);
+  float dw[kBackPieces][VEC], db[kBackPieces][VEC];
+  float nmu = 0.0f, nr = 0.0f;
+  if (row < M) {
+    if (VECTOR) {
+#pragma unroll
+      for (int k = 0; k < K::STAGES; ++k) fetch(after(row, k), k);
+    }
+    nmu = mean[row], nr = rstd[row];
+  }
   if (g == 0) {
-    cols.params(weight, param_dtype, 1.0f, dw);
-    ws[0][t] = make_float4(dw[0], dw[1], dw[2], dw[3]);
-    ws[1][t] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+#pragma unroll
+    for (int c = 0; c < kBackPieces; ++c) {
+      columns(c).params(weight, param_dtype, 1.0f, dw[c]);
+      ws[(2 * c) * T + t] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
+      ws[(2 * c + 1) * T + t] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) dw[i] = db[i] = 0.0f;
-  int buf = 0;
-  while (row < M) {
-    const int next = M - row > step ? row + step : M;
-    const float r = nr;
-    float xh[VEC], d[VEC];
+  for (int c = 0; c < kBackPieces; ++c)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      xh[i] = (to_f32(nx[i]) - nmu) * r;
-      d[i] = to_f32(nd[i]);
-    }
-    if (next < M) fetch(next);
-    const float4 w0 = ws[0][t], w1 = ws[1][t];
-    const float w[VEC] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    for (int i = 0; i < VEC; ++i) dw[c][i] = db[c][i] = 0.0f;
+  for (int buf = 0, stage = 0; row < M; buf ^= 1) {
+    const float mu = nmu, r = nr;
+    float xh[kBackPieces][VEC], d[kBackPieces][VEC];
     float s[2] = {0.0f, 0.0f};
+    if (VECTOR) ring.wait();
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {  // (dy reads as 0 past the row's end)
-      dw[i] = fmaf(d[i], xh[i], dw[i]);
-      db[i] += d[i];
-      d[i] *= w[i];
-      s[0] += d[i];
-      s[1] = fmaf(d[i], xh[i], s[1]);
+    for (int c = 0; c < kBackPieces; ++c) {
+      alignas(16) TI ex[VEC];
+      alignas(16) TI ed[VEC];
+      if (VECTOR) {
+#pragma unroll
+        for (int k = 0; k < PW; ++k) {
+          const bool in = columns(c).in(0);
+          reinterpret_cast<uint4 *>(ex)[k] = in ? *ring.slot(stage, 2 * c * PW + k) : uint4{0, 0, 0, 0};
+          reinterpret_cast<uint4 *>(ed)[k] = in ? *ring.slot(stage, (2 * c + 1) * PW + k) : uint4{0, 0, 0, 0};
+        }
+      } else {
+        columns(c).load(x + row * ldx, ex);
+        columns(c).load(dy + row * lddy, ed);
+      }
+      const float4 w0 = ws[(2 * c) * T + t], w1 = ws[(2 * c + 1) * T + t];
+      const float w[VEC] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {  // (dy reads as 0 past the row's end)
+        xh[c][i] = (to_f32(ex[i]) - mu) * r;
+        const float e = to_f32(ed[i]);
+        dw[c][i] = fmaf(e, xh[c][i], dw[c][i]);
+        db[c][i] += e;
+        d[c][i] = e * w[i];
+        s[0] += d[c][i];
+        s[1] = fmaf(d[c][i], xh[c][i], s[1]);
+      }
     }
+    if (VECTOR) {
+      fetch(after(row, K::STAGES), stage);  // into the slots just read
+      stage ^= 1;
+    }
+    const int next = after(row, 1);
+    if (next < M) nmu = mean[next], nr = rstd[next];
     group_sum<T, 2>(s, red[g][buf], g);
-    buf ^= 1;
     if (dx) {
-      const float n = static_cast<float>(N);
-      const float a = s[0] / n, b = s[1] / n;
+      const float a = mean_of(s[0], n, inv_n), b = mean_of(s[1], n, inv_n);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) d[i] = r * (d[i] - a - xh[i] * b);
-      cols.store(dx + row * lddx, d);
+      for (int c = 0; c < kBackPieces; ++c) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) d[c][i] = r * (d[c][i] - a - xh[c][i] * b);
+        columns(c).store(dx + row * lddx, d[c]);
+      }
     }
     row = next;
   }
   if (!partials) return;
-  if (G > 1) {  // in the groups' order
+  if (G > 1) {  // joined in the groups' order, over the weight's place
+    float *join = reinterpret_cast<float *>(ws);
     for (int k = 0; k < G; ++k) {
+      __syncthreads();
       if (g == k) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          join[0][i * T + t] = k ? join[0][i * T + t] + dw[i] : dw[i];
-          join[1][i * T + t] = k ? join[1][i * T + t] + db[i] : db[i];
-        }
-      }
-      __syncthreads();
-    }
-    if (g != 0) return;
+        for (int c = 0; c < kBackPieces; ++c)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      dw[i] = join[0][i * T + t];
-      db[i] = join[1][i * T + t];
+          for (int i = 0; i < VEC; ++i) {
+            float *w = join + (c * VEC + i) * T + t, *b = w + K::COLUMNS;
+            dw[c][i] = *w = k ? *w + dw[c][i] : dw[c][i];
+            db[c][i] = *b = k ? *b + db[c][i] : db[c][i];
+          }
+      }
     }
+    if (g != G - 1) return;  // the last group holds the sums
   }
   float *out = partials + static_cast<int64_t>(blockIdx.x) * 2 * N;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    if (cols.in(i)) {
-      out[cols.at(i)] = dw[i];
-      out[N + cols.at(i)] = db[i];
-    }
+  for (int c = 0; c < kBackPieces; ++c)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (columns(c).in(i)) {
+        out[columns(c).at(i)] = dw[c][i];
+        out[N + columns(c).at(i)] = db[c][i];
+      }
 }
 
 // Longer rows, and a dy of another type than x: the rows' means first, then columns.
@@ -365,18 +479,19 @@ __global__ void __launch_bounds__(256)
                           const float *__restrict__ mean, const float *__restrict__ rstd,
                           float2 *__restrict__ means, int64_t M, int64_t N) {
   const float n = static_cast<float>(N);
+  Columns<32, VECTOR> cols{0, N, static_cast<int>(threadIdx.x % 32)};
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; row < M;
        row += static_cast<int64_t>(gridDim.x) * 8) {
     const float mu = mean[row], r = rstd[row];
     float a = 0.0f, b = 0.0f;
-    for (int64_t j0 = (threadIdx.x % 32) * VEC; j0 < N; j0 += 32 * VEC) {
-      float vx[VEC], vd[VEC];
-      load_piece<TI, VEC, VECTOR>(x + row * ldx, j0, N, vx);
-      load_piece<TG, VEC, VECTOR>(dy + row * lddy, j0, N, vd);
+    for (cols.first = 0; cols.first < N; cols.first += 32 * VEC) {
+      float vx[VEC], vd[VEC], w[VEC];
+      cols.load_f32(x + row * ldx, vx);
+      cols.load_f32(dy + row * lddy, vd);
+      cols.params(weight, param_dtype, 1.0f, w);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float w = weight && j0 + i < N ? load_any(weight, param_dtype, j0 + i) : 1.0f;
-        const float v = vd[i] * w;  // 0 past the row's end: dy reads as 0 there
+        const float v = vd[i] * w[i];  // 0 past the row's end: dy reads as 0 there
         a += v;
         b = fmaf(v, (vx[i] - mu) * r, b);
       }
@@ -387,7 +502,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-//
 // dx and the sums of dy xh and dy over a band of rows, from the rows' means: a warp covers
 // 256 columns, a CTA's eight warps eight rows at a time.
 template <typename TG, typename TI, bool VECTOR>
@@ -399,21 +513,19 @@ __global__ void __launch_bounds__(256)
                         float *__restrict__ partials, int64_t M, int64_t N, int64_t band) {
   __shared__ float red[2][8][32 * VEC];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * VEC;
+  const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * 32 * VEC, N, lane};
   const int64_t lo = static_cast<int64_t>(blockIdx.y) * band;
   const int64_t hi = lo + band < M ? lo + band : M;
   float w[VEC], dw[VEC], db[VEC];
+  cols.params(weight, param_dtype, 1.0f, w);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    w[i] = weight && j0 + i < N ? load_any(weight, param_dtype, j0 + i) : 1.0f;
-    dw[i] = db[i] = 0.0f;
-  }
-  if (j0 < N) {
+  for (int i = 0; i < VEC; ++i) dw[i] = db[i] = 0.0f;
+  if (cols.in(0)) {
 #pragma unroll 2
     for (int64_t row = lo + warp; row < hi; row += 8) {
       float vx[VEC], vd[VEC];
-      load_piece<TI, VEC, VECTOR>(x + row * ldx, j0, N, vx);
-      load_piece<TG, VEC, VECTOR>(dy + row * lddy, j0, N, vd);
+      cols.load_f32(x + row * ldx, vx);
+      cols.load_f32(dy + row * lddy, vd);
       const float mu = mean[row], r = rstd[row];
       const float2 m = means[row];
 #pragma unroll
@@ -423,7 +535,7 @@ __global__ void __launch_bounds__(256)
         db[i] += vd[i];
         vx[i] = r * (fmaf(vd[i], w[i], -m.x) - xh * m.y);
       }
-      if (dx) store_piece<TI, VEC, VECTOR>(dx + row * lddx, j0, N, vx);
+      if (dx) cols.store(dx + row * lddx, vx);
     }
   }
   if (!partials) return;
@@ -440,9 +552,10 @@ __global__ void __launch_bounds__(256)
     a += red[0][k][i * 32 + lane];
     b += red[1][k][i * 32 + lane];
   }
-  if (j0 + i < N) {
-    partials[(static_cast<int64_t>(blockIdx.y) * 2) * N + j0 + i] = a;
-    partials[(static_cast<int64_t>(blockIdx.y) * 2 + 1) * N + j0 + i] = b;
+  if (cols.in(i)) {
+    float *out = partials + static_cast<int64_t>(blockIdx.y) * 2 * N + cols.at(i);
+    out[0] = a;
+    out[N] = b;
   }
 }
 
@@ -469,40 +582,64 @@ int grid_of(int64_t ctas, int sm_count, int per_sm) {
   return static_cast<int>(ctas < 1 ? 1 : ctas < cap ? ctas : cap);
 }
 
-template <typename TI, int T, int CH>
+template <typename TI, int T>
 void launch_rows(const NormArgs &a) {
-  const int grid = grid_of((a.M + Cta<T>::GROUPS - 1) / Cta<T>::GROUPS, a.sm_count, Cta<T>::PER_SM);
-  auto kernel = a.vec ? norm_rows_kernel<TI, T, CH, true> : norm_rows_kernel<TI, T, CH, false>;
-  kernel<<<grid, Cta<T>::THREADS, 0, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias,
-                                            a.param_dtype, a.y, a.ldy, a.out_dtype, a.mean, a.rstd,
-                                            a.eps, a.M, a.N);
+  using C = Cta<T, 256>;
+  const int grid = grid_of((a.M + C::GROUPS - 1) / C::GROUPS, a.sm_count, 1024 / C::THREADS);
+  auto kernel = a.vec ? norm_rows_kernel<TI, T, true> : norm_rows_kernel<TI, T, false>;
+  kernel<<<grid, C::THREADS, 0, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias,
+                                       a.param_dtype, a.y, a.ldy, a.out_dtype, a.mean, a.rstd,
+                                       a.eps, a.M, a.N);
 }
 
-// Threads that hold a row of N columns, eight each: 32 .. 1024.
-int row_threads(int64_t N) {
+template <typename TI, int T>
+void launch_wide_rows(const NormArgs &a) {
+  using K = WideNorm<TI, T>;
+  const int grid = grid_of((a.M + K::C::GROUPS - 1) / K::C::GROUPS, a.sm_count, K::PER_SM);
+  auto kernel = norm_wide_rows_kernel<TI, T>;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
+  kernel<<<grid, K::C::THREADS, K::SMEM, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight,
+                                                a.bias, a.param_dtype, a.y, a.ldy, a.out_dtype,
+                                                a.mean, a.rstd, a.eps, a.M, a.N);
+}
+
+// Threads that hold a row of N columns, `each` a thread: 32 .. 1024.
+int row_threads(int64_t N, int each) {
   int t = 32;
-  while (t < 1024 && t * VEC < N) t *= 2;
+  while (t < 1024 && static_cast<int64_t>(t) * each < N) t *= 2;
   return t;
 }
-constexpr int64_t kOnePassColumns = 1024 * VEC;
 
 template <typename TI>
 void dispatch_rows(const NormArgs &a) {
-  if (a.N > 2 * kOnePassColumns) {
+  // Wide threads from eight rows an SM on: fewer rows leave most of their groups idle and take
+  // one row's time, which narrow threads make shorter. Rows past narrow threads' 8192 columns
+  // go to wide ones in any number.
+  const bool wide = a.vec && a.N > 256 && a.N <= 512 * 32 &&
+                    (a.M >= 8 * static_cast<int64_t>(a.sm_count) || a.N > 1024 * VEC);
+  if (wide) {
+    switch (row_threads(a.N, kWidePieces * VEC)) {
+      case 32: return launch_wide_rows<TI, 32>(a);
+      case 64: return launch_wide_rows<TI, 64>(a);
+      case 128: return launch_wide_rows<TI, 128>(a);
+      case 256: return launch_wide_rows<TI, 256>(a);
+      default: return launch_wide_rows<TI, 512>(a);
+    }
+  }
+  if (a.N > 1024 * VEC) {
     auto kernel = a.vec ? norm_long_rows_kernel<TI, true> : norm_long_rows_kernel<TI, false>;
     kernel<<<grid_of(a.M, a.sm_count, 64), 512, 0, a.s>>>(
         static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias, a.param_dtype, a.y, a.ldy,
         a.out_dtype, a.mean, a.rstd, a.eps, a.M, a.N);
     return;
   }
-  if (a.N > kOnePassColumns) return launch_rows<TI, 1024, 2>(a);
-  switch (row_threads(a.N)) {
-    case 32: return launch_rows<TI, 32, 1>(a);
-    case 64: return launch_rows<TI, 64, 1>(a);
-    case 128: return launch_rows<TI, 128, 1>(a);
-    case 256: return launch_rows<TI, 256, 1>(a);
-    case 512: return launch_rows<TI, 512, 1>(a);
-    default: return launch_rows<TI, 1024, 1>(a);
+  switch (row_threads(a.N, VEC)) {
+    case 32: return launch_rows<TI, 32>(a);
+    case 64: return launch_rows<TI, 64>(a);
+    case 128: return launch_rows<TI, 128>(a);
+    case 256: return launch_rows<TI, 256>(a);
+    case 512: return launch_rows<TI, 512>(a);
+    default: return launch_rows<TI, 1024>(a);
   }
 }
 
@@ -539,20 +676,28 @@ struct NormBackwardArgs {
   cudaStream_t s;
 };
 
-template <typename TI, int T>
+template <typename TI, int T, bool VECTOR>
 void launch_backward(const NormBackwardArgs &a) {
-  auto kernel = a.vec ? norm_backward_kernel<TI, T, true> : norm_backward_kernel<TI, T, false>;
-  kernel<<<a.grid, Cta<T>::THREADS, 0, a.s>>>(
+  using K = NormBackward<TI, T, VECTOR>;
+  auto kernel = norm_backward_kernel<TI, T, VECTOR>;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
+  kernel<<<a.grid, K::C::THREADS, K::SMEM, a.s>>>(
       static_cast<const TI *>(a.dy), a.lddy, static_cast<const TI *>(a.x), a.ldx, a.weight,
       a.param_dtype, a.mean, a.rstd, static_cast<TI *>(a.dx), a.lddx, a.partials,
       static_cast<int32_t>(a.M), a.N);
 }
+template <typename TI, int T>
+void launch_backward(const NormBackwardArgs &a) {
+  a.vec ? launch_backward<TI, T, true>(a) : launch_backward<TI, T, false>(a);
+}
 
-// Grid of the one-pass kernel: as many CTAs as stay on the SMs, or as have rows.
+// The one-pass kernel takes rows of up to 512 threads; its grid: as many CTAs as stay on the
+// SMs, or as have rows.
+constexpr int64_t kOnePassColumns = 512 * kBackPieces * VEC;
 int backward_grid(int64_t M, int64_t N, int sm_count) {
-  const int t = row_threads(N);
+  const int t = row_threads(N, kBackPieces * VEC);
   const int64_t groups = t < 256 ? 256 / t : 1;
-  return grid_of((M + groups - 1) / groups, sm_count, t < 256 ? 4 : 1024 / t);
+  return grid_of((M + groups - 1) / groups, sm_count, t < 512 ? 2 : 1);
 }
 
 }  // namespace
@@ -571,22 +716,21 @@ cudaError_t layer_norm_backward_launch(const void *dy, int64_t lddy, int grad_dt
                                        void *workspace, int64_t M, int64_t N, int sm_count,
                                        int *launches, cudaStream_t s) {
   const int is = esize(in_dtype);
-  const bool vec = aligned16(dy, lddy, esize(grad_dtype)) && aligned16(x, ldx, is) &&
-                   aligned16(dx, lddx, is);
+  const bool vec = N % VEC == 0 && aligned16(dy, lddy, esize(grad_dtype)) &&
+                   aligned16(x, ldx, is) && aligned16(dx, lddx, is) && aligned16(weight, 0, 4);
   if (N <= kOnePassColumns && grad_dtype == in_dtype) {
     float *sums = static_cast<float *>(workspace);
     const int grid = backward_grid(M, N, sm_count);
     const NormBackwardArgs a{dy, lddy, x, ldx, weight, param_dtype, mean, rstd, dx, lddx,
                              dweight || dbias ? sums : nullptr, M, N,
-                             vec && aligned16(weight, 0, 4) && N % VEC == 0, grid, s};
+                             vec, grid, s};
     FF_TYPED(in_dtype, TI, {
-      switch (row_threads(N)) {
+      switch (row_threads(N, kBackPieces * VEC)) {
         case 32: launch_backward<TI, 32>(a); break;
         case 64: launch_backward<TI, 64>(a); break;
         case 128: launch_backward<TI, 128>(a); break;
         case 256: launch_backward<TI, 256>(a); break;
-        case 512: launch_backward<TI, 512>(a); break;
-        default: launch_backward<TI, 1024>(a); break;
+        default: launch_backward<TI, 512>(a); break;
       }
     })
     ++*launches;

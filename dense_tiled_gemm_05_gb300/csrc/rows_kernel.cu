@@ -5,9 +5,9 @@
 //   dg = dh u act'(g),  du = dh act(g)
 //   dz = dy act'(pre),  dbias_j = sum_i dz_ij
 //
-// All are bound by the bytes they read and write. A warp covers 32 consecutive pieces of a
-// row (16 bytes of the narrowest type a lane, 512 bytes a warp), so every request is whole
-// sectors; a CTA's eight warps take eight rows at a time. Sums over rows are kept in fp32
+// All are bound by the bytes they read and write. A warp covers 256 columns of a row, eight a
+// lane: consecutive ones in 16-byte accesses where the rows allow it, else every 32nd, so that
+// a request's lanes are neighbours. A CTA's eight warps take eight rows at a time. Sums over rows are kept in fp32
 // registers over a band of rows and joined over the CTA's warps in shared memory, then over
 // the bands in a second kernel, always in the same order.
 #include "activation.cuh"
@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int VEC = 8;                // columns a lane
 constexpr int kCols = 32 * VEC;       // columns a CTA
 
 bool aligned16(const void *p, int64_t ld, int es) {
@@ -27,41 +26,52 @@ bool aligned16(const void *p, int64_t ld, int es) {
 }
 int esize(int dt) { return dt == GEMM_F32 ? 4 : 2; }
 
-// Rows a CTA takes: all of them over gridDim.y CTAs, kWarps at a time.
+// A warp walks rows of its 256 columns, so that the loads of several rows overlap: about ten
+// CTAs for every one of 152 SMs, whatever the matrix (more rows a warp and fewer CTAs start
+// unevenly, one row a warp spends its time starting CTAs: 8192 x 8192 slopes took 191 us).
 dim3 rows_grid(int64_t M, int64_t N) {
   const int64_t gx = (N + kCols - 1) / kCols;
-  int64_t gy = (M + kWarps - 1) / kWarps;
+  const int64_t all = (M + kWarps - 1) / kWarps;
+  int64_t gy = (1520 + gx - 1) / gx;
+  if (gy > all) gy = all;
   if (gy > 65535) gy = 65535;
   return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
 }
 
-// (z and y may be one buffer: a lane reads its piece before it writes it)
+#define FF_ROWS(i, M)                                                                     \
+  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; i < M;   \
+       i += static_cast<int64_t>(gridDim.y) * kWarps)
+
+template <bool VECTOR>
+__device__ __forceinline__ Columns<32, VECTOR> my_columns(int64_t N) {
+  return {static_cast<int64_t>(blockIdx.x) * kCols, N, static_cast<int>(threadIdx.x % 32)};
+}
+
+// (z and y may be one buffer: a lane reads its columns before it writes them)
 template <typename TO, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     epilogue_rows_kernel(const float *z, int64_t ldz, TO *y, int64_t ldy, const Epilogue ep,
                          int64_t M, int64_t N) {
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kCols + (threadIdx.x % 32) * VEC;
-  if (j0 >= N) return;
+  const auto cols = my_columns<VECTOR>(N);
+  if (!cols.in(0)) return;
   float b[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i)
-    b[i] = ep.bias && j0 + i < N ? load_any(ep.bias, ep.bias_dtype, j0 + i) : 0.0f;
-  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; i < M;
-       i += static_cast<int64_t>(gridDim.y) * kWarps) {
+    b[i] = ep.bias && cols.in(i) ? load_any(ep.bias, ep.bias_dtype, cols.at(i)) : 0.0f;
+#pragma unroll 2
+  FF_ROWS(i, M) {
     float v[VEC], r[VEC];
-    load_piece<float, VEC, VECTOR>(z + i * ldz, j0, N, v);
-    if (ep.residual)
-      load_piece<TO, VEC, VECTOR>(static_cast<const TO *>(ep.residual) + i * ep.ld_residual, j0, N, r);
+    cols.load_f32(z + i * ldz, v);
+    if (ep.residual) cols.load_f32(static_cast<const TO *>(ep.residual) + i * ep.ld_residual, r);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) v[c] += b[c];
-    if (ep.pre) store_piece<TO, VEC, VECTOR>(static_cast<TO *>(ep.pre) + i * ep.ld_pre, j0, N, v);
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) v[c] = activate<false>(v[c], ep.act);
+    if (ep.pre) cols.store(static_cast<TO *>(ep.pre) + i * ep.ld_pre, v);
+    activate_all<false>(v, ep.act);
     if (ep.residual) {
 #pragma unroll
       for (int c = 0; c < VEC; ++c) v[c] += r[c];
     }
-    store_piece<TO, VEC, VECTOR>(y + i * ldy, j0, N, v);
+    cols.store(y + i * ldy, v);
   }
 }
 
@@ -69,16 +79,17 @@ template <typename TO, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     gated_rows_kernel(const float *__restrict__ g, int64_t ldg, const float *__restrict__ u,
                       int64_t ldu, TO *__restrict__ h, int64_t ldh, int act, int64_t M, int64_t F) {
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kCols + (threadIdx.x % 32) * VEC;
-  if (j0 >= F) return;
-  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; i < M;
-       i += static_cast<int64_t>(gridDim.y) * kWarps) {
+  const auto cols = my_columns<VECTOR>(F);
+  if (!cols.in(0)) return;
+#pragma unroll 2
+  FF_ROWS(i, M) {
     float a[VEC], b[VEC];
-    load_piece<float, VEC, VECTOR>(g + i * ldg, j0, F, a);
-    load_piece<float, VEC, VECTOR>(u + i * ldu, j0, F, b);
+    cols.load_f32(g + i * ldg, a);
+    cols.load_f32(u + i * ldu, b);
+    activate_all<false>(a, act);
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) a[c] = activate<false>(a[c], act) * b[c];
-    store_piece<TO, VEC, VECTOR>(h + i * ldh, j0, F, a);
+    for (int c = 0; c < VEC; ++c) a[c] *= b[c];
+    cols.store(h + i * ldh, a);
   }
 }
 
@@ -88,24 +99,23 @@ __global__ void __launch_bounds__(kThreads)
                         int64_t ldg, const T *__restrict__ u, int64_t ldu, T *__restrict__ dg,
                         int64_t lddg, T *__restrict__ du, int64_t lddu, int act, int64_t M,
                         int64_t F) {
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kCols + (threadIdx.x % 32) * VEC;
-  if (j0 >= F) return;
-  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; i < M;
-       i += static_cast<int64_t>(gridDim.y) * kWarps) {
-    float vh[VEC], vg[VEC], vu[VEC];
-    load_piece<T, VEC, VECTOR>(dh + i * lddh, j0, F, vh);
-    load_piece<T, VEC, VECTOR>(g + i * ldg, j0, F, vg);
-    load_piece<T, VEC, VECTOR>(u + i * ldu, j0, F, vu);
+  const auto cols = my_columns<VECTOR>(F);
+  if (!cols.in(0)) return;
+#pragma unroll 2
+  FF_ROWS(i, M) {
+    float vh[VEC], vg[VEC], vu[VEC], a[VEC], d[VEC];
+    cols.load_f32(dh + i * lddh, vh);
+    cols.load_f32(g + i * ldg, vg);
+    cols.load_f32(u + i * ldu, vu);
+    activate_slope_all<sizeof(T) == 2>(vg, act, a, d);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      float a, d;
-      activate_slope<sizeof(T) == 2>(vg[c], act, a, d);
-      vg[c] = vh[c] * vu[c] * d;
-      vu[c] = vh[c] * a;
+      vg[c] = vh[c] * vu[c] * d[c];
+      vu[c] = vh[c] * a[c];
     }
     // (16-bit types: the rounding that makes dg and du operands of the tensor cores)
-    store_piece<T, VEC, VECTOR>(dg + i * lddg, j0, F, vg);
-    store_piece<T, VEC, VECTOR>(du + i * lddu, j0, F, vu);
+    cols.store(dg + i * lddg, vg);
+    cols.store(du + i * lddu, vu);
   }
 }
 
@@ -113,16 +123,16 @@ template <typename TO, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     add_rows_kernel(const float *a, int64_t lda, const float *__restrict__ b, int64_t ldb, TO *y,
                     int64_t ldy, int64_t M, int64_t N) {
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kCols + (threadIdx.x % 32) * VEC;
-  if (j0 >= N) return;
-  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; i < M;
-       i += static_cast<int64_t>(gridDim.y) * kWarps) {
+  const auto cols = my_columns<VECTOR>(N);
+  if (!cols.in(0)) return;
+#pragma unroll 2
+  FF_ROWS(i, M) {
     float v[VEC], w[VEC];
-    load_piece<float, VEC, VECTOR>(a + i * lda, j0, N, v);
-    load_piece<float, VEC, VECTOR>(b + i * ldb, j0, N, w);
+    cols.load_f32(a + i * lda, v);
+    cols.load_f32(b + i * ldb, w);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) v[c] += w[c];
-    store_piece<TO, VEC, VECTOR>(y + i * ldy, j0, N, v);
+    cols.store(y + i * ldy, v);
   }
 }
 
@@ -134,63 +144,63 @@ __global__ void __launch_bounds__(kThreads)
                            float *__restrict__ partials, int64_t M, int64_t N, int64_t band) {
   __shared__ float red[kWarps][kCols];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kCols + lane * VEC;
+  const auto cols = my_columns<VECTOR>(N);
   const int64_t lo = static_cast<int64_t>(blockIdx.y) * band;
   const int64_t hi = lo + band < M ? lo + band : M;
   float sum[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) sum[c] = 0.0f;
-  if (j0 < N) {
+  if (cols.in(0)) {
 #pragma unroll 2
     for (int64_t i = lo + warp; i < hi; i += kWarps) {
-      float v[VEC], z[VEC];
-      load_piece<TG, VEC, VECTOR>(dy + i * lddy, j0, N, v);
+      float v[VEC];
+      cols.load_f32(dy + i * lddy, v);
       if (pre) {
-        load_piece<TG, VEC, VECTOR>(pre + i * ld_pre, j0, N, z);
+        float z[VEC], a[VEC], d[VEC];
+        cols.load_f32(pre + i * ld_pre, z);
+        activate_slope_all<sizeof(TZ) == 2>(z, act, a, d);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          float a, d;
-          activate_slope<sizeof(TZ) == 2>(z[c], act, a, d);
-          v[c] *= d;
-        }
+        for (int c = 0; c < VEC; ++c) v[c] *= d[c];
       }
 #pragma unroll
       for (int c = 0; c < VEC; ++c) sum[c] += v[c];
-      if (dz) store_piece<TZ, VEC, VECTOR>(dz + i * lddz, j0, N, v);
+      if (dz) cols.store(dz + i * lddz, v);
     }
   }
   if (!partials) return;
 #pragma unroll
   for (int c = 0; c < VEC; ++c) red[warp][c * 32 + lane] = sum[c];
   __syncthreads();
-  // thread t sums column (t % 32) * VEC + t / 32 of the CTA over the warps
+  // thread t joins piece t / 32 of lane t % 32 over the warps
   const int c = threadIdx.x / 32;
   float s = 0.0f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) s += red[w][c * 32 + lane];
-  if (j0 + c < N) partials[static_cast<int64_t>(blockIdx.y) * N + j0 + c] = s;
+  if (cols.in(c)) partials[static_cast<int64_t>(blockIdx.y) * N + cols.at(c)] = s;
 }
 
-__global__ void __launch_bounds__(256)
+// 32 columns a CTA; its 32 warps take every 32nd band, eight loads in flight each, and are
+// joined in their order. (Eight warps took 9 us for 304 bands of 4096 columns.)
+__global__ void __launch_bounds__(1024)
     column_finish_kernel(const float *__restrict__ partials, int64_t bands, int sums,
                          void *out0, void *out1, int dtype, int64_t N) {
-  // 32 columns a CTA; its eight warps take every eighth band, joined in order
-  __shared__ float red[8][32];
+  __shared__ float red[32][33];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const int which = blockIdx.y;
   float s = 0.0f;
   if (j < N) {
-#pragma unroll 4
-    for (int64_t b = warp; b < bands; b += 8) s += partials[(b * sums + which) * N + j];
+#pragma unroll 8
+    for (int64_t b = warp; b < bands; b += 32) s += partials[(b * sums + which) * N + j];
   }
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && j < N) {
+  // warp w joins column w of the CTA: lane l holds warp l's sum
+  s = red[lane][warp];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
-    store_any(which ? out1 : out0, dtype, j, s);
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && col < N) store_any(which ? out1 : out0, dtype, col, s);
 }
 
 }  // namespace
@@ -209,7 +219,7 @@ int64_t column_bands(int64_t M, int64_t N, int sm_count) {
 cudaError_t epilogue_rows_launch(const float *z, int64_t ldz, void *y, int64_t ldy, int out_dtype,
                                  const Epilogue &ep, int64_t M, int64_t N, cudaStream_t s) {
   const int os = esize(out_dtype);
-  const bool vec = aligned16(z, ldz, 4) && aligned16(y, ldy, os) &&
+  const bool vec = N % VEC == 0 && aligned16(z, ldz, 4) && aligned16(y, ldy, os) &&
                    aligned16(ep.residual, ep.ld_residual, os) && aligned16(ep.pre, ep.ld_pre, os);
   const dim3 grid = rows_grid(M, N);
   FF_TYPED(out_dtype, T, {
@@ -224,7 +234,7 @@ cudaError_t epilogue_rows_launch(const float *z, int64_t ldz, void *y, int64_t l
 cudaError_t gated_rows_launch(const float *g, int64_t ldg, const float *u, int64_t ldu, void *h,
                               int64_t ldh, int out_dtype, int act, int64_t M, int64_t F,
                               cudaStream_t s) {
-  const bool vec = aligned16(g, ldg, 4) && aligned16(u, ldu, 4) && aligned16(h, ldh, esize(out_dtype));
+  const bool vec = F % VEC == 0 && aligned16(g, ldg, 4) && aligned16(u, ldu, 4) && aligned16(h, ldh, esize(out_dtype));
   const dim3 grid = rows_grid(M, F);
   FF_TYPED(out_dtype, T, {
     if (vec)
@@ -240,7 +250,7 @@ cudaError_t gated_slopes_launch(const void *dh, int64_t lddh, const void *g, int
                                 int64_t lddu, int dtype, int act, int64_t M, int64_t F,
                                 cudaStream_t s) {
   const int es = esize(dtype);
-  const bool vec = aligned16(dh, lddh, es) && aligned16(g, ldg, es) && aligned16(u, ldu, es) &&
+  const bool vec = F % VEC == 0 && aligned16(dh, lddh, es) && aligned16(g, ldg, es) && aligned16(u, ldu, es) &&
                    aligned16(dg, lddg, es) && aligned16(du, lddu, es);
   const dim3 grid = rows_grid(M, F);
   FF_TYPED(dtype, T, {
@@ -254,7 +264,7 @@ cudaError_t gated_slopes_launch(const void *dh, int64_t lddh, const void *g, int
 
 cudaError_t add_rows_launch(const float *a, int64_t lda, const float *b, int64_t ldb, void *y,
                             int64_t ldy, int out_dtype, int64_t M, int64_t N, cudaStream_t s) {
-  const bool vec = aligned16(a, lda, 4) && aligned16(b, ldb, 4) && aligned16(y, ldy, esize(out_dtype));
+  const bool vec = N % VEC == 0 && aligned16(a, lda, 4) && aligned16(b, ldb, 4) && aligned16(y, ldy, esize(out_dtype));
   const dim3 grid = rows_grid(M, N);
   FF_TYPED(out_dtype, T, {
     if (vec)
@@ -268,7 +278,7 @@ cudaError_t add_rows_launch(const float *a, int64_t lda, const float *b, int64_t
 cudaError_t column_finish_launch(const float *partials, int64_t bands, int sums, void *out0,
                                  void *out1, int dtype, int64_t N, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>(out1 ? 2 : 1));
-  column_finish_kernel<<<grid, 256, 0, s>>>(partials, bands, sums, out0, out1, dtype, N);
+  column_finish_kernel<<<grid, 1024, 0, s>>>(partials, bands, sums, out0, out1, dtype, N);
   return cudaGetLastError();
 }
 
@@ -277,7 +287,7 @@ cudaError_t epilogue_slopes_launch(const void *dy, int64_t lddy, const void *pre
                                    void *dbias, int bias_dtype, float *partials, int64_t M,
                                    int64_t N, int sm_count, cudaStream_t s) {
   const int gs = esize(grad_dtype);
-  const bool vec = aligned16(dy, lddy, gs) && aligned16(pre, ld_pre, gs) &&
+  const bool vec = N % VEC == 0 && aligned16(dy, lddy, gs) && aligned16(pre, ld_pre, gs) &&
                    aligned16(dz, lddz, esize(dz_dtype));
   const int64_t bands = column_bands(M, N, sm_count);
   const int64_t band = (M + bands - 1) / bands;
