@@ -15,6 +15,7 @@ column-major view stride (1, ld) (e.g. ``b_storage.t()`` for a B stored as
 [N, K]). The output is row-major.
 """
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -22,6 +23,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libgemm_gb300.so")
+NATIVE_PATH = os.path.join(_PKG, "_lib", "gemm_gb300_torch.so")
 
 # enums of include/gemm.h
 F32, F16, BF16 = 0, 1, 2
@@ -34,7 +36,7 @@ OPTIONS = {"wait_timeout_us": 0, "force_path": 1, "group_m": 2, "max_ctas": 3,
            "fault_stall_producer": 4, "force_staging": 5, "cta_pair": 6,
            "block_n": 7, "exact_chunk": 8, "stream_k": 9, "host_panel": 10, "acc_chunk": 11, "stage_k": 12,
            "tile_rows": 13, "tf32_transpose": 14}
-ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu", "sigmoid")  # gemm_activation_t
 PATHS = {0: "none", 1: "zero_fill", 2: "tcgen05", 3: "fma", 4: "tcgen05_3xtf32",
          5: "tcgen05_f16acc"}
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -206,74 +208,26 @@ def operand_layout(x):
     raise ValueError("operand must be row- or column-major, got stride %s" % (x.stride(),))
 
 
-# The feed-forward operators' calls are short enough that a generation loop waits for the
-# host: these helpers ask a tensor for each thing once, in the cheapest form (device indices
-# instead of device objects, the raw stream handle instead of a torch.cuda.Stream).
-
-def _rows(x, what):
-    """(rows, columns, leading dimension) of a CUDA matrix with contiguous rows."""
-    if x.dim() != 2:
-        raise ValueError("%s must be 2-D" % what)
-    rows, cols = x.shape
-    s0, s1 = x.stride()
-    if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
-        raise ValueError("rows of %s must be contiguous" % what)
-    return rows, cols, s0 if rows > 1 else cols or 1
+_native_module = None
 
 
-def _row_ld(x, rows, cols, what, dev):
-    """Leading dimension of a rows x cols matrix on device `dev`."""
-    r, c, ld = _rows(x, what)
-    if r != rows or c != cols:
-        raise ValueError("%s must be a %d x %d tensor, got %d x %d" % (what, rows, cols, r, c))
-    if x.get_device() != dev:
-        raise ValueError("%s must be a CUDA tensor on the operands' device" % what)
-    return ld
-
-
-def _vector(x, n, what, dev):
-    """Data pointer of a contiguous vector of n values (0 for None)."""
-    if x is None:
-        return 0
-    if x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
-        raise ValueError("%s must be a contiguous vector of %d values" % (what, n))
-    if x.get_device() != dev:
-        raise ValueError("%s must be a CUDA tensor on the operands' device" % what)
-    return x.data_ptr()
-
-
-def _code(dtype):
-    """gemm_dtype_t of a torch dtype."""
-    code = _DT.get(dtype)
-    if code is None:
-        raise TypeError("unsupported dtype %s" % dtype)
-    return code
-
-
-def _cuda_index(x, what):
-    dev = x.get_device()
-    if dev < 0:
-        raise ValueError("%s must be a CUDA tensor" % what)
-    return dev
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _activation(name):
-    if name not in ACTIVATIONS:
-        raise ValueError("unknown activation %r (one of %s)"
-                         % (name, ", ".join(str(k) for k in ACTIVATIONS)))
-    return ACTIVATIONS[name]
-
-
-def _like(x):
-    """An empty tensor of x's shape in x's layout (row- or column-major), tight."""
-    r, c = x.shape
-    if operand_layout(x)[0] == ROW:
-        return torch.empty((r, c), dtype=x.dtype, device=x.device)
-    return torch.empty((c, r), dtype=x.dtype, device=x.device).t()
+def native():
+    """The compiled binding of the feed-forward operators, with the C functions it calls;
+    raises if it has not been built."""
+    global _native_module
+    if _native_module is None:
+        L = lib()
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError("gemm_gb300_torch.so is not built; run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("gemm_gb300_torch", NATIVE_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.init(*[ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "gemm_run_epilogue", "gemm_run_epilogue_backward", "gemm_run_gated",
+            "gemm_run_gated_backward", "gemm_layer_norm", "gemm_layer_norm_backward")], _check)
+        _native_module = m
+    return _native_module
 
 
 def _dtype_code(d):
@@ -294,11 +248,13 @@ class Gemm:
         h = ctypes.c_void_p()
         _check(lib().gemm_create(ctypes.byref(h), self.device), "gemm_create")
         self._h = h
+        self._address = h.value
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
             lib().gemm_destroy(self._h)
             self._h = None
+            self._address = 0
 
     def __del__(self):
         try:
@@ -431,21 +387,6 @@ class Gemm:
 
     # ------------------------------------------------------- feed-forward operators
 
-    def _two(self, a, b):
-        """Checked extents and device of a product's operands."""
-        dev = a.get_device()
-        if dev < 0 or b.get_device() != dev:
-            raise ValueError("operands must be CUDA tensors on one device")
-        if a.dtype != b.dtype:
-            raise TypeError("operands must share a dtype")
-        if a.dim() != 2 or b.dim() != 2:
-            raise ValueError("operands must be 2-D")
-        M, K = a.shape
-        K2, N = b.shape
-        if K != K2:
-            raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
-        return M, N, K, dev
-
     def matmul_epilogue(self, a, b, bias=None, activation=None, residual=None, out=None,
                         out_dtype=None, precision="default", save=False, stream=None):
         """act(a @ b + bias) + residual: a is M x K, b is K x N (row- or column-major views;
@@ -453,34 +394,8 @@ class Gemm:
         M x N of the output's dtype (``out=residual`` updates it in place). activation: None,
         "relu", "gelu", "gelu_tanh", "silu" or "sigmoid". ``save=True`` returns (out, pre)
         with pre = a @ b + bias for :meth:`matmul_epilogue_backward`."""
-        M, N, K, dev = self._two(a, b)
-        dtype = a.dtype
-        in_code = _code(dtype)
-        if out is not None:
-            dtype, ldc = out.dtype, _row_ld(out, M, N, "out", dev)
-        else:
-            if out_dtype is not None:
-                dtype = _TORCH_OF[_dtype_code(out_dtype)]
-            out, ldc = torch.empty((M, N), dtype=dtype, device=a.device), N or 1
-        ld_residual = residual_ptr = 0
-        if residual is not None:
-            if residual.dtype != dtype:
-                raise TypeError("residual must have the output's dtype")
-            ld_residual = _row_ld(residual, M, N, "residual", dev)
-            residual_ptr = residual.data_ptr()
-        pre = torch.empty((M, N), dtype=dtype, device=a.device) if save else None
-        ep = Epilogue(_vector(bias, N, "bias", dev), residual_ptr, ld_residual,
-                      pre.data_ptr() if save else 0, N or 1,
-                      0 if bias is None else _code(bias.dtype), _activation(activation))
-        al, lda = operand_layout(a)
-        bl, ldb = operand_layout(b)
-        code = (_lib or lib()).gemm_run_epilogue(
-            self._h, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldc, in_code,
-            _code(dtype), PREC[precision], al, bl, ep,
-            _raw_stream(dev) if stream is None else stream.cuda_stream)
-        if code:
-            raise GemmError(code, "gemm_run_epilogue")
-        return (out, pre) if save else out
+        return (_native_module or native()).matmul_epilogue(
+            self._address, a, b, bias, activation, residual, out, out_dtype, precision, save, stream)
 
     def matmul_epilogue_backward(self, grad, a, b, pre=None, activation=None,
                                  need=(True, True, True), bias_dtype=None, precision="default",
@@ -489,50 +404,8 @@ class Gemm:
         saved pre (needed unless there is no activation): (da, db, dbias), each None where
         ``need`` says so; da and db in the layouts of a and b, dbias in ``bias_dtype``
         (default: a's). The residual's gradient is grad itself."""
-        M, N, K, dev = self._two(a, b)
-        act = _activation(activation)
-        lddy = _row_ld(grad, M, N, "grad", dev)
-        ldz = 0
-        if act:
-            if pre is None:
-                raise ValueError("the backward pass of an activation needs the saved pre")
-            if pre.dtype != grad.dtype:
-                raise TypeError("pre must have grad's dtype")
-            ldz = _row_ld(pre, M, N, "pre", dev)
-        da = _like(a) if need[0] else None
-        db = _like(b) if need[1] else None
-        dbias = None
-        if need[2]:
-            bd = _TORCH_OF[_dtype_code(bias_dtype)] if bias_dtype is not None else a.dtype
-            dbias = torch.empty(N, dtype=bd, device=a.device)
-        al, lda = operand_layout(a)
-        bl, ldb = operand_layout(b)
-        code = (_lib or lib()).gemm_run_epilogue_backward(
-            self._h, M, N, K, grad.data_ptr(), lddy, pre.data_ptr() if act else 0, ldz,
-            a.data_ptr(), lda, b.data_ptr(), ldb,
-            da.data_ptr() if need[0] else 0, operand_layout(da)[1] if need[0] else 0,
-            db.data_ptr() if need[1] else 0, operand_layout(db)[1] if need[1] else 0,
-            dbias.data_ptr() if need[2] else 0, _code(dbias.dtype) if need[2] else 0,
-            _code(a.dtype), _code(grad.dtype), PREC[precision], al, bl, act,
-            _raw_stream(dev) if stream is None else stream.cuda_stream)
-        if code:
-            raise GemmError(code, "gemm_run_epilogue_backward")
-        return da, db, dbias
-
-    def _gated_args(self, x, w_gate, w_up):
-        M, F, K, dev = self._two(x, w_gate)
-        if w_up.shape != w_gate.shape:
-            raise ValueError("w_gate and w_up must have one shape")
-        if w_up.dtype != x.dtype:
-            raise TypeError("operands must share a dtype")
-        if w_up.get_device() != dev:
-            raise ValueError("operands must be CUDA tensors on one device")
-        ldx = _rows(x, "x")[2]
-        wl, ldg = operand_layout(w_gate)
-        wl2, ldu = operand_layout(w_up)
-        if wl != wl2:
-            raise ValueError("w_gate and w_up must have one layout")
-        return M, F, K, dev, ldx, wl, ldg, ldu
+        return (_native_module or native()).matmul_epilogue_backward(
+            self._address, grad, a, b, pre, activation, need, bias_dtype, precision, stream)
 
     def gated(self, x, w_gate, w_up, activation="silu", out=None, precision="default",
               save=False, stream=None):
@@ -540,118 +413,31 @@ class Gemm:
         with contiguous rows, both weights K x F in one layout (stored as [F, K]: pass
         ``w.t()``). ``save=True`` returns (out, gate, up) with the two products for
         :meth:`gated_backward` (column ranges of one M x 2F buffer)."""
-        M, F, K, dev, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
-        dtype = x.dtype
-        if out is None:
-            out, ldh = torch.empty((M, F), dtype=dtype, device=x.device), F or 1
-        else:
-            if out.dtype != dtype:
-                raise TypeError("out must have x's dtype")
-            ldh = _row_ld(out, M, F, "out", dev)
-        gate = up = None
-        if save:
-            both = torch.empty((M, 2 * F), dtype=dtype, device=x.device)
-            gate, up = both[:, :F], both[:, F:]
-        code = (_lib or lib()).gemm_run_gated(
-            self._h, M, F, K, x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
-            out.data_ptr(), ldh, gate.data_ptr() if save else 0, 2 * F,
-            up.data_ptr() if save else 0, 2 * F, _code(dtype), PREC[precision], wl,
-            _activation(activation), _raw_stream(dev) if stream is None else stream.cuda_stream)
-        if code:
-            raise GemmError(code, "gemm_run_gated")
-        return (out, gate, up) if save else out
+        return (_native_module or native()).gated(
+            self._address, x, w_gate, w_up, activation, out, precision, save, stream)
 
     def gated_backward(self, grad, x, w_gate, w_up, gate, up, activation="silu",
                        need=(True, True, True), precision="default", stream=None):
         """Gradients of :meth:`gated` from grad (M x F) and the saved gate and up: (dx, dw_gate,
         dw_up), each None where ``need`` says so, the weights' in the weights' layout."""
-        M, F, K, dev, ldx, wl, ldg, ldu = self._gated_args(x, w_gate, w_up)
-        dtype = x.dtype
-        for t in (grad, gate, up):
-            if t.dtype != dtype:
-                raise TypeError("grad, gate and up must have x's dtype")
-        lds = [_row_ld(t, M, F, n, dev) for t, n in ((grad, "grad"), (gate, "gate"), (up, "up"))]
-        dx = torch.empty((M, K), dtype=dtype, device=x.device) if need[0] else None
-        dwg = dwu = None
-        if need[1] and need[2] and wl == COL:
-            both = torch.empty((2 * F, K), dtype=dtype, device=x.device)
-            dwg, dwu = both[:F].t(), both[F:].t()
-        else:
-            dwg = _like(w_gate) if need[1] else None
-            dwu = _like(w_up) if need[2] else None
-        ldw = max(K if wl == COL else F, 1)
-        code = (_lib or lib()).gemm_run_gated_backward(
-            self._h, M, F, K, grad.data_ptr(), lds[0], gate.data_ptr(), lds[1], up.data_ptr(),
-            lds[2], x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
-            dx.data_ptr() if need[0] else 0, max(K, 1), dwg.data_ptr() if need[1] else 0, ldw,
-            dwu.data_ptr() if need[2] else 0, ldw, _code(dtype), PREC[precision], wl,
-            _activation(activation), _raw_stream(dev) if stream is None else stream.cuda_stream)
-        if code:
-            raise GemmError(code, "gemm_run_gated_backward")
-        return dx, dwg, dwu
+        return (_native_module or native()).gated_backward(
+            self._address, grad, x, w_gate, w_up, gate, up, activation, need, precision, stream)
 
     def layer_norm(self, x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None,
                    save=False, stream=None):
         """Layer norm of each row of a CUDA matrix with contiguous rows; weight and bias (None:
         1 and 0) share a dtype of their own. ``out=x`` runs in place. ``save=True`` returns
         (out, mean, rstd) with the rows' fp32 statistics for :meth:`layer_norm_backward`."""
-        dev = _cuda_index(x, "x")
-        M, N, ldx = _rows(x, "x")
-        dtype = x.dtype
-        in_code = out_code = _code(dtype)
-        params = F32
-        if weight is not None:
-            params = _code(weight.dtype)
-            if bias is not None and bias.dtype != weight.dtype:
-                raise TypeError("weight and bias must share a dtype")
-        elif bias is not None:
-            params = _code(bias.dtype)
-        if out is not None:
-            out_code, ldy = _code(out.dtype), _row_ld(out, M, N, "out", dev)
-        else:
-            if out_dtype is not None:
-                out_code = _dtype_code(out_dtype)
-                dtype = _TORCH_OF[out_code]
-            out, ldy = torch.empty((M, N), dtype=dtype, device=x.device), N or 1
-        mean = rstd = None
-        if save:
-            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device)
-        code = (_lib or lib()).gemm_layer_norm(
-            self._h, M, N, x.data_ptr(), ldx, _vector(weight, N, "weight", dev),
-            _vector(bias, N, "bias", dev), out.data_ptr(), ldy, mean.data_ptr() if save else 0,
-            rstd.data_ptr() if save else 0, eps, in_code, params, out_code,
-            _raw_stream(dev) if stream is None else stream.cuda_stream)
-        if code:
-            raise GemmError(code, "gemm_layer_norm")
-        return (out, mean, rstd) if save else out
+        return (_native_module or native()).layer_norm(
+            self._address, x, weight, bias, eps, out, out_dtype, save, stream)
 
     def layer_norm_backward(self, grad, x, weight, mean, rstd, need=(True, True, True),
                             param_dtype=None, stream=None):
         """Gradients of :meth:`layer_norm` from grad (the output's dtype), x, weight (or None)
         and the saved statistics: (dx, dweight, dbias), each None where ``need`` says so; the
         last two in ``param_dtype`` (default: weight's, or float32)."""
-        dev = _cuda_index(x, "x")
-        M, N, ldx = _rows(x, "x")
-        lddy = _row_ld(grad, M, N, "grad", dev)
-        if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
-            raise TypeError("mean and rstd must be float32")
-        pd = weight.dtype if weight is not None else torch.float32
-        if param_dtype is not None:
-            pd = _TORCH_OF[_dtype_code(param_dtype)]
-            if weight is not None and weight.dtype != pd:
-                raise TypeError("param_dtype must be weight's dtype")
-        dx = torch.empty((M, N), dtype=x.dtype, device=x.device) if need[0] else None
-        dw = torch.empty(N, dtype=pd, device=x.device) if need[1] else None
-        db = torch.empty(N, dtype=pd, device=x.device) if need[2] else None
-        code = (_lib or lib()).gemm_layer_norm_backward(
-            self._h, M, N, grad.data_ptr(), lddy, x.data_ptr(), ldx,
-            _vector(weight, N, "weight", dev), _vector(mean, M, "mean", dev),
-            _vector(rstd, M, "rstd", dev), dx.data_ptr() if need[0] else 0, N or 1,
-            dw.data_ptr() if need[1] else 0, db.data_ptr() if need[2] else 0, _code(x.dtype),
-            _code(pd), _code(grad.dtype), _raw_stream(dev) if stream is None else stream.cuda_stream)
-        if code:
-            raise GemmError(code, "gemm_layer_norm_backward")
-        return dx, dw, db
+        return (_native_module or native()).layer_norm_backward(
+            self._address, grad, x, weight, mean, rstd, need, param_dtype, stream)
 
     def tune_clear(self):
         _check(lib().gemm_tune_clear(self._h), "gemm_tune_clear")
@@ -769,7 +555,7 @@ def matmul(a, b, out=None, out_dtype=None, precision="default"):
 
 def softmax_rows(x, out=None, out_dtype=None):
     """Row softmax with the default handle of x's device; see :meth:`Gemm.softmax_rows`."""
-    return handle(x.get_device()).softmax_rows(x, out=out, out_dtype=out_dtype)
+    return handle(x.device.index).softmax_rows(x, out=out, out_dtype=out_dtype)
 
 
 def matmul_epilogue(a, b, **kw):

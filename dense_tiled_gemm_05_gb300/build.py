@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libgemm_gb300.so")
+BINDING_SRC = os.path.join(PKG, "binding", "torch_binding.cpp")
+BINDING = os.path.join(OUT_DIR, "gemm_gb300_torch.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "gemm_gb300")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -38,14 +41,33 @@ def _deps():
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(INCLUDE, "gemm.h"))
     deps.append(os.path.abspath(__file__))
+    deps.append(BINDING_SRC)
     return deps
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_binding():
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           BINDING_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the binding does not compile:\n%s%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
 
 
 def _compile(nvcc, src, verbose):
@@ -67,13 +89,15 @@ def build(force=False, verbose=None):
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(OUT_DIR, exist_ok=True)
     objs = []
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_build_binding)
         for src, obj, r in ex.map(lambda s: _compile(nvcc, s, verbose), sources()):
             if r.returncode != 0:
                 raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
             if verbose:
                 sys.stderr.write(r.stdout + r.stderr)
             objs.append(obj)
+        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"],
                        capture_output=True, text=True)
