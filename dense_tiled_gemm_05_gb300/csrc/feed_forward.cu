@@ -183,7 +183,7 @@ GEMM_API gemm_status_t gemm_run_epilogue(gemm_handle_t h, int64_t M, int64_t N, 
   if (!g.ok) return GEMM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (ep.empty()) return product(h, P, s);
-  if (precision_mode == GEMM_PREC_DEFAULT) {
+  if (precision_mode != GEMM_PREC_F16_ACC) {
     ff::FusedProduct q;
     q.M = M, q.N = N, q.K = K;
     q.X.ptr = A, q.X.ld = lda, q.X.layout = a_layout;

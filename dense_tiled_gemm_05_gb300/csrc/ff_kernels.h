@@ -54,6 +54,21 @@ cudaError_t few_launch(bool gated, bool w_mn, const CUtensorMap &tmX, const CUte
                        const CUtensorMap &tmX2, const CUtensorMap &tmW2, const FewParams &p,
                        cudaStream_t s);
 
+// Token kernel: one to eight tokens against K-contiguous weights of any alignment, on fp32
+// fused multiply-adds.
+struct TokenParams {
+  FusedParams f;        // (k_blocks, kb_first and idesc unused)
+  const void *X;
+  int64_t ldx;
+  const void *W, *W2;   // W2: gated only
+  int64_t ldw, ldw2;
+  int64_t K;
+  int32_t k_warps;      // warps of a CTA that share a feature's K: 1, 2, 4 or 8
+};
+constexpr int kTokenMax = 8;
+// vector: X and weights allow 16-byte accesses and K is a multiple of them.
+cudaError_t token_launch(bool gated, int dtype, bool vector, const TokenParams &p, cudaStream_t s);
+
 // Many-token kernel: CTA pairs, 256 x 256 accumulators (gated: 128 columns of each product).
 struct PairParams {
   FusedParams f;

@@ -54,6 +54,40 @@ void plan_few(FusedProduct *q, int64_t k_blocks, int sm_count) {
   p.stages = static_cast<int>(stages < 1 ? 1 : stages);
 }
 
+// The token kernel's rule: weights stored [features, K], one product, and few enough tokens
+// that its multiply-adds hide under the stream of weights. Measured on one GB300, us, token
+// kernel against few-token kernel: bf16 1 x 1024 x 1024 2.9 / 5.2, 1 x 4096 x 4096 (34 MB of
+// weights) 9.4 / 10.8, 1 x 8192 x 8192 (134 MB) 25.7 / 25.0, two tokens 34 MB 10.0 / 10.7, 134
+// MB 30 / 24, four tokens 17 MB 7.5 / 10.1, 34 MB 12.2 / 10.8: up to 80 MB of weights times
+// tokens. Rows TMA cannot address it reads as they are, where the few-token kernel copies all
+// weights first (1 x 4097 x 1001: 7.4 / 23). fp32: up to eight tokens, against the exact
+// product on the tensor cores with its 30 us of fixed cost (8 x 4096 x 4096: 36 / 108).
+bool plan_token(FusedProduct *q, int sm_count) {
+  const int es = esize_of(q->in_dtype);
+  if (q->M > kTokenMax || q->K2 > 0 || q->W.layout != GEMM_COL_MAJOR ||
+      q->X.layout != GEMM_ROW_MAJOR || q->N > (int64_t{1} << 30))
+    return false;
+  q->vector = q->K % (16 / es) == 0 && tma_legal(q->X.ptr, q->X.ld, q->M, es) &&
+              tma_legal(q->W.ptr, q->W.ld, q->N, es) &&
+              (!q->gated || tma_legal(q->W2.ptr, q->W2.ld, q->N, es));
+  const int64_t rows = q->gated ? 2 * q->N : q->N;
+  if (q->in_dtype != GEMM_F32 &&
+      (q->M > 4 || (q->vector && rows * q->K * es * q->M > int64_t{80} << 20)))
+    return false;
+  // Warps that share a weight row's K, in steps of 512 bytes: eight steps a warp, or down to
+  // four where the rows would not make up 24 warps an SM (best of 1, 2, 4, 8 within 10 % on
+  // most of the sizes above).
+  const int64_t steps = (q->K * es + 511) / 512;
+  const int64_t tasks = (rows + (q->M <= 2 ? 1 : 3)) / (q->M <= 2 ? 2 : 4);
+  q->k_warps = 1;
+  while (q->k_warps < 8 &&
+         (steps >= 16 * q->k_warps ||
+          (steps >= 8 * q->k_warps && tasks * q->k_warps < 24 * static_cast<int64_t>(sm_count))))
+    q->k_warps *= 2;
+  q->kind = FusedProduct::kToken;
+  return true;
+}
+
 cudaError_t stage(const FusedOperand &o, int64_t lines, int64_t len, char *buf, cudaStream_t s) {
   if (o.transpose) return transpose_launch(o.ptr, o.ld, buf + o.offset, o.staged_ld, lines, len, 2, s);
   return repack_launch(o.ptr, o.ld, buf + o.offset, o.staged_ld, lines, len, 2, s);
@@ -66,9 +100,11 @@ bool aligned(const void *p, int64_t ld, int es, int elems) {
 }  // namespace
 
 bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
-  if (q->in_dtype == GEMM_F32 || q->M < 1 || q->N < 1 || q->K < 1) return false;
+  if (q->M < 1 || q->N < 1 || q->K < 1) return false;
   if (h->force_path == 2) return false;  // the FMA kernel was asked for
   if (q->gated && q->out_dtype != q->in_dtype) return false;
+  if (!h->cta_pair && plan_token(q, h->sm_count)) return true;
+  if (q->in_dtype == GEMM_F32) return false;
   const int64_t k_blocks = (q->K + 63) / 64 + (q->K2 + 63) / 64;
   const int64_t tile_n = q->gated ? 128 : 256;
   q->tiles_m = (q->M + 255) / 256;
@@ -77,9 +113,10 @@ bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
   if (q->tiles_m * q->tiles_n > INT32_MAX / 8 || k_blocks > INT32_MAX) return false;
   // Few tiles of 256 rows, or rows that would fill less than half of one: the few-token
   // kernel, whose tiles are smaller and share their K-loops over clusters.
-  q->few = q->M <= 128 || 2 * q->tiles_m * q->tiles_n <= clusters;
-  if (h->cta_pair) q->few = h->cta_pair == 1;  // GEMM_OPT_CTA_PAIR
-  if (q->few) plan_few(q, k_blocks, h->sm_count);
+  bool few = q->M <= 128 || 2 * q->tiles_m * q->tiles_n <= clusters;
+  if (h->cta_pair) few = h->cta_pair == 1;  // GEMM_OPT_CTA_PAIR
+  q->kind = few ? FusedProduct::kFew : FusedProduct::kPair;
+  if (few) plan_few(q, k_blocks, h->sm_count);
   plan_x(&q->X, q->M, q->K, carve);
   plan_w(&q->W, q->K, q->N, carve);
   if (q->gated) {
@@ -93,6 +130,32 @@ bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
 
 gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
+  FusedParams f{};
+  f.M = static_cast<int32_t>(q.M), f.N = static_cast<int32_t>(q.N);
+  f.out_dtype = q.out_dtype;
+  f.act = q.ep.act;
+  f.bias = q.ep.bias, f.bias_dtype = q.ep.bias_dtype;
+  f.residual = q.ep.residual, f.ld_residual = q.ep.ld_residual;
+  f.C = q.C, f.ldc = q.ldc;
+  f.pre = q.ep.pre, f.ld_pre = q.ep.ld_pre;
+  f.pre2 = q.pre2, f.ld_pre2 = q.ld_pre2;
+  f.status = h->status;
+  f.timeout_ns = h->timeout_us * 1000ull;
+  f.debug_flags = stall_flags(h->stall_producer);
+  if (q.kind == FusedProduct::kToken) {
+    TokenParams p{};
+    p.f = f;
+    p.X = q.X.ptr, p.ldx = q.X.ld;
+    p.W = q.W.ptr, p.ldw = q.W.ld;
+    p.W2 = q.W2.ptr, p.ldw2 = q.W2.ld;
+    p.K = q.K;
+    p.k_warps = q.k_warps;
+    e = token_launch(q.gated, q.in_dtype, q.vector, p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "token kernel launch");
+    h->launches += 1;
+    return GEMM_OK;
+  }
+  const bool few = q.kind == FusedProduct::kFew;
   const bool two_x = !q.gated && q.K2 > 0, two_w = q.gated || q.K2 > 0;
   struct Use {
     const FusedOperand *o;
@@ -102,7 +165,7 @@ gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaS
   const Use uses[4] = {{&q.X, true, false, q.K}, {&q.W, true, true, q.K}, {&q.X2, two_x, false, q.K2},
                        {&q.W2, two_w, true, q.gated ? q.K : q.K2}};
   // Operand boxes are one 128-byte row of K (or, for row-major weights, of N) wide.
-  const uint32_t x_rows = q.few ? static_cast<uint32_t>(q.few_params.tile_t) : 128u;
+  const uint32_t x_rows = few ? static_cast<uint32_t>(q.few_params.tile_t) : 128u;
   CUtensorMap maps[4];
   for (int i = 0; i < 4; ++i) {
     if (!uses[i].used) {
@@ -130,23 +193,11 @@ gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaS
     const uint32_t rows = w ? (row ? 64u : 128u) : x_rows;
     if (!encode_2d(&maps[i], q.in_dtype, ptr, len, lines, ld, 64, rows)) return GEMM_ERR_CUDA;
   }
-  FusedParams f{};
-  f.M = static_cast<int32_t>(q.M), f.N = static_cast<int32_t>(q.N);
   f.kb_first = static_cast<int32_t>((q.K + 63) / 64);
   f.k_blocks = f.kb_first + static_cast<int32_t>(two_x ? (q.K2 + 63) / 64 : 0);
-  f.out_dtype = q.out_dtype;
-  f.act = q.ep.act;
-  f.bias = q.ep.bias, f.bias_dtype = q.ep.bias_dtype;
-  f.residual = q.ep.residual, f.ld_residual = q.ep.ld_residual;
-  f.C = q.C, f.ldc = q.ldc;
-  f.pre = q.ep.pre, f.ld_pre = q.ep.ld_pre;
-  f.pre2 = q.pre2, f.ld_pre2 = q.ld_pre2;
-  f.status = h->status;
-  f.timeout_ns = h->timeout_us * 1000ull;
-  f.debug_flags = stall_flags(h->stall_producer);
   const bool w_mn = q.W.layout == GEMM_ROW_MAJOR;
   const int os = esize_of(q.out_dtype);
-  if (q.few) {
+  if (few) {
     FewParams p = q.few_params;
     p.f = f;
     p.f.idesc = make_idesc(q.in_dtype, w_mn, false, p.tile_t, 128);

@@ -1,4 +1,4 @@
-// ff_launch.h -- the fused products of 16-bit operands: what a call asks for, whether and how
+// ff_launch.h -- the fused products: what a call asks for, whether and how
 // the tensor-core kernels take it, and the launch. Internal to the library.
 #pragma once
 
@@ -42,13 +42,16 @@ struct FusedProduct {
   void *pre2 = nullptr;
   int64_t ld_pre2 = 0;
   // plan
-  bool few = false;
+  enum Kind { kToken, kFew, kPair } kind = kPair;
+  int k_warps = 1;         // token kernel
+  bool vector = false;     // token kernel: 16-byte accesses
   FewParams few_params{};
   int64_t tiles_m = 0, tiles_n = 0;
 };
 
-// Whether the fused kernels take the product; fills the plan and adds the staged copies to
-// `carve`. False: a type, size or option they do not handle.
+// Whether the fused kernels take the product (16-bit types, and fp32 for a few tokens); fills
+// the plan and adds the staged copies to `carve`. False: a type, size or option they do not
+// handle.
 bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve);
 // `buf`: the buffer the offsets of plan_fused refer to.
 gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaStream_t s);

@@ -128,3 +128,23 @@ def test_bounded_waits_expire_and_the_next_call_is_right(g, cta_pair, stall):
     check_gated(h, a, b, b, "silu", save=True)
     assert h.status() == 0
     h.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 8), (3, 1)])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 1), (7, 8), (129, 40), (70, 513), (1030, 1024), (33, 8200)])
+def test_token_kernel(g, M, N, K, pad, offset, dtype):
+    """One to eight tokens on the default choice of kernels: features and K around a warp's
+    steps, aligned and unaligned rows."""
+    h = g.Gemm(0)
+    t = TYPES[dtype]
+    a, b = operands(M, N, K, dtype, M + N, "row", "col", pad, offset)
+    bias = matrix(1, N, t, 5)[0]
+    check_epilogue(h, a, b, "gelu", bias, matrix(M, N, t, 6, pad=pad, offset=offset))
+    r = matrix(M, N, t, 6)
+    check_epilogue(h, a, b, None, None, r, out=r, save=False)
+    wu = matrix(K, N, t, 9, "col", pad, offset, scale=K ** -0.5)
+    check_gated(h, a, b, wu, "silu", save=M % 2 == 0)
+    assert h.status() == 0
+    h.close()
