@@ -13,7 +13,8 @@
 // of 2, 4 or 8 CTAs shares it: each accumulates its K-blocks in TMEM, writes the fp32 partial
 // to its shared memory (over the drained ring), and after a cluster barrier every CTA sums a
 // share of the outputs over all partials through distributed shared memory, in rank order,
-// applies the epilogue and stores. No workspace, no second launch, the same bits every time.
+// applies the epilogue and stores. No workspace, no second launch, the same bits every time. A
+// tile that is not split goes from TMEM to memory directly.
 //
 // The gated pair runs as two MMAs a K-step, both weights' rows against the same token tile.
 #include "activation.cuh"
@@ -27,6 +28,9 @@ namespace {
 
 using namespace tc;
 
+// Warp 0 loads, warp 1 issues the MMAs, warps 4-11 (two for each quarter of the TMEM lanes)
+// read the accumulators; all twelve sum the partials of a split tile.
+constexpr int kFewThreads = 384;
 constexpr int kBlockK = 64;                          // K elements per 128-byte K-block
 constexpr int kWBytes = kFewFeatures * kRowBytes;    // one weight box
 constexpr int kPanelBytes = kBlockK * kRowBytes;     // MN-major weights: 64 K-rows x 128 bytes
@@ -103,8 +107,50 @@ __device__ __forceinline__ void finish4(const FusedParams &p, bool vec, int64_t 
   store4(static_cast<TO *>(p.C) + m * p.ldc, n, p.N, vec, a);
 }
 
+// One feature a lane, 16 tokens of its TMEM columns: the epilogue of a tile that one CTA
+// computed alone. A warp's 32 features of a token are neighbours in memory.
+template <typename TO, bool GATED>
+__device__ __forceinline__ void finish_columns(const FusedParams &p, int64_t m0, int tokens, int64_t n,
+                                               float bias, float (&a)[16], float (&b)[16]) {
+  if (n >= p.N) return;
+  if (GATED) {
+    if (p.pre) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < tokens) {
+          static_cast<TO *>(p.pre)[(m0 + j) * p.ld_pre + n] = from_f32<TO>(a[j]);
+          static_cast<TO *>(p.pre2)[(m0 + j) * p.ld_pre2 + n] = from_f32<TO>(b[j]);
+        }
+    }
+    activate_all<true>(a, p.act);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a[j] *= b[j];
+  } else {
+    if (p.residual) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        b[j] = j < tokens ? to_f32(static_cast<const TO *>(p.residual)[(m0 + j) * p.ld_residual + n]) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a[j] += bias;
+    if (p.pre) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < tokens) static_cast<TO *>(p.pre)[(m0 + j) * p.ld_pre + n] = from_f32<TO>(a[j]);
+    }
+    activate_all<true>(a, p.act);
+    if (p.residual) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a[j] += b[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < tokens) static_cast<TO *>(p.C)[(m0 + j) * p.ldc + n] = from_f32<TO>(a[j]);
+}
+
 template <bool GATED, bool W_MN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kFewThreads)
     few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmX2, const __grid_constant__ CUtensorMap tmW2,
                const FewParams p) {
@@ -117,7 +163,7 @@ __global__ void __launch_bounds__(kThreads)
   const int accs = GATED ? 2 : 1;
   const int plane = p.tile_t * kFewFeatures;  // fp32 values of one accumulator's partial
   const int ring = p.stages * stage_bytes;
-  const int part = accs * plane * static_cast<int>(sizeof(float));
+  const int part = p.splits > 1 ? accs * plane * static_cast<int>(sizeof(float)) : 0;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + (ring > part ? ring : part));
   uint64_t *empty = full + kMaxStages;
   uint64_t *acc_full = empty + kMaxStages;
@@ -233,10 +279,11 @@ __global__ void __launch_bounds__(kThreads)
       drain_wait(drain, 0, p.f.timeout_ns);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------- accumulators to shared memory
-    const int quarter = warp & 3;
-    if (warp == 2 && rank == 0 && !GATED) {
+  } else if (warp >= 4) {
+    // ------------------------------- accumulators: to the outputs, or to shared memory
+    const int quarter = warp & 3, half = (warp - 4) / 4;
+    const int64_t n = f0 + quarter * 32 + lane;
+    if (p.splits > 1 && warp == 4 && rank == 0 && !GATED) {
       // what the epilogue reads besides the sums is on its way to L2 meanwhile
       const int es = p.f.out_dtype == GEMM_F32 ? 4 : 2;
       const int cols = min(kFewFeatures, p.f.N - f0);
@@ -249,30 +296,48 @@ __global__ void __launch_bounds__(kThreads)
             prefetch_l2(static_cast<const char *>(p.f.residual) +
                         ((t0 + t) * p.f.ld_residual + f0 + lane * 4) * es);
     }
+    const float bias = !GATED && p.splits == 1 && p.f.bias && n < p.f.N
+                           ? load_any(p.f.bias, p.f.bias_dtype, n)
+                           : 0.0f;
     bool ok = mbar_wait(acc_full, 0, wd);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       // (the ring is drained: every stage was loaded and read before this barrier completed)
       tc_fence_after();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
       float *P = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
+      for (int c0 = half * 16; c0 < tokens; c0 += 32) {
+        uint32_t r[2][16];
+        tmem_ld_32x32b_x16(t_row + c0, r[0]);
+        if (GATED) tmem_ld_32x32b_x16(t_row + acc_stride(p.tile_t) + c0, r[1]);
+        tmem_wait_ld();
+        if (p.splits > 1) {
 #pragma unroll
-      for (int i = 0; i < (GATED ? 2 : 1); ++i) {
-        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                               i * acc_stride(p.tile_t);
-        for (int c0 = 0; c0 < tokens; c0 += 16) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(t_row + c0, r);
-          tmem_wait_ld();
+          for (int i = 0; i < (GATED ? 2 : 1); ++i)
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < tokens) P[i * plane + (c0 + j) * kFewFeatures] = __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j)
+              if (c0 + j < tokens) P[i * plane + (c0 + j) * kFewFeatures] = __uint_as_float(r[i][j]);
+        } else {
+          float a[16], b[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            a[j] = __uint_as_float(r[0][j]);
+            b[j] = GATED ? __uint_as_float(r[1][j]) : 0.0f;
+          }
+          const int left = tokens - c0;
+          if (p.f.out_dtype == GEMM_BF16)
+            finish_columns<__nv_bfloat16, GATED>(p.f, t0 + c0, left, n, bias, a, b);
+          else if (p.f.out_dtype == GEMM_F16)
+            finish_columns<__half, GATED>(p.f, t0 + c0, left, n, bias, a, b);
+          else
+            finish_columns<float, GATED>(p.f, t0 + c0, left, n, bias, a, b);
         }
       }
       tc_fence_before();
     }
   }
 
-  // Every partial of the tile is in its CTA's shared memory after this.
+  // Every partial of a split tile is in its CTA's shared memory after this.
   if (p.splits > 1)
     cluster_sync();
   else
@@ -280,9 +345,9 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t base = smem_u32(smem);
   // A thread's items are BATCH at a time: all their partials are on the way before the first
   // sum, or each would wait for the other SMs' shared memory in turn.
-  constexpr int BATCH = GATED ? 2 : 4;
-  const int items = tokens * (kFewFeatures / 4), stride = p.splits * kThreads;
-  for (int i0 = rank * kThreads + threadIdx.x; i0 < items; i0 += BATCH * stride) {
+  constexpr int BATCH = GATED ? 3 : 6;
+  const int items = p.splits > 1 ? tokens * (kFewFeatures / 4) : 0, stride = p.splits * kFewThreads;
+  for (int i0 = rank * kFewThreads + threadIdx.x; i0 < items; i0 += BATCH * stride) {
     float a[BATCH][4], b[BATCH][4];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
@@ -294,8 +359,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {
         const int i = min(i0 + j * stride, items - 1);
-        const uint32_t off = base + static_cast<uint32_t>(i) * 16;
-        const uint32_t at = p.splits > 1 ? mapa_shared(off, static_cast<uint32_t>(q)) : off;
+        const uint32_t at = mapa_shared(base + static_cast<uint32_t>(i) * 16, static_cast<uint32_t>(q));
         v[j] = ld_cluster_f4(at);
         if (GATED) w[j] = ld_cluster_f4(at + plane * static_cast<uint32_t>(sizeof(float)));
       }
@@ -342,7 +406,7 @@ template <bool GATED, bool W_MN>
 cudaError_t launch_few(const CUtensorMap &tmX, const CUtensorMap &tmW, const CUtensorMap &tmX2,
                        const CUtensorMap &tmW2, const FewParams &p, cudaStream_t s) {
   auto kernel = few_kernel<GATED, W_MN>;
-  const size_t smem = few_smem_bytes(GATED, p.tile_t, p.stages);
+  const size_t smem = few_smem_bytes(GATED, p.tile_t, p.stages, p.splits > 1);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -354,7 +418,7 @@ cudaError_t launch_few(const CUtensorMap &tmX, const CUtensorMap &tmW, const CUt
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dependency_wait
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(p.tiles_t * p.tiles_f * p.splits), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -364,6 +428,36 @@ cudaError_t launch_few(const CUtensorMap &tmX, const CUtensorMap &tmW, const CUt
 
 }  // namespace
 
+int few_max_clusters(int splits, int per_sm) {
+  // The limit comes from how many SMs each GPC has, so one kernel and one shared-memory size
+  // a resident count stand for all.
+  static int cached[4][2];
+  const int i = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
+  int &n = cached[i][per_sm > 1];
+  if (n > 0) return n;
+  auto kernel = few_kernel<false, false>;
+  const int smem = (per_sm > 1 ? 113 : 226) * 1024;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(splits), 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int got = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess || got < 1) {
+    cudaGetLastError();
+    return 1;
+  }
+  n = got;
+  return n;
+}
+
 size_t few_stage_bytes(bool gated, int tile_t) {
   return static_cast<size_t>((gated ? 2 : 1) * kWBytes + tile_t * kRowBytes);
 }
@@ -372,9 +466,9 @@ size_t few_stage_bytes(bool gated, int tile_t) {
 // column, 1 KB a CTA being the system's): CTAs whose shared memory fits an SM together then
 // also find their TMEM there, whichever kernels they belong to, and no cluster ever waits for
 // columns that another waiting cluster holds.
-size_t few_smem_bytes(bool gated, int tile_t, int stages) {
+size_t few_smem_bytes(bool gated, int tile_t, int stages, bool split) {
   const size_t ring = static_cast<size_t>(stages) * few_stage_bytes(gated, tile_t);
-  const size_t part = static_cast<size_t>(gated ? 2 : 1) * tile_t * kFewFeatures * sizeof(float);
+  const size_t part = split ? static_cast<size_t>(gated ? 2 : 1) * tile_t * kFewFeatures * sizeof(float) : 0;
   const size_t use = (ring > part ? ring : part) + kBarBytes + 1024;
   const size_t least = static_cast<size_t>((gated ? 2 : 1) * acc_stride(tile_t)) * 456 - 1024;
   return use > least ? use : least;
@@ -384,7 +478,7 @@ cudaError_t few_launch(bool gated, bool w_mn, const CUtensorMap &tmX, const CUte
                        const CUtensorMap &tmX2, const CUtensorMap &tmW2, const FewParams &p,
                        cudaStream_t s) {
   if (p.stages < 1 || p.stages > kMaxStages || p.tile_t % 16 || p.tile_t < 16 ||
-      p.tile_t > (gated ? 128 : 256) || few_smem_bytes(gated, p.tile_t, p.stages) > 232448)
+      p.tile_t > (gated ? 128 : 256) || few_smem_bytes(gated, p.tile_t, p.stages, p.splits > 1) > 232448)
     return cudaErrorInvalidValue;
   if (gated)
     return w_mn ? launch_few<true, true>(tmX, tmW, tmX2, tmW2, p, s)

@@ -31,27 +31,57 @@ void plan_w(FusedOperand *o, int64_t K, int64_t N, Carve *carve) {
   o->offset = carve->take(lines * o->staged_ld, 2);
 }
 
-// Tiles and cluster split of the few-token kernel.
+// Tiles and cluster split of the few-token kernel: the token tile and the number of CTAs that
+// share a tile's K with the least estimated time. The estimate, in SM cycles: per 64-long
+// K-block a CTA's tile costs the larger of its MMAs (half a cycle a token and K-step, or what
+// their operands take from shared memory) and its bytes at 64 a cycle; CTAs on one SM add up;
+// all bytes together at the rate HBM gives the whole GPU; and, per round of CTAs, the start
+// and the joining of partials.
 void plan_few(FusedProduct *q, int64_t k_blocks, int sm_count) {
-  FewParams &p = q->few_params;
-  const int most = q->gated ? 128 : 256;
-  p.tile_t = static_cast<int>(q->M >= most ? most : round_up(q->M, 16));
-  p.tiles_t = static_cast<int>((q->M + p.tile_t - 1) / p.tile_t);
-  p.tiles_f = static_cast<int>((q->N + kFewFeatures - 1) / kFewFeatures);
-  const int64_t tiles = static_cast<int64_t>(p.tiles_t) * p.tiles_f;
-  // Two CTAs share an SM while their rings leave each several stages; a token tile wide
-  // enough to fill the SM's shared memory runs alone.
-  const size_t stage = few_stage_bytes(q->gated, p.tile_t);
-  const bool two = few_smem_bytes(q->gated, p.tile_t, 3) <= 113 * 1024;
-  const int64_t slots = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * (two ? 2 : 1);
-  // The widest split that still fits one round of slots, with at least four K-blocks each.
-  p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= slots && k_blocks >= 8 * p.splits) p.splits *= 2;
-  int64_t stages = static_cast<int64_t>(((two ? 113 : 226) * 1024 - kFewFixedBytes) / stage);
-  const int64_t per_cta = (k_blocks + p.splits - 1) / p.splits;
-  if (stages > per_cta) stages = per_cta;
-  if (stages > 16) stages = 16;
-  p.stages = static_cast<int>(stages < 1 ? 1 : stages);
+  const int accs = q->gated ? 2 : 1;
+  const int64_t sms = sm_count > 0 ? sm_count : 1;
+  const int64_t tiles_f = (q->N + kFewFeatures - 1) / kFewFeatures;
+  const int64_t most = q->gated ? 128 : 256;
+  const double hbm = 3500.0;  // bytes a cycle
+  double best = 1e300;
+  for (int64_t t = 16; t <= most; t = t < 64 ? t + 16 : t + 32) {
+    if (t > 16 && t - (t <= 64 ? 16 : 32) >= q->M) break;  // a narrower tile holds all tokens
+    const int64_t tiles_t = (q->M + t - 1) / t, tiles = tiles_t * tiles_f;
+    const double bytes = static_cast<double>(few_stage_bytes(q->gated, static_cast<int>(t)));
+    const double mma = 4.0 * accs * (t / 2.0 > 32 + t / 4.0 ? t / 2.0 : 32 + t / 4.0);
+    const double kb = mma > bytes / 64 ? mma : bytes / 64;
+    const double all = static_cast<double>(accs * tiles_f * kFewFeatures + tiles_t * t) * k_blocks * 128 / hbm;
+    for (int c = 1; c <= 8; c *= 2) {
+      if (c > 1 && k_blocks < 2 * c) break;
+      for (int per_sm = 1; per_sm <= 2; ++per_sm) {
+        const size_t room = static_cast<size_t>(per_sm == 2 ? 113 : 226) * 1024;
+        if (few_smem_bytes(q->gated, static_cast<int>(t), 2, c > 1) > room) continue;
+        const int64_t clusters = few_max_clusters(c, per_sm);
+        const int64_t rounds = (tiles + clusters - 1) / clusters;
+        // CTAs of the busiest SM over all rounds
+        const int64_t full = tiles / clusters, rest = tiles % clusters;
+        const int64_t busy = full * per_sm + (rest * c + sms - 1) / sms;
+        const double join = c == 1 ? 300 + 10.0 * accs * t
+                                   : 2500 + 4.0 * accs * t + 40.0 * accs * t / c;
+        const double stream = busy * kb * static_cast<double>((k_blocks + c - 1) / c);
+        const double cost = (stream > all ? stream : all) + rounds * (1500 + join);
+        if (cost < best) {
+          best = cost;
+          FewParams &p = q->few_params;
+          p.tile_t = static_cast<int>(t);
+          p.tiles_t = static_cast<int>(tiles_t);
+          p.tiles_f = static_cast<int>(tiles_f);
+          p.splits = c;
+          int64_t stages = static_cast<int64_t>((room - kFewFixedBytes) / few_stage_bytes(q->gated, p.tile_t));
+          const int64_t per_cta = (k_blocks + c - 1) / c;
+          if (stages > per_cta) stages = per_cta;
+          if (stages > 16) stages = 16;
+          p.stages = static_cast<int>(stages);
+        }
+      }
+    }
+  }
+  q->cost = best;
 }
 
 // The token kernel's rule: weights stored [features, K], one product, and few enough tokens

@@ -46,6 +46,7 @@ struct FusedProduct {
   int k_warps = 1;         // token kernel
   bool vector = false;     // token kernel: 16-byte accesses
   FewParams few_params{};
+  double cost = 0.0;       // few-token kernel's estimate, SM cycles
   int64_t tiles_m = 0, tiles_n = 0;
 };
 
