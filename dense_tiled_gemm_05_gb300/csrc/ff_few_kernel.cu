@@ -428,15 +428,12 @@ cudaError_t launch_few(const CUtensorMap &tmX, const CUtensorMap &tmW, const CUt
 
 }  // namespace
 
-int few_max_clusters(int splits, int per_sm) {
-  // The limit comes from how many SMs each GPC has, so one kernel and one shared-memory size
-  // a resident count stand for all.
-  static int cached[4][2];
-  const int i = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
-  int &n = cached[i][per_sm > 1];
+// The limit comes from how many SMs each GPC has: one kernel, at one CTA an SM, stands for all.
+int few_max_clusters(int splits) {
+  static int cached[4];
+  int &n = cached[splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3];
   if (n > 0) return n;
   auto kernel = few_kernel<false, false>;
-  const int smem = (per_sm > 1 ? 113 : 226) * 1024;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -445,7 +442,7 @@ int few_max_clusters(int splits, int per_sm) {
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(splits), 1, 1);
   cfg.blockDim = dim3(kFewThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.dynamicSmemBytes = 226 * 1024;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int got = 0;

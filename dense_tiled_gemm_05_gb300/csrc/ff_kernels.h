@@ -50,8 +50,8 @@ constexpr int kFewFeatures = 128;  // features per tile
 constexpr size_t kFewFixedBytes = 2048;  // barriers and alignment (at most)
 size_t few_stage_bytes(bool gated, int tile_t);
 size_t few_smem_bytes(bool gated, int tile_t, int stages, bool split);
-// Clusters of `splits` CTAs, one or two of them an SM, that run at once on the current device.
-int few_max_clusters(int splits, int per_sm);
+// Clusters of `splits` CTAs, one an SM, that run at once on the current device.
+int few_max_clusters(int splits);
 cudaError_t few_launch(bool gated, bool w_mn, const CUtensorMap &tmX, const CUtensorMap &tmW,
                        const CUtensorMap &tmX2, const CUtensorMap &tmW2, const FewParams &p,
                        cudaStream_t s);

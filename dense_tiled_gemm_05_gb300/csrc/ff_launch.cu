@@ -31,40 +31,50 @@ void plan_w(FusedOperand *o, int64_t K, int64_t N, Carve *carve) {
   o->offset = carve->take(lines * o->staged_ld, 2);
 }
 
-// Tiles and cluster split of the few-token kernel: the token tile and the number of CTAs that
-// share a tile's K with the least estimated time. The estimate, in SM cycles: per 64-long
-// K-block a CTA's tile costs the larger of its MMAs (half a cycle a token and K-step, or what
-// their operands take from shared memory) and its bytes at 64 a cycle; CTAs on one SM add up;
-// all bytes together at the rate HBM gives the whole GPU; and, per round of CTAs, the start
-// and the joining of partials.
+// Tiles and cluster split of the few-token kernel: the token tile, the number of CTAs that
+// share a tile's K, and one or two CTAs an SM, with the least estimated time. The estimate, in
+// SM cycles: a 64-long K-block of a CTA's tile costs the larger of its MMAs (half a cycle a
+// token and K-step, or what their operands take from shared memory) and its bytes at 41 a
+// cycle (one SM's TMA stream; two CTAs on an SM get 1.6 times that); the weights and tokens
+// together take HBM's rate, and all copies the L2's; and each round of CTAs has its start, its
+// epilogue and, for a split tile, the joining of partials. The constants are fitted to 750
+// measured configurations of 31 products (one GB300, 1 to 8192 tokens, plain and gated, from
+// graphs); over those the choice takes 2.8 % more than the best on average, 27 % at most.
 void plan_few(FusedProduct *q, int64_t k_blocks, int sm_count) {
   const int accs = q->gated ? 2 : 1;
   const int64_t sms = sm_count > 0 ? sm_count : 1;
   const int64_t tiles_f = (q->N + kFewFeatures - 1) / kFewFeatures;
-  const int64_t most = q->gated ? 128 : 256;
-  const double hbm = 3500.0;  // bytes a cycle
   double best = 1e300;
-  for (int64_t t = 16; t <= most; t = t < 64 ? t + 16 : t + 32) {
-    if (t > 16 && t - (t <= 64 ? 16 : 32) >= q->M) break;  // a narrower tile holds all tokens
+  int64_t narrower = 0;
+  for (const int64_t t : {16, 32, 48, 64, 96, 128, 192, 256}) {
+    if (narrower >= q->M || (q->gated && t > 128)) break;  // a narrower tile holds all tokens
+    narrower = t;
     const int64_t tiles_t = (q->M + t - 1) / t, tiles = tiles_t * tiles_f;
     const double bytes = static_cast<double>(few_stage_bytes(q->gated, static_cast<int>(t)));
-    const double mma = 4.0 * accs * (t / 2.0 > 32 + t / 4.0 ? t / 2.0 : 32 + t / 4.0);
-    const double kb = mma > bytes / 64 ? mma : bytes / 64;
-    const double all = static_cast<double>(accs * tiles_f * kFewFeatures + tiles_t * t) * k_blocks * 128 / hbm;
+    const double mma = 4.4 * accs * (t / 2.0 > 32 + t / 4.0 ? t / 2.0 : 32 + t / 4.0);
+    const double kb = mma > bytes / 41 ? mma : bytes / 41;
+    const double hbm = static_cast<double>(accs * tiles_f * kFewFeatures + tiles_t * t) * k_blocks * 128 / 3200;
+    const double l2 = static_cast<double>(tiles) * k_blocks * bytes / 9000;
     for (int c = 1; c <= 8; c *= 2) {
       if (c > 1 && k_blocks < 2 * c) break;
+      const int64_t per_cta = (k_blocks + c - 1) / c;
       for (int per_sm = 1; per_sm <= 2; ++per_sm) {
-        const size_t room = static_cast<size_t>(per_sm == 2 ? 113 : 226) * 1024;
+        const size_t room = static_cast<size_t>(per_sm == 2 ? 112 : 226) * 1024;
         if (few_smem_bytes(q->gated, static_cast<int>(t), 2, c > 1) > room) continue;
-        const int64_t clusters = few_max_clusters(c, per_sm);
+        const int64_t one = few_max_clusters(c);
+        // (two clusters' CTAs on an SM pack less than twice as many; of four, hardly more)
+        const int64_t clusters = per_sm == 1 ? one : c == 1 ? 2 * one : c == 4 ? one * 7 / 5 : one * 9 / 5;
         const int64_t rounds = (tiles + clusters - 1) / clusters;
-        // CTAs of the busiest SM over all rounds
+        // CTAs of the busiest SM in the full rounds and in the last one
         const int64_t full = tiles / clusters, rest = tiles % clusters;
-        const int64_t busy = full * per_sm + (rest * c + sms - 1) / sms;
-        const double join = c == 1 ? 300 + 10.0 * accs * t
-                                   : 2500 + 4.0 * accs * t + 40.0 * accs * t / c;
-        const double stream = busy * kb * static_cast<double>((k_blocks + c - 1) / c);
-        const double cost = (stream > all ? stream : all) + rounds * (1500 + join);
+        const int64_t last = (rest * c + sms - 1) / sms < per_sm ? (rest * c + sms - 1) / sms : per_sm;
+        auto shared = [](int64_t n) { return n < 2 ? static_cast<double>(n) : n / 1.6; };
+        double time = kb * per_cta * (full * shared(per_sm) + shared(last));
+        if (time < hbm) time = hbm;
+        if (time < l2) time = l2;
+        const double tail = c == 1 ? 1100 + 18.0 * accs * t
+                                   : 550 + 36.0 * accs * t + 48.0 * accs * t / c + 460.0 * c;
+        const double cost = time + rounds * (7700 + tail);
         if (cost < best) {
           best = cost;
           FewParams &p = q->few_params;
@@ -73,7 +83,6 @@ void plan_few(FusedProduct *q, int64_t k_blocks, int sm_count) {
           p.tiles_f = static_cast<int>(tiles_f);
           p.splits = c;
           int64_t stages = static_cast<int64_t>((room - kFewFixedBytes) / few_stage_bytes(q->gated, p.tile_t));
-          const int64_t per_cta = (k_blocks + c - 1) / c;
           if (stages > per_cta) stages = per_cta;
           if (stages > 16) stages = 16;
           p.stages = static_cast<int>(stages);
@@ -81,7 +90,21 @@ void plan_few(FusedProduct *q, int64_t k_blocks, int sm_count) {
       }
     }
   }
-  q->cost = best;
+  q->few_cost = best;
+}
+
+// The CTA-pair kernel's estimate, in the same cycles: 512 a K-block and round of tiles, and
+// about 16000 for the first loads and the last tile's epilogue; a tile's epilogue runs under
+// the next one's K-loop unless that is shorter (8000); and no less than HBM's time.
+double pair_cost(const FusedProduct &q, int64_t k_blocks, int64_t clusters, int stream_k) {
+  const int64_t tiles = q.tiles_m * q.tiles_n;
+  double rounds = static_cast<double>((tiles + clusters - 1) / clusters);
+  if (tiles > clusters && use_split_k(stream_k, tiles, k_blocks, clusters))
+    rounds = static_cast<double>(tiles) / clusters;
+  const double loop = 512.0 * k_blocks;
+  const double time = loop + (rounds - 1) * (loop > 8000 ? loop : 8000);
+  const double hbm = static_cast<double>((q.gated ? 2 : 1) * q.N + q.M) * k_blocks * 128 / 3200;
+  return 16000 + (time > hbm ? time : hbm);
 }
 
 // The token kernel's rule: weights stored [features, K], one product, and few enough tokens
@@ -141,12 +164,12 @@ bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
   q->tiles_n = (q->N + tile_n - 1) / tile_n;
   const int64_t clusters = h->sm_count > 1 ? h->sm_count / 2 : 1;
   if (q->tiles_m * q->tiles_n > INT32_MAX / 8 || k_blocks > INT32_MAX) return false;
-  // Few tiles of 256 rows, or rows that would fill less than half of one: the few-token
-  // kernel, whose tiles are smaller and share their K-loops over clusters.
-  bool few = q->M <= 128 || 2 * q->tiles_m * q->tiles_n <= clusters;
+  // Where the 256-row tiles are few, or few of their rows are tokens, the few-token kernel's
+  // smaller tiles, which share their K-loops over clusters, take less time.
+  plan_few(q, k_blocks, h->sm_count);
+  bool few = q->few_cost < pair_cost(*q, k_blocks, clusters, h->stream_k);
   if (h->cta_pair) few = h->cta_pair == 1;  // GEMM_OPT_CTA_PAIR
   q->kind = few ? FusedProduct::kFew : FusedProduct::kPair;
-  if (few) plan_few(q, k_blocks, h->sm_count);
   plan_x(&q->X, q->M, q->K, carve);
   plan_w(&q->W, q->K, q->N, carve);
   if (q->gated) {

@@ -46,7 +46,7 @@ struct FusedProduct {
   int k_warps = 1;         // token kernel
   bool vector = false;     // token kernel: 16-byte accesses
   FewParams few_params{};
-  double cost = 0.0;       // few-token kernel's estimate, SM cycles
+  double few_cost = 0.0;   // few-token kernel's estimate, SM cycles
   int64_t tiles_m = 0, tiles_n = 0;
 };
 

@@ -37,18 +37,23 @@ constexpr int A_BYTES = BM * kRowBytes;
 constexpr int B_BYTES = (BN / 2) * kRowBytes;
 constexpr int PANEL_BYTES = BK * kRowBytes;   // MN-major weights: 64 K-rows x 128 bytes
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGES = 6;
+// Eight epilogue warps, two for each quarter of the TMEM lanes, each with half of the
+// accumulator's columns: four left each scheduler one warp, whose exponentials, TMEM reads and
+// TMA waits then ran one after another (silu and a residual took 8 us a tile). Their boxes
+// leave room for five stages.
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int HALF = BN / 2;                  // accumulator columns of an epilogue warp
+constexpr int STAGES = 5;
 constexpr int EPI_OFFSET = STAGES * STAGE_BYTES;
-constexpr int BIAS_OFFSET = EPI_OFFSET + kEpiWarps * 2 * kStoreBufBytes;
-constexpr int BAR_OFFSET = BIAS_OFFSET + kEpiWarps * 64 * 4;
-constexpr int OWNER_SLICE = 48 * 1024;        // stage bytes an owner warp borrows
-constexpr int PART_BYTES = BN * 32 * 4;       // one partial's 32 rows, fp32
+constexpr int BIAS_OFFSET = EPI_OFFSET + kPairEpiWarps * 2 * kStoreBufBytes;
+constexpr int BAR_OFFSET = BIAS_OFFSET + kPairEpiWarps * 32 * 4;
+constexpr int PART_BYTES = HALF * 32 * 4;     // one partial's 32 rows of a warp, fp32
 // stages, accumulators, drain; per epilogue warp one partial load and two residual boxes
-constexpr int NUM_BARS = 2 * STAGES + 5 + kEpiWarps * 3;
+constexpr int NUM_BARS = 2 * STAGES + 5 + kPairEpiWarps * 3;
 constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 32 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(kEpiWarps * OWNER_SLICE <= STAGES * STAGE_BYTES && PART_BYTES <= OWNER_SLICE,
-              "owner slices fit the stages");
+static_assert(kPairEpiWarps * PART_BYTES <= STAGES * STAGE_BYTES, "owners' partials fit the stages");
 
 // COLS consecutive accumulator columns of this lane's row, as fp32.
 template <int COLS>
@@ -114,7 +119,7 @@ __device__ __forceinline__ void add_box_row(uint32_t row_addr, int lane, float (
 // A warp's two staging boxes and the residual loads into them.
 struct Boxes {
   uint8_t *mem;         // two boxes of kStoreBufBytes
-  float *bias;          // 64 floats
+  float *bias;          // 32 floats
   uint64_t *bars;       // residual load of each box
   uint32_t phases;      // their parities
   int next;             // box of the next store
@@ -164,7 +169,7 @@ __device__ __forceinline__ bool plain_boxes(const PairMaps &maps, const PairPara
                                             uint32_t t_row, int row0, int n0, const Watchdog &wd) {
   constexpr int COLS = OUT == GEMM_F32 ? 32 : 64;
   const int lane = bx.lane;
-  const int n = box_count<OUT>(p, row0, n0, BN);
+  const int n = box_count<OUT>(p, row0, n0, HALF);
   const bool res_box = residual_boxes(p);
   float b0 = 0.0f, b1 = 0.0f;  // the next piece's bias, two columns a lane
   auto load_bias = [&](int c) {
@@ -179,16 +184,19 @@ __device__ __forceinline__ bool plain_boxes(const PairMaps &maps, const PairPara
     float v[COLS];
     read_columns<COLS>(t_row + c * COLS, v);
     if (p.f.bias) {
-      __syncwarp();  // the previous piece's bias has been read
-      bx.bias[lane] = b0;
-      if (COLS == 64) bx.bias[lane + 32] = b1;
-      __syncwarp();
-      load_bias(c + 1);
 #pragma unroll
-      for (int i = 0; i < COLS; i += 4) {
-        const float4 q = *reinterpret_cast<const float4 *>(bx.bias + i);
-        v[i] += q.x, v[i + 1] += q.y, v[i + 2] += q.z, v[i + 3] += q.w;
+      for (int h = 0; h < COLS / 32; ++h) {
+        __syncwarp();  // the previous columns' bias has been read
+        bx.bias[lane] = h ? b1 : b0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 q = *reinterpret_cast<const float4 *>(bx.bias + i);
+          float *o = &v[32 * h + i];
+          o[0] += q.x, o[1] += q.y, o[2] += q.z, o[3] += q.w;
+        }
       }
+      load_bias(c + 1);
     }
     if (p.f.pre) {
       const int b = bx.take();
@@ -222,42 +230,38 @@ __device__ __forceinline__ bool plain_boxes(const PairMaps &maps, const PairPara
   return true;
 }
 
-// Gated pair, TMA form: g in columns 0-127, u in columns 128-255.
+// Gated pair, TMA form: 64 columns of g and, 128 accumulator columns on, of u.
 template <int OUT>
 __device__ __forceinline__ void gated_boxes(const PairMaps &maps, const PairParams &p, Boxes &bx,
-                                            uint32_t t_row, int row0, int n0) {
-  constexpr int COLS = 64;
+                                            uint32_t t_row, int row0, int col) {
+  constexpr int COLS = HALF / 2;
   const int lane = bx.lane;
-  const int n = box_count<OUT>(p, row0, n0, BN / 2);
-#pragma unroll 1
-  for (int c = 0; c < n; ++c) {
-    const int col = n0 + c * COLS;
-    float g[COLS], u[COLS];
-    read_columns<COLS>(t_row + c * COLS, g);
-    if (p.f.pre) {
-      const int b = bx.take();
-      write_box_row<OUT>(bx.row(b), lane, g);
-      bx.store(b, &maps.Z, col, row0);
-    }
-    read_columns<COLS>(t_row + BN / 2 + c * COLS, u);
-    if (p.f.pre) {
-      const int b = bx.take();
-      write_box_row<OUT>(bx.row(b), lane, u);
-      bx.store(b, &maps.Z2, col, row0);
-    }
-    activate_all<true>(g, p.f.act);
-#pragma unroll
-    for (int i = 0; i < COLS; ++i) g[i] *= u[i];
+  if (box_count<OUT>(p, row0, col, COLS) == 0) return;
+  float g[COLS], u[COLS];
+  read_columns<COLS>(t_row, g);
+  if (p.f.pre) {
     const int b = bx.take();
     write_box_row<OUT>(bx.row(b), lane, g);
-    bx.store(b, &maps.C, col, row0);
+    bx.store(b, &maps.Z, col, row0);
   }
+  read_columns<COLS>(t_row + BN / 2, u);
+  if (p.f.pre) {
+    const int b = bx.take();
+    write_box_row<OUT>(bx.row(b), lane, u);
+    bx.store(b, &maps.Z2, col, row0);
+  }
+  activate_all<true>(g, p.f.act);
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) g[i] *= u[i];
+  const int b = bx.take();
+  write_box_row<OUT>(bx.row(b), lane, g);
+  bx.store(b, &maps.C, col, row0);
 }
 
 // Outputs or a residual TMA cannot address: each lane reads and writes its row's elements.
 template <typename T, bool GATED>
 __device__ __forceinline__ void direct_rows(const PairParams &p, uint32_t t_row, int row, int n0) {
-  const int cols = GATED ? BN / 2 : BN;
+  const int cols = GATED ? HALF / 2 : HALF;  // this warp's
 #pragma unroll 1
   for (int c0 = 0; c0 < cols; c0 += 32) {
     float v[32], u[32];
@@ -301,7 +305,7 @@ __device__ __forceinline__ void direct_rows(const PairParams &p, uint32_t t_row,
 }
 
 template <bool GATED, bool W_MN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -311,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *tmem_full = empty + STAGES;
   uint64_t *tmem_empty = tmem_full + 2;
   uint64_t *drain = tmem_empty + 2;
-  uint64_t *part_bar = drain + 1;              // [kEpiWarps]
-  uint64_t *res_bar = part_bar + kEpiWarps;    // [kEpiWarps][2]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_bar + 2 * kEpiWarps);
+  uint64_t *part_bar = drain + 1;                  // [kPairEpiWarps]
+  uint64_t *res_bar = part_bar + kPairEpiWarps;    // [kPairEpiWarps][2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_bar + 2 * kPairEpiWarps);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   // Teardown words, as in tc2_kernel.cu: fills this CTA's loader issued, fills the MMA issuer
   // consumed, fills the peer's loader issued, whether the other CTA aborted.
@@ -332,10 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tmem_full[b], 1);
-      mbar_init(&tmem_empty[b], 2 * kEpiWarps);
+      mbar_init(&tmem_empty[b], 2 * kPairEpiWarps);
     }
     mbar_init(drain, 1);
-    for (int w = 0; w < 3 * kEpiWarps; ++w) mbar_init(&part_bar[w], 1);
+    for (int w = 0; w < 3 * kPairEpiWarps; ++w) mbar_init(&part_bar[w], 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) xs[i] = 0;
     fence_barrier_init();
@@ -455,8 +459,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3;
     const int e = warp - 2;
+    const int half = e / 4;  // its columns: of the accumulator, and (gated: halved) of the tile
+    const int out_half = half * TILE_N / 2;
     Boxes bx{smem + EPI_OFFSET + e * 2 * kStoreBufBytes,
-             reinterpret_cast<float *>(smem + BIAS_OFFSET) + e * 64, res_bar + 2 * e, 0, 0, lane};
+             reinterpret_cast<float *>(smem + BIAS_OFFSET) + e * 32, res_bar + 2 * e, 0, 0, lane};
+    // The accumulator columns a warp hands over or joins are those its epilogue reads: half of
+    // them, or half of g's and half of u's.
+    constexpr int PARTS = GATED ? 2 : 1, PART_COLS = HALF / PARTS;
+    auto part_col = [&](int i) { return i * (BN / 2) + half * PART_COLS; };
     uint32_t acc = 0, acc_phase = 0, part_phase = 0;
     WorkIter work(sched, cluster_id);
     SkSegment seg;
@@ -466,12 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pm, pn;
       tile_coords(seg.tile, p.tiles_m, p.tiles_n, p.group_m, pm, pn);
       const int row0 = pm * (2 * BM) + static_cast<int>(rank) * BM + quarter * 32;
-      const int n0 = pn * TILE_N;
+      const int n0 = pn * TILE_N + out_half;
       if (!GATED && seg.role != kSegPartial && residual_boxes(p)) {
         // the first two pieces of the residual, ahead of the accumulator
         const int cols = p.f.out_dtype == GEMM_F32 ? 32 : 64;
-        loads = p.f.out_dtype == GEMM_F32 ? box_count<GEMM_F32>(p, row0, n0, BN)
-                                          : box_count<GEMM_BF16>(p, row0, n0, BN);
+        loads = p.f.out_dtype == GEMM_F32 ? box_count<GEMM_F32>(p, row0, n0, HALF)
+                                          : box_count<GEMM_BF16>(p, row0, n0, HALF);
         loads = min(loads, 2);
         for (int c = 0; c < loads; ++c) bx.load(c, &maps.R, n0 + c * cols, row0);
       }
@@ -482,12 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
       auto part_row0 = [&](int w) { return (w * 2 + static_cast<int>(rank)) * BM + quarter * 32; };
       if (seg.role == kSegPartial) {
-        epilogue_tma<BN, GEMM_F32>(&maps.P, t_row, bx.mem, bx.next, lane, part_row0(cluster_id), 0,
-                                   INT32_MAX, BN);
+        for (int i = 0; i < PARTS; ++i)
+          epilogue_tma<PART_COLS, GEMM_F32>(&maps.P, t_row + part_col(i), bx.mem, bx.next, lane,
+                                            part_row0(cluster_id), part_col(i), INT32_MAX, BN);
         if (lane == 0) {
           bulk_wait_group<0>();
           fence_proxy_async_global();
-          st_release_gpu(p.sk_flags + (cluster_id * 2 + rank) * 4 + quarter, epoch);
+          st_release_gpu(p.sk_flags + (cluster_id * 2 + rank) * kPairEpiWarps + e, epoch);
         }
         __syncwarp();
       } else {
@@ -495,9 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The workers first_src..last_src computed the start of this tile: add their
           // partials in order. The owner piece is its worker's last, so the ring is idle and
           // each warp borrows a slice of it for the partial's rows.
-          uint8_t *slice = smem + e * OWNER_SLICE;
+          uint8_t *slice = smem + e * PART_BYTES;
           for (int w = seg.first_src; ok && w <= seg.last_src; ++w) {
-            ok = wait_flag(p.sk_flags + (w * 2 + rank) * 4 + quarter, epoch, wd);
+            ok = wait_flag(p.sk_flags + (w * 2 + rank) * kPairEpiWarps + e, epoch, wd);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_proxy_async_global();
@@ -508,9 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               mbar_arrive_expect_tx(&part_bar[e], PART_BYTES);
 #pragma unroll
-              for (int c = 0; c < BN / 32; ++c)
+              for (int c = 0; c < HALF / 32; ++c)
                 tma_load_2d(smem_u32(slice + c * kStoreBufBytes), &maps.P, smem_u32(&part_bar[e]),
-                            c * 32, part_row0(w));
+                            part_col(c * 32 / PART_COLS) + c * 32 % PART_COLS, part_row0(w));
             }
             ok = mbar_wait(&part_bar[e], part_phase, wd);
             ok = __all_sync(0xffffffffu, ok);
@@ -520,30 +531,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             part_phase ^= 1;
-            add_partial_into_tmem<BN>(t_row, slice, lane);
+            for (int i = 0; i < PARTS; ++i)
+              add_partial_into_tmem<PART_COLS>(t_row + part_col(i),
+                                               slice + i * (PART_BYTES / PARTS), lane);
           }
           if (!ok) break;
         }
+        const uint32_t t_cols = t_row + out_half;  // g's columns in the gated accumulator
         if (p.tma_out) {
           if (GATED) {
             if (p.f.out_dtype == GEMM_BF16)
-              gated_boxes<GEMM_BF16>(maps, p, bx, t_row, row0, n0);
+              gated_boxes<GEMM_BF16>(maps, p, bx, t_cols, row0, n0);
             else
-              gated_boxes<GEMM_F16>(maps, p, bx, t_row, row0, n0);
+              gated_boxes<GEMM_F16>(maps, p, bx, t_cols, row0, n0);
           } else if (p.f.out_dtype == GEMM_BF16) {
-            ok = plain_boxes<GEMM_BF16>(maps, p, bx, t_row, row0, n0, wd);
+            ok = plain_boxes<GEMM_BF16>(maps, p, bx, t_cols, row0, n0, wd);
           } else if (p.f.out_dtype == GEMM_F16) {
-            ok = plain_boxes<GEMM_F16>(maps, p, bx, t_row, row0, n0, wd);
+            ok = plain_boxes<GEMM_F16>(maps, p, bx, t_cols, row0, n0, wd);
           } else {
-            ok = plain_boxes<GEMM_F32>(maps, p, bx, t_row, row0, n0, wd);
+            ok = plain_boxes<GEMM_F32>(maps, p, bx, t_cols, row0, n0, wd);
           }
           if (!ok) break;
         } else if (p.f.out_dtype == GEMM_BF16) {
-          direct_rows<__nv_bfloat16, GATED>(p, t_row, row0 + lane, n0);
+          direct_rows<__nv_bfloat16, GATED>(p, t_cols, row0 + lane, n0);
         } else if (p.f.out_dtype == GEMM_F16) {
-          direct_rows<__half, GATED>(p, t_row, row0 + lane, n0);
+          direct_rows<__half, GATED>(p, t_cols, row0 + lane, n0);
         } else if (!GATED) {
-          direct_rows<float, GATED>(p, t_row, row0 + lane, n0);
+          direct_rows<float, GATED>(p, t_cols, row0 + lane, n0);
         }
       }
       loads = 0;
@@ -597,7 +611,7 @@ cudaError_t launch_pair(const PairMaps &maps, const PairParams &p, int grid, cud
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dependency_wait
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = s;
   cfg.attrs = attr;

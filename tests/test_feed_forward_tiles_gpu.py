@@ -112,10 +112,11 @@ def test_many_rounds_of_tiles(g):
 @pytest.mark.parametrize("cta_pair", [1, 2])
 def test_bounded_waits_expire_and_the_next_call_is_right(g, cta_pair, stall):
     """A loader that issues nothing, or stops after some stage fills: the call ends, the status
-    word says so, and the handle's next calls are right (also with a residual on its way)."""
+    word says so, and the handle's next calls are right (also with a residual on its way). (K:
+    64 K-blocks, so that a loader has more fills to do even where eight CTAs share them.)"""
     h = g.Gemm(0)
     h.set_option("cta_pair", cta_pair)
-    a, b = operands(300, 520, 1024, "bf16", 3)
+    a, b = operands(300, 520, 4096, "bf16", 3)
     r = matrix(300, 520, torch.bfloat16, 6)
     h.set_option("wait_timeout_us", 20000)
     h.set_option("fault_stall_producer", stall)
