@@ -78,8 +78,19 @@ gemm_status_t ensure_ff(gemm_handle_t h, size_t bytes) {
   return GEMM_OK;
 }
 
-// One product through the planner (its argument checks are the caller's own).
+// One product (its argument checks are the caller's own): small exact fp32 ones on the fused
+// operators' fp32 kernels, others through the planner.
 gemm_status_t product(gemm_handle_t h, const Problem &P, cudaStream_t s) {
+  if (P.in_dtype == GEMM_F32 && P.precision != GEMM_PREC_TF32) {
+    ff::FusedProduct q;
+    q.M = P.M, q.N = P.N, q.K = P.K;
+    q.X.ptr = P.A, q.X.ld = P.lda, q.X.layout = P.a_layout;
+    q.W.ptr = P.B, q.W.ld = P.ldb, q.W.layout = P.b_layout;
+    q.in_dtype = P.in_dtype, q.out_dtype = P.out_dtype;
+    q.C = P.C, q.ldc = P.ldc;
+    Carve none;  // these kernels stage nothing
+    if (ff::plan_fused(h, &q, &none)) return ff::run_fused(h, q, nullptr, s);
+  }
   Plan pl;
   const gemm_status_t st = make_plan(P, options_for(h, P), h->sm_count, &pl);
   return st == GEMM_OK ? execute(h, P, pl, s) : st;
@@ -189,6 +200,7 @@ GEMM_API gemm_status_t gemm_run_epilogue(gemm_handle_t h, int64_t M, int64_t N, 
     q.X.ptr = A, q.X.ld = lda, q.X.layout = a_layout;
     q.W.ptr = B, q.W.ld = ldb, q.W.layout = b_layout;
     q.in_dtype = in_dtype, q.out_dtype = out_dtype;
+    q.exact = precision_mode != GEMM_PREC_TF32;
     q.C = C, q.ldc = ldc;
     q.ep = ep;
     bool taken = false;
@@ -315,6 +327,7 @@ GEMM_API gemm_status_t gemm_run_gated(gemm_handle_t h, int64_t M, int64_t F, int
   q.W.ptr = Wg, q.W.ld = ldwg, q.W.layout = w_layout;
   q.W2.ptr = Wu, q.W2.ld = ldwu, q.W2.layout = w_layout;
   q.in_dtype = q.out_dtype = dtype;
+  q.exact = precision_mode != GEMM_PREC_TF32;
   q.C = H, q.ldc = ldh;
   q.ep.act = activation;
   q.ep.pre = gate, q.ep.ld_pre = ld_gate;
@@ -421,12 +434,34 @@ GEMM_API gemm_status_t gemm_run_gated_backward(
                   "gated backward launch");
     if (st != GEMM_OK) return st;
   }
+  bool summed = false;
   if (taken) {
     q.X.ptr = dg, q.X2.ptr = du;
     st = ff::run_fused(h, q, buf, s);
     if (st != GEMM_OK) return st;
   } else if (make_dx) {
-    // two products in fp32, added and rounded once
+    // two products in fp32, added and rounded once; in one step with the second product where
+    // an fp32 kernel takes it
+    if (dtype == GEMM_F32) {
+      ff::FusedProduct r;
+      r.M = M, r.N = K, r.K = F;
+      r.X.ptr = du, r.X.ld = ldd;
+      r.W.ptr = Wu, r.W.ld = ldwu, r.W.layout = flip(w_layout);
+      r.in_dtype = r.out_dtype = GEMM_F32;
+      r.exact = precision_mode != GEMM_PREC_TF32;
+      r.C = dX, r.ldc = lddx;
+      r.ep.residual = dX, r.ep.ld_residual = lddx;
+      Carve none;
+      if (ff::plan_fused(h, &r, &none)) {
+        st = product(h, Problem{M, K, F, dg, ldd, Wg, ldwg, dX, lddx, dtype, dtype, precision_mode,
+                                GEMM_ROW_MAJOR, flip(w_layout)}, s);
+        if (st == GEMM_OK) st = ff::run_fused(h, r, nullptr, s);
+        if (st != GEMM_OK) return st;
+        summed = true;
+      }
+    }
+  }
+  if (!taken && make_dx && !summed) {
     float *x32 = reinterpret_cast<float *>(buf + x_off), *x2 = reinterpret_cast<float *>(buf + x2_off);
     st = product(h, Problem{M, K, F, dg, ldd, Wg, ldwg, x32, ld32, dtype, GEMM_F32, precision_mode,
                             GEMM_ROW_MAJOR, flip(w_layout)}, s);

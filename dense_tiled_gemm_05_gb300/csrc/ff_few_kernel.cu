@@ -17,9 +17,7 @@
 // tile that is not split goes from TMEM to memory directly.
 //
 // The gated pair runs as two MMAs a K-step, both weights' rows against the same token tile.
-#include "activation.cuh"
-#include "ff_kernels.h"
-#include "ptx.cuh"
+#include "ff_join.cuh"
 #include "tc_common.cuh"
 
 namespace gemm_gb300 {
@@ -53,58 +51,8 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-template <typename T>
-__device__ __forceinline__ void store4(T *row, int64_t n, int64_t N, bool vec, const float (&v)[4]) {
-  if (vec)
-    store_piece<T, 4, true>(row, n, N, v);
-  else
-    store_piece<T, 4, false>(row, n, N, v);
-}
-
-// Epilogue of four consecutive features n.. of token m from their fp32 sums.
-template <typename TO, bool GATED>
-__device__ __forceinline__ void finish4(const FusedParams &p, bool vec, int64_t m, int64_t n,
-                                        float (&a)[4], float (&b)[4]) {
-  if (GATED) {
-    if (p.pre) {
-      store4(static_cast<TO *>(p.pre) + m * p.ld_pre, n, p.N, vec, a);
-      store4(static_cast<TO *>(p.pre2) + m * p.ld_pre2, n, p.N, vec, b);
-    }
-    activate_all<true>(a, p.act);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] *= b[i];
-  } else {
-    if (p.bias) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) a[i] += load_any(p.bias, p.bias_dtype, n + i);
-    }
-    if (p.pre) store4(static_cast<TO *>(p.pre) + m * p.ld_pre, n, p.N, vec, a);
-    activate_all<true>(a, p.act);
-    if (p.residual) {
-      const TO *r = static_cast<const TO *>(p.residual) + m * p.ld_residual;
-      if (vec)
-        load_piece<TO, 4, true>(r, n, p.N, b);
-      else
-        load_piece<TO, 4, false>(r, n, p.N, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] += b[i];
-    }
-  }
-  store4(static_cast<TO *>(p.C) + m * p.ldc, n, p.N, vec, a);
 }
 
 // One feature a lane, 16 tokens of its TMEM columns: the epilogue of a tile that one CTA
@@ -342,46 +290,9 @@ __global__ void __launch_bounds__(kFewThreads)
     cluster_sync();
   else
     __syncthreads();
-  const uint32_t base = smem_u32(smem);
-  // A thread's items are BATCH at a time: all their partials are on the way before the first
-  // sum, or each would wait for the other SMs' shared memory in turn.
-  constexpr int BATCH = GATED ? 3 : 6;
-  const int items = p.splits > 1 ? tokens * (kFewFeatures / 4) : 0, stride = p.splits * kFewThreads;
-  for (int i0 = rank * kFewThreads + threadIdx.x; i0 < items; i0 += BATCH * stride) {
-    float a[BATCH][4], b[BATCH][4];
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[j][i] = b[j][i] = 0.0f;
-#pragma unroll 2
-    for (int q = 0; q < p.splits; ++q) {
-      float4 v[BATCH], w[BATCH];
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int i = min(i0 + j * stride, items - 1);
-        const uint32_t at = mapa_shared(base + static_cast<uint32_t>(i) * 16, static_cast<uint32_t>(q));
-        v[j] = ld_cluster_f4(at);
-        if (GATED) w[j] = ld_cluster_f4(at + plane * static_cast<uint32_t>(sizeof(float)));
-      }
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        a[j][0] += v[j].x, a[j][1] += v[j].y, a[j][2] += v[j].z, a[j][3] += v[j].w;
-        if (GATED) b[j][0] += w[j].x, b[j][1] += w[j].y, b[j][2] += w[j].z, b[j][3] += w[j].w;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int i = i0 + j * stride, f = i % (kFewFeatures / 4) * 4;
-      if (i >= items || f0 + f >= p.f.N) continue;
-      const int64_t m = t0 + i / (kFewFeatures / 4), n = f0 + f;
-      if (p.f.out_dtype == GEMM_BF16)
-        finish4<__nv_bfloat16, GATED>(p.f, p.vec, m, n, a[j], b[j]);
-      else if (p.f.out_dtype == GEMM_F16)
-        finish4<__half, GATED>(p.f, p.vec, m, n, a[j], b[j]);
-      else
-        finish4<float, GATED>(p.f, p.vec, m, n, a[j], b[j]);
-    }
-  }
+  if (p.splits > 1)
+    join_partials<GATED, true, kFewFeatures, kFewThreads, GATED ? 3 : 6>(
+        p.f, p.vec, smem_u32(smem), plane, tokens, p.splits, rank, t0, f0);
   if (threadIdx.x == 0 && *abort_flag) {
     // After an abort, let every copy already issued land: the last fill of stage s is fill
     // number f (f % stages == s), completing parity (f / stages) & 1.

@@ -71,6 +71,23 @@ constexpr int kTokenMax = 8;
 // vector: X and weights allow 16-byte accesses and K is a multiple of them.
 cudaError_t token_launch(bool gated, int dtype, bool vector, const TokenParams &p, cudaStream_t s);
 
+// fp32 tile kernel: exact products on fused multiply-adds, operands of any layout and
+// alignment. X is M x K, W is K x N; *_k: K is the contiguous axis.
+struct TileParams {
+  FusedParams f;        // (k_blocks, kb_first and idesc unused)
+  const float *X, *W, *W2;
+  int64_t ldx, ldw, ldw2;
+  int32_t x_k, w_k;
+  int64_t K;
+  int32_t splits;       // CTAs (one cluster) that share a tile's K: 1, 2, 4 or 8
+  int32_t vec;          // as FewParams
+};
+constexpr int kTileK = 16;  // K elements per step
+// Rows and columns of a tile (gated: columns of each product) for a size of 64 or 128.
+inline int tile_rows(int size) { return size; }
+inline int tile_cols(bool gated, int size) { return gated ? size / 2 : size; }
+cudaError_t tile_launch(bool gated, int size, const TileParams &p, cudaStream_t s);
+
 // Many-token kernel: CTA pairs, 256 x 256 accumulators (gated: 128 columns of each product).
 struct PairParams {
   FusedParams f;

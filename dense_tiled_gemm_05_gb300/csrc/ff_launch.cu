@@ -141,13 +141,59 @@ bool plan_token(FusedProduct *q, int sm_count) {
   return true;
 }
 
+// Whether the outputs and the residual allow accesses of four elements.
+bool four_wide(const FusedProduct &q) {
+  const int es = esize_of(q.out_dtype);
+  auto ok = [&](const void *p, int64_t ld) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && ld % 4 == 0);
+  };
+  return ok(q.C, q.ldc) && ok(q.ep.pre, q.ep.ld_pre) && ok(q.pre2, q.ld_pre2) &&
+         ok(q.ep.residual, q.ep.ld_residual);
+}
+
+// Tile and cluster split of the fp32 tile kernel by estimated time in SM cycles -- about 11000
+// outside the K-loop, and 45 to 105 multiply-adds a cycle by how many warps an SM holds -- and
+// whether that is less than the exact product's on the tensor cores: 32 us, 18 us per 1024 of
+// K (the chunk drains; shared out over idle clusters from some 3000 on), the writing and reading
+// of the split operands, and 14 us where rows of the output are unaligned. Measured on one GB300, us, this kernel against that (with
+// silu and a residual): 512^3 13 / 43, 512 x 1024 x 1024 35 / 52, 64 x 2048 x 8192 66 / 102,
+// 1023 x 1000 x 1025 60 / 70, 2048 x 1024 x 1024 109 / 57, gated 1000 x 500 x 1000 61 / 86.
+bool plan_tile(FusedProduct *q, int sm_count) {
+  if (!q->exact || q->K2 > 0) return false;
+  const int64_t sms = sm_count > 0 ? sm_count : 1;
+  const int64_t steps = (q->K + kTileK - 1) / kTileK;
+  const int products = q->gated ? 2 : 1;
+  double best = 1e300;
+  for (const int size : {64, 128}) {
+    const int64_t bm = tile_rows(size), bn = tile_cols(q->gated, size);
+    const int64_t tiles = ((q->M + bm - 1) / bm) * ((q->N + bn - 1) / bn);
+    if (tiles > (int64_t{1} << 26)) continue;
+    for (int c = 1; c <= 8; c *= 2) {
+      if (c > 1 && steps < 4 * c) break;
+      const int64_t busy = (tiles * c + sms - 1) / sms;  // CTAs of the busiest SM
+      const double rate = size == 128 ? (busy > 1 ? 105 : 77) : busy > 2 ? 75 : busy > 1 ? 62 : 45;
+      // (an SM with more CTAs than the average has the last of them to itself)
+      const double ctas = busy > 1 ? 0.5 * (busy + static_cast<double>(tiles * c) / sms) : 1.0;
+      const double work = ctas * bm * bn * products * ((steps + c - 1) / c) * kTileK;
+      const double join = c > 1 ? (size == 128 ? 7000 : 1500) + 300.0 * c : 0.0;
+      const double cost = 11000 + work / rate + join;
+      if (cost < best) best = cost, q->tile_size = size, q->tile_splits = c;
+    }
+  }
+  const int64_t tensor_tiles = ((q->M + 255) / 256) * ((q->N + 255) / 256);
+  const int64_t clusters = sms > 1 ? sms / 2 : 1;
+  const double k1024 = q->K / 1024.0;
+  const double loop = (18 * k1024 < 55 ? 18 * k1024 : 55) * ((tensor_tiles + clusters - 1) / clusters);
+  const double split = 16.0 * (q->M + q->N) * q->K / 5e6;
+  const double ragged = four_wide(*q) && q->N % 4 == 0 ? 0 : 14;  // stores that TMA cannot make
+  if (best >= products * 1900.0 * (32 + loop + split + ragged)) return false;
+  q->kind = FusedProduct::kTile;
+  return true;
+}
+
 cudaError_t stage(const FusedOperand &o, int64_t lines, int64_t len, char *buf, cudaStream_t s) {
   if (o.transpose) return transpose_launch(o.ptr, o.ld, buf + o.offset, o.staged_ld, lines, len, 2, s);
   return repack_launch(o.ptr, o.ld, buf + o.offset, o.staged_ld, lines, len, 2, s);
-}
-
-bool aligned(const void *p, int64_t ld, int es, int elems) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % (es * elems) == 0 && ld % elems == 0);
 }
 
 }  // namespace
@@ -157,7 +203,7 @@ bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
   if (h->force_path == 2) return false;  // the FMA kernel was asked for
   if (q->gated && q->out_dtype != q->in_dtype) return false;
   if (!h->cta_pair && plan_token(q, h->sm_count)) return true;
-  if (q->in_dtype == GEMM_F32) return false;
+  if (q->in_dtype == GEMM_F32) return !h->cta_pair && plan_tile(q, h->sm_count);
   const int64_t k_blocks = (q->K + 63) / 64 + (q->K2 + 63) / 64;
   const int64_t tile_n = q->gated ? 128 : 256;
   q->tiles_m = (q->M + 255) / 256;
@@ -208,6 +254,20 @@ gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaS
     h->launches += 1;
     return GEMM_OK;
   }
+  if (q.kind == FusedProduct::kTile) {
+    TileParams p{};
+    p.f = f;
+    p.X = static_cast<const float *>(q.X.ptr), p.ldx = q.X.ld, p.x_k = q.X.layout == GEMM_ROW_MAJOR;
+    p.W = static_cast<const float *>(q.W.ptr), p.ldw = q.W.ld, p.w_k = q.W.layout == GEMM_COL_MAJOR;
+    p.W2 = static_cast<const float *>(q.W2.ptr), p.ldw2 = q.W2.ld;
+    p.K = q.K;
+    p.splits = q.tile_splits;
+    p.vec = four_wide(q);
+    e = tile_launch(q.gated, q.tile_size, p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "fp32 tile kernel launch");
+    h->launches += 1;
+    return GEMM_OK;
+  }
   const bool few = q.kind == FusedProduct::kFew;
   const bool two_x = !q.gated && q.K2 > 0, two_w = q.gated || q.K2 > 0;
   struct Use {
@@ -254,8 +314,7 @@ gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaS
     FewParams p = q.few_params;
     p.f = f;
     p.f.idesc = make_idesc(q.in_dtype, w_mn, false, p.tile_t, 128);
-    p.vec = aligned(q.C, q.ldc, os, 4) && aligned(f.pre, f.ld_pre, os, 4) &&
-            aligned(f.pre2, f.ld_pre2, os, 4) && aligned(f.residual, f.ld_residual, os, 4);
+    p.vec = four_wide(q);
     e = few_launch(q.gated, w_mn, maps[0], maps[1], maps[2], maps[3], p, s);
     if (e != cudaSuccess) return cuda_fail(e, "few-token kernel launch");
     h->launches += 1;

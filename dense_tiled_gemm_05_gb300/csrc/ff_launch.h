@@ -36,13 +36,16 @@ struct FusedProduct {
   int64_t K = 0, K2 = 0;   // K2 > 0: the sum of two products
   FusedOperand X, W, X2, W2;  // gated: W2 is the second projection, K2 is 0
   int in_dtype = GEMM_BF16, out_dtype = GEMM_BF16;
+  bool exact = true;       // fp32 inputs at full precision (else tf32)
   void *C = nullptr;
   int64_t ldc = 0;
   Epilogue ep;             // gated: act, pre and ld_pre only
   void *pre2 = nullptr;
   int64_t ld_pre2 = 0;
   // plan
-  enum Kind { kToken, kFew, kPair } kind = kPair;
+  enum Kind { kToken, kTile, kFew, kPair } kind = kPair;
+  int tile_size = 64;      // tile kernel
+  int tile_splits = 1;
   int k_warps = 1;         // token kernel
   bool vector = false;     // token kernel: 16-byte accesses
   FewParams few_params{};
@@ -50,8 +53,8 @@ struct FusedProduct {
   int64_t tiles_m = 0, tiles_n = 0;
 };
 
-// Whether the fused kernels take the product (16-bit types, and fp32 for a few tokens); fills
-// the plan and adds the staged copies to `carve`. False: a type, size or option they do not
+// Whether the fused kernels take the product (16-bit types, and fp32 for a few tokens or
+// small exact products); fills the plan and adds the staged copies to `carve`. False: a type, size or option they do not
 // handle.
 bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve);
 // `buf`: the buffer the offsets of plan_fused refer to.

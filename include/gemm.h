@@ -319,8 +319,8 @@ typedef struct {
 /* z = A @ B + bias, C = act(z) + residual; z is also stored to `pre` when that is given (the
  * backward pass reads it). Products, layouts, precision modes and checks are gemm_run_ex's;
  * z, act(z) and the sum are fp32 and rounded once each where they are stored. C may be the
- * residual itself (same address and leading dimension). `epilogue` NULL or empty is
- * gemm_run_ex. 16-bit inputs run in one kernel: with few rows the outputs' features are the
+ * residual itself (same address and leading dimension). `epilogue` NULL or empty is the
+ * product alone. 16-bit inputs run in one kernel: with few rows the outputs' features are the
  * rows of the tensor-core tile and K is split over a cluster; with many, 256 x 256 tiles on
  * CTA pairs (GEMM_OPT_CTA_PAIR 1 and 2 choose the one or the other, GEMM_OPT_STREAM_K the
  * split of the pairs' last rounds, GEMM_OPT_FORCE_PATH 2 neither). fp32 inputs run the product of their precision mode and then a kernel for what follows it.

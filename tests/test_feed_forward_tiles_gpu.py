@@ -149,3 +149,27 @@ def test_token_kernel(g, M, N, K, pad, offset, dtype):
     check_gated(h, a, b, wu, "silu", save=M % 2 == 0)
     assert h.status() == 0
     h.close()
+
+
+@pytest.mark.parametrize("x_layout,w_layout", [("row", "col"), ("row", "row"), ("col", "row"),
+                                               ("col", "col")])
+@pytest.mark.parametrize("M,N,K", [(9, 1, 1), (9, 64, 15), (17, 65, 16), (64, 64, 17), (65, 130, 513),
+                                   (127, 129, 100), (130, 33, 1000), (200, 260, 64), (500, 500, 400)])
+def test_fp32_tile_kernel(g, M, N, K, x_layout, w_layout):
+    """Small exact fp32 products of every layout, around the tiles' and steps' edges, with
+    unaligned rows; and their gradients, whose products are small too."""
+    h = g.Gemm(0)
+    t = torch.float32
+    for pad, offset in ((0, 0), (3, 1)):
+        a, b = operands(M, N, K, "f32", M + N, x_layout, w_layout, pad, offset)
+        r = matrix(M, N, t, 6, pad=pad, offset=offset)
+        check_epilogue(h, a, b, "gelu", matrix(1, N, t, 5)[0], r)
+        check_epilogue(h, a, b, None, None, r, out=r, save=False)
+        pre, dy = matrix(M, N, t, 7, pad=pad), matrix(M, N, t, 8, pad=pad)
+        check_epilogue_backward(h, dy, a, b, pre, "silu")
+    if x_layout == "row":
+        wu = matrix(K, N, t, 9, w_layout, 3, 1, scale=K ** -0.5)
+        check_gated(h, a, b, wu, "silu", save=M % 2 == 0)
+        check_gated_backward(h, dy, a, b, wu, pre, matrix(M, N, t, 11), "silu")
+    assert h.status() == 0
+    h.close()
