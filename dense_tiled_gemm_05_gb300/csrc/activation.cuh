@@ -168,6 +168,36 @@ struct Columns {
   }
 };
 
+// Two fp32 values in one register pair: Blackwell's packed add, multiply and multiply-add round
+// each half as the scalar instruction does and take one issue slot for both.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() : v(0) {}
+  __device__ __forceinline__ F2(float lo, float hi) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 c;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 c;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
 // 1 / (1 + exp(-z)). FAST (kernels whose inputs are 16-bit, so that z already carries errors
 // of 2^-9): the hardware exponential and division, a few fp32 ulps for |z| of ordinary size.
 // Both saturate to exactly 0 and 1.

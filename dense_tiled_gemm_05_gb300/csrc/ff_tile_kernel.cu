@@ -76,22 +76,6 @@ struct Loader {
 };
 static_assert(kTileK == 16, "the K of two warps");
 
-// Two fp32 multiply-adds in one instruction (each rounded as fmaf's): twice the multiply-adds
-// an issue slot, which is what bounds the kernel.
-__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-
 template <int BM_, int BN_, int TM_, int TN_, bool GATED>
 struct Tile {
   static constexpr int S = GATED ? 2 : 1;
@@ -145,13 +129,7 @@ __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint64_t acc[S][TM / 2][TN];  // pairs of rows
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int i = 0; i < TM / 2; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[s][i][j] = 0;
+  F2 acc[S][TM / 2][TN];  // pairs of rows: two multiply-adds an instruction
   for (int k = 0; k < kStages - 1; ++k) fetch(k);
   for (int step = 0; step < n_steps; ++step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -170,9 +148,10 @@ __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
         for (int j = 0; j < TN; j += 4) read4(&g.w[s][k][j * T::TX + tx * 4], &b[j]);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          const uint64_t bb = pair(b[j], b[j]);
+          const F2 bb(b[j], b[j]);
 #pragma unroll
-          for (int i = 0; i < TM / 2; ++i) fma2(acc[s][i][j], pair(a[2 * i], a[2 * i + 1]), bb);
+          for (int i = 0; i < TM / 2; ++i)
+            acc[s][i][j] = fma2(F2(a[2 * i], a[2 * i + 1]), bb, acc[s][i][j]);
         }
       }
     }
@@ -191,7 +170,7 @@ __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
       for (int j = 0; j < TN; j += 4) {
         float2 v[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = unpair(acc[s][i / 2][j + c]);
+        for (int c = 0; c < 4; ++c) v[c] = acc[s][i / 2][j + c].get();
         float *d = part + s * BM * BN + r * BN + j * T::TX + tx * 4;
         *reinterpret_cast<float4 *>(d) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
         *reinterpret_cast<float4 *>(d + BN) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);

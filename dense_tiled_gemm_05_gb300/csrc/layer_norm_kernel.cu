@@ -14,6 +14,8 @@
 // statistics are fp32.
 #include "activation.cuh"
 #include "ff_internal.h"
+#include "pdl.h"
+#include "ptx.cuh"
 
 namespace gemm_gb300 {
 namespace ff {
@@ -119,6 +121,8 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 1024 / Cta<T, 256>::THRE
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
   if (row >= M) return;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const Columns<T, VECTOR> cols{0, N, t};
   alignas(16) TI next[VEC];
   float w[VEC], b[VEC];
@@ -199,6 +203,8 @@ __global__ void __launch_bounds__(WideNorm<TI, T>::C::THREADS, 1024 / WideNorm<T
     }
     ring.commit();
   };
+  grid_dependency_wait();
+  grid_launch_dependents();
 #pragma unroll
   for (int k = 0; k < K::STAGES; ++k) fetch(row + k * step, k);
   if (g == 0) {
@@ -368,8 +374,10 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREA
     }
     ring.commit();
   };
-  float dw[kBackPieces][VEC], db[kBackPieces][VEC];
+  F2 dw[kBackPieces][VEC / 2], db[kBackPieces][VEC / 2];
   float nmu = 0.0f, nr = 0.0f;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (row < M) {
     if (VECTOR) {
 #pragma unroll
@@ -380,20 +388,16 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREA
   if (g == 0) {
 #pragma unroll
     for (int c = 0; c < kBackPieces; ++c) {
-      columns(c).params(weight, param_dtype, 1.0f, dw[c]);
-      ws[(2 * c) * T + t] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
-      ws[(2 * c + 1) * T + t] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+      float w[VEC];
+      columns(c).params(weight, param_dtype, 1.0f, w);
+      ws[(2 * c) * T + t] = make_float4(w[0], w[1], w[2], w[3]);
+      ws[(2 * c + 1) * T + t] = make_float4(w[4], w[5], w[6], w[7]);
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int c = 0; c < kBackPieces; ++c)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) dw[c][i] = db[c][i] = 0.0f;
   for (int buf = 0, stage = 0; row < M; buf ^= 1) {
-    const float mu = nmu, r = nr;
-    float xh[kBackPieces][VEC], d[kBackPieces][VEC];
-    float s[2] = {0.0f, 0.0f};
+    const F2 mu(-nmu, -nmu), r(nr, nr);
+    F2 xh[kBackPieces][VEC / 2], d[kBackPieces][VEC / 2], s0, s1;
     if (VECTOR) ring.wait();
 #pragma unroll
     for (int c = 0; c < kBackPieces; ++c) {
@@ -411,16 +415,16 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREA
         columns(c).load(dy + row * lddy, ed);
       }
       const float4 w0 = ws[(2 * c) * T + t], w1 = ws[(2 * c + 1) * T + t];
-      const float w[VEC] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const F2 w[VEC / 2] = {F2(w0.x, w0.y), F2(w0.z, w0.w), F2(w1.x, w1.y), F2(w1.z, w1.w)};
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {  // (dy reads as 0 past the row's end)
-        xh[c][i] = (to_f32(ex[i]) - mu) * r;
-        const float e = to_f32(ed[i]);
-        dw[c][i] = fmaf(e, xh[c][i], dw[c][i]);
-        db[c][i] += e;
+      for (int i = 0; i < VEC / 2; ++i) {  // (dy reads as 0 past the row's end)
+        xh[c][i] = (F2(to_f32(ex[2 * i]), to_f32(ex[2 * i + 1])) + mu) * r;
+        const F2 e(to_f32(ed[2 * i]), to_f32(ed[2 * i + 1]));
+        dw[c][i] = fma2(e, xh[c][i], dw[c][i]);
+        db[c][i] = db[c][i] + e;
         d[c][i] = e * w[i];
-        s[0] += d[c][i];
-        s[1] = fmaf(d[c][i], xh[c][i], s[1]);
+        s0 = s0 + d[c][i];
+        s1 = fma2(d[c][i], xh[c][i], s1);
       }
     }
     if (VECTOR) {
@@ -429,45 +433,60 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREA
     }
     const int next = after(row, 1);
     if (next < M) nmu = mean[next], nr = rstd[next];
+    float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
     group_sum<T, 2>(s, red[g][buf], g);
     if (dx) {
-      const float a = mean_of(s[0], n, inv_n), b = mean_of(s[1], n, inv_n);
+      const float a = -mean_of(s[0], n, inv_n), b = -mean_of(s[1], n, inv_n);
+      const F2 a2(a, a), b2(b, b);
 #pragma unroll
       for (int c = 0; c < kBackPieces; ++c) {
+        float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) d[c][i] = r * (d[c][i] - a - xh[c][i] * b);
-        columns(c).store(dx + row * lddx, d[c]);
+        for (int i = 0; i < VEC / 2; ++i) {
+          const float2 v = (r * fma2(xh[c][i], b2, d[c][i] + a2)).get();
+          o[2 * i] = v.x, o[2 * i + 1] = v.y;
+        }
+        columns(c).store(dx + row * lddx, o);
       }
     }
     row = next;
   }
   if (!partials) return;
+  float sums[2][kBackPieces][VEC];  // of dy xh, of dy
+#pragma unroll
+  for (int c = 0; c < kBackPieces; ++c)
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      const float2 w = dw[c][i].get(), b = db[c][i].get();
+      sums[0][c][2 * i] = w.x, sums[0][c][2 * i + 1] = w.y;
+      sums[1][c][2 * i] = b.x, sums[1][c][2 * i + 1] = b.y;
+    }
   if (G > 1) {  // joined in the groups' order, over the weight's place
     float *join = reinterpret_cast<float *>(ws);
     for (int k = 0; k < G; ++k) {
       __syncthreads();
       if (g == k) {
 #pragma unroll
-        for (int c = 0; c < kBackPieces; ++c)
+        for (int which = 0; which < 2; ++which)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            float *w = join + (c * VEC + i) * T + t, *b = w + K::COLUMNS;
-            dw[c][i] = *w = k ? *w + dw[c][i] : dw[c][i];
-            db[c][i] = *b = k ? *b + db[c][i] : db[c][i];
-          }
+          for (int c = 0; c < kBackPieces; ++c)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              float *at = join + which * K::COLUMNS + (c * VEC + i) * T + t;
+              sums[which][c][i] = *at = k ? *at + sums[which][c][i] : sums[which][c][i];
+            }
       }
     }
     if (g != G - 1) return;  // the last group holds the sums
   }
   float *out = partials + static_cast<int64_t>(blockIdx.x) * 2 * N;
 #pragma unroll
-  for (int c = 0; c < kBackPieces; ++c)
+  for (int which = 0; which < 2; ++which)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      if (columns(c).in(i)) {
-        out[columns(c).at(i)] = dw[c][i];
-        out[N + columns(c).at(i)] = db[c][i];
-      }
+    for (int c = 0; c < kBackPieces; ++c)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (columns(c).in(i)) out[which * N + columns(c).at(i)] = sums[which][c][i];
 }
 
 // Longer rows, and a dy of another type than x: the rows' means first, then columns.
@@ -587,9 +606,8 @@ void launch_rows(const NormArgs &a) {
   using C = Cta<T, 256>;
   const int grid = grid_of((a.M + C::GROUPS - 1) / C::GROUPS, a.sm_count, 1024 / C::THREADS);
   auto kernel = a.vec ? norm_rows_kernel<TI, T, true> : norm_rows_kernel<TI, T, false>;
-  kernel<<<grid, C::THREADS, 0, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight, a.bias,
-                                       a.param_dtype, a.y, a.ldy, a.out_dtype, a.mean, a.rstd,
-                                       a.eps, a.M, a.N);
+  launch_pdl(kernel, dim3(grid), C::THREADS, 0, a.s, static_cast<const TI *>(a.x), a.ldx, a.weight,
+             a.bias, a.param_dtype, a.y, a.ldy, a.out_dtype, a.mean, a.rstd, a.eps, a.M, a.N);
 }
 
 template <typename TI, int T>
@@ -598,9 +616,8 @@ void launch_wide_rows(const NormArgs &a) {
   const int grid = grid_of((a.M + K::C::GROUPS - 1) / K::C::GROUPS, a.sm_count, K::PER_SM);
   auto kernel = norm_wide_rows_kernel<TI, T>;
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
-  kernel<<<grid, K::C::THREADS, K::SMEM, a.s>>>(static_cast<const TI *>(a.x), a.ldx, a.weight,
-                                                a.bias, a.param_dtype, a.y, a.ldy, a.out_dtype,
-                                                a.mean, a.rstd, a.eps, a.M, a.N);
+  launch_pdl(kernel, dim3(grid), K::C::THREADS, K::SMEM, a.s, static_cast<const TI *>(a.x), a.ldx,
+             a.weight, a.bias, a.param_dtype, a.y, a.ldy, a.out_dtype, a.mean, a.rstd, a.eps, a.M, a.N);
 }
 
 // Threads that hold a row of N columns, `each` a thread: 32 .. 1024.
@@ -681,10 +698,9 @@ void launch_backward(const NormBackwardArgs &a) {
   using K = NormBackward<TI, T, VECTOR>;
   auto kernel = norm_backward_kernel<TI, T, VECTOR>;
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
-  kernel<<<a.grid, K::C::THREADS, K::SMEM, a.s>>>(
-      static_cast<const TI *>(a.dy), a.lddy, static_cast<const TI *>(a.x), a.ldx, a.weight,
-      a.param_dtype, a.mean, a.rstd, static_cast<TI *>(a.dx), a.lddx, a.partials,
-      static_cast<int32_t>(a.M), a.N);
+  launch_pdl(kernel, dim3(a.grid), K::C::THREADS, K::SMEM, a.s, static_cast<const TI *>(a.dy),
+             a.lddy, static_cast<const TI *>(a.x), a.ldx, a.weight, a.param_dtype, a.mean, a.rstd,
+             static_cast<TI *>(a.dx), a.lddx, a.partials, static_cast<int32_t>(a.M), a.N);
 }
 template <typename TI, int T>
 void launch_backward(const NormBackwardArgs &a) {

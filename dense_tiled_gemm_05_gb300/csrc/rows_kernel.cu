@@ -12,6 +12,8 @@
 // the bands in a second kernel, always in the same order.
 #include "activation.cuh"
 #include "ff_internal.h"
+#include "pdl.h"
+#include "ptx.cuh"
 
 namespace gemm_gb300 {
 namespace ff {
@@ -52,6 +54,8 @@ template <typename TO, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     epilogue_rows_kernel(const float *z, int64_t ldz, TO *y, int64_t ldy, const Epilogue ep,
                          int64_t M, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const auto cols = my_columns<VECTOR>(N);
   if (!cols.in(0)) return;
   float b[VEC];
@@ -79,6 +83,8 @@ template <typename TO, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     gated_rows_kernel(const float *__restrict__ g, int64_t ldg, const float *__restrict__ u,
                       int64_t ldu, TO *__restrict__ h, int64_t ldh, int act, int64_t M, int64_t F) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const auto cols = my_columns<VECTOR>(F);
   if (!cols.in(0)) return;
 #pragma unroll 2
@@ -99,6 +105,8 @@ __global__ void __launch_bounds__(kThreads)
                         int64_t ldg, const T *__restrict__ u, int64_t ldu, T *__restrict__ dg,
                         int64_t lddg, T *__restrict__ du, int64_t lddu, int act, int64_t M,
                         int64_t F) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const auto cols = my_columns<VECTOR>(F);
   if (!cols.in(0)) return;
 #pragma unroll 2
@@ -123,6 +131,8 @@ template <typename TO, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     add_rows_kernel(const float *a, int64_t lda, const float *__restrict__ b, int64_t ldb, TO *y,
                     int64_t ldy, int64_t M, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const auto cols = my_columns<VECTOR>(N);
   if (!cols.in(0)) return;
 #pragma unroll 2
@@ -144,6 +154,8 @@ __global__ void __launch_bounds__(kThreads)
                            float *__restrict__ partials, int64_t M, int64_t N, int64_t band) {
   __shared__ float red[kWarps][kCols];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const auto cols = my_columns<VECTOR>(N);
   const int64_t lo = static_cast<int64_t>(blockIdx.y) * band;
   const int64_t hi = lo + band < M ? lo + band : M;
@@ -188,6 +200,8 @@ __global__ void __launch_bounds__(1024)
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const int which = blockIdx.y;
+  grid_dependency_wait();
+  grid_launch_dependents();
   float s = 0.0f;
   if (j < N) {
 #pragma unroll 8
@@ -224,9 +238,9 @@ cudaError_t epilogue_rows_launch(const float *z, int64_t ldz, void *y, int64_t l
   const dim3 grid = rows_grid(M, N);
   FF_TYPED(out_dtype, T, {
     if (vec)
-      epilogue_rows_kernel<T, true><<<grid, kThreads, 0, s>>>(z, ldz, static_cast<T *>(y), ldy, ep, M, N);
+      launch_pdl(epilogue_rows_kernel<T, true>, grid, kThreads, 0, s, z, ldz, static_cast<T *>(y), ldy, ep, M, N);
     else
-      epilogue_rows_kernel<T, false><<<grid, kThreads, 0, s>>>(z, ldz, static_cast<T *>(y), ldy, ep, M, N);
+      launch_pdl(epilogue_rows_kernel<T, false>, grid, kThreads, 0, s, z, ldz, static_cast<T *>(y), ldy, ep, M, N);
   })
   return cudaGetLastError();
 }
@@ -238,9 +252,9 @@ cudaError_t gated_rows_launch(const float *g, int64_t ldg, const float *u, int64
   const dim3 grid = rows_grid(M, F);
   FF_TYPED(out_dtype, T, {
     if (vec)
-      gated_rows_kernel<T, true><<<grid, kThreads, 0, s>>>(g, ldg, u, ldu, static_cast<T *>(h), ldh, act, M, F);
+      launch_pdl(gated_rows_kernel<T, true>, grid, kThreads, 0, s, g, ldg, u, ldu, static_cast<T *>(h), ldh, act, M, F);
     else
-      gated_rows_kernel<T, false><<<grid, kThreads, 0, s>>>(g, ldg, u, ldu, static_cast<T *>(h), ldh, act, M, F);
+      launch_pdl(gated_rows_kernel<T, false>, grid, kThreads, 0, s, g, ldg, u, ldu, static_cast<T *>(h), ldh, act, M, F);
   })
   return cudaGetLastError();
 }
@@ -255,7 +269,7 @@ cudaError_t gated_slopes_launch(const void *dh, int64_t lddh, const void *g, int
   const dim3 grid = rows_grid(M, F);
   FF_TYPED(dtype, T, {
     auto kernel = vec ? gated_slopes_kernel<T, true> : gated_slopes_kernel<T, false>;
-    kernel<<<grid, kThreads, 0, s>>>(static_cast<const T *>(dh), lddh, static_cast<const T *>(g), ldg,
+    launch_pdl(kernel, grid, kThreads, 0, s, static_cast<const T *>(dh), lddh, static_cast<const T *>(g), ldg,
                                      static_cast<const T *>(u), ldu, static_cast<T *>(dg), lddg,
                                      static_cast<T *>(du), lddu, act, M, F);
   })
@@ -268,9 +282,9 @@ cudaError_t add_rows_launch(const float *a, int64_t lda, const float *b, int64_t
   const dim3 grid = rows_grid(M, N);
   FF_TYPED(out_dtype, T, {
     if (vec)
-      add_rows_kernel<T, true><<<grid, kThreads, 0, s>>>(a, lda, b, ldb, static_cast<T *>(y), ldy, M, N);
+      launch_pdl(add_rows_kernel<T, true>, grid, kThreads, 0, s, a, lda, b, ldb, static_cast<T *>(y), ldy, M, N);
     else
-      add_rows_kernel<T, false><<<grid, kThreads, 0, s>>>(a, lda, b, ldb, static_cast<T *>(y), ldy, M, N);
+      launch_pdl(add_rows_kernel<T, false>, grid, kThreads, 0, s, a, lda, b, ldb, static_cast<T *>(y), ldy, M, N);
   })
   return cudaGetLastError();
 }
@@ -278,7 +292,7 @@ cudaError_t add_rows_launch(const float *a, int64_t lda, const float *b, int64_t
 cudaError_t column_finish_launch(const float *partials, int64_t bands, int sums, void *out0,
                                  void *out1, int dtype, int64_t N, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>(out1 ? 2 : 1));
-  column_finish_kernel<<<grid, 1024, 0, s>>>(partials, bands, sums, out0, out1, dtype, N);
+  launch_pdl(column_finish_kernel, grid, 1024, 0, s, partials, bands, sums, out0, out1, dtype, N);
   return cudaGetLastError();
 }
 
@@ -296,7 +310,7 @@ cudaError_t epilogue_slopes_launch(const void *dy, int64_t lddy, const void *pre
   FF_TYPED(grad_dtype, TG, {
     FF_TYPED(dz_dtype, TZ, {
       auto kernel = vec ? epilogue_slopes_kernel<TG, TZ, true> : epilogue_slopes_kernel<TG, TZ, false>;
-      kernel<<<grid, kThreads, 0, s>>>(static_cast<const TG *>(dy), lddy, static_cast<const TG *>(pre),
+      launch_pdl(kernel, grid, kThreads, 0, s, static_cast<const TG *>(dy), lddy, static_cast<const TG *>(pre),
                                        ld_pre, act, static_cast<TZ *>(dz), lddz, part, M, N, band);
     })
   })
