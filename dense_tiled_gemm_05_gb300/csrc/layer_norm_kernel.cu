@@ -38,34 +38,42 @@ __device__ __forceinline__ void group_sync(int g) {
   asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(T) : "memory");
 }
 
-// Sums of one or two values over the T threads of a group; every thread gets them. `red`: K
-// times T / 32 floats of the group's own; consecutive calls alternate between two such
-// arrays, so that one barrier a call is enough (a thread writes an array again only after the
-// barrier of the call in between).
-template <int T, int K>
-__device__ __forceinline__ void group_sum(float (&v)[K], float *red, int g) {
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if (T == 32) return;
-  constexpr int WARPS = T / 32;
-  const int lane = threadIdx.x % 32;
-  if (lane == 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) red[k * WARPS + (threadIdx.x % T) / 32] = v[k];
-  }
-  group_sync<T>(g);
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    v[k] = red[k * WARPS + lane % WARPS];
-#pragma unroll
-    for (int o = WARPS / 2; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  }
-}
+// Sum of a value over the T threads of a group; every thread gets it. `red`: T / 32 floats of
+// the group's own; consecutive calls alternate between two such arrays, so that one barrier a
+// call is enough (a thread writes an array again only after the barrier of the call in between).
 template <int T>
 __device__ __forceinline__ float group_sum(float v, float *red, int g) {
-  float a[1] = {v};
-  group_sum<T, 1>(a, red, g);
-  return a[0];
+  v = warp_sum(v);
+  if (T == 32) return v;
+  constexpr int WARPS = T / 32;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) red[(threadIdx.x % T) / 32] = v;
+  group_sync<T>(g);
+  v = red[lane % WARPS];
+#pragma unroll
+  for (int o = WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Two sums at once (T at most 512; `red`: twice as many floats): the lower half of a warp
+// carries the first value's sum and the upper half the second's, in half the shuffles.
+template <int T>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float *red, int g) {
+  static_assert(T <= 512, "a half warp holds the warps' sums");
+  constexpr int WARPS = T / 32;
+  const int lane = threadIdx.x % 32;
+  const bool low = lane < 16;
+  float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (T > 32) {
+    if (lane % 16 == 0) red[(low ? 0 : WARPS) + (threadIdx.x % T) / 32] = v;
+    group_sync<T>(g);
+    v = red[(low ? 0 : WARPS) + lane % WARPS];
+#pragma unroll
+    for (int o = WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
+  return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
 }
 
 // Threads of a CTA: one group of T threads, or as many as make up `AT_LEAST`.
@@ -327,6 +335,13 @@ __global__ void __launch_bounds__(512)
 // two pieces, x and dy read once (the next rows on their way in the ring where rows are 16-byte
 // aligned), dx written, and the columns' sums of dy xh and dy kept in registers over all of the
 // group's rows. The groups of a CTA join theirs at the end; column_finish adds the CTAs.
+//
+// 16384 x 4096 bf16 on one GB300, with the finish: 82 us, 4.9 TB/s. Sixteen warps an SM
+// (118 registers) leave it waiting for its own row-long chain of loads, sums and barrier (0.47
+// instructions issued a cycle and scheduler). Measured and not kept, each with the finish: a
+// third ring stage (the same), eight columns a thread with the next row in registers (92 us;
+// with the ring it spilled at 64 registers, 100 us), and dx a row behind the sums with both
+// recomputed from the ring, three CTAs an SM (99 us).
 constexpr int kBackPieces = 2;
 template <typename TI, int T, bool VECTOR>
 struct NormBackward {
@@ -358,7 +373,10 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREA
   const int step = static_cast<int>(gridDim.x) * G;
   int row = static_cast<int>(blockIdx.x) * G + g;
   auto columns = [&](int c) { return Columns<T, VECTOR>{static_cast<int64_t>(c) * T * VEC, N, t}; };
-  auto after = [&](int i, int k) { return (M - 1 - i) / step >= k ? i + k * step : M; };
+  auto after = [&](int i, int k) {  // the group's k-th row from row i on, or M
+    const int64_t v = i + static_cast<int64_t>(k) * step;
+    return v < M ? static_cast<int>(v) : M;
+  };
   auto fetch = [&](int i, int stage) {
     if (i < M) {
 #pragma unroll
@@ -433,10 +451,9 @@ __global__ void __launch_bounds__(Cta<T, 256>::THREADS, 512 / Cta<T, 256>::THREA
     }
     const int next = after(row, 1);
     if (next < M) nmu = mean[next], nr = rstd[next];
-    float s[2] = {s0.get().x + s0.get().y, s1.get().x + s1.get().y};
-    group_sum<T, 2>(s, red[g][buf], g);
+    const float2 s = group_sum2<T>(s0.get().x + s0.get().y, s1.get().x + s1.get().y, red[g][buf], g);
     if (dx) {
-      const float a = -mean_of(s[0], n, inv_n), b = -mean_of(s[1], n, inv_n);
+      const float a = -mean_of(s.x, n, inv_n), b = -mean_of(s.y, n, inv_n);
       const F2 a2(a, a), b2(b, b);
 #pragma unroll
       for (int c = 0; c < kBackPieces; ++c) {
