@@ -320,10 +320,13 @@ typedef struct {
  * backward pass reads it). Products, layouts, precision modes and checks are gemm_run_ex's;
  * z, act(z) and the sum are fp32 and rounded once each where they are stored. C may be the
  * residual itself (same address and leading dimension). `epilogue` NULL or empty is the
- * product alone. 16-bit inputs run in one kernel: with few rows the outputs' features are the
- * rows of the tensor-core tile and K is split over a cluster; with many, 256 x 256 tiles on
- * CTA pairs (GEMM_OPT_CTA_PAIR 1 and 2 choose the one or the other, GEMM_OPT_STREAM_K the
- * split of the pairs' last rounds, GEMM_OPT_FORCE_PATH 2 neither). fp32 inputs run the product of their precision mode and then a kernel for what follows it.
+ * product alone. 16-bit inputs run in one kernel: up to eight rows against K-contiguous weights
+ * on plain multiply-adds, where that is estimated to be quicker; few rows with the outputs'
+ * features as the rows of the tensor-core tile and K split over a cluster; many in 256 x 256
+ * tiles on CTA pairs (GEMM_OPT_CTA_PAIR 1 and 2 choose the second or the third, GEMM_OPT_STREAM_K
+ * the split of the pairs' last rounds, GEMM_OPT_FORCE_PATH 2 none of them). fp32 inputs run in
+ * one kernel too for up to eight rows and for small exact products, otherwise the product of
+ * their precision mode and then a kernel for what follows it.
  * Errors: those of gemm_run_ex; INVALID_ARG for an unknown activation or bias type, a leading
  * dimension below N, or overlapping buffers; ALIGNMENT for a bias, residual or pre pointer
  * that is not aligned to its element size. */

@@ -131,6 +131,33 @@ def test_bounded_waits_expire_and_the_next_call_is_right(g, cta_pair, stall):
     h.close()
 
 
+@pytest.mark.parametrize("stall", [1, 2, 3, 6, 7])
+@pytest.mark.parametrize("cta_pair", [1, 2])
+def test_bounded_waits_with_few_fills(g, cta_pair, stall):
+    """16 K-blocks: a CTA pair's loader has all of them to fill, so each stall is reached. The
+    few-row kernel may share them over eight CTAs, two fills each: a loader that would stop after
+    three (stalls 6 and 7) then has nothing left to hold back, and the call has to be right."""
+    h = g.Gemm(0)
+    h.set_option("cta_pair", cta_pair)
+    a, b = operands(300, 520, 1024, "bf16", 3)
+    r = matrix(300, 520, torch.bfloat16, 6)
+    want = h.matmul_epilogue(a, b, residual=r), h.gated(a, b, b)
+    assert h.status() == 0
+    reached = cta_pair == 2 or stall < 6
+    h.set_option("wait_timeout_us", 20000)
+    h.set_option("fault_stall_producer", stall)
+    for call, w in ((lambda: h.matmul_epilogue(a, b, residual=r), want[0]),
+                    (lambda: h.gated(a, b, b), want[1])):
+        got = call()
+        status = h.status()
+        assert status == 6 or (not reached and status == 0 and torch.equal(got, w))
+    h.set_option("fault_stall_producer", 0)
+    check_epilogue(h, a, b, None, None, r, save=False)
+    check_gated(h, a, b, b, "silu", save=True)
+    assert h.status() == 0
+    h.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (8, 8), (3, 1)])
 @pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
