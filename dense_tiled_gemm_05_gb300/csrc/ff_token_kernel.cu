@@ -136,12 +136,12 @@ __global__ void __launch_bounds__(kThreads)
       store_any(p.f.pre, p.f.out_dtype, m * p.f.ld_pre + n, sum[0]);
       store_any(p.f.pre2, p.f.out_dtype, m * p.f.ld_pre2 + n, sum[S - 1]);
     }
-    y = activate<FAST>(sum[0], p.f.act) * sum[S - 1];
+    y = activate_one<FAST>(sum[0], p.f.act) * sum[S - 1];
   } else {
     float z = sum[0];
     if (p.f.bias) z += load_any(p.f.bias, p.f.bias_dtype, n);
     if (p.f.pre) store_any(p.f.pre, p.f.out_dtype, m * p.f.ld_pre + n, z);
-    y = activate<FAST>(z, p.f.act);
+    y = activate_one<FAST>(z, p.f.act);
     if (p.f.residual) y += load_any(p.f.residual, p.f.out_dtype, m * p.f.ld_residual + n);
   }
   store_any(p.f.C, p.f.out_dtype, m * p.f.ldc + n, y);
