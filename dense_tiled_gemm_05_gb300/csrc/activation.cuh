@@ -168,6 +168,10 @@ struct Columns {
   }
 };
 
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Two fp32 values in one register pair: Blackwell's packed add, multiply and multiply-add round
 // each half as the scalar instruction does and take one issue slot for both.
 struct F2 {
@@ -273,7 +277,7 @@ __device__ __forceinline__ void activate_slope(float z, int act, float &a, float
 // flushed (a few fp32 ulps, against the 2^-9 of the inputs' rounding; both saturate to exactly
 // 0 and 1). It is for the slopes kernels, which have six bytes of HBM traffic an element to hide
 // the arithmetic under: bias gradient alone, 4096 x 4096 bf16 on one GB300, against unpacked
-// calls of the full-range functions: gelu 20 us (32), its tanh form 16 (22), silu 15 (19). The
+// __expf, __fdividef and erff: gelu 20 us (32), its tanh form 16 (22), silu 15 (19). The
 // products' epilogues run it too, at the same speed as before.
 __device__ __forceinline__ F2 exp2_fast(F2 x) {
   float2 f = x.get();

@@ -57,12 +57,31 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int kw = p.k_warps, groups = kWarps / kw;
   const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * groups + warp / kw) * R;
-  grid_dependency_wait();
-  grid_launch_dependents();
   const T *x = static_cast<const T *>(p.X);
   const T *w[S] = {static_cast<const T *>(p.W)};
   int64_t ldw[S] = {p.ldw};
   if (GATED) w[S - 1] = static_cast<const T *>(p.W2), ldw[S - 1] = p.ldw2;
+  using L = Lane<T, VECTOR>;
+  const int64_t steps = (p.K + L::STEP - 1) / L::STEP;
+  // The weights' first lines are asked into L2 while the previous kernel ends. They are read
+  // after the wait, from L2, so that weights which that kernel writes are seen as written.
+  // (1 x 4096 x 4096 bf16, calls one after another: 9.5 us without, 9.2 with; 8192^2: no change.)
+  if (lane % 8 == 0) {
+#pragma unroll
+    for (int u = 0; u < 2 * U; ++u) {
+      const int64_t k = (warp % kw + static_cast<int64_t>(u) * kw) * L::STEP + lane * L::E;
+      if (k >= p.K) break;
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int64_t n = n0 + r < p.f.N ? n0 + r : p.f.N - 1;
+          prefetch_l2(w[s] + n * ldw[s] + k);
+        }
+    }
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
   float acc[S][R][MT];
 #pragma unroll
   for (int s = 0; s < S; ++s)
@@ -70,9 +89,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[s][r][m] = 0.0f;
-  using L = Lane<T, VECTOR>;
   // Rows past the last feature or token read the last one again; their sums are not stored.
-  const int64_t steps = (p.K + L::STEP - 1) / L::STEP;
   for (int64_t i0 = warp % kw; i0 < steps; i0 += static_cast<int64_t>(kw) * U) {
     L wv[U][S][R];
 #pragma unroll

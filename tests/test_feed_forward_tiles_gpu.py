@@ -200,3 +200,29 @@ def test_fp32_tile_kernel(g, M, N, K, x_layout, w_layout):
         check_gated_backward(h, dy, a, b, wu, pre, matrix(M, N, t, 11), "silu")
     assert h.status() == 0
     h.close()
+
+
+@pytest.mark.parametrize("M", [1, 4, 64])
+def test_weights_written_by_the_call_before(g, M):
+    """Weights that the previous kernel on the stream writes, with no host wait in between: a
+    product that starts under that kernel's end has to read them as written, bit for bit."""
+    h = g.Gemm(0)
+    x = matrix(M, 1024, torch.bfloat16, 3)
+    w, w2 = (torch.zeros(2048, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    up = [matrix(2048, 64, torch.bfloat16, 10 + i) for i in range(4)]
+    across = matrix(64, 1024, torch.bfloat16, 9)
+    got = []
+    for i in range(12):
+        h.matmul_epilogue(up[(i + 1) % 4], across, out=w2)
+        h.matmul_epilogue(up[i % 4], across, out=w)
+        got.append((h.matmul_epilogue(x, w.t()), h.gated(x, w2.t(), w.t())))
+    torch.cuda.synchronize()
+    for i in range(4):
+        wi = h.matmul_epilogue(up[i], across)
+        wj = h.matmul_epilogue(up[(i + 1) % 4], across)
+        torch.cuda.synchronize()
+        y, z = h.matmul_epilogue(x, wi.t()), h.gated(x, wj.t(), wi.t())
+        for k in range(i, 12, 4):
+            assert torch.equal(got[k][0], y) and torch.equal(got[k][1], z)
+    assert h.status() == 0
+    h.close()
