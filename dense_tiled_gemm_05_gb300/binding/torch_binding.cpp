@@ -187,10 +187,15 @@ const void *vector(const Tensor &t, int64_t n, const char *what, int dev) {
 Tensor empty(const Tensor &like, at::IntArrayRef sizes, at::ScalarType t) {
   return at::empty(sizes, like.options().dtype(t));
 }
-// An empty tensor of t's shape in t's layout, tight.
-Tensor empty_like_layout(const Tensor &t) {
-  if (Layout(t).layout == GEMM_ROW_MAJOR) return empty(t, {t.size(0), t.size(1)}, t.scalar_type());
+int64_t least1(int64_t v) { return v > 0 ? v : 1; }
+// An empty tensor of t's shape, tight in the layout t was read in, and its leading dimension. (The
+// layout cannot be read back from the new tensor: a matrix of one row or column has both.)
+Tensor empty_like_layout(const Tensor &t, gemm_layout_t layout) {
+  if (layout == GEMM_ROW_MAJOR) return empty(t, {t.size(0), t.size(1)}, t.scalar_type());
   return empty(t, {t.size(1), t.size(0)}, t.scalar_type()).t();
+}
+int64_t tight_ld(gemm_layout_t layout, int64_t rows, int64_t cols) {
+  return least1(layout == GEMM_ROW_MAJOR ? cols : rows);
 }
 
 struct Product {
@@ -210,7 +215,6 @@ struct Product {
 };
 
 void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
-int64_t least1(int64_t v) { return v > 0 ? v : 1; }
 
 PyObject *wrap(const Tensor &t) {
   if (!t.defined()) Py_RETURN_NONE;
@@ -320,13 +324,13 @@ PyObject *matmul_epilogue_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
   const Layout la(a), lb(b);
   void *stream = stream_arg(v[9], p.dev);
   Tensor da, db, dbias;
-  if (need.v[0]) da = empty_like_layout(a);
-  if (need.v[1]) db = empty_like_layout(b);
+  if (need.v[0]) da = empty_like_layout(a, la.layout);
+  if (need.v[1]) db = empty_like_layout(b, lb.layout);
   if (need.v[2]) dbias = empty(a, {p.N}, bd);
   check(run_epilogue_backward(
             handle_arg(v[0]), p.M, p.N, p.K, grad.data_ptr(), lddy, ptr(pre), ldz, a.data_ptr(),
-            la.ld, b.data_ptr(), lb.ld, ptr(da), need.v[0] ? Layout(da).ld : 0, ptr(db),
-            need.v[1] ? Layout(db).ld : 0, ptr(dbias), static_cast<gemm_dtype_t>(code_of(bd)),
+            la.ld, b.data_ptr(), lb.ld, ptr(da), tight_ld(la.layout, p.M, p.K), ptr(db),
+            tight_ld(lb.layout, p.K, p.N), ptr(dbias), static_cast<gemm_dtype_t>(code_of(bd)),
             static_cast<gemm_dtype_t>(code_of(a)), static_cast<gemm_dtype_t>(code_of(grad)), prec,
             la.layout, lb.layout, act, stream),
         "gemm_run_epilogue_backward");
@@ -405,10 +409,10 @@ PyObject *gated_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
     dwg = both.narrow(0, 0, p.N).t();
     dwu = both.narrow(0, p.N, p.N).t();
   } else {
-    if (need.v[1]) dwg = empty_like_layout(wg);
-    if (need.v[2]) dwu = empty_like_layout(wu);
+    if (need.v[1]) dwg = empty_like_layout(wg, q.g.layout);
+    if (need.v[2]) dwu = empty_like_layout(wu, q.u.layout);
   }
-  const int64_t ldw = least1(q.g.layout == GEMM_COL_MAJOR ? p.K : p.N);
+  const int64_t ldw = tight_ld(q.g.layout, p.K, p.N);
   check(run_gated_backward(handle_arg(v[0]), p.M, p.N, p.K, grad.data_ptr(), ldh, gate.data_ptr(),
                            ldg, up.data_ptr(), ldu, x.data_ptr(), q.ldx, wg.data_ptr(), q.g.ld,
                            wu.data_ptr(), q.u.ld, ptr(dx), least1(p.K), ptr(dwg), ldw, ptr(dwu), ldw,
