@@ -80,12 +80,14 @@ struct TileParams {
   int32_t x_k, w_k;
   int64_t K;
   int32_t splits;       // CTAs (one cluster) that share a tile's K: 1, 2, 4 or 8
+  int32_t run_steps;    // K-steps an accumulator adds up before its sum moves on (tile_run_steps)
   int32_t vec;          // as FewParams
 };
 constexpr int kTileK = 16;  // K elements per step
 // Rows and columns of a tile (gated: columns of each product) for a size of 64 or 128.
 inline int tile_rows(int size) { return size; }
 inline int tile_cols(bool gated, int size) { return gated ? size / 2 : size; }
+int tile_run_steps(int64_t K);
 cudaError_t tile_launch(bool gated, int size, const TileParams &p, cudaStream_t s);
 
 // Many-token kernel: CTA pairs, 256 x 256 accumulators (gated: 128 columns of each product).

@@ -262,6 +262,7 @@ gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaS
     p.W2 = static_cast<const float *>(q.W2.ptr), p.ldw2 = q.W2.ld;
     p.K = q.K;
     p.splits = q.tile_splits;
+    p.run_steps = tile_run_steps(q.K);
     p.vec = four_wide(q);
     e = tile_launch(q.gated, q.tile_size, p, s);
     if (e != cudaSuccess) return cuda_fail(e, "fp32 tile kernel launch");

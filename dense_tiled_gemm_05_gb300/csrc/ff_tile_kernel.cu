@@ -13,13 +13,18 @@
 // Issue slots bound it (0.71 of them used, the multiply-add pipe at 0.52, before multiply-adds
 // went two to an instruction): 42 TFLOP/s on 3000 x 1000 x 2000 (one GB300), cuBLAS 51.
 // Where tiles are few, a cluster's CTAs share each tile's K and join as in ff_join.cuh.
+//
+// A share of K is added up in runs (tile_run_steps), whose sums are added in shared memory: a sum
+// of n terms of one sign in a row loses about sqrt(n) roundings of its own size (n = 8192 in each
+// of eight shares: 2e-6 of sum |x w|, twice the bound of exact products; in runs 3e-7), at 1 to
+// 4 % of the time of long products.
+#include <cmath>
+
 #include "ff_join.cuh"
 
 namespace gemm_gb300 {
 namespace ff {
 namespace {
-
-constexpr int kStages = 3;
 
 // One thread's share of the loads of a ROWS x 16 operand tile into smem[k][row], zero outside
 // the operand. k_inner: element (r, k) is at p[r * ld + k], and the threads of a tile's row
@@ -76,18 +81,23 @@ struct Loader {
 };
 static_assert(kTileK == 16, "the K of two warps");
 
-template <int BM_, int BN_, int TM_, int TN_, bool GATED>
+// RUNS: shares of K of several runs.
+template <int BM_, int BN_, int TM_, int TN_, bool GATED, bool RUNS_>
 struct Tile {
   static constexpr int S = GATED ? 2 : 1;
+  static constexpr bool RUNS = RUNS_;
+  // (the sums of a 128 x 128 tile leave room for two stages where two CTAs share an SM)
+  static constexpr int STAGES = RUNS && BM_ == 128 ? 2 : 3;
   static constexpr int BM = BM_, BN = BN_, TM = TM_, TN = TN_;
   static constexpr int TX = BN / TN, TY = BM / TM, THREADS = TX * TY;
   struct Stage {
     float x[kTileK][BM + 4];
     float w[S][kTileK][BN + 4];
   };
-  static constexpr int RING = kStages * static_cast<int>(sizeof(Stage));
+  static constexpr int RING = STAGES * static_cast<int>(sizeof(Stage));
   static constexpr int PART = S * BM * BN * 4;
-  static constexpr int SMEM = RING > PART ? RING : PART;
+  // the partial lies over the ring, or behind it where runs are added up there
+  static constexpr int SMEM = RUNS ? RING + PART : RING > PART ? RING : PART;
   static_assert(BM * kTileK % THREADS == 0 && BN * kTileK % THREADS == 0 && THREADS % BM == 0 &&
                     THREADS % BN == 0 && TM % 4 == 0 && TN % 4 == 0,
                 "whole shares");
@@ -102,6 +112,7 @@ template <typename T, bool GATED>
 __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
     tile_kernel(const TileParams p) {
   constexpr int S = T::S, BM = T::BM, BN = T::BN, TM = T::TM, TN = T::TN, THREADS = T::THREADS;
+  constexpr int STAGES = T::STAGES;
   extern __shared__ __align__(16) uint8_t dyn[];
   typename T::Stage *ring = reinterpret_cast<typename T::Stage *>(dyn);
   const int rank = static_cast<int>(blockIdx.x) % p.splits;
@@ -121,7 +132,7 @@ __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
   grid_launch_dependents();
   auto fetch = [&](int step) {
     if (step < n_steps) {
-      typename T::Stage &g = ring[step % kStages];
+      typename T::Stage &g = ring[step % STAGES];
       const int64_t left = p.K - k0 - int64_t{step} * kTileK;
       lx.load(&g.x[0][0], left);
       lw.load(&g.w[0][0][0], left);
@@ -130,12 +141,43 @@ __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   F2 acc[S][TM / 2][TN];  // pairs of rows: two multiply-adds an instruction
-  for (int k = 0; k < kStages - 1; ++k) fetch(k);
+  // The partial, [row][column], over the drained ring or (RUNS) behind it: the accumulators
+  // replace it or, after the first run, are added to it. A thread's elements are its own.
+  float *part = reinterpret_cast<float *>(dyn + (T::RUNS ? T::RING : 0));
+  bool begun = false;
+  int run_left = p.run_steps;
+  auto to_partial = [&] {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < TM; i += 2) {
+        const int r = i / 4 * 4 * T::TY + ty * 4 + i % 4;
+#pragma unroll
+        for (int j = 0; j < TN; j += 4) {
+          float2 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = acc[s][i / 2][j + c].get();
+          float *d = part + s * BM * BN + r * BN + j * T::TX + tx * 4;
+          float4 lo = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+          float4 hi = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+          if (T::RUNS && begun) {
+            const float4 a = *reinterpret_cast<const float4 *>(d);
+            const float4 b = *reinterpret_cast<const float4 *>(d + BN);
+            lo.x += a.x, lo.y += a.y, lo.z += a.z, lo.w += a.w;
+            hi.x += b.x, hi.y += b.y, hi.z += b.z, hi.w += b.w;
+          }
+          *reinterpret_cast<float4 *>(d) = lo;
+          *reinterpret_cast<float4 *>(d + BN) = hi;
+        }
+      }
+    begun = true;
+  };
+  for (int k = 0; k < STAGES - 1; ++k) fetch(k);
   for (int step = 0; step < n_steps; ++step) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     __syncthreads();  // the step's tiles are there; everyone is done with the stage refilled next
-    fetch(step + kStages - 1);
-    const typename T::Stage &g = ring[step % kStages];
+    fetch(step + STAGES - 1);
+    const typename T::Stage &g = ring[step % STAGES];
 #pragma unroll
     for (int k = 0; k < kTileK; ++k) {
       float a[TM];
@@ -155,27 +197,20 @@ __global__ void __launch_bounds__(T::THREADS, 512 / T::THREADS)
         }
       }
     }
+    if (T::RUNS && --run_left == 0 && step + 1 < n_steps) {
+      run_left = p.run_steps;
+      to_partial();
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < TM / 2; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[s][i][j] = F2();
+    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // the ring is free
-  // The partial, [row][column]; also of a tile computed alone, so that the stores that follow
-  // are whole rows.
-  float *part = reinterpret_cast<float *>(dyn);
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int i = 0; i < TM; i += 2) {
-      const int r = i / 4 * 4 * T::TY + ty * 4 + i % 4;
-#pragma unroll
-      for (int j = 0; j < TN; j += 4) {
-        float2 v[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = acc[s][i / 2][j + c].get();
-        float *d = part + s * BM * BN + r * BN + j * T::TX + tx * 4;
-        *reinterpret_cast<float4 *>(d) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
-        *reinterpret_cast<float4 *>(d + BN) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
-      }
-    }
+  to_partial();  // also of a tile computed alone, so that the stores that follow are whole rows
   if (p.splits > 1)
     cluster_sync();
   else
@@ -209,16 +244,29 @@ cudaError_t launch_tile(const TileParams &p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <bool GATED, bool RUNS>
+cudaError_t dispatch(int size, const TileParams &p, cudaStream_t s) {
+  if (size == 128) return launch_tile<Tile<128, GATED ? 64 : 128, 8, GATED ? 4 : 8, GATED, RUNS>, GATED>(p, s);
+  if (size == 64) return launch_tile<Tile<64, GATED ? 32 : 64, GATED ? 4 : 8, 4, GATED, RUNS>, GATED>(p, s);
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace
 
+// Steps an accumulator adds up in a row: at least 128 products, or 8 sqrt(K). The K / r runs of
+// r products are summed in order, and their errors, of some sqrt(r) roundings of a run's sum,
+// average out to r / sqrt(K) roundings of the whole: 8 of 2^-24, 5e-7.
+int tile_run_steps(int64_t K) {
+  const double r = 8.0 * std::sqrt(static_cast<double>(K));
+  return static_cast<int>(r < 128.0 ? 128.0 : r) / kTileK;
+}
+
 cudaError_t tile_launch(bool gated, int size, const TileParams &p, cudaStream_t s) {
-  if (size == 128)
-    return gated ? launch_tile<Tile<128, 64, 8, 4, true>, true>(p, s)
-                 : launch_tile<Tile<128, 128, 8, 8, false>, false>(p, s);
-  if (size == 64)
-    return gated ? launch_tile<Tile<64, 32, 4, 4, true>, true>(p, s)
-                 : launch_tile<Tile<64, 64, 8, 4, false>, false>(p, s);
-  return cudaErrorInvalidValue;
+  const int64_t steps = (p.K + kTileK - 1) / kTileK;
+  const bool runs = (steps + p.splits - 1) / p.splits > p.run_steps;
+  if (p.run_steps < 1) return cudaErrorInvalidValue;
+  if (gated) return runs ? dispatch<true, true>(size, p, s) : dispatch<true, false>(size, p, s);
+  return runs ? dispatch<false, true>(size, p, s) : dispatch<false, false>(size, p, s);
 }
 
 }  // namespace ff
