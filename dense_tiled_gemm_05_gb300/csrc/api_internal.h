@@ -20,12 +20,23 @@ struct TuneEntry {
   gemm_tune_result_t choice;
 };
 
+// A device buffer that the handle enlarges when a call needs more (reserve in launch.cu).
+struct Workspace {
+  void *ptr = nullptr;
+  size_t bytes = 0;
+  bool captured = false;  // a call that uses it was captured: a graph holds its address
+};
+// A buffer outgrown while a graph may still use it; freed with the handle.
+struct RetiredBuffer {
+  void *ptr;
+  RetiredBuffer *next;
+};
+
 struct gemm_handle_s {
   int device = 0;
   int sm_count = 0;
   int *status = nullptr;  // device status word
-  void *workspace = nullptr;
-  size_t workspace_bytes = 0;
+  Workspace staging;      // staged operands
   uint64_t launches = 0;
   // options
   uint64_t timeout_us = 2000000;
@@ -44,18 +55,15 @@ struct gemm_handle_s {
   int tf32_transpose = 0;  // 1: MN-major tf32 operands staged transposed (K-major)
   int host_panel = 0;  // gemm_run_host panel width (rows of A, columns of B), 0 auto
   // split-K workspace of the CTA-pair kernel: partial tiles and flags
-  void *sk_ws = nullptr;
-  size_t sk_ws_bytes = 0;
+  Workspace split;
   // host-buffer pipeline (gemm_run_host): device copies of A, B, C, streams and events
   static constexpr int kMaxPanels = 48;  // per operand; steps <= 2 * kMaxPanels
-  void *hp_buf = nullptr;
+  Workspace host;
   // six-stride interface (gemm_run_strided): gathered operands and the C temporary
-  void *st_buf = nullptr;
-  size_t st_bytes = 0;
-  size_t hp_bytes = 0;
+  Workspace strided;
   // feed-forward operators: products kept in fp32, slopes, partial column sums
-  void *ff_buf = nullptr;
-  size_t ff_bytes = 0;
+  Workspace ff;
+  RetiredBuffer *retired = nullptr;
   cudaStream_t hp_stream[3] = {nullptr, nullptr, nullptr};  // H2D, compute, D2H
   cudaEvent_t hp_event[2 + 4 * kMaxPanels] = {};
   bool hp_ready = false;
@@ -178,6 +186,9 @@ cudaError_t stage_operand(const OperandPlan &o, void *dst, int es, cudaStream_t 
 gemm_status_t launch_tc(const Problem &P, const Plan &pl, const void *a_ptr, int64_t a_ld,
                         const void *b_ptr, int64_t b_ld, int *status, uint64_t timeout_ns,
                         int group_m, int debug_flags, SplitK sk, cudaStream_t s);
+// At least `bytes` in one of the handle's buffers, for work on stream s; the first `zero` bytes
+// of a new buffer are set to 0. May be called during stream capture.
+gemm_status_t reserve(gemm_handle_t h, Workspace &w, size_t bytes, cudaStream_t s, size_t zero = 0);
 // tcgen05 instruction descriptor of 16-bit or tf32 operands with an fp32 accumulator.
 uint32_t make_idesc(int in_dtype, bool a_mn, bool b_mn, int n, int m);
 // The handle's split-K workspace for `slots` workers and block_n-wide partial tiles.

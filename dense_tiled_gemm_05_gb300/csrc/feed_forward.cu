@@ -61,23 +61,6 @@ bool bad_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int layou
   return !p || ld < (layout == GEMM_ROW_MAJOR ? cols : rows);
 }
 
-gemm_status_t ensure_ff(gemm_handle_t h, size_t bytes) {
-  if (bytes <= h->ff_bytes) return GEMM_OK;
-  if (h->ff_buf) {
-    cudaFree(h->ff_buf);  // synchronises: no launched work still uses it
-    h->ff_buf = nullptr;
-    h->ff_bytes = 0;
-  }
-  void *p = nullptr;
-  if (cudaMalloc(&p, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_NO_MEMORY;
-  }
-  h->ff_buf = p;
-  h->ff_bytes = bytes;
-  return GEMM_OK;
-}
-
 // One product (its argument checks are the caller's own): few tokens and small exact fp32
 // products on the fused operators' kernels, others through the planner, whose kernels for many
 // tokens have no epilogue to make room for (1 x 4096 x 4096 bf16 on one GB300: 9.1 us against
@@ -141,8 +124,8 @@ gemm_status_t fused(gemm_handle_t h, ff::FusedProduct &q, bool *taken, cudaStrea
   Carve carve;
   *taken = ff::plan_fused(h, &q, &carve);
   if (!*taken) return GEMM_OK;
-  const gemm_status_t st = ensure_ff(h, carve.bytes);
-  return st == GEMM_OK ? ff::run_fused(h, q, static_cast<char *>(h->ff_buf), s) : st;
+  const gemm_status_t st = reserve(h, h->ff, carve.bytes, s);
+  return st == GEMM_OK ? ff::run_fused(h, q, static_cast<char *>(h->ff.ptr), s) : st;
 }
 
 gemm_status_t check_epilogue(const Problem &P, const gemm_epilogue_t &E) {
@@ -218,9 +201,9 @@ GEMM_API gemm_status_t gemm_run_epilogue(gemm_handle_t h, int64_t M, int64_t N, 
   Q.out_dtype = GEMM_F32;
   if (out_dtype != GEMM_F32 || ep.residual == C) {
     Q.ldc = round_up(N, 4);
-    st = ensure_ff(h, static_cast<size_t>(M * Q.ldc) * sizeof(float));
+    st = reserve(h, h->ff, static_cast<size_t>(M * Q.ldc) * sizeof(float), s);
     if (st != GEMM_OK) return st;
-    Q.C = h->ff_buf;
+    Q.C = h->ff.ptr;
   }
   st = product(h, Q, s);
   if (st != GEMM_OK) return st;
@@ -275,9 +258,9 @@ GEMM_API gemm_status_t gemm_run_epilogue_backward(
   const size_t dz_off = make_dz ? carve.take(M * lddz, is) : 0;
   const size_t part_off =
       dbias ? carve.take(static_cast<int64_t>(ff::column_partials_bytes(M, N, 1, h->sm_count)), 1) : 0;
-  gemm_status_t st = ensure_ff(h, carve.bytes);
+  gemm_status_t st = reserve(h, h->ff, carve.bytes, s);
   if (st != GEMM_OK) return st;
-  char *buf = static_cast<char *>(h->ff_buf);
+  char *buf = static_cast<char *>(h->ff.ptr);
   void *dz = make_dz ? buf + dz_off : nullptr;
   if ((make_dz || dbias) && N > 0) {
     st = launched(h,
@@ -351,10 +334,10 @@ GEMM_API gemm_status_t gemm_run_gated(gemm_handle_t h, int64_t M, int64_t F, int
     Carve carve;
     const size_t off = carve.take(M * PG.ldc, 4);
     const size_t off_u = carve.take(M * PG.ldc, 4);
-    st = ensure_ff(h, carve.bytes);
+    st = reserve(h, h->ff, carve.bytes, s);
     if (st != GEMM_OK) return st;
-    PG.C = static_cast<char *>(h->ff_buf) + off;
-    PU.C = static_cast<char *>(h->ff_buf) + off_u;
+    PG.C = static_cast<char *>(h->ff.ptr) + off;
+    PU.C = static_cast<char *>(h->ff.ptr) + off_u;
   }
   st = product(h, PG, s);
   if (st == GEMM_OK) st = product(h, PU, s);
@@ -429,9 +412,9 @@ GEMM_API gemm_status_t gemm_run_gated_backward(
   const bool taken = make_dx && ff::plan_fused(h, &q, &carve);
   const size_t x_off = make_dx && !taken ? carve.take(M * ld32, 4) : 0;
   const size_t x2_off = make_dx && !taken ? carve.take(M * ld32, 4) : 0;
-  gemm_status_t st = ensure_ff(h, carve.bytes);
+  gemm_status_t st = reserve(h, h->ff, carve.bytes, s);
   if (st != GEMM_OK) return st;
-  char *buf = static_cast<char *>(h->ff_buf);
+  char *buf = static_cast<char *>(h->ff.ptr);
   char *dg = buf + d_off, *du = dg + Fp * es;
   if (M > 0 && F > 0) {
     st = launched(h, ff::gated_slopes_launch(dH, lddh, gate, ld_gate, up, ld_up, dg, ldd, du, ldd,
@@ -550,12 +533,14 @@ GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int6
   if (!dX && !dweight && !dbias) return GEMM_OK;
   DeviceGuard g(h->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  gemm_status_t st = ensure_ff(h, ff::layer_norm_backward_bytes(M, N, in_dtype == out_dtype, h->sm_count));
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  gemm_status_t st = reserve(
+      h, h->ff, ff::layer_norm_backward_bytes(M, N, in_dtype == out_dtype, h->sm_count), s);
   if (st != GEMM_OK) return st;
   int launches = 0;
   const cudaError_t e = ff::layer_norm_backward_launch(
       dY, lddy, out_dtype, X, ldx, in_dtype, weight, param_dtype, mean, rstd, dX, lddx, dweight,
-      dbias, h->ff_buf, M, N, h->sm_count, &launches, static_cast<cudaStream_t>(cuda_stream));
+      dbias, h->ff.ptr, M, N, h->sm_count, &launches, s);
   return launched(h, e, "layer norm backward launch", launches);
 }
 

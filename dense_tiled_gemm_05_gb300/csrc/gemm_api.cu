@@ -86,11 +86,13 @@ GEMM_API void gemm_destroy(gemm_handle_t h) {
   if (!h) return;
   DeviceGuard g(h->device);
   cudaDeviceSynchronize();
-  if (h->workspace) cudaFree(h->workspace);
-  if (h->sk_ws) cudaFree(h->sk_ws);
-  if (h->hp_buf) cudaFree(h->hp_buf);
-  if (h->st_buf) cudaFree(h->st_buf);
-  if (h->ff_buf) cudaFree(h->ff_buf);
+  for (const Workspace *w : {&h->staging, &h->split, &h->host, &h->strided, &h->ff})
+    if (w->ptr) cudaFree(w->ptr);
+  while (RetiredBuffer *r = h->retired) {
+    h->retired = r->next;
+    cudaFree(r->ptr);
+    delete r;
+  }
   for (cudaStream_t st : h->hp_stream)
     if (st) cudaStreamDestroy(st);
   for (cudaEvent_t ev : h->hp_event)

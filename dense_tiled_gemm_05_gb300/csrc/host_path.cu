@@ -85,19 +85,10 @@ GEMM_API gemm_status_t gemm_run_host(gemm_handle_t h, int64_t M, int64_t N, int6
   const size_t c_bytes = static_cast<size_t>(M * ldc_d * os);
   st = host_pipeline_setup(h);
   if (st != GEMM_OK) return st;
-  if (a_bytes + b_bytes + c_bytes > h->hp_bytes) {
-    // earlier calls may still copy from or into the old buffer
-    for (cudaStream_t hs : h->hp_stream) cudaStreamSynchronize(hs);
-    if (h->hp_buf) cudaFree(h->hp_buf);
-    h->hp_buf = nullptr;
-    h->hp_bytes = 0;
-    if (cudaMalloc(&h->hp_buf, a_bytes + b_bytes + c_bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_NO_MEMORY;
-    }
-    h->hp_bytes = a_bytes + b_bytes + c_bytes;
-  }
-  char *dA = static_cast<char *>(h->hp_buf);
+  // (growth frees the old buffer, which waits for earlier calls' copies)
+  st = reserve(h, h->host, a_bytes + b_bytes + c_bytes, user);
+  if (st != GEMM_OK) return st;
+  char *dA = static_cast<char *>(h->host.ptr);
   char *dB = dA + a_bytes;
   char *dC = dB + b_bytes;
   const char *hA = static_cast<const char *>(A), *hB = static_cast<const char *>(B);

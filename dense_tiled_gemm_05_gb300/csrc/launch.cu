@@ -5,6 +5,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "api_internal.h"
 
@@ -120,22 +121,71 @@ uint32_t make_idesc(int in_dtype, bool a_mn, bool b_mn, int n, int m) {
   return d;
 }
 
-static gemm_status_t ensure_workspace(gemm_handle_t h, size_t bytes) {
-  if (bytes <= h->workspace_bytes) return GEMM_OK;
+static bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream while another one is captured)
+    return false;
+  }
+  return st != cudaStreamCaptureStatusNone;
+}
+
+// Allows the calling thread's allocations while a capture is under way, on its stream or another.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Zeros now, whatever is captured: memset on a stream of its own.
+static cudaError_t zero_now(void *p, size_t bytes) {
+  cudaStream_t t = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&t, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p, 0, bytes, t);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(t);
+  cudaStreamDestroy(t);
+  return e;
+}
+
+// A captured call's kernels hold the buffer's address in their frozen parameters and tensor
+// maps, so a buffer that was used in a capture is kept when a later call outgrows it; others are
+// freed.
+gemm_status_t reserve(gemm_handle_t h, Workspace &w, size_t bytes, cudaStream_t s, size_t zero) {
+  if (bytes == 0) return GEMM_OK;
+  const bool in_capture = capturing(s);
+  if (bytes <= w.bytes) {
+    w.captured |= in_capture;
+    return GEMM_OK;
+  }
   const char *fi = std::getenv("GEMM_FAULT_INJECT");
   if (fi && std::strcmp(fi, "alloc") == 0) return GEMM_ERR_NO_MEMORY;
-  if (h->workspace) {
-    cudaFree(h->workspace);  // synchronises: no launched work still uses it
-    h->workspace = nullptr;
-    h->workspace_bytes = 0;
+  RelaxedCapture relaxed;
+  if (w.ptr) {
+    if (w.captured || in_capture) {
+      RetiredBuffer *r = new (std::nothrow) RetiredBuffer{w.ptr, h->retired};
+      if (!r) return GEMM_ERR_NO_MEMORY;
+      h->retired = r;
+    } else {
+      cudaFree(w.ptr);  // synchronises: no launched work still uses it
+    }
+    w = Workspace{};
   }
   void *p = nullptr;
   if (cudaMalloc(&p, bytes) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_NO_MEMORY;
   }
-  h->workspace = p;
-  h->workspace_bytes = bytes;
+  const cudaError_t e = zero == 0      ? cudaSuccess
+                        : in_capture ? zero_now(p, zero)
+                                     : cudaMemsetAsync(p, 0, zero, s);
+  if (e != cudaSuccess) {
+    cudaFree(p);
+    return cuda_fail(e, "clear a workspace");
+  }
+  w.ptr = p;
+  w.bytes = bytes;
+  w.captured = in_capture;
   return GEMM_OK;
 }
 
@@ -145,29 +195,6 @@ cudaError_t stage_operand(const OperandPlan &o, void *dst, int es, cudaStream_t 
                          static_cast<float *>(dst), o.staged_ld, o.rows, o.k, o.split_kp, s);
   if (o.transpose) return transpose_launch(o.ptr, o.ld, dst, o.staged_ld, o.outer, o.inner, es, s);
   return repack_launch(o.ptr, o.ld, dst, o.staged_ld, o.outer, o.inner, es, s);
-}
-
-static gemm_status_t ensure_sk_workspace(gemm_handle_t h, size_t bytes, size_t flag_bytes,
-                                         cudaStream_t s) {
-  if (bytes <= h->sk_ws_bytes) return GEMM_OK;
-  if (h->sk_ws) {
-    cudaFree(h->sk_ws);
-    h->sk_ws = nullptr;
-    h->sk_ws_bytes = 0;
-  }
-  void *p = nullptr;
-  if (cudaMalloc(&p, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_NO_MEMORY;
-  }
-  // The epoch word, the arrival count and every flag start at 0.
-  if (cudaMemsetAsync(p, 0, flag_bytes, s) != cudaSuccess) {
-    cudaFree(p);
-    return GEMM_ERR_CUDA;
-  }
-  h->sk_ws = p;
-  h->sk_ws_bytes = bytes;
-  return GEMM_OK;
 }
 
 // The split-K workspace of `slots` workers and its tensor map.
@@ -180,11 +207,12 @@ gemm_status_t split_workspace(gemm_handle_t h, int64_t slots, int block_n, int *
   const size_t flag_region =
       static_cast<size_t>(round_up(static_cast<int64_t>((2 + 8 * ctas_max) * sizeof(int)), 256));
   const size_t part_bytes = static_cast<size_t>(slots) * 2 * kTcBlockM * block_n * sizeof(float);
-  const gemm_status_t st = ensure_sk_workspace(h, flag_region + part_bytes, flag_region, s);
+  // (the epoch word, the arrival count and every flag start at 0)
+  const gemm_status_t st = reserve(h, h->split, flag_region + part_bytes, s, flag_region);
   if (st != GEMM_OK) return st;
-  *epoch_word = static_cast<int *>(h->sk_ws);
+  *epoch_word = static_cast<int *>(h->split.ptr);
   *flags = *epoch_word + 2;
-  *partials = reinterpret_cast<float *>(static_cast<char *>(h->sk_ws) + flag_region);
+  *partials = reinterpret_cast<float *>(static_cast<char *>(h->split.ptr) + flag_region);
   // partial tiles: rows [worker][cta rank][128], block_n fp32 columns; 32 x 32 boxes
   return encode_2d(tmP, GEMM_F32, *partials, block_n, slots * 2 * kTcBlockM, block_n, 32, 32)
              ? GEMM_OK
@@ -335,7 +363,7 @@ gemm_status_t execute(gemm_handle_t h, const Problem &P, const Plan &pl, cudaStr
   }
   // Tensor-core path.
   const int es = esize_of(P.in_dtype);
-  gemm_status_t st = ensure_workspace(h, static_cast<size_t>(I.workspace_bytes));
+  gemm_status_t st = reserve(h, h->staging, static_cast<size_t>(I.workspace_bytes), s);
   if (st != GEMM_OK) return st;
   const void *a_ptr = pl.a.ptr;
   int64_t a_ld = pl.a.ld;
@@ -343,7 +371,7 @@ gemm_status_t execute(gemm_handle_t h, const Problem &P, const Plan &pl, cudaStr
   int64_t b_ld = pl.b.ld;
   for (const OperandPlan *o : {&pl.a, &pl.b}) {
     if (!o->staged) continue;
-    void *dst = static_cast<char *>(h->workspace) + o->ws_offset;
+    void *dst = static_cast<char *>(h->staging.ptr) + o->ws_offset;
     e = stage_operand(*o, dst, es, s);
     if (e != cudaSuccess) return cuda_fail(e, "stage operand");
     h->launches += 1;

@@ -18,7 +18,7 @@ namespace {
 // scattered.
 
 struct StridedPlan {
-  Problem P;             // the problem the planner sees (pointers into st_buf where gathered)
+  Problem P;             // the problem the planner sees (pointers into the handle's buffer where gathered)
   bool gather_a, gather_b;
   int c_mode;            // gemm_strided_info_t::c_mode
   const void *src_a, *src_b;
@@ -196,20 +196,12 @@ GEMM_API gemm_status_t gemm_run_strided(gemm_handle_t h, int64_t M, int64_t N, i
   DeviceGuard g(h->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (S.bytes > h->st_bytes) {
-    if (h->st_buf) cudaFree(h->st_buf);  // synchronises: no launched work still uses it
-    h->st_buf = nullptr;
-    h->st_bytes = 0;
-    if (cudaMalloc(&h->st_buf, S.bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_NO_MEMORY;
-    }
-    h->st_bytes = S.bytes;
-  }
+  st = reserve(h, h->strided, S.bytes, s);
+  if (st != GEMM_OK) return st;
   // the same plan with the real buffer
   st = make_strided_plan(M, N, K, A, stride_am, stride_ak, B, stride_bk, stride_bn, C, stride_cm,
                          stride_cn, in_dtype, out_dtype, precision_mode,
-                         static_cast<char *>(h->st_buf), &S);
+                         static_cast<char *>(h->strided.ptr), &S);
   if (st == GEMM_OK) st = make_plan(S.P, options_for(h, S.P), h->sm_count, &pl);
   if (st != GEMM_OK) return st;
   const int es = esize_of(in_dtype), os = esize_of(out_dtype);

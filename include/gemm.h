@@ -68,6 +68,11 @@
  * another on the GPU: one stream, or streams ordered by events. Work that runs
  * concurrently takes one handle per stream. (gemm_run_host orders its own
  * internal streams.)
+ *
+ * CUDA graphs: calls may be captured, also a handle's first ones. A replay uses the
+ * handle's device buffers like the calls it was captured from, so it takes its turn among
+ * them, and a buffer that a captured call uses is kept until gemm_destroy even when later
+ * calls outgrow it. Destroy the handle after the last replay.
  */
 #ifndef GEMM_GB300_H
 #define GEMM_GB300_H
