@@ -174,10 +174,14 @@ constexpr double kBandwidthBound = 256.0;
 double intensity_of(const Problem &P);
 gemm_status_t check_args(const Problem &P);
 bool use_split_k(int stream_k, int64_t tiles, int64_t k_blocks, int64_t slots);
+// Tile slots of the CTA-pair kernel: one cluster of two SMs each, under the CTA cap.
+int64_t pair_slots(int sm_count, int max_ctas);
 gemm_status_t make_plan(const Problem &P, const Options &opt, int sm_count, Plan *out);
 Options options_of(gemm_handle_t h);
 const TuneEntry *find_tuned(gemm_handle_t h, const Problem &P);
 Options options_for(gemm_handle_t h, const Problem &P);
+// Whether an option of the handle, or a tuned choice for P, steers the planner's kernel for P.
+bool options_steer(gemm_handle_t h, const Problem &P);
 
 // launch.cu
 bool encode_2d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64_t outer,

@@ -64,11 +64,12 @@ bool bad_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int layou
 // One product (its argument checks are the caller's own): few tokens and small exact fp32
 // products on the fused operators' kernels, others through the planner, whose kernels for many
 // tokens have no epilogue to make room for (1 x 4096 x 4096 bf16 on one GB300: 9.1 us against
-// the planner's 21.6, 64 tokens 12.4 against 21.6). Not where the fused
-// kernels would have to stage an operand: the handle's buffer may hold this one's.
+// the planner's 21.6, 64 tokens 12.4 against 21.6). Not where the caller steers the planner by
+// options or gemm_tune, and not where the fused kernels would have to stage an operand: the
+// handle's buffer may hold this one's.
 gemm_status_t product(gemm_handle_t h, const Problem &P, cudaStream_t s) {
   const bool f32 = P.in_dtype == GEMM_F32;
-  if (f32 ? P.precision != GEMM_PREC_TF32 : P.precision != GEMM_PREC_F16_ACC && !h->cta_pair) {
+  if (P.precision != (f32 ? GEMM_PREC_TF32 : GEMM_PREC_F16_ACC) && !options_steer(h, P)) {
     ff::FusedProduct q;
     q.M = P.M, q.N = P.N, q.K = P.K;
     q.X.ptr = P.A, q.X.ld = P.lda, q.X.layout = P.a_layout;

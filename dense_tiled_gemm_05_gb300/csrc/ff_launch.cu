@@ -202,13 +202,15 @@ bool plan_fused(gemm_handle_t h, FusedProduct *q, Carve *carve) {
   if (q->M < 1 || q->N < 1 || q->K < 1) return false;
   if (h->force_path == 2) return false;  // the FMA kernel was asked for
   if (q->gated && q->out_dtype != q->in_dtype) return false;
-  if (!h->cta_pair && plan_token(q, h->sm_count)) return true;
-  if (q->in_dtype == GEMM_F32) return !h->cta_pair && plan_tile(q, h->sm_count);
+  // (the multiply-add kernels only where no tensor-core kernel is asked for)
+  const bool multiply_adds = !h->cta_pair && h->force_path != 1;
+  if (multiply_adds && plan_token(q, h->sm_count)) return true;
+  if (q->in_dtype == GEMM_F32) return multiply_adds && plan_tile(q, h->sm_count);
   const int64_t k_blocks = (q->K + 63) / 64 + (q->K2 + 63) / 64;
   const int64_t tile_n = q->gated ? 128 : 256;
   q->tiles_m = (q->M + 255) / 256;
   q->tiles_n = (q->N + tile_n - 1) / tile_n;
-  const int64_t clusters = h->sm_count > 1 ? h->sm_count / 2 : 1;
+  const int64_t clusters = pair_slots(h->sm_count, h->max_ctas);
   if (q->tiles_m * q->tiles_n > INT32_MAX / 8 || k_blocks > INT32_MAX) return false;
   // Where the 256-row tiles are few, or few of their rows are tokens, the few-token kernel's
   // smaller tiles, which share their K-loops over clusters, take less time.
@@ -343,7 +345,7 @@ gemm_status_t run_fused(gemm_handle_t h, const FusedProduct &q, char *buf, cudaS
   const int64_t fit = tc2_max_active_clusters();
   if (fit <= 0) return GEMM_ERR_CUDA;
   const int64_t tiles = q.tiles_m * q.tiles_n;
-  int64_t slots = h->sm_count > 1 ? h->sm_count / 2 : 1;
+  int64_t slots = pair_slots(h->sm_count, h->max_ctas);
   if (slots > fit) slots = fit;
   const int32_t t32 = static_cast<int32_t>(tiles), s32 = static_cast<int32_t>(slots);
   p.sk_dp_tiles = sk_dp_tiles(t32, p.f.k_blocks, s32, use_split_k(h->stream_k, tiles, p.f.k_blocks, slots));

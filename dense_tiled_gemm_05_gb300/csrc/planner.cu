@@ -122,8 +122,7 @@ double intensity_of(const Problem &P) {
   return 2.0 * m * n * k / (es * (m * k + k * n) + os * m * n);
 }
 
-// Tile slots of the CTA-pair kernel: one cluster of two SMs each, under the CTA cap.
-static int64_t pair_slots(int sm_count, int max_ctas) {
+int64_t pair_slots(int sm_count, int max_ctas) {
   int64_t clusters = sm_count > 1 ? sm_count / 2 : 1;
   if (max_ctas > 0 && max_ctas / 2 < clusters) clusters = max_ctas / 2 > 0 ? max_ctas / 2 : 1;
   return clusters;
@@ -389,6 +388,12 @@ Options options_of(gemm_handle_t h) {
     o.tf32_transpose = h->tf32_transpose;
   }
   return o;
+}
+
+bool options_steer(gemm_handle_t h, const Problem &P) {
+  const Options o = options_of(h);
+  return o.force_path || o.max_ctas || o.force_staging || o.cta_pair || o.block_n || o.stream_k ||
+         o.stage_k || o.tile_rows || (P.in_dtype == GEMM_F32 && o.exact_chunk) || find_tuned(h, P);
 }
 
 const TuneEntry *find_tuned(gemm_handle_t h, const Problem &P) {

@@ -330,9 +330,14 @@ typedef struct {
  * on plain multiply-adds, where that is estimated to be quicker; few rows with the outputs'
  * features as the rows of the tensor-core tile and K split over a cluster; many in 256 x 256
  * tiles on CTA pairs (GEMM_OPT_CTA_PAIR 1 and 2 choose the second or the third, GEMM_OPT_STREAM_K
- * the split of the pairs' last rounds, GEMM_OPT_FORCE_PATH 2 none of them). fp32 inputs run in
+ * the split of the pairs' last rounds, GEMM_OPT_GROUP_M their raster groups, GEMM_OPT_MAX_CTAS
+ * caps their CTAs, the only persistent ones; GEMM_OPT_FORCE_PATH 1 leaves out the multiply-adds
+ * for fp32 and 16-bit inputs, 2 runs none of these kernels). fp32 inputs run in
  * one kernel too for up to eight rows and for small exact products, otherwise the product of
- * their precision mode and then a kernel for what follows it.
+ * their precision mode and then a kernel for what follows it. A product alone, here and in the
+ * backward passes, runs as in gemm_run_ex when an option of the handle or gemm_tune steers that
+ * call's kernel, and else by the choice above; the other tile-shape options, GEMM_OPT_FORCE_STAGING
+ * and gemm_set_kernel_events have no effect on the kernels with an epilogue.
  * Errors: those of gemm_run_ex; INVALID_ARG for an unknown activation or bias type, a leading
  * dimension below N, or overlapping buffers; ALIGNMENT for a bias, residual or pre pointer
  * that is not aligned to its element size. */
