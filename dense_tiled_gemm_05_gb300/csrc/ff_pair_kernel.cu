@@ -211,6 +211,7 @@ __device__ __forceinline__ bool plain_boxes(const PairMaps &maps, const PairPara
       add_box_row<OUT>(bx.row(b), lane, v);
       write_box_row<OUT>(bx.row(b), lane, v);
       bx.store(b, &maps.C, col, row0);
+      bx.next = b ^ 1;  // (a split tile's partial may follow, through the other box first)
       if (c + 2 < n) bx.load(b, &maps.R, col + 2 * COLS, row0);
       continue;
     }
