@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kFewThreads)
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
       float *P = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
       for (int c0 = half * 16; c0 < tokens; c0 += 32) {
+        __syncwarp();  // (lanes past N finish early; TMEM is read by whole warps)
         uint32_t r[2][16];
         tmem_ld_32x32b_x16(t_row + c0, r[0]);
         if (GATED) tmem_ld_32x32b_x16(t_row + acc_stride(p.tile_t) + c0, r[1]);

@@ -55,9 +55,11 @@ constexpr int SMEM_BYTES = BAR_OFFSET + NUM_BARS * 8 + 32 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(kPairEpiWarps * PART_BYTES <= STAGES * STAGE_BYTES, "owners' partials fit the stages");
 
-// COLS consecutive accumulator columns of this lane's row, as fp32.
+// COLS consecutive accumulator columns of this lane's row, as fp32. By whole warps, whose lanes
+// may come from rows past M or from a store that one of them issued.
 template <int COLS>
 __device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[COLS]) {
+  __syncwarp();
   uint32_t r[COLS / 32][32];
 #pragma unroll
   for (int h = 0; h < COLS / 32; ++h) tmem_ld_32x32b_x32(taddr + h * 32, r[h]);

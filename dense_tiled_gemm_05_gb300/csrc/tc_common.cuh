@@ -93,6 +93,7 @@ __device__ __forceinline__ void epilogue_tma(const CUtensorMap *tmC, uint32_t t_
   const bool rows_in = row0 < M;
 #pragma unroll 1
   for (int c0 = 0; c0 < BN; c0 += OUT_COLS) {
+    __syncwarp();  // (one lane stored the previous box; TMEM is read by whole warps)
     uint32_t r0[32], r1[32];
     tmem_ld_32x32b_x32(t_row + c0, r0);
     if (OUT_COLS == 64) tmem_ld_32x32b_x32(t_row + c0 + 32, r1);
@@ -139,6 +140,7 @@ __device__ __forceinline__ void epilogue_direct(const TcParams &p, uint32_t t_ro
             typename std::conditional<OUT == GEMM_BF16, __nv_bfloat16, __half>::type>::type;
 #pragma unroll 1
   for (int c0 = 0; c0 < BN; c0 += 32) {
+    __syncwarp();  // (lanes past M store nothing; TMEM is read by whole warps)
     uint32_t r[32];
     tmem_ld_32x32b_x32(t_row + c0, r);
     tmem_wait_ld();
