@@ -558,34 +558,43 @@ def softmax_rows(x, out=None, out_dtype=None):
     return handle(x.device.index).softmax_rows(x, out=out, out_dtype=out_dtype)
 
 
+def _handle_of(t):
+    """The default handle of an operand's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("operands must be tensors")
+    if not t.is_cuda:
+        raise ValueError("operands must be CUDA tensors")
+    return handle(t.get_device())
+
+
 def matmul_epilogue(a, b, **kw):
     """act(a @ b + bias) + residual; see :meth:`Gemm.matmul_epilogue`."""
-    return handle(a.get_device()).matmul_epilogue(a, b, **kw)
+    return _handle_of(a).matmul_epilogue(a, b, **kw)
 
 
 def matmul_epilogue_backward(grad, a, b, **kw):
     """Gradients of :func:`matmul_epilogue`; see :meth:`Gemm.matmul_epilogue_backward`."""
-    return handle(a.get_device()).matmul_epilogue_backward(grad, a, b, **kw)
+    return _handle_of(a).matmul_epilogue_backward(grad, a, b, **kw)
 
 
 def gated(x, w_gate, w_up, **kw):
     """act(x @ w_gate) * (x @ w_up); see :meth:`Gemm.gated`."""
-    return handle(x.get_device()).gated(x, w_gate, w_up, **kw)
+    return _handle_of(x).gated(x, w_gate, w_up, **kw)
 
 
 def gated_backward(grad, x, w_gate, w_up, gate, up, **kw):
     """Gradients of :func:`gated`; see :meth:`Gemm.gated_backward`."""
-    return handle(x.get_device()).gated_backward(grad, x, w_gate, w_up, gate, up, **kw)
+    return _handle_of(x).gated_backward(grad, x, w_gate, w_up, gate, up, **kw)
 
 
 def layer_norm(x, weight=None, bias=None, **kw):
     """Layer norm of the rows of x; see :meth:`Gemm.layer_norm`."""
-    return handle(x.get_device()).layer_norm(x, weight, bias, **kw)
+    return _handle_of(x).layer_norm(x, weight, bias, **kw)
 
 
 def layer_norm_backward(grad, x, weight, mean, rstd, **kw):
     """Gradients of :func:`layer_norm`; see :meth:`Gemm.layer_norm_backward`."""
-    return handle(x.get_device()).layer_norm_backward(grad, x, weight, mean, rstd, **kw)
+    return _handle_of(x).layer_norm_backward(grad, x, weight, mean, rstd, **kw)
 
 
 def matmul_host(a, b, out=None, out_dtype=None, precision="default", device=None):
