@@ -238,8 +238,34 @@ def _dtype_code(d):
     raise TypeError("unsupported dtype %s" % d)
 
 
+class _Streams:
+    """The stream of a call: the current one, or another that the caller names. On another, the
+    call does what it would with that stream current -- its output comes from that stream's
+    memory -- and the allocator learns of every tensor that two streams use."""
+
+    def __init__(self, stream, device):
+        self.call = self.current = torch.cuda.current_stream(device)
+        if stream is not None and stream.cuda_stream != self.current.cuda_stream:
+            self.call = (stream if isinstance(stream, torch.cuda.Stream)
+                         else torch.cuda.ExternalStream(stream.cuda_stream, device))
+
+    def empty(self, shape, dtype, device):
+        if self.call is self.current:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.call):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def used(self, out, *operands):
+        if self.call is not self.current:
+            for t in (out,) + operands:
+                t.record_stream(self.call)
+            out.record_stream(self.current)
+
+
 class Gemm:
-    """A library handle bound to one CUDA device."""
+    """A library handle bound to one CUDA device. A call's ``stream`` (default: the current one)
+    runs it as if that stream were current; ordering it after the operands' work, and other
+    work after it, is the caller's."""
 
     def __init__(self, device=None):
         if device is None:
@@ -312,12 +338,13 @@ class Gemm:
         if K != K2:
             raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
         in_dt = _dtype_code(a.dtype)
+        streams = _Streams(stream, a.device)
+        s = streams.call
         if out is None:
             od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else a.dtype
-            out = torch.empty((M, N), dtype=od, device=a.device)
+            out = streams.empty((M, N), od, a.device)
         if out.dim() != 2 or out.shape != (M, N):
             raise ValueError("out must be an M x N tensor")
-        s = torch.cuda.current_stream(a.device) if stream is None else stream
         ptr = lambda t: ctypes.c_void_p(t.data_ptr())
         try:
             al, lda = operand_layout(a)
@@ -338,6 +365,7 @@ class Gemm:
                                           _dtype_code(out.dtype), PREC[precision],
                                           ctypes.c_void_p(s.cuda_stream))
             _check(code, "gemm_run_strided")
+        streams.used(out, a, b)
         return out
 
     def tune(self, a, b, out=None, out_dtype=None, precision="default", iters=5, stream=None):
@@ -346,12 +374,13 @@ class Gemm:
         as a dict (see gemm_tune). C is written."""
         M, K = a.shape
         N = b.shape[1]
+        streams = _Streams(stream, a.device)
+        s = streams.call
         if out is None:
             od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else a.dtype
-            out = torch.empty((M, N), dtype=od, device=a.device)
+            out = streams.empty((M, N), od, a.device)
         al, lda = operand_layout(a)
         bl, ldb = operand_layout(b)
-        s = torch.cuda.current_stream(a.device) if stream is None else stream
         r = TuneResult()
         code = lib().gemm_tune(self._h, M, N, K, ctypes.c_void_p(a.data_ptr()), lda,
                                ctypes.c_void_p(b.data_ptr()), ldb, ctypes.c_void_p(out.data_ptr()),
@@ -359,6 +388,7 @@ class Gemm:
                                _dtype_code(out.dtype), PREC[precision], al, bl,
                                ctypes.c_void_p(s.cuda_stream), int(iters), ctypes.byref(r))
         _check(code, "gemm_tune")
+        streams.used(out, a, b)
         return r.as_dict()
 
     def softmax_rows(self, x, out=None, out_dtype=None, stream=None):
@@ -370,12 +400,13 @@ class Gemm:
         M, N = x.shape
         if N > 1 and x.stride(1) != 1:
             raise ValueError("rows of x must be contiguous")
+        streams = _Streams(stream, x.device)
+        s = streams.call
         if out is None:
             od = _TORCH_OF[_dtype_code(out_dtype)] if out_dtype is not None else x.dtype
-            out = torch.empty((M, N), dtype=od, device=x.device)
+            out = streams.empty((M, N), od, x.device)
         if out.shape != (M, N) or (N > 1 and out.stride(1) != 1):
             raise ValueError("out must be an M x N tensor with contiguous rows")
-        s = torch.cuda.current_stream(x.device) if stream is None else stream
         code = lib().gemm_softmax_rows(self._h, M, N, ctypes.c_void_p(x.data_ptr()),
                                        max(x.stride(0) if M > 1 else N, N, 1),
                                        ctypes.c_void_p(out.data_ptr()),
@@ -383,6 +414,7 @@ class Gemm:
                                        _dtype_code(x.dtype), _dtype_code(out.dtype),
                                        ctypes.c_void_p(s.cuda_stream))
         _check(code, "gemm_softmax_rows")
+        streams.used(out, x)
         return out
 
     # ------------------------------------------------------- feed-forward operators

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -15,6 +16,8 @@
 
 #include <cstdarg>
 #include <cstring>
+#include <initializer_list>
+#include <optional>
 
 #include "gemm.h"
 
@@ -116,15 +119,42 @@ gemm_handle_t handle_arg(PyObject *o) {
   return static_cast<gemm_handle_t>(p);
 }
 
-void *stream_arg(PyObject *o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-  PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
-  if (!v) throw python_error();
-  void *s = PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  if (!s && PyErr_Occurred()) throw python_error();
-  return s;
-}
+// The stream of a call: the current one, or another that the caller names. On another, the call
+// does what it would with that stream current -- its outputs come from that stream's memory, or
+// they could lie where the current stream's work is not done yet -- and the allocator learns of
+// every tensor that two streams use.
+class CallStream {
+ public:
+  CallStream(PyObject *o, int dev)
+      : current_(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev))) {
+    ptr_ = current_.stream();
+    if (o == Py_None) return;
+    PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
+    if (!v) throw python_error();
+    void *s = PyLong_AsVoidPtr(v);
+    Py_DECREF(v);
+    if (!s && PyErr_Occurred()) throw python_error();
+    if (s == ptr_) return;
+    ptr_ = s;
+    other_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s),
+                                                    static_cast<c10::DeviceIndex>(dev)));
+  }
+  void *get() const { return ptr_; }
+  // The caller's tensors, before the call; its new ones, after.
+  void uses(std::initializer_list<const Tensor *> tensors) const { record(tensors, true); }
+  void gives(std::initializer_list<const Tensor *> tensors) const { record(tensors, false); }
+
+ private:
+  void record(std::initializer_list<const Tensor *> tensors, bool on_call) const {
+    if (!other_) return;
+    const c10::Stream s = on_call ? other_->current_stream().unwrap() : current_.unwrap();
+    for (const Tensor *t : tensors)
+      if (t->defined() && t->numel() > 0) t->record_stream(s);
+  }
+  c10::cuda::CUDAStream current_;
+  std::optional<c10::cuda::CUDAStreamGuard> other_;
+  void *ptr_;
+};
 
 // ------------------------------------------------------------------- operands
 
@@ -285,7 +315,8 @@ PyObject *matmul_epilogue(PyObject *, PyObject *const *v, Py_ssize_t n) {
   const Layout la(a), lb(b);
   const gemm_precision_t prec = precision_arg(v[8]);
   const bool save = truth(v[9]);
-  void *stream = stream_arg(v[10], p.dev);
+  const CallStream stream(v[10], p.dev);
+  stream.uses({&a, &b, &bias, &residual, &out});
   if (!out.defined()) out = empty(a, {p.M, p.N}, od);
   if (save) {
     pre = empty(a, {p.M, p.N}, od);
@@ -294,8 +325,9 @@ PyObject *matmul_epilogue(PyObject *, PyObject *const *v, Py_ssize_t n) {
   }
   check(run_epilogue(handle_arg(v[0]), p.M, p.N, p.K, a.data_ptr(), la.ld, b.data_ptr(), lb.ld,
                      out.data_ptr(), ldc, static_cast<gemm_dtype_t>(in),
-                     static_cast<gemm_dtype_t>(code_of(od)), prec, la.layout, lb.layout, &ep, stream),
+                     static_cast<gemm_dtype_t>(code_of(od)), prec, la.layout, lb.layout, &ep, stream.get()),
         "gemm_run_epilogue");
+  stream.gives({&out, &pre});
   if (!save) return wrap(out);
   PyObject *x = wrap(out), *y = wrap(pre);
   return x && y ? Py_BuildValue("(NN)", x, y) : nullptr;
@@ -322,7 +354,8 @@ PyObject *matmul_epilogue_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
   const at::ScalarType bd = dtype_arg(v[7], a.scalar_type());
   const gemm_precision_t prec = precision_arg(v[8]);
   const Layout la(a), lb(b);
-  void *stream = stream_arg(v[9], p.dev);
+  const CallStream stream(v[9], p.dev);
+  stream.uses({&grad, &a, &b, &pre});
   Tensor da, db, dbias;
   if (need.v[0]) da = empty_like_layout(a, la.layout);
   if (need.v[1]) db = empty_like_layout(b, lb.layout);
@@ -332,8 +365,9 @@ PyObject *matmul_epilogue_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
             la.ld, b.data_ptr(), lb.ld, ptr(da), tight_ld(la.layout, p.M, p.K), ptr(db),
             tight_ld(lb.layout, p.K, p.N), ptr(dbias), static_cast<gemm_dtype_t>(code_of(bd)),
             static_cast<gemm_dtype_t>(code_of(a)), static_cast<gemm_dtype_t>(code_of(grad)), prec,
-            la.layout, lb.layout, act, stream),
+            la.layout, lb.layout, act, stream.get()),
         "gemm_run_epilogue_backward");
+  stream.gives({&da, &db, &dbias});
   return wrap3(da, db, dbias);
   END_HANDLE_TH_ERRORS
 }
@@ -361,16 +395,16 @@ PyObject *gated(PyObject *, PyObject *const *v, Py_ssize_t n) {
   const gemm_precision_t prec = precision_arg(v[6]);
   const bool save = truth(v[7]);
   const auto dt = static_cast<gemm_dtype_t>(code_of(x));
-  void *stream = stream_arg(v[8], p.dev);
+  const CallStream stream(v[8], p.dev);
   Tensor out, gate, up;
   int64_t ldh = least1(p.N);
   if (v[5] != Py_None) {
     out = tensor(v[5], "out");
     if (out.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
     ldh = row_ld(out, p.M, p.N, "out", p.dev);
-  } else {
-    out = empty(x, {p.M, p.N}, x.scalar_type());
   }
+  stream.uses({&x, &wg, &wu, &out});
+  if (!out.defined()) out = empty(x, {p.M, p.N}, x.scalar_type());
   if (save) {  // column ranges of one buffer, as the backward pass keeps their gradients
     const Tensor both = empty(x, {p.M, 2 * p.N}, x.scalar_type());
     gate = both.narrow(1, 0, p.N);
@@ -378,8 +412,9 @@ PyObject *gated(PyObject *, PyObject *const *v, Py_ssize_t n) {
   }
   check(run_gated(handle_arg(v[0]), p.M, p.N, p.K, x.data_ptr(), q.ldx, wg.data_ptr(), q.g.ld,
                   wu.data_ptr(), q.u.ld, out.data_ptr(), ldh, ptr(gate), 2 * p.N, ptr(up), 2 * p.N,
-                  dt, prec, q.g.layout, act, stream),
+                  dt, prec, q.g.layout, act, stream.get()),
         "gemm_run_gated");
+  stream.gives({&out, &gate, &up});
   return save ? wrap3(out, gate, up) : wrap(out);
   END_HANDLE_TH_ERRORS
 }
@@ -400,7 +435,8 @@ PyObject *gated_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
   const Need need(v[8]);
   const gemm_precision_t prec = precision_arg(v[9]);
   const auto dt = static_cast<gemm_dtype_t>(code_of(x));
-  void *stream = stream_arg(v[10], p.dev);
+  const CallStream stream(v[10], p.dev);
+  stream.uses({&grad, &x, &wg, &wu, &gate, &up});
   Tensor dx, dwg, dwu;
   if (need.v[0]) dx = empty(x, {p.M, p.K}, x.scalar_type());
   if (need.v[1] && need.v[2] && q.g.layout == GEMM_COL_MAJOR) {
@@ -416,8 +452,9 @@ PyObject *gated_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
   check(run_gated_backward(handle_arg(v[0]), p.M, p.N, p.K, grad.data_ptr(), ldh, gate.data_ptr(),
                            ldg, up.data_ptr(), ldu, x.data_ptr(), q.ldx, wg.data_ptr(), q.g.ld,
                            wu.data_ptr(), q.u.ld, ptr(dx), least1(p.K), ptr(dwg), ldw, ptr(dwu), ldw,
-                           dt, prec, q.g.layout, act, stream),
+                           dt, prec, q.g.layout, act, stream.get()),
         "gemm_run_gated_backward");
+  stream.gives({&dx, &dwg, &dwu});
   return wrap3(dx, dwg, dwu);
   END_HANDLE_TH_ERRORS
 }
@@ -451,10 +488,11 @@ PyObject *layer_norm(PyObject *, PyObject *const *v, Py_ssize_t n) {
   if (v[5] != Py_None) {
     out = tensor(v[5], "out");
     ldy = row_ld(out, r.rows, r.cols, "out", dev);
-  } else {
-    out = empty(x, {r.rows, r.cols}, dtype_arg(v[6], x.scalar_type()));
   }
   const bool save = truth(v[7]);
+  const CallStream stream(v[8], dev);
+  stream.uses({&x, &weight, &bias, &out});
+  if (!out.defined()) out = empty(x, {r.rows, r.cols}, dtype_arg(v[6], x.scalar_type()));
   if (save) {
     const Tensor both = empty(x, {2, r.rows}, at::kFloat);
     mean = both.select(0, 0);
@@ -464,8 +502,9 @@ PyObject *layer_norm(PyObject *, PyObject *const *v, Py_ssize_t n) {
                        ldy, static_cast<float *>(ptr(mean)), static_cast<float *>(ptr(rstd)),
                        static_cast<float>(eps), static_cast<gemm_dtype_t>(in),
                        static_cast<gemm_dtype_t>(params), static_cast<gemm_dtype_t>(code_of(out)),
-                       stream_arg(v[8], dev)),
+                       stream.get()),
         "gemm_layer_norm");
+  stream.gives({&out, &mean, &rstd});
   return save ? wrap3(out, mean, rstd) : wrap(out);
   END_HANDLE_TH_ERRORS
 }
@@ -498,6 +537,8 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
   }
   const Need need(v[6]);
   const int in = code_of(x), params = code_of(pd), g = code_of(grad);
+  const CallStream stream(v[8], dev);
+  stream.uses({&grad, &x, &weight, &mean, &rstd});
   Tensor dx, dw, db;
   if (need.v[0]) dx = empty(x, {r.rows, r.cols}, x.scalar_type());
   if (need.v[1]) dw = empty(x, {r.cols}, pd);
@@ -506,8 +547,9 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
                                 x.data_ptr(), r.ld, wp, mp, rp, ptr(dx), least1(r.cols), ptr(dw),
                                 ptr(db), static_cast<gemm_dtype_t>(in),
                                 static_cast<gemm_dtype_t>(params), static_cast<gemm_dtype_t>(g),
-                                stream_arg(v[8], dev)),
+                                stream.get()),
         "gemm_layer_norm_backward");
+  stream.gives({&dx, &dw, &db});
   return wrap3(dx, dw, db);
   END_HANDLE_TH_ERRORS
 }
