@@ -17,6 +17,8 @@
 // tile that is not split goes from TMEM to memory directly.
 //
 // The gated pair runs as two MMAs a K-step, both weights' rows against the same token tile.
+#include <atomic>
+
 #include "ff_join.cuh"
 #include "tc_common.cuh"
 
@@ -365,8 +367,14 @@ cudaError_t launch_few(const CUtensorMap &tmX, const CUtensorMap &tmW, const CUt
 
 // The limit comes from how many SMs each GPC has: one kernel, at one CTA an SM, stands for all.
 int few_max_clusters(int splits) {
-  static int cached[4];
-  int &n = cached[splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3];
+  static std::atomic<int> cached[64][4];  // per device; 0 = not queried yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 1;
+  }
+  std::atomic<int> &known = cached[dev][splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3];
+  const int n = known.load(std::memory_order_relaxed);
   if (n > 0) return n;
   auto kernel = few_kernel<false, false>;
   cudaLaunchConfig_t cfg = {};
@@ -386,8 +394,8 @@ int few_max_clusters(int splits) {
     cudaGetLastError();
     return 1;
   }
-  n = got;
-  return n;
+  known.store(got, std::memory_order_relaxed);
+  return got;
 }
 
 size_t few_stage_bytes(bool gated, int tile_t) {

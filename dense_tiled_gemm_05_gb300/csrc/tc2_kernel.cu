@@ -24,6 +24,8 @@
 // row or column only is loaded as first to evict from L2, and every piece of a K-loop
 // then starts at a staggered K-block (k_rotate); pieces of tiles split along K hand their
 // fp32 sums to the tile's owner through the workspace (sk_schedule.h).
+#include <atomic>
+
 #include "tc_common.cuh"
 
 namespace gemm_gb300 {
@@ -466,7 +468,7 @@ cudaError_t launch_pair_majors(const TcVariant &v, const CUtensorMap &tmA, const
 }  // namespace
 
 int tc2_max_active_clusters() {
-  static int cached[64];  // per device; 0 = not queried yet
+  static std::atomic<int> cached[64];  // per device; 0 = not queried yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();

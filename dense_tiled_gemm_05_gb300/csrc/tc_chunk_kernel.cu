@@ -35,6 +35,8 @@
 //   warp 1      MMA issuer (leader CTA): tcgen05.mma.cta_group::2, M=256, N=256;
 //   warps 2-9   epilogue (both CTAs): warp w reads TMEM lanes 32*(w%4).. and one 128-column
 //               half of the tile, keeps 128 running sums per thread, stores once per tile.
+#include <atomic>
+
 #include "tc_common.cuh"
 
 namespace gemm_gb300 {
@@ -533,7 +535,7 @@ cudaLaunchConfig_t chunk_config(int grid, cudaStream_t s, cudaLaunchAttribute *a
 
 template <bool F16ACC>
 int max_active_clusters() {
-  static int cached[64];
+  static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
