@@ -2,8 +2,7 @@
 count: products of one input z and a weight of 1 (exact in every kernel), fp32 outputs.
 
 Bounds, relative to the sum of the magnitudes of the terms that a formula adds up: 3e-6 for the
-approximations (the normal tail's fit 1.2e-6, exponential and reciprocal 2 ulps each, a few
-roundings), and for the rounding of an exponent's argument t, formed in at most five steps,
+approximations (exponential and reciprocal 2 ulps each, the normal tail's fit, a few roundings), and for the rounding of an exponent's argument t, formed in at most five steps,
 5 2^-24 |t|: the relative error of e^t is the absolute one of t. Where a sigmoid s is close to 1,
 s (1 - s) carries s's own rounding of 2^-24, times z and, for tanh-gelu, its inner slope w. What
 is smaller than the least normal number may be flushed to 0, times up to 400 for z w."""
@@ -132,3 +131,32 @@ def test_gated_slopes_in_32_bits(h, act):
     assert_close(dx[:, 0], slope, magnitude, arg, near)
     dx, _, _ = h.gated_backward(dh, x, 0 * one, one, g, u, activation=act)
     assert_close(dx[:, 0], value, value.abs(), arg)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype,cta_pair,tokens", [("bf16", 1, 0), ("bf16", 2, 0), ("f16", 1, 0),
+                                                   ("f16", 2, 0), ("f32", 0, 0), ("bf16", 0, 1),
+                                                   ("f16", 0, 3), ("f32", 0, 1)])
+@pytest.mark.parametrize("long", [False, True])
+def test_fp32_outputs_have_fp32_activations(h, long, dtype, cta_pair, tokens, act):
+    """Also from 16-bit operands: 4 ulps of the complementary error function, or 2 of the
+    exponential, one of the reciprocal, 3e-7 of the tail's fit and two products, are below 1e-6.
+    (long: zeros up to a K that the few-token kernel shares out over a cluster.)"""
+    z, t = points(), TYPES[dtype]
+    k = 2048 if long else 1
+    x, w = torch.zeros(max(tokens, 1) if tokens else len(z), k, dtype=t, device="cuda"), None
+    if tokens:
+        w = torch.zeros(len(z), k, dtype=t, device="cuda")
+        x[:, 0], w[:, 0] = 1, z.to(t)
+        kept = w[:, 0]
+    else:
+        w = torch.zeros(8, k, dtype=t, device="cuda")
+        x[:, 0], w[:, 0] = z.to(t), 1
+        kept = x[:, 0]
+    h.set_option("cta_pair", cta_pair)
+    want, _, arg, _, _ = definition(kept, act)
+    y = h.matmul_epilogue(x, w.t(), activation=act, out_dtype="f32")
+    for v in y if tokens else y.t():
+        over = (v.double() - want).abs() - (1e-6 + 5 * 2.0 ** -24 * arg) * want.abs() - FLUSH
+        i = int(over.argmax())
+        assert float(over.max()) <= 0, "at point %d: %.9g, want %.9g" % (i, float(v[i]), float(want[i]))
