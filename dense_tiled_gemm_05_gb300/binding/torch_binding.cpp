@@ -189,7 +189,8 @@ int64_t row_ld(const Tensor &t, int64_t rows, int64_t cols, const char *what, in
   return r.ld;
 }
 
-// A row- or column-major operand (the rule of the ctypes binding's operand_layout).
+// A row- or column-major operand (the rule of the ctypes binding's operand_layout; a single row
+// or column may also have any stride along itself).
 struct Layout {
   gemm_layout_t layout;
   int64_t ld;
@@ -200,11 +201,24 @@ struct Layout {
       layout = GEMM_ROW_MAJOR, ld = most(most(s0, c), 1);
     } else if (s0 == 1 && (s1 >= most(r, 1) || c <= 1)) {
       layout = GEMM_COL_MAJOR, ld = most(most(s1, r), 1);
+    } else if (c == 1 && s0 >= 1) {
+      layout = GEMM_ROW_MAJOR, ld = s0;
+    } else if (r == 1 && s1 >= 1) {
+      layout = GEMM_COL_MAJOR, ld = s1;
     } else {
       fail(PyExc_ValueError, "operand must be row- or column-major, got stride (%lld, %lld)",
                        static_cast<long long>(s0), static_cast<long long>(s1));
     }
   }
+  // The same operand in the other layout, where a single row or column of it has both.
+  void become(gemm_layout_t other, const Tensor &t) {
+    if (layout == other) return;
+    if (other == GEMM_COL_MAJOR ? t.size(0) != 1 : t.size(1) != 1) return;
+    layout = other, ld = most1(t.stride(other == GEMM_COL_MAJOR ? 1 : 0));
+  }
+
+ private:
+  static int64_t most1(int64_t v) { return v > 1 ? v : 1; }
 };
 
 const void *vector(const Tensor &t, int64_t n, const char *what, int dev) {
@@ -380,6 +394,8 @@ struct Gated {
   Gated(const Tensor &x, const Tensor &wg, const Tensor &wu)
       : p(x, wg), ldx(Rows(x, "x").ld), g(wg), u((Product(x, wu), wu)) {
     if (wu.size(1) != p.N) fail(PyExc_ValueError, "w_gate and w_up must have one shape");
+    g.become(u.layout, wg);
+    u.become(g.layout, wu);
     if (g.layout != u.layout) fail(PyExc_ValueError, "w_gate and w_up must have one layout");
   }
 };

@@ -55,3 +55,29 @@ def test_gated_pair_of_one_input(h, M, F, need, dtype):
     check_gated(h, x, wg, wu, "silu", save=True)
     check_gated_backward(h, matrix(M, F, t, 4), x, wg, wu, matrix(M, F, t, 5), matrix(M, F, t, 6),
                          "silu", need)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_single_rows_and_columns_of_any_stride(h, dtype):
+    """X[:1, ::3] is a row, W[::2, :1] a column: each reads as a matrix of one line."""
+    t = TYPES[dtype]
+    a, b = matrix(4, 300, t, 1)[2:3, ::3], matrix(100, 40, t, 2, "col", scale=0.1)
+    assert a.shape == (1, 100) and a.stride() == (300, 3)
+    check_epilogue(h, a, b, "silu", None, None)
+    check_epilogue_backward(h, matrix(1, 40, t, 4), a, b, matrix(1, 40, t, 5), "silu")
+    a, b = matrix(9, 100, t, 1), matrix(200, 5, t, 2, scale=0.1)[::2, 1:2]
+    assert b.shape == (100, 1)
+    check_epilogue(h, a, b, "silu", None, None)
+    check_epilogue_backward(h, matrix(9, 1, t, 4), a, b, matrix(9, 1, t, 5), "silu")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("swap", [False, True])
+def test_gated_weights_of_one_row_or_column(h, swap, dtype):
+    """One weight tight, the other cut from a wider buffer: both have a common layout."""
+    t = TYPES[dtype]
+    for K, F, wg, wu in ((1, 40, matrix(1, 40, t, 2), column(40, t, 3)),
+                         (24, 1, matrix(24, 1, t, 2, "col"), matrix(24, 3, t, 3)[:, 1:2])):
+        x, wg, wu = matrix(7, K, t, 1), *((wu, wg) if swap else (wg, wu))
+        check_gated(h, x, wg, wu, "silu", save=True)
+        check_gated_backward(h, matrix(7, F, t, 4), x, wg, wu, matrix(7, F, t, 5), matrix(7, F, t, 6), "silu")
