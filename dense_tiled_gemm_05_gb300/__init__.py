@@ -418,6 +418,9 @@ class Gemm:
         return out
 
     # ------------------------------------------------------- feed-forward operators
+    #
+    # Like matmul they record nothing for automatic differentiation: outputs require no
+    # gradient, whatever the inputs do, and the backward methods are called by name.
 
     def matmul_epilogue(self, a, b, bias=None, activation=None, residual=None, out=None,
                         out_dtype=None, precision="default", save=False, stream=None):
@@ -425,7 +428,8 @@ class Gemm:
         a weight stored as [N, K] is passed as ``w.t()``), bias has N values, residual is
         M x N of the output's dtype (``out=residual`` updates it in place). activation: None,
         "relu", "gelu", "gelu_tanh", "silu" or "sigmoid". ``save=True`` returns (out, pre)
-        with pre = a @ b + bias for :meth:`matmul_epilogue_backward`."""
+        with pre = a @ b + bias for :meth:`matmul_epilogue_backward` (which a program calls
+        itself: no automatic differentiation, as in the other methods here)."""
         return (_native_module or native()).matmul_epilogue(
             self._address, a, b, bias, activation, residual, out, out_dtype, precision, save, stream)
 
@@ -435,7 +439,8 @@ class Gemm:
         """Gradients of :meth:`matmul_epilogue` from grad (M x N, the output's dtype) and the
         saved pre (needed unless there is no activation): (da, db, dbias), each None where
         ``need`` says so; da and db in the layouts of a and b, dbias in ``bias_dtype``
-        (default: a's). The residual's gradient is grad itself."""
+        (default: a's). The residual's gradient is grad itself. For 16-bit operands the slopes
+        are rounded to that type, with its range (f16: 65504), before the products."""
         return (_native_module or native()).matmul_epilogue_backward(
             self._address, grad, a, b, pre, activation, need, bias_dtype, precision, stream)
 

@@ -1,5 +1,5 @@
 // ff_internal.h -- launchers of the feed-forward operators' kernels, shared by the C ABI
-// (feed_forward.cu, layer_norm.cu) and the kernels' translation units. Internal to the
+// (feed_forward.cu) and the kernels' translation units. Internal to the
 // library.
 #pragma once
 

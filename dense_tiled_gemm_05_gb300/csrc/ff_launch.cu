@@ -109,12 +109,12 @@ double pair_cost(const FusedProduct &q, int64_t k_blocks, int64_t clusters, int 
 
 // The token kernel's rule: weights stored [features, K], one product, and few enough tokens
 // that its multiply-adds hide under the stream of weights. Measured on one GB300, us, token
-// kernel against few-token kernel: bf16 1 x 1024 x 1024 2.9 / 5.2, 1 x 4096 x 4096 (34 MB of
-// weights) 9.4 / 10.8, 1 x 8192 x 8192 (134 MB) 25.7 / 25.0, two tokens 34 MB 10.0 / 10.7, 134
-// MB 30 / 24, four tokens 17 MB 7.5 / 10.1, 34 MB 12.2 / 10.8: up to 80 MB of weights times
+// kernel against few-token kernel: bf16 1 x 1024 x 1024 2.9 / 5.9, 1 x 4096 x 4096 (34 MB of
+// weights) 9.3 / 11.3, 1 x 8192 x 8192 (134 MB) 25.7 / 25.0, two tokens 34 MB 9.9 / 11.3, 134
+// MB 30 / 24, four tokens 17 MB 6.2 / 8.0, 34 MB 12.2 / 10.8: up to 80 MB of weights times
 // tokens. Rows TMA cannot address it reads as they are, where the few-token kernel copies all
-// weights first (1 x 4097 x 1001: 7.4 / 23). fp32: up to eight tokens, against the exact
-// product on the tensor cores with its 30 us of fixed cost (8 x 4096 x 4096: 36 / 108).
+// weights first (1 x 4097 x 1001: 4.4 / 22). fp32: up to eight tokens, against the exact
+// product on the tensor cores with its 30 us of fixed cost (8 x 4096 x 4096: 45 / 109).
 bool plan_token(FusedProduct *q, int sm_count) {
   const int es = esize_of(q->in_dtype);
   if (q->M > kTokenMax || q->K2 > 0 || q->W.layout != GEMM_COL_MAJOR ||
@@ -156,8 +156,10 @@ bool four_wide(const FusedProduct &q) {
 // whether that is less than the exact product's on the tensor cores: 32 us, 18 us per 1024 of
 // K (the chunk drains; shared out over idle clusters from some 3000 on), the writing and reading
 // of the split operands, and 14 us where rows of the output are unaligned. Measured on one GB300, us, this kernel against that (with
-// silu and a residual): 512^3 13 / 43, 512 x 1024 x 1024 35 / 52, 64 x 2048 x 8192 66 / 102,
-// 1023 x 1000 x 1025 60 / 70, 2048 x 1024 x 1024 109 / 57, gated 1000 x 500 x 1000 61 / 86.
+// silu and a residual): 512^3 14 / 41, 512 x 1024 x 1024 35 / 51, 300 x 64 x 4096 26 / 83,
+// 64 x 2048 x 8192 73 / 136, 3000 x 64 x 8192 131 / 146, 2048 x 1024 x 1024 109 / 57, gated
+// 1000 x 500 x 1000 61 / 101. It errs where the two are close (1023 x 1000 x 1025 65 / 58) and
+// on the longest K (2432 x 64 x 65536 915 / 677).
 bool plan_tile(FusedProduct *q, int sm_count) {
   if (!q->exact || q->K2 > 0) return false;
   const int64_t sms = sm_count > 0 ? sm_count : 1;

@@ -10,14 +10,15 @@
 // multiply-adds for four or three 16-byte shared-memory reads. Operands arrive by 4-byte
 // cp.async -- any alignment, the ragged edges filled with zeros -- and are laid down K-major,
 // transposed on the way where K is their contiguous axis, in a ring of three 16-long steps.
-// Issue slots bound it (0.71 of them used, the multiply-add pipe at 0.52, before multiply-adds
-// went two to an instruction): 42 TFLOP/s on 3000 x 1000 x 2000 (one GB300), cuBLAS 51.
+// At 128 registers an SM holds 16 warps, which leave half of the issue slots unused (0.45 issued
+// a cycle and scheduler on 1023 x 1025 x 1000: 60.4 us, 35 TFLOP/s, one GB300; 42 on 3000 x 1000
+// x 2000, cuBLAS 51).
 // Where tiles are few, a cluster's CTAs share each tile's K and join as in ff_join.cuh.
 //
 // A share of K is added up in runs (tile_run_steps), whose sums are added in shared memory: a sum
 // of n terms of one sign in a row loses about sqrt(n) roundings of its own size (n = 8192 in each
-// of eight shares: 2e-6 of sum |x w|, twice the bound of exact products; in runs 3e-7), at 1 to
-// 4 % of the time of long products.
+// of eight shares: 2e-6 of sum |x w|, twice the bound of exact products; in runs 6e-7). On
+// one GB300 that takes 2 % of 1023 x 1025 x 1000 and 7 % of 64 x 2048 x 8192.
 #include <cmath>
 
 #include "ff_join.cuh"

@@ -12,8 +12,8 @@
 // shared memory in a fixed order.
 //
 // On one GB300 the tensor-core kernel (ff_few_kernel.cu) has about 5 us outside the stream,
-// this one about 3, but streams at up to 5.8 TB/s against 6.9, and its multiply-adds grow with
-// the tokens (plan_token in ff_launch.cu has the measurements and the rule).
+// this one about 3; on 134 MB of weights the two are level, and this one's multiply-adds grow
+// with the tokens (plan_token in ff_launch.cu has the measurements and the rule).
 #include "activation.cuh"
 #include "ff_kernels.h"
 #include "ptx.cuh"

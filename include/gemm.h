@@ -301,7 +301,12 @@ GEMM_API gemm_status_t gemm_softmax_rows(gemm_handle_t h, int64_t M, int64_t N, 
  * rows are then written as zeros); element sizes, alignment, precision modes, streams and
  * errors are those of gemm_run_ex (any alignment to the element size is accepted); an output
  * may not overlap an input or another output except where an entry says so; NaN and infinite
- * inputs give what the formulas give. Sums, statistics and activations are computed in fp32. */
+ * inputs give what the formulas give. Sums, statistics and activations are computed in fp32.
+ *
+ * The backward passes' slopes dz, dg and du are operands of tensor-core products and so rounded
+ * to the operands' type, with its range: for fp16, a slope above 65504 in magnitude is infinite
+ * in the gradients of the operands (not in dbias), and one below 6e-8 is 0. Scale the loss
+ * accordingly, or use bf16. */
 
 typedef enum {
   GEMM_ACT_NONE = 0,
