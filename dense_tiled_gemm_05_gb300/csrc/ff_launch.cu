@@ -156,8 +156,8 @@ bool four_wide(const FusedProduct &q) {
 // whether that is less than the exact product's on the tensor cores: 32 us, 18 us per 1024 of
 // K (the chunk drains; shared out over idle clusters from some 3000 on), the writing and reading
 // of the split operands, and 14 us where rows of the output are unaligned. Measured on one GB300, us, this kernel against that (with
-// silu and a residual): 512^3 14 / 41, 512 x 1024 x 1024 35 / 51, 300 x 64 x 4096 26 / 83,
-// 64 x 2048 x 8192 73 / 136, 3000 x 64 x 8192 131 / 146, 2048 x 1024 x 1024 109 / 57, gated
+// silu and a residual): 512^3 14 / 41, 512 x 1024 x 1024 35 / 51, 1023 x 1025 x 1000 60 / 69,
+// 300 x 64 x 4096 26 / 83, 64 x 2048 x 8192 73 / 136, 3000 x 64 x 8192 131 / 146, 2048 x 1024 x 1024 109 / 57, gated
 // 1000 x 500 x 1000 61 / 101. It errs where the two are close (1023 x 1000 x 1025 65 / 58) and
 // on the longest K (2432 x 64 x 65536 915 / 677).
 bool plan_tile(FusedProduct *q, int sm_count) {
