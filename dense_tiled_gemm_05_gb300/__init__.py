@@ -50,7 +50,9 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_ex", "gemm_get_s
            "gemm_run_strided", "gemm_plan_strided", "gemm_tune", "gemm_tune_clear",
            "gemm_softmax_rows", "gemm_set_kernel_events", "gemm_run_epilogue",
            "gemm_run_epilogue_backward", "gemm_run_gated", "gemm_run_gated_backward",
-           "gemm_layer_norm", "gemm_layer_norm_backward")
+           "gemm_layer_norm", "gemm_layer_norm_backward", "gemm_expert_sort",
+           "gemm_expert_gather", "gemm_expert_combine", "gemm_expert_combine_backward",
+           "gemm_dropout")
 
 
 class GemmError(RuntimeError):
@@ -156,6 +158,20 @@ def lib():
                 L.gemm_layer_norm_backward.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp,
                                                        vp, i64, vp, vp, i32, i32, i32, vp]
                 L.gemm_layer_norm_backward.restype = i32
+                L.gemm_expert_sort.argtypes = [vp, i64, i64, i64, vp, i64, i32, vp, vp, vp]
+                L.gemm_expert_sort.restype = i32
+                L.gemm_expert_gather.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, i32,
+                                                 vp]
+                L.gemm_expert_gather.restype = i32
+                L.gemm_expert_combine.argtypes = [vp, i64, i64, i64, vp, i64, i64, vp, vp, i32, vp,
+                                                  i64, vp, i64, i32, i32, vp]
+                L.gemm_expert_combine.restype = i32
+                L.gemm_expert_combine_backward.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, i64,
+                                                           vp, vp, i32, vp, i64, vp, i32, i32, vp]
+                L.gemm_expert_combine_backward.restype = i32
+                L.gemm_dropout.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64,
+                                           ctypes.c_double, vp, i32, vp]
+                L.gemm_dropout.restype = i32
                 L.gemm_tune_clear.argtypes = [vp]
                 L.gemm_tune_clear.restype = i32
                 L.gemm_get_status.argtypes = [vp, vp]
@@ -212,8 +228,8 @@ _native_module = None
 
 
 def native():
-    """The compiled binding of the feed-forward operators, with the C functions it calls;
-    raises if it has not been built."""
+    """The compiled binding of the feed-forward operators and those of experts, with the C
+    functions it calls; raises if it has not been built."""
     global _native_module
     if _native_module is None:
         L = lib()
@@ -225,7 +241,9 @@ def native():
         spec.loader.exec_module(m)
         m.init(*[ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "gemm_run_epilogue", "gemm_run_epilogue_backward", "gemm_run_gated",
-            "gemm_run_gated_backward", "gemm_layer_norm", "gemm_layer_norm_backward")], _check)
+            "gemm_run_gated_backward", "gemm_layer_norm", "gemm_layer_norm_backward",
+            "gemm_expert_sort", "gemm_expert_gather", "gemm_expert_combine",
+            "gemm_expert_combine_backward", "gemm_dropout")], _check)
         _native_module = m
     return _native_module
 
@@ -476,6 +494,60 @@ class Gemm:
         return (_native_module or native()).layer_norm_backward(
             self._address, grad, x, weight, mean, rstd, need, param_dtype, stream)
 
+    # --------------------------------------------------------- operators of experts
+    #
+    # ``position`` (int32, tokens x k) and ``offsets`` (int32, experts + 1) are those that
+    # expert_sort gives: pair (t, j) is token t's j-th choice and has row position[t, j] in the
+    # order by expert, expert e has the rows offsets[e] up to offsets[e + 1].
+
+    def expert_sort(self, ids, experts, stream=None):
+        """The stable order by expert of the tokens' choices: ids is tokens x k (int64 or int32,
+        as topk gives them), ``experts`` their number (at most 1024). Returns (position,
+        offsets); position is -1 where an id is outside [0, experts): no expert, as for the
+        padding of a batch."""
+        return (_native_module or native()).expert_sort(self._address, ids, experts, stream)
+
+    def expert_gather(self, x, position, out=None, stream=None):
+        """Rows in the order by expert: out[position[t, j]] = x[t]. out has tokens * k rows (or,
+        when given, as many as it has); those without a pair are left as they were."""
+        return (_native_module or native()).expert_gather(self._address, x, position, out, stream)
+
+    def expert_gather_backward(self, grad, position, stream=None):
+        """Gradient of :meth:`expert_gather`: dx[t] = sum_j grad[position[t, j]]."""
+        return (_native_module or native()).expert_combine(
+            self._address, grad, position, None, None, None, None, stream)
+
+    def expert_combine(self, rows, position, weights=None, residual=None, out=None, out_dtype=None,
+                       stream=None):
+        """The tokens' rows back from the order by expert, weighted: out[t] = sum_j weights[t, j]
+        rows[position[t, j]] + residual[t], a pair without a row adding nothing. weights (None:
+        1) is tokens x k in a dtype of its own, residual of the output's dtype
+        (``out=residual`` updates it in place)."""
+        return (_native_module or native()).expert_combine(
+            self._address, rows, position, weights, residual, out, out_dtype, stream)
+
+    def expert_combine_backward(self, grad, rows, position, weights=None, need=(True, True),
+                                out=None, stream=None):
+        """Gradients of :meth:`expert_combine` from grad (tokens x N): (drows, dweights), each
+        None where ``need`` says so (dweights also without weights). Rows without a pair are left
+        as they were in drows (``out``, when given). The residual's gradient is grad itself."""
+        return (_native_module or native()).expert_combine_backward(
+            self._address, grad, rows, position, weights, need, out, stream)
+
+    # --------------------------------------------------------------------- dropout
+
+    def dropout(self, x, p, key, residual=None, out=None, stream=None):
+        """residual + x * mask / (1 - p), with the mask of :meth:`dropout_backward` of the same
+        key: two int64 values in CUDA memory, a seed and an offset that a program advances from
+        call to call (also between replays of a captured graph, which reads them anew). p is
+        rounded to a multiple of 1 / 65536. ``out=x`` and ``out=residual`` run in place."""
+        return (_native_module or native()).dropout(self._address, x, p, key, residual, out, stream)
+
+    def dropout_backward(self, grad, p, key, out=None, stream=None):
+        """Gradient of :meth:`dropout` for x: grad * mask / (1 - p), the mask made again from the
+        key's values, which must be the forward call's. The residual's gradient is grad itself."""
+        return (_native_module or native()).dropout(self._address, grad, p, key, None, out, stream)
+
     def tune_clear(self):
         _check(lib().gemm_tune_clear(self._h), "gemm_tune_clear")
 
@@ -632,6 +704,41 @@ def layer_norm(x, weight=None, bias=None, **kw):
 def layer_norm_backward(grad, x, weight, mean, rstd, **kw):
     """Gradients of :func:`layer_norm`; see :meth:`Gemm.layer_norm_backward`."""
     return _handle_of(x).layer_norm_backward(grad, x, weight, mean, rstd, **kw)
+
+
+def expert_sort(ids, experts, **kw):
+    """The order of the tokens' choices by expert; see :meth:`Gemm.expert_sort`."""
+    return _handle_of(ids).expert_sort(ids, experts, **kw)
+
+
+def expert_gather(x, position, **kw):
+    """The tokens' rows in the order by expert; see :meth:`Gemm.expert_gather`."""
+    return _handle_of(x).expert_gather(x, position, **kw)
+
+
+def expert_gather_backward(grad, position, **kw):
+    """Gradient of :func:`expert_gather`; see :meth:`Gemm.expert_gather_backward`."""
+    return _handle_of(grad).expert_gather_backward(grad, position, **kw)
+
+
+def expert_combine(rows, position, weights=None, **kw):
+    """The rows back at their tokens, weighted; see :meth:`Gemm.expert_combine`."""
+    return _handle_of(rows).expert_combine(rows, position, weights, **kw)
+
+
+def expert_combine_backward(grad, rows, position, weights=None, **kw):
+    """Gradients of :func:`expert_combine`; see :meth:`Gemm.expert_combine_backward`."""
+    return _handle_of(grad).expert_combine_backward(grad, rows, position, weights, **kw)
+
+
+def dropout(x, p, key, **kw):
+    """residual + x * mask / (1 - p); see :meth:`Gemm.dropout`."""
+    return _handle_of(x).dropout(x, p, key, **kw)
+
+
+def dropout_backward(grad, p, key, **kw):
+    """Gradient of :func:`dropout`; see :meth:`Gemm.dropout_backward`."""
+    return _handle_of(grad).dropout_backward(grad, p, key, **kw)
 
 
 def matmul_host(a, b, out=None, out_dtype=None, precision="default", device=None):

@@ -1,4 +1,5 @@
-// torch_binding.cpp -- the feed-forward operators' calls on torch tensors, compiled.
+// torch_binding.cpp -- the calls of the feed-forward operators, of the operators of experts and
+// of dropout on torch tensors, compiled.
 //
 // A generation step calls them with a few microseconds of work each, so the host's part of a
 // call is part of its latency: marshalled in Python a layer norm took 11 us on the host (Grace
@@ -29,6 +30,11 @@ decltype(&gemm_run_gated) run_gated = nullptr;
 decltype(&gemm_run_gated_backward) run_gated_backward = nullptr;
 decltype(&gemm_layer_norm) run_layer_norm = nullptr;
 decltype(&gemm_layer_norm_backward) run_layer_norm_backward = nullptr;
+decltype(&gemm_expert_sort) run_expert_sort = nullptr;
+decltype(&gemm_expert_gather) run_expert_gather = nullptr;
+decltype(&gemm_expert_combine) run_expert_combine = nullptr;
+decltype(&gemm_expert_combine_backward) run_expert_combine_backward = nullptr;
+decltype(&gemm_dropout) run_dropout = nullptr;
 PyObject *raise_status = nullptr;  // raise_status(code, function name) raises
 
 using at::Tensor;
@@ -570,13 +576,220 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---------------------------------------------------------- operators of experts
+
+// The tokens' positions: int32, tokens x k.
+struct Pairs {
+  int64_t tokens, k;
+  int dev;
+  const int32_t *ptr;
+  explicit Pairs(const Tensor &t) {
+    dev = device_of(t, "position");
+    if (t.scalar_type() != at::kInt) fail(PyExc_TypeError, "position must be int32");
+    if (t.dim() != 2 || !t.is_contiguous())
+      fail(PyExc_ValueError, "position must be a contiguous tokens x k tensor");
+    tokens = t.size(0), k = t.size(1);
+    ptr = static_cast<const int32_t *>(t.data_ptr());
+  }
+};
+// One value for every pair.
+const void *pair_values(const Tensor &t, const Pairs &p, const char *what) {
+  if (t.dim() != 2 || t.size(0) != p.tokens || t.size(1) != p.k || !t.is_contiguous())
+    fail(PyExc_ValueError, "%s must be a contiguous %lld x %lld tensor", what,
+         static_cast<long long>(p.tokens), static_cast<long long>(p.k));
+  on_device(t, p.dev, what);
+  return t.data_ptr();
+}
+gemm_dtype_t type_of(const Tensor &t) { return static_cast<gemm_dtype_t>(code_of(t)); }
+
+// handle, ids, experts, stream
+PyObject *expert_sort(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 4);
+  const Tensor ids = tensor(v[1], "ids");
+  const int dev = device_of(ids, "ids");
+  if (ids.scalar_type() != at::kLong && ids.scalar_type() != at::kInt)
+    fail(PyExc_TypeError, "ids must be int64 or int32");
+  const Rows r(ids, "ids");
+  const long long experts = PyLong_AsLongLong(v[2]);
+  if (experts == -1 && PyErr_Occurred()) throw python_error();
+  if (experts < 1) fail(PyExc_ValueError, "experts must be at least 1");
+  const CallStream stream(v[3], dev);
+  stream.uses({&ids});
+  const Tensor position = empty(ids, {r.rows, r.cols}, at::kInt);
+  const Tensor offsets = empty(ids, {experts + 1}, at::kInt);
+  check(run_expert_sort(handle_arg(v[0]), r.rows, r.cols, experts, ids.data_ptr(), r.ld,
+                        static_cast<int32_t>(ids.element_size()),
+                        static_cast<int32_t *>(position.data_ptr()),
+                        static_cast<int32_t *>(offsets.data_ptr()), stream.get()),
+        "gemm_expert_sort");
+  stream.gives({&position, &offsets});
+  PyObject *a = wrap(position), *b = wrap(offsets);
+  return a && b ? Py_BuildValue("(NN)", a, b) : nullptr;
+  END_HANDLE_TH_ERRORS
+}
+
+// handle, x, position, out, stream
+PyObject *expert_gather(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 5);
+  const Tensor x = tensor(v[1], "x"), position = tensor(v[2], "position");
+  const Pairs p(position);
+  const Rows r(x, "x");
+  on_device(x, p.dev, "x");
+  if (r.rows != p.tokens) fail(PyExc_ValueError, "x and position must have one row a token");
+  const gemm_dtype_t dt = type_of(x);
+  Tensor out;
+  int64_t rows = p.tokens * p.k, ldy = least1(r.cols);
+  if (v[3] != Py_None) {
+    out = tensor(v[3], "out");
+    if (out.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
+    if (out.dim() != 2) fail(PyExc_ValueError, "out must be 2-D");
+    rows = out.size(0);
+    ldy = row_ld(out, rows, r.cols, "out", p.dev);
+  }
+  const CallStream stream(v[4], p.dev);
+  stream.uses({&x, &position, &out});
+  if (!out.defined()) out = empty(x, {rows, r.cols}, x.scalar_type());
+  check(run_expert_gather(handle_arg(v[0]), p.tokens, p.k, r.cols, x.data_ptr(), r.ld, p.ptr, rows,
+                          out.data_ptr(), ldy, dt, stream.get()),
+        "gemm_expert_gather");
+  stream.gives({&out});
+  return wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// handle, rows, position, weights, residual, out, out_dtype, stream
+PyObject *expert_combine(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 8);
+  const Tensor z = tensor(v[1], "rows"), position = tensor(v[2], "position");
+  const Pairs p(position);
+  const Rows r(z, "rows");
+  on_device(z, p.dev, "rows");
+  const gemm_dtype_t in = type_of(z);
+  Tensor weights, residual, out;
+  const void *wp = nullptr;
+  gemm_dtype_t wd = GEMM_F32;
+  if (v[3] != Py_None) {
+    weights = tensor(v[3], "weights");
+    wp = pair_values(weights, p, "weights");
+    wd = type_of(weights);
+  }
+  at::ScalarType od;
+  int64_t ldy = least1(r.cols), ldr = 0;
+  if (v[5] != Py_None) {
+    out = tensor(v[5], "out");
+    od = out.scalar_type();
+    code_of(od);
+    ldy = row_ld(out, p.tokens, r.cols, "out", p.dev);
+  } else {
+    od = dtype_arg(v[6], z.scalar_type());
+  }
+  if (v[4] != Py_None) {
+    residual = tensor(v[4], "residual");
+    if (residual.scalar_type() != od) fail(PyExc_TypeError, "residual must have the output's dtype");
+    ldr = row_ld(residual, p.tokens, r.cols, "residual", p.dev);
+  }
+  const CallStream stream(v[7], p.dev);
+  stream.uses({&z, &position, &weights, &residual, &out});
+  if (!out.defined()) out = empty(z, {p.tokens, r.cols}, od);
+  check(run_expert_combine(handle_arg(v[0]), p.tokens, p.k, r.cols, z.data_ptr(), r.ld, r.rows, p.ptr,
+                           wp, wd, ptr(residual), ldr, out.data_ptr(), ldy, in,
+                           static_cast<gemm_dtype_t>(code_of(od)), stream.get()),
+        "gemm_expert_combine");
+  stream.gives({&out});
+  return wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// handle, grad, rows, position, weights, need, out, stream
+PyObject *expert_combine_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 8);
+  const Tensor grad = tensor(v[1], "grad"), z = tensor(v[2], "rows"), position = tensor(v[3], "position");
+  const Pairs p(position);
+  const Rows r(z, "rows");
+  on_device(z, p.dev, "rows");
+  const int64_t lddy = row_ld(grad, p.tokens, r.cols, "grad", p.dev);
+  const gemm_dtype_t in = type_of(z), gt = type_of(grad);
+  if (!PyTuple_Check(v[5]) || PyTuple_GET_SIZE(v[5]) != 2)
+    fail(PyExc_ValueError, "need must be a tuple of two truth values");
+  const bool need_rows = truth(PyTuple_GET_ITEM(v[5], 0));
+  bool need_weights = truth(PyTuple_GET_ITEM(v[5], 1));
+  Tensor weights, dz, dw;
+  const void *wp = nullptr;
+  gemm_dtype_t wd = GEMM_F32;
+  if (v[4] != Py_None) {
+    weights = tensor(v[4], "weights");
+    wp = pair_values(weights, p, "weights");
+    wd = type_of(weights);
+  } else {
+    need_weights = false;
+  }
+  int64_t ldd = least1(r.cols);
+  if (need_rows && v[6] != Py_None) {
+    dz = tensor(v[6], "out");
+    if (dz.scalar_type() != z.scalar_type()) fail(PyExc_TypeError, "out must have rows' dtype");
+    ldd = row_ld(dz, r.rows, r.cols, "out", p.dev);
+  }
+  const CallStream stream(v[7], p.dev);
+  stream.uses({&grad, &z, &position, &weights, &dz});
+  if (need_rows && !dz.defined()) dz = empty(z, {r.rows, r.cols}, z.scalar_type());
+  if (need_weights) dw = empty(z, {p.tokens, p.k}, weights.scalar_type());
+  check(run_expert_combine_backward(handle_arg(v[0]), p.tokens, p.k, r.cols, grad.data_ptr(), lddy,
+                                    z.data_ptr(), r.ld, r.rows, p.ptr, wp, wd, ptr(dz), ldd, ptr(dw),
+                                    in, gt, stream.get()),
+        "gemm_expert_combine_backward");
+  stream.gives({&dz, &dw});
+  PyObject *a = wrap(dz), *b = wrap(dw);
+  return a && b ? Py_BuildValue("(NN)", a, b) : nullptr;
+  END_HANDLE_TH_ERRORS
+}
+
+// handle, x, p, key, residual, out, stream
+PyObject *dropout(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 7);
+  const Tensor x = tensor(v[1], "x"), key = tensor(v[3], "key");
+  const int dev = device_of(x, "x");
+  const Rows r(x, "x");
+  const gemm_dtype_t dt = type_of(x);
+  const double p = PyFloat_AsDouble(v[2]);
+  if (p == -1.0 && PyErr_Occurred()) throw python_error();
+  if (key.scalar_type() != at::kLong) fail(PyExc_TypeError, "key must be int64");
+  const void *kp = vector(key, 2, "key", dev);
+  Tensor residual, out;
+  int64_t ldr = 0, ldy = least1(r.cols);
+  if (v[4] != Py_None) {
+    residual = tensor(v[4], "residual");
+    if (residual.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "residual must have x's dtype");
+    ldr = row_ld(residual, r.rows, r.cols, "residual", dev);
+  }
+  if (v[5] != Py_None) {
+    out = tensor(v[5], "out");
+    if (out.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
+    ldy = row_ld(out, r.rows, r.cols, "out", dev);
+  }
+  const CallStream stream(v[6], dev);
+  stream.uses({&x, &key, &residual, &out});
+  if (!out.defined()) out = empty(x, {r.rows, r.cols}, x.scalar_type());
+  check(run_dropout(handle_arg(v[0]), r.rows, r.cols, x.data_ptr(), r.ld, ptr(residual), ldr,
+                    out.data_ptr(), ldy, p, static_cast<const uint64_t *>(kp), dt, stream.get()),
+        "gemm_dropout");
+  stream.gives({&out});
+  return wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 // Addresses of the C functions, in the order of the operators above, and the callable that
 // raises a status code.
 PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count(n, 7);
-  void *f[6];
-  for (int i = 0; i < 6; ++i) {
+  constexpr int kFunctions = 11;
+  count(n, kFunctions + 1);
+  void *f[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     f[i] = PyLong_AsVoidPtr(v[i]);
     if (!f[i]) fail(PyExc_ValueError, "address of a library function missing");
   }
@@ -586,9 +799,14 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
   run_gated_backward = reinterpret_cast<decltype(run_gated_backward)>(f[3]);
   run_layer_norm = reinterpret_cast<decltype(run_layer_norm)>(f[4]);
   run_layer_norm_backward = reinterpret_cast<decltype(run_layer_norm_backward)>(f[5]);
-  Py_INCREF(v[6]);
+  run_expert_sort = reinterpret_cast<decltype(run_expert_sort)>(f[6]);
+  run_expert_gather = reinterpret_cast<decltype(run_expert_gather)>(f[7]);
+  run_expert_combine = reinterpret_cast<decltype(run_expert_combine)>(f[8]);
+  run_expert_combine_backward = reinterpret_cast<decltype(run_expert_combine_backward)>(f[9]);
+  run_dropout = reinterpret_cast<decltype(run_dropout)>(f[10]);
+  Py_INCREF(v[kFunctions]);
   Py_XDECREF(raise_status);
-  raise_status = v[6];
+  raise_status = v[kFunctions];
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -597,7 +815,9 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init), FAST(matmul_epilogue), FAST(matmul_epilogue_backward),
                          FAST(gated), FAST(gated_backward), FAST(layer_norm),
-                         FAST(layer_norm_backward), {nullptr, nullptr, 0, nullptr}};
+                         FAST(layer_norm_backward), FAST(expert_sort), FAST(expert_gather),
+                         FAST(expert_combine), FAST(expert_combine_backward), FAST(dropout),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gemm_gb300_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,47 @@
+// expert_internal.h -- launchers of the kernels behind the operators of experts and of dropout,
+// shared by their C entries (experts.cu) and the kernels' translation units. Internal to the
+// library.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gemm.h"
+
+namespace gemm_gb300 {
+namespace ff {
+
+constexpr int64_t kMaxExperts = 1024;
+
+// Workspace of expert_sort_launch (0 when one CTA takes all ids).
+size_t expert_sort_bytes(int64_t n, int64_t experts);
+// position and offsets of `tokens` x `k` expert ids (8 or 4 bytes each), rows ld_ids apart.
+cudaError_t expert_sort_launch(const void *ids, int64_t ld_ids, bool wide, int64_t tokens, int64_t k,
+                               int64_t experts, int32_t *position, int32_t *offsets,
+                               void *workspace, int *launches, cudaStream_t s);
+
+// y[position[t, j]] = x[t] for the positions inside [0, rows).
+cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *position, void *y,
+                                 int64_t ldy, int es, int64_t tokens, int64_t k, int64_t rows,
+                                 int64_t N, cudaStream_t s);
+
+// y[t] = sum_j w[t, j] z[position[t, j]] + residual[t] (w null: 1; residual null: 0).
+cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
+                                  const void *w, int w_dtype, const void *residual, int64_t ldr,
+                                  void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
+                                  int64_t rows, int64_t N, cudaStream_t s);
+
+// dz[position[t, j]] = w[t, j] dy[t] (or null), dw[t, j] = dy[t] . z[position[t, j]] (or null).
+cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int grad_dtype,
+                                           const void *z, int64_t ldz, const int32_t *position,
+                                           const void *w, int w_dtype, void *dz, int64_t lddz,
+                                           int in_dtype, void *dw, int64_t tokens, int64_t k,
+                                           int64_t rows, int64_t N, int sm_count, cudaStream_t s);
+
+// y = x * mask * scale + residual (null: 0); key: two 64-bit words on the device.
+cudaError_t dropout_launch(const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
+                           int64_t ldy, int dtype, uint32_t threshold, float scale,
+                           const uint64_t *key, int64_t M, int64_t N, cudaStream_t s);
+
+}  // namespace ff
+}  // namespace gemm_gb300

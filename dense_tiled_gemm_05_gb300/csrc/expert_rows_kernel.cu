@@ -1,0 +1,266 @@
+// expert_rows_kernel.cu -- rows to their experts' order and back:
+//
+//   y[position[t, j]] = x[t]                                          (gather)
+//   y[t]  = sum_j w[t, j] z[position[t, j]] + residual[t]             (combine)
+//   dz[position[t, j]] = w[t, j] dy[t],  dw[t, j] = dy[t] . z[position[t, j]]
+//
+// All are bound by the bytes they move. A warp covers 256 columns, eight a lane, in 16-byte
+// accesses where the rows allow it. It reads a token's positions (and weights) with one load,
+// lane j the j-th, and hands them round by shuffles, so that all of a token's rows are on the
+// way at once. Each row is read and written once; every output element belongs to one lane,
+// which adds in the order of j in fp32 and rounds once. Positions outside [0, rows) are passed
+// over: nothing is read or written for them.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "expert_internal.h"
+#include "pdl.h"
+#include "ptx.cuh"
+
+namespace gemm_gb300 {
+namespace ff {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCols = 32 * VEC;  // columns a warp covers at a time
+
+bool aligned16(const void *p, int64_t ld, int es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0);
+}
+int esize(int dt) { return dt == GEMM_F32 ? 4 : 2; }
+
+// Column blocks along x; along y as many CTAs as keep 152 SMs busy, each warp walking tokens.
+dim3 token_grid(int64_t tokens, int64_t N) {
+  const int64_t gx = (N + kCols - 1) / kCols;
+  const int64_t all = (tokens + kWarps - 1) / kWarps;
+  int64_t gy = (3040 + gx - 1) / gx;
+  if (gy > all) gy = all;
+  if (gy > 65535) gy = 65535;
+  return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+}
+
+#define FF_TOKENS(t, tokens)                                                              \
+  for (int64_t t = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; t < tokens; \
+       t += static_cast<int64_t>(gridDim.y) * kWarps)
+
+// Row of a position, or -1.
+__device__ __forceinline__ int64_t row_of(int32_t position, int64_t rows) {
+  return position >= 0 && position < rows ? position : -1;
+}
+
+// The bits of a row's eight columns a lane (E: any type of their size).
+template <typename E, bool VECTOR>
+__device__ __forceinline__ void store_raw(const Columns<32, VECTOR> &cols, E *row, const E (&e)[VEC]) {
+  if (VECTOR) {
+    if (!cols.in(0)) return;
+#pragma unroll
+    for (int w = 0; w < VEC * static_cast<int>(sizeof(E)) / 16; ++w)
+      reinterpret_cast<uint4 *>(row + cols.at(0))[w] = reinterpret_cast<const uint4 *>(e)[w];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (cols.in(i)) row[cols.at(i)] = e[i];
+  }
+}
+
+template <typename E, bool VECTOR>
+__global__ void __launch_bounds__(kThreads)
+    gather_kernel(const E *__restrict__ x, int64_t ldx, const int32_t *__restrict__ position,
+                  E *__restrict__ y, int64_t ldy, int64_t tokens, int k, int64_t rows, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
+#pragma unroll 2
+  FF_TOKENS(t, tokens) {
+    alignas(16) E e[VEC];
+    cols.load(x + t * ldx, e);
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      const int n = min(32, k - j0);
+      const int32_t p = lane < n ? position[t * k + j0 + lane] : -1;
+      for (int j = 0; j < n; ++j) {
+        const int64_t r = row_of(__shfl_sync(0xffffffffu, p, j), rows);
+        if (r >= 0) store_raw(cols, y + r * ldy, e);
+      }
+    }
+  }
+}
+
+template <typename TI, typename TO, bool VECTOR>
+__global__ void __launch_bounds__(kThreads)
+    combine_kernel(const TI *__restrict__ z, int64_t ldz, const int32_t *__restrict__ position,
+                   const void *__restrict__ w, int w_dtype, const TO *residual, int64_t ldr, TO *y,
+                   int64_t ldy, int64_t tokens, int k, int64_t rows, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
+  constexpr int BATCH = sizeof(TI) == 4 ? 2 : 4;  // rows on the way at once
+  FF_TOKENS(t, tokens) {
+    float sum[VEC];
+    alignas(16) TO res[VEC];  // (y may be the residual: a lane reads its columns before it writes them)
+    if (residual) cols.load(residual + t * ldr, res);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) sum[c] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += 32) {
+      const int n = min(32, k - j0);
+      const int32_t p = lane < n ? position[t * k + j0 + lane] : -1;
+      const float f = !w ? 1.0f : lane < n ? load_any(w, w_dtype, t * k + j0 + lane) : 0.0f;
+      for (int j = 0; j < n; j += BATCH) {
+        alignas(16) TI e[BATCH][VEC];
+        float wj[BATCH];
+        bool has[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const int from = min(j + b, 31);
+          const int64_t r = row_of(__shfl_sync(0xffffffffu, p, from), rows);
+          wj[b] = __shfl_sync(0xffffffffu, f, from);
+          has[b] = j + b < n && r >= 0;
+          if (has[b]) cols.load(z + r * ldz, e[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+          if (has[b]) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) sum[c] = fmaf(wj[b], to_f32(e[b][c]), sum[c]);
+          }
+      }
+    }
+    if (residual) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) sum[c] += to_f32(res[c]);
+    }
+    cols.store(y + t * ldy, sum);
+  }
+}
+
+// `share` warps (1, 2, 4 or 8) take the row of one pair (t, j) together, 256 columns each in
+// turn, and add their sums in their order. The pairs of a token are neighbours, so that its dy
+// comes from L1 after the first.
+template <typename TG, typename TZ, bool VECTOR>
+__global__ void __launch_bounds__(kThreads)
+    combine_backward_kernel(const TG *__restrict__ dy, int64_t lddy, const TZ *__restrict__ z,
+                            int64_t ldz, const int32_t *__restrict__ position,
+                            const void *__restrict__ w, int w_dtype, TZ *__restrict__ dz,
+                            int64_t lddz, void *__restrict__ dw, int64_t tokens, int k, int64_t rows,
+                            int64_t N, int share) {
+  __shared__ float part[kWarps];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per_cta = kWarps / share, slot = warp / share, part_of = warp % share;
+  const int64_t pairs = tokens * k;
+  // (the CTA's warps walk together: barriers below)
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * per_cta; i0 < pairs;
+       i0 += static_cast<int64_t>(gridDim.x) * per_cta) {
+    const int64_t i = i0 + slot;
+    float dot = 0.0f;
+    if (i < pairs) {
+      const int64_t t = i / k;
+      const int64_t r = row_of(position[i], rows);
+      if (r >= 0) {
+        const float f = w ? load_any(w, w_dtype, i) : 1.0f;
+#pragma unroll 2
+        for (int64_t c0 = static_cast<int64_t>(part_of) * kCols; c0 < N;
+             c0 += static_cast<int64_t>(share) * kCols) {
+          const Columns<32, VECTOR> cols{c0, N, lane};
+          float g[VEC], v[VEC];
+          cols.load_f32(dy + t * lddy, g);
+          if (dw) {
+            cols.load_f32(z + r * ldz, v);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) dot = fmaf(g[c], v[c], dot);
+          }
+          if (dz) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[c] = f * g[c];
+            cols.store(dz + r * lddz, v);
+          }
+        }
+      }
+    }
+    if (!dw) continue;
+#pragma unroll
+    for (int d = 16; d; d /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (share == 1) {
+      if (lane == 0 && i < pairs) store_any(dw, w_dtype, i, dot);
+      continue;
+    }
+    if (lane == 0) part[warp] = dot;
+    __syncthreads();
+    if (part_of == 0 && lane == 0 && i < pairs) {
+      for (int q = 1; q < share; ++q) dot += part[warp + q];
+      store_any(dw, w_dtype, i, dot);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *position, void *y,
+                                 int64_t ldy, int es, int64_t tokens, int64_t k, int64_t rows,
+                                 int64_t N, cudaStream_t s) {
+  const bool vector = aligned16(x, ldx, es) && aligned16(y, ldy, es) && N % VEC == 0;
+  auto go = [&](auto *type, auto vec) {
+    using E = std::remove_pointer_t<decltype(type)>;
+    launch_pdl(gather_kernel<E, decltype(vec)::value>, token_grid(tokens, N), kThreads, 0, s,
+               static_cast<const E *>(x), ldx, position, static_cast<E *>(y), ldy, tokens,
+               static_cast<int>(k), rows, N);
+  };
+  if (es == 4)
+    vector ? go(static_cast<float *>(nullptr), std::true_type{}) : go(static_cast<float *>(nullptr), std::false_type{});
+  else
+    vector ? go(static_cast<__half *>(nullptr), std::true_type{}) : go(static_cast<__half *>(nullptr), std::false_type{});
+  return cudaGetLastError();
+}
+
+cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
+                                  const void *w, int w_dtype, const void *residual, int64_t ldr,
+                                  void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
+                                  int64_t rows, int64_t N, cudaStream_t s) {
+  const bool vector = aligned16(z, ldz, esize(in_dtype)) && aligned16(y, ldy, esize(out_dtype)) &&
+                      aligned16(residual, ldr, esize(out_dtype)) && N % VEC == 0;
+  FF_TYPED(in_dtype, TI, {
+    FF_TYPED(out_dtype, TO, {
+      auto go = [&](auto kernel) {
+        launch_pdl(kernel, token_grid(tokens, N), kThreads, 0, s, static_cast<const TI *>(z), ldz,
+                   position, w, w_dtype, static_cast<const TO *>(residual), ldr,
+                   static_cast<TO *>(y), ldy, tokens, static_cast<int>(k), rows, N);
+      };
+      vector ? go(combine_kernel<TI, TO, true>) : go(combine_kernel<TI, TO, false>);
+    })
+  })
+  return cudaGetLastError();
+}
+
+cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int grad_dtype,
+                                           const void *z, int64_t ldz, const int32_t *position,
+                                           const void *w, int w_dtype, void *dz, int64_t lddz,
+                                           int in_dtype, void *dw, int64_t tokens, int64_t k,
+                                           int64_t rows, int64_t N, int sm_count, cudaStream_t s) {
+  const int is = esize(in_dtype);
+  const bool vector = aligned16(dy, lddy, esize(grad_dtype)) && aligned16(dw ? z : nullptr, ldz, is) &&
+                      aligned16(dz, lddz, is) && N % VEC == 0;
+  // A pair's row is shared by warps while they have columns and the pairs alone do not fill the GPU.
+  const int64_t pairs = tokens * k, target = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * 32;
+  int share = 1;
+  while (share < kWarps && pairs * share < target && N > static_cast<int64_t>(share) * kCols) share *= 2;
+  const int per_cta = kWarps / share;
+  const int64_t ctas = std::min<int64_t>((pairs + per_cta - 1) / per_cta, int64_t{152} * 64);
+  FF_TYPED(grad_dtype, TG, {
+    FF_TYPED(in_dtype, TZ, {
+      auto go = [&](auto kernel) {
+        launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), kThreads, 0, s,
+                   static_cast<const TG *>(dy), lddy, static_cast<const TZ *>(z), ldz, position, w,
+                   w_dtype, static_cast<TZ *>(dz), lddz, dw, tokens, static_cast<int>(k), rows, N, share);
+      };
+      vector ? go(combine_backward_kernel<TG, TZ, true>) : go(combine_backward_kernel<TG, TZ, false>);
+    })
+  })
+  return cudaGetLastError();
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

@@ -5,61 +5,22 @@
 #include <cmath>
 
 #include "api_internal.h"
+#include "ff_checks.h"
 #include "ff_launch.h"
 
 using namespace gemm_gb300;
 using namespace gemm_gb300::api;
+using ff::bad_matrix;
 using ff::Carve;
+using ff::disjoint;
+using ff::launched;
+using ff::matrix_span;
+using ff::misaligned;
+using ff::Span;
+using ff::valid_act;
+using ff::vector_span;
 
 namespace {
-
-bool valid_act(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SIGMOID; }
-
-// A buffer of a call: the bytes it spans and, for a matrix, its line pitch and the bytes of a
-// line, to keep outputs off inputs and each other.
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // empty: lo == hi
-  uintptr_t pitch = 0, line = 0;
-  bool meets(const Span &o) const {
-    if (!(lo < o.hi && o.lo < hi)) return false;
-    // column ranges of one wider matrix share a span, but no element
-    if (pitch == 0 || pitch != o.pitch) return true;
-    const uintptr_t d = (lo < o.lo ? o.lo - lo : pitch - (lo - o.lo) % pitch) % pitch;
-    return d < line || d + o.line > pitch;
-  }
-};
-
-Span matrix_span(const void *p, int64_t rows, int64_t cols, int64_t ld, int layout, int es) {
-  Span s;
-  if (!p || rows <= 0 || cols <= 0) return s;
-  span_of(p, rows, cols, ld, layout, es, &s.lo, &s.hi);
-  s.pitch = static_cast<uintptr_t>(ld * es);
-  s.line = static_cast<uintptr_t>((layout == GEMM_ROW_MAJOR ? cols : rows) * es);
-  return s;
-}
-Span vector_span(const void *p, int64_t n, int es) {
-  return matrix_span(p, 1, n, n, GEMM_ROW_MAJOR, es);
-}
-
-// Outputs may meet neither inputs nor each other.
-template <int NO, int NI>
-bool disjoint(const Span (&outs)[NO], const Span (&ins)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    for (int j = 0; j < i; ++j)
-      if (outs[i].meets(outs[j])) return false;
-    for (int j = 0; j < NI; ++j)
-      if (outs[i].meets(ins[j])) return false;
-  }
-  return true;
-}
-
-bool misaligned(const void *p, int es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
-
-// A row-major or column-major operand of a call that is used: pointer and leading dimension.
-bool bad_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int layout) {
-  if (rows == 0 || cols == 0) return false;
-  return !p || ld < (layout == GEMM_ROW_MAJOR ? cols : rows);
-}
 
 // One product (its argument checks are the caller's own): few tokens and small exact fp32
 // products on the fused operators' kernels, others through the planner, whose kernels for many
@@ -83,12 +44,6 @@ gemm_status_t product(gemm_handle_t h, const Problem &P, cudaStream_t s) {
   Plan pl;
   const gemm_status_t st = make_plan(P, options_for(h, P), h->sm_count, &pl);
   return st == GEMM_OK ? execute(h, P, pl, s) : st;
-}
-
-gemm_status_t launched(gemm_handle_t h, cudaError_t e, const char *what, int n = 1) {
-  if (e != cudaSuccess) return cuda_fail(e, what);
-  h->launches += static_cast<uint64_t>(n);
-  return GEMM_OK;
 }
 
 int flip(int layout) { return layout == GEMM_ROW_MAJOR ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR; }

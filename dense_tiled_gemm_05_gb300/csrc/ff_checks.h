@@ -1,0 +1,66 @@
+// ff_checks.h -- argument checks shared by the C entries of the feed-forward operators and of
+// the operators of experts: the spans of a call's buffers, which outputs have to keep off, and
+// alignment. Host only; internal to the library.
+#pragma once
+
+#include "api_internal.h"
+
+namespace gemm_gb300 {
+namespace ff {
+
+inline bool valid_act(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SIGMOID; }
+
+// A buffer of a call: the bytes it spans and, for a matrix, its line pitch and the bytes of a
+// line, to keep outputs off inputs and each other.
+struct Span {
+  uintptr_t lo = 0, hi = 0;  // empty: lo == hi
+  uintptr_t pitch = 0, line = 0;
+  bool meets(const Span &o) const {
+    if (!(lo < o.hi && o.lo < hi)) return false;
+    // column ranges of one wider matrix share a span, but no element
+    if (pitch == 0 || pitch != o.pitch) return true;
+    const uintptr_t d = (lo < o.lo ? o.lo - lo : pitch - (lo - o.lo) % pitch) % pitch;
+    return d < line || d + o.line > pitch;
+  }
+};
+
+inline Span matrix_span(const void *p, int64_t rows, int64_t cols, int64_t ld, int layout, int es) {
+  Span s;
+  if (!p || rows <= 0 || cols <= 0) return s;
+  api::span_of(p, rows, cols, ld, layout, es, &s.lo, &s.hi);
+  s.pitch = static_cast<uintptr_t>(ld * es);
+  s.line = static_cast<uintptr_t>((layout == GEMM_ROW_MAJOR ? cols : rows) * es);
+  return s;
+}
+inline Span vector_span(const void *p, int64_t n, int es) {
+  return matrix_span(p, 1, n, n, GEMM_ROW_MAJOR, es);
+}
+
+// Outputs may meet neither inputs nor each other.
+template <int NO, int NI>
+bool disjoint(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (outs[i].meets(outs[j])) return false;
+    for (int j = 0; j < NI; ++j)
+      if (outs[i].meets(ins[j])) return false;
+  }
+  return true;
+}
+
+inline bool misaligned(const void *p, int es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
+
+// A row-major or column-major operand of a call that is used: pointer and leading dimension.
+inline bool bad_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int layout) {
+  if (rows == 0 || cols == 0) return false;
+  return !p || ld < (layout == GEMM_ROW_MAJOR ? cols : rows);
+}
+
+inline gemm_status_t launched(gemm_handle_t h, cudaError_t e, const char *what, int n = 1) {
+  if (e != cudaSuccess) return api::cuda_fail(e, what);
+  h->launches += static_cast<uint64_t>(n);
+  return GEMM_OK;
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

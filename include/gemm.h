@@ -420,6 +420,75 @@ GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int6
                                                 gemm_dtype_t in_dtype, gemm_dtype_t param_dtype,
                                                 gemm_dtype_t out_dtype, void *cuda_stream);
 
+/* --------------------------------------------------------- operators of experts
+ *
+ * The parts of a feed-forward block that is split over experts: the order of its tokens by
+ * expert, rows into that order and back, and dropout. Each of `tokens` tokens chooses `k` of
+ * `experts` experts; pair (t, j) is token t's j-th choice. Rows, types, alignment, streams,
+ * overlaps and errors are those of the feed-forward operators; sizes are at most INT32_MAX, and
+ * so is tokens * k (else GEMM_ERR_UNSUPPORTED). */
+
+/* The stable order of the pairs by expert: with ids[t, j] at ids + t * ld_ids + j (ld_ids >= k, in
+ * elements; integers of id_bytes bytes, 4 or 8),
+ *     offsets[e]  = number of pairs with an id in [0, e),                     e in [0, experts],
+ *     position[t * k + j] = offsets[id] + number of pairs before (t, j), row by row, with its id,
+ * and -1 for an id outside [0, experts): a pair without an expert, such as the padding of a batch.
+ * The pairs of expert e then have the rows offsets[e] .. offsets[e + 1] - 1. offsets has
+ * experts + 1 values. experts in [1, 1024] (more: UNSUPPORTED). tokens == 0 or k == 0 writes the
+ * offsets (zeros). */
+GEMM_API gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t k,
+                                        int64_t experts, const void *ids, int64_t ld_ids,
+                                        int32_t id_bytes, int32_t *position, int32_t *offsets,
+                                        void *cuda_stream);
+
+/* Y[position[t, j]] = X[t], bit for bit, for every pair whose position is in [0, rows): X is
+ * tokens x N, Y rows x N. Other rows of Y are left as they were. Two pairs with one position leave
+ * one of their tokens there. Its gradient is gemm_expert_combine without weights. */
+GEMM_API gemm_status_t gemm_expert_gather(gemm_handle_t h, int64_t tokens, int64_t k, int64_t N,
+                                          const void *X, int64_t ldx, const int32_t *position,
+                                          int64_t rows, void *Y, int64_t ldy, gemm_dtype_t dtype,
+                                          void *cuda_stream);
+
+/* Y[t] = sum_j weights[t, j] Z[position[t, j]] + residual[t], summed in fp32 in the order of j:
+ * Z is rows x N of in_dtype, Y tokens x N of out_dtype. A pair whose position is outside
+ * [0, rows) adds nothing, whatever its weight. weights: tokens x k contiguous values of
+ * weight_dtype, or NULL (1). residual: tokens x N of out_dtype, or NULL; Y may be the residual
+ * itself (same address and leading dimension). */
+GEMM_API gemm_status_t gemm_expert_combine(gemm_handle_t h, int64_t tokens, int64_t k, int64_t N,
+                                           const void *Z, int64_t ldz, int64_t rows,
+                                           const int32_t *position, const void *weights,
+                                           gemm_dtype_t weight_dtype, const void *residual,
+                                           int64_t ld_residual, void *Y, int64_t ldy,
+                                           gemm_dtype_t in_dtype, gemm_dtype_t out_dtype,
+                                           void *cuda_stream);
+
+/* Backward pass of gemm_expert_combine from dY (tokens x N of out_dtype):
+ *     dZ[position[t, j]] = weights[t, j] dY[t]                (rows x N of in_dtype),
+ *     dweights[t, j] = sum_n dY[t, n] Z[position[t, j], n]    (tokens x k of weight_dtype),
+ * 0 for a pair without a row; the residual's gradient is dY itself. Rows of dZ that no pair has
+ * are left as they were. Either of dZ and dweights may be NULL; Z is read for dweights only. The
+ * sums run in a fixed order: the same call gives the same bits. */
+GEMM_API gemm_status_t gemm_expert_combine_backward(
+    gemm_handle_t h, int64_t tokens, int64_t k, int64_t N, const void *dY, int64_t lddy,
+    const void *Z, int64_t ldz, int64_t rows, const int32_t *position, const void *weights,
+    gemm_dtype_t weight_dtype, void *dZ, int64_t lddz, void *dweights, gemm_dtype_t in_dtype,
+    gemm_dtype_t out_dtype, void *cuda_stream);
+
+/* Dropout: with q = floor(65536 p + 1/2), every element of the M x N matrix X is dropped with
+ * probability q / 65536, the others scaled by 65536 / (65536 - q),
+ *     Y_ij = (kept: X_ij * scale, dropped: 0, whatever X_ij is) + residual_ij,
+ * in fp32, rounded once. The mask is never stored: element (i, j) takes 16-bit number j % 8 (the
+ * low half of a word first) of the Philox4x32-10 block at the counter (j / 8, i, offset low,
+ * offset high) under the key (seed low, seed high), where key[0] = seed and key[1] = offset are
+ * two 64-bit words in DEVICE memory, 8-byte aligned, read when the call runs: a captured call takes the
+ * values of its replay. Calls with other offsets have other masks. The gradient is the same call
+ * on dY without the residual. residual may be NULL. Y may be X or the residual (same address and
+ * leading dimension). p in [0, 1), and q at most 65535; else INVALID_ARG. */
+GEMM_API gemm_status_t gemm_dropout(gemm_handle_t h, int64_t M, int64_t N, const void *X,
+                                    int64_t ldx, const void *residual, int64_t ld_residual,
+                                    void *Y, int64_t ldy, double p, const uint64_t *key,
+                                    gemm_dtype_t dtype, void *cuda_stream);
+
 /* ------------------------------------------------------------------- tuning */
 
 typedef struct {
