@@ -52,7 +52,8 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_run_ex", "gemm_get_s
            "gemm_run_epilogue_backward", "gemm_run_gated", "gemm_run_gated_backward",
            "gemm_layer_norm", "gemm_layer_norm_backward", "gemm_expert_sort",
            "gemm_expert_gather", "gemm_expert_combine", "gemm_expert_combine_backward",
-           "gemm_dropout")
+           "gemm_run_expert", "gemm_run_expert_backward", "gemm_run_expert_gated",
+           "gemm_run_expert_gated_backward", "gemm_dropout")
 
 
 class GemmError(RuntimeError):
@@ -169,6 +170,21 @@ def lib():
                 L.gemm_expert_combine_backward.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, i64,
                                                            vp, vp, i32, vp, i64, vp, i32, i32, vp]
                 L.gemm_expert_combine_backward.restype = i32
+                L.gemm_run_expert.argtypes = ([vp] + [i64] * 4 + [vp, i64, vp, i64, i64, vp, vp, i64]
+                                              + [i32] * 2 + [vp])
+                L.gemm_run_expert.restype = i32
+                L.gemm_run_expert_backward.argtypes = (
+                    [vp] + [i64] * 4 + [vp, i64, vp, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64]
+                    + [i32] * 2 + [vp])
+                L.gemm_run_expert_backward.restype = i32
+                L.gemm_run_expert_gated.argtypes = (
+                    [vp] + [i64] * 4 + [vp, i64] + [vp, i64, i64] * 2 + [vp] + [vp, i64] * 3
+                    + [i32] * 3 + [vp])
+                L.gemm_run_expert_gated.restype = i32
+                L.gemm_run_expert_gated_backward.argtypes = (
+                    [vp] + [i64] * 4 + [vp, i64] * 4 + [vp, i64, i64] * 2 + [vp, vp, i64]
+                    + [vp, i64, i64] * 2 + [i32] * 3 + [vp])
+                L.gemm_run_expert_gated_backward.restype = i32
                 L.gemm_dropout.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64,
                                            ctypes.c_double, vp, i32, vp]
                 L.gemm_dropout.restype = i32
@@ -243,7 +259,8 @@ def native():
             "gemm_run_epilogue", "gemm_run_epilogue_backward", "gemm_run_gated",
             "gemm_run_gated_backward", "gemm_layer_norm", "gemm_layer_norm_backward",
             "gemm_expert_sort", "gemm_expert_gather", "gemm_expert_combine",
-            "gemm_expert_combine_backward", "gemm_dropout")], _check)
+            "gemm_expert_combine_backward", "gemm_run_expert", "gemm_run_expert_backward",
+            "gemm_run_expert_gated", "gemm_run_expert_gated_backward", "gemm_dropout")], _check)
         _native_module = m
     return _native_module
 
@@ -534,6 +551,37 @@ class Gemm:
         return (_native_module or native()).expert_combine_backward(
             self._address, grad, rows, position, weights, need, out, stream)
 
+    def expert_matmul(self, x, w, offsets, out=None, stream=None):
+        """Each expert's rows against its weights: out[r] = x[r] @ w[e] for the rows r of e. x is
+        rows x K in the order by expert, w is experts x K x N (each row- or column-major; weights
+        stored as [experts, N, K] are passed as ``w.transpose(1, 2)``), f16 or bf16. Rows from
+        offsets[experts] on are left as they were (``out``, when given) and not read."""
+        return (_native_module or native()).expert_matmul(self._address, x, w, offsets, out, stream)
+
+    def expert_matmul_backward(self, grad, x, w, offsets, need=(True, True), out=None, stream=None):
+        """Gradients of :meth:`expert_matmul` from grad (rows x N): (dx, dw), each None where
+        ``need`` says so; dw in w's layout, zeros for an expert without rows. ``out`` receives dx,
+        whose rows without an expert are left as they were."""
+        return (_native_module or native()).expert_matmul_backward(
+            self._address, grad, x, w, offsets, need, out, stream)
+
+    def expert_gated(self, x, w_gate, w_up, offsets, activation="silu", out=None, save=False,
+                     stream=None):
+        """The gated pair of every expert: act(x[r] @ w_gate[e]) * (x[r] @ w_up[e]) for the rows r
+        of e; operands as for :meth:`expert_matmul`, both weights of one shape and layout.
+        ``save=True`` returns (out, gate, up) with the two products for
+        :meth:`expert_gated_backward` (column ranges of one rows x 2F buffer)."""
+        return (_native_module or native()).expert_gated(
+            self._address, x, w_gate, w_up, offsets, activation, out, save, stream)
+
+    def expert_gated_backward(self, grad, x, w_gate, w_up, gate, up, offsets, activation="silu",
+                              need=(True, True, True), out=None, stream=None):
+        """Gradients of :meth:`expert_gated` from grad (rows x F) and the saved gate and up: (dx,
+        dw_gate, dw_up), each None where ``need`` says so, the weights' in the weights' layout.
+        The slopes are rounded to the operands' type before the products. ``out`` receives dx."""
+        return (_native_module or native()).expert_gated_backward(
+            self._address, grad, x, w_gate, w_up, gate, up, offsets, activation, need, out, stream)
+
     # --------------------------------------------------------------------- dropout
 
     def dropout(self, x, p, key, residual=None, out=None, stream=None):
@@ -729,6 +777,26 @@ def expert_combine(rows, position, weights=None, **kw):
 def expert_combine_backward(grad, rows, position, weights=None, **kw):
     """Gradients of :func:`expert_combine`; see :meth:`Gemm.expert_combine_backward`."""
     return _handle_of(grad).expert_combine_backward(grad, rows, position, weights, **kw)
+
+
+def expert_matmul(x, w, offsets, **kw):
+    """Each expert's rows against its weights; see :meth:`Gemm.expert_matmul`."""
+    return _handle_of(x).expert_matmul(x, w, offsets, **kw)
+
+
+def expert_matmul_backward(grad, x, w, offsets, **kw):
+    """Gradients of :func:`expert_matmul`; see :meth:`Gemm.expert_matmul_backward`."""
+    return _handle_of(grad).expert_matmul_backward(grad, x, w, offsets, **kw)
+
+
+def expert_gated(x, w_gate, w_up, offsets, **kw):
+    """The gated pair of every expert; see :meth:`Gemm.expert_gated`."""
+    return _handle_of(x).expert_gated(x, w_gate, w_up, offsets, **kw)
+
+
+def expert_gated_backward(grad, x, w_gate, w_up, gate, up, offsets, **kw):
+    """Gradients of :func:`expert_gated`; see :meth:`Gemm.expert_gated_backward`."""
+    return _handle_of(grad).expert_gated_backward(grad, x, w_gate, w_up, gate, up, offsets, **kw)
 
 
 def dropout(x, p, key, **kw):

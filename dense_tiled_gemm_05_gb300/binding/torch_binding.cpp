@@ -34,6 +34,10 @@ decltype(&gemm_expert_sort) run_expert_sort = nullptr;
 decltype(&gemm_expert_gather) run_expert_gather = nullptr;
 decltype(&gemm_expert_combine) run_expert_combine = nullptr;
 decltype(&gemm_expert_combine_backward) run_expert_combine_backward = nullptr;
+decltype(&gemm_run_expert) run_expert = nullptr;
+decltype(&gemm_run_expert_backward) run_expert_backward = nullptr;
+decltype(&gemm_run_expert_gated) run_expert_gated = nullptr;
+decltype(&gemm_run_expert_gated_backward) run_expert_gated_backward = nullptr;
 decltype(&gemm_dropout) run_dropout = nullptr;
 PyObject *raise_status = nullptr;  // raise_status(code, function name) raises
 
@@ -200,8 +204,8 @@ int64_t row_ld(const Tensor &t, int64_t rows, int64_t cols, const char *what, in
 struct Layout {
   gemm_layout_t layout;
   int64_t ld;
-  explicit Layout(const Tensor &t) {
-    const int64_t r = t.size(0), c = t.size(1), s0 = t.stride(0), s1 = t.stride(1);
+  explicit Layout(const Tensor &t) : Layout(t.size(0), t.size(1), t.stride(0), t.stride(1)) {}
+  Layout(int64_t r, int64_t c, int64_t s0, int64_t s1) {
     auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
     if (s1 == 1 && (s0 >= most(c, 1) || r <= 1)) {
       layout = GEMM_ROW_MAJOR, ld = most(most(s0, c), 1);
@@ -747,6 +751,205 @@ PyObject *expert_combine_backward(PyObject *, PyObject *const *v, Py_ssize_t n) 
   END_HANDLE_TH_ERRORS
 }
 
+// The experts' weights: experts x K x N, each K x N row- or column-major.
+struct Weights {
+  int64_t experts, K, N, stride;
+  Layout layout;
+  explicit Weights(const Tensor &w)
+      : experts(w.dim() == 3 ? w.size(0) : 0),
+        K(w.dim() == 3 ? w.size(1) : 0),
+        N(w.dim() == 3 ? w.size(2) : 0),
+        stride(w.dim() == 3 ? w.stride(0) : 0),
+        layout(w.dim() == 3 ? Layout(K, N, w.stride(1), w.stride(2)) : Layout(0, 0, 1, 1)) {
+    if (w.dim() != 3) fail(PyExc_ValueError, "weights must be 3-D (experts x inputs x outputs)");
+    if (experts < 1) fail(PyExc_ValueError, "weights must have at least one expert");
+  }
+  // A gradient of the weights' shape in their layout, tight.
+  Tensor gradient(const Tensor &w) const {
+    if (layout.layout == GEMM_ROW_MAJOR) return empty(w, {experts, K, N}, w.scalar_type());
+    return empty(w, {experts, N, K}, w.scalar_type()).transpose(1, 2);
+  }
+  int64_t gradient_ld() const { return tight_ld(layout.layout, K, N); }
+  int64_t gradient_stride() const { return K * N; }
+};
+
+// The operands of an expert product: rows (rows x K), weights, offsets.
+struct ExpertOperands {
+  Weights w;
+  int dev;
+  int64_t rows, ldx;
+  const int32_t *offsets;
+  gemm_dtype_t dt;
+  ExpertOperands(const Tensor &x, const Tensor &wt, const Tensor &o) : w(wt) {
+    dev = device_of(x, "x");
+    on_device(wt, dev, "weights");
+    if (x.scalar_type() != wt.scalar_type()) fail(PyExc_TypeError, "operands must share a dtype");
+    dt = type_of(x);
+    const Rows r(x, "x");
+    if (r.cols != w.K)
+      fail(PyExc_ValueError, "inner dimensions differ: %lld vs %lld", static_cast<long long>(r.cols),
+           static_cast<long long>(w.K));
+    rows = r.rows, ldx = r.ld;
+    if (o.scalar_type() != at::kInt) fail(PyExc_TypeError, "offsets must be int32");
+    offsets = static_cast<const int32_t *>(vector(o, w.experts + 1, "offsets", dev));
+  }
+};
+
+// handle, x, w, offsets, out, stream
+PyObject *expert_matmul(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 6);
+  const Tensor x = tensor(v[1], "x"), w = tensor(v[2], "w"), offsets = tensor(v[3], "offsets");
+  const ExpertOperands q(x, w, offsets);
+  Tensor out;
+  int64_t ldy = least1(q.w.N);
+  if (v[4] != Py_None) {
+    out = tensor(v[4], "out");
+    if (out.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
+    ldy = row_ld(out, q.rows, q.w.N, "out", q.dev);
+  }
+  const CallStream stream(v[5], q.dev);
+  stream.uses({&x, &w, &offsets, &out});
+  if (!out.defined()) out = empty(x, {q.rows, q.w.N}, x.scalar_type());
+  check(run_expert(handle_arg(v[0]), q.w.experts, q.rows, q.w.N, q.w.K, x.data_ptr(), q.ldx, w.data_ptr(),
+                   q.w.layout.ld, q.w.stride, q.offsets, out.data_ptr(), ldy, q.dt, q.w.layout.layout,
+                   stream.get()),
+        "gemm_run_expert");
+  stream.gives({&out});
+  return wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// handle, grad, x, w, offsets, need, out, stream
+PyObject *expert_matmul_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 8);
+  const Tensor grad = tensor(v[1], "grad"), x = tensor(v[2], "x"), w = tensor(v[3], "w"),
+               offsets = tensor(v[4], "offsets");
+  const ExpertOperands q(x, w, offsets);
+  if (grad.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "grad must have x's dtype");
+  const int64_t lddy = row_ld(grad, q.rows, q.w.N, "grad", q.dev);
+  if (!PyTuple_Check(v[5]) || PyTuple_GET_SIZE(v[5]) != 2)
+    fail(PyExc_ValueError, "need must be a tuple of two truth values");
+  const bool need_x = truth(PyTuple_GET_ITEM(v[5], 0)), need_w = truth(PyTuple_GET_ITEM(v[5], 1));
+  Tensor dx, dw;
+  int64_t lddx = least1(q.w.K);
+  if (need_x && v[6] != Py_None) {
+    dx = tensor(v[6], "out");
+    if (dx.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
+    lddx = row_ld(dx, q.rows, q.w.K, "out", q.dev);
+  }
+  const CallStream stream(v[7], q.dev);
+  stream.uses({&grad, &x, &w, &offsets, &dx});
+  if (need_x && !dx.defined()) dx = empty(x, {q.rows, q.w.K}, x.scalar_type());
+  if (need_w) dw = q.w.gradient(w);
+  check(run_expert_backward(handle_arg(v[0]), q.w.experts, q.rows, q.w.N, q.w.K, grad.data_ptr(), lddy,
+                            x.data_ptr(), q.ldx, w.data_ptr(), q.w.layout.ld, q.w.stride, q.offsets,
+                            ptr(dx), lddx, ptr(dw), q.w.gradient_ld(), q.w.gradient_stride(), q.dt,
+                            q.w.layout.layout, stream.get()),
+        "gemm_run_expert_backward");
+  stream.gives({&dx, &dw});
+  PyObject *a = wrap(dx), *b = wrap(dw);
+  return a && b ? Py_BuildValue("(NN)", a, b) : nullptr;
+  END_HANDLE_TH_ERRORS
+}
+
+// The operands of the experts' gated pair.
+struct ExpertGated {
+  ExpertOperands q;
+  Weights u;
+  ExpertGated(const Tensor &x, const Tensor &wg, const Tensor &wu, const Tensor &offsets)
+      : q(x, wg, offsets), u(wu) {
+    if (wu.scalar_type() != wg.scalar_type()) fail(PyExc_TypeError, "operands must share a dtype");
+    on_device(wu, q.dev, "w_up");
+    if (u.experts != q.w.experts || u.K != q.w.K || u.N != q.w.N)
+      fail(PyExc_ValueError, "w_gate and w_up must have one shape");
+    if (u.layout.layout != q.w.layout.layout) {  // (a single row or column has both layouts)
+      const Tensor g0 = wg.select(0, 0), u0 = wu.select(0, 0);
+      q.w.layout.become(u.layout.layout, g0);
+      u.layout.become(q.w.layout.layout, u0);
+    }
+    if (u.layout.layout != q.w.layout.layout)
+      fail(PyExc_ValueError, "w_gate and w_up must have one layout");
+  }
+};
+
+// handle, x, w_gate, w_up, offsets, activation, out, save, stream
+PyObject *expert_gated(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 9);
+  const Tensor x = tensor(v[1], "x"), wg = tensor(v[2], "w_gate"), wu = tensor(v[3], "w_up"),
+               offsets = tensor(v[4], "offsets");
+  const ExpertGated e(x, wg, wu, offsets);
+  const ExpertOperands &q = e.q;
+  const int64_t F = q.w.N;
+  const gemm_activation_t act = activation_arg(v[5]);
+  const bool save = truth(v[7]);
+  Tensor out, gate, up;
+  int64_t ldh = least1(F);
+  if (v[6] != Py_None) {
+    out = tensor(v[6], "out");
+    if (out.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
+    ldh = row_ld(out, q.rows, F, "out", q.dev);
+  }
+  const CallStream stream(v[8], q.dev);
+  stream.uses({&x, &wg, &wu, &offsets, &out});
+  if (!out.defined()) out = empty(x, {q.rows, F}, x.scalar_type());
+  if (save) {  // column ranges of one buffer
+    const Tensor both = empty(x, {q.rows, 2 * F}, x.scalar_type());
+    gate = both.narrow(1, 0, F);
+    up = both.narrow(1, F, F);
+  }
+  check(run_expert_gated(handle_arg(v[0]), q.w.experts, q.rows, F, q.w.K, x.data_ptr(), q.ldx,
+                         wg.data_ptr(), q.w.layout.ld, q.w.stride, wu.data_ptr(), e.u.layout.ld,
+                         e.u.stride, q.offsets, out.data_ptr(), ldh, ptr(gate), 2 * F, ptr(up), 2 * F,
+                         q.dt, q.w.layout.layout, act, stream.get()),
+        "gemm_run_expert_gated");
+  stream.gives({&out, &gate, &up});
+  return save ? wrap3(out, gate, up) : wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// handle, grad, x, w_gate, w_up, gate, up, offsets, activation, need, out, stream
+PyObject *expert_gated_backward(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 12);
+  const Tensor grad = tensor(v[1], "grad"), x = tensor(v[2], "x"), wg = tensor(v[3], "w_gate"),
+               wu = tensor(v[4], "w_up"), gate = tensor(v[5], "gate"), up = tensor(v[6], "up"),
+               offsets = tensor(v[7], "offsets");
+  const ExpertGated e(x, wg, wu, offsets);
+  const ExpertOperands &q = e.q;
+  const int64_t F = q.w.N;
+  for (const Tensor *t : {&grad, &gate, &up})
+    if (t->scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "grad, gate and up must have x's dtype");
+  const int64_t lddh = row_ld(grad, q.rows, F, "grad", q.dev);
+  const int64_t ldg = row_ld(gate, q.rows, F, "gate", q.dev), ldu = row_ld(up, q.rows, F, "up", q.dev);
+  const gemm_activation_t act = activation_arg(v[8]);
+  const Need need(v[9]);
+  Tensor dx, dwg, dwu;
+  int64_t lddx = least1(q.w.K);
+  if (need.v[0] && v[10] != Py_None) {
+    dx = tensor(v[10], "out");
+    if (dx.scalar_type() != x.scalar_type()) fail(PyExc_TypeError, "out must have x's dtype");
+    lddx = row_ld(dx, q.rows, q.w.K, "out", q.dev);
+  }
+  const CallStream stream(v[11], q.dev);
+  stream.uses({&grad, &x, &wg, &wu, &gate, &up, &offsets, &dx});
+  if (need.v[0] && !dx.defined()) dx = empty(x, {q.rows, q.w.K}, x.scalar_type());
+  if (need.v[1]) dwg = q.w.gradient(wg);
+  if (need.v[2]) dwu = e.u.gradient(wu);
+  const int64_t ldw = q.w.gradient_ld(), step = q.w.gradient_stride();
+  check(run_expert_gated_backward(
+            handle_arg(v[0]), q.w.experts, q.rows, F, q.w.K, grad.data_ptr(), lddh, gate.data_ptr(), ldg,
+            up.data_ptr(), ldu, x.data_ptr(), q.ldx, wg.data_ptr(), q.w.layout.ld, q.w.stride,
+            wu.data_ptr(), e.u.layout.ld, e.u.stride, q.offsets, ptr(dx), lddx, ptr(dwg), ldw, step,
+            ptr(dwu), ldw, step, q.dt, q.w.layout.layout, act, stream.get()),
+        "gemm_run_expert_gated_backward");
+  stream.gives({&dx, &dwg, &dwu});
+  return wrap3(dx, dwg, dwu);
+  END_HANDLE_TH_ERRORS
+}
+
 // handle, x, p, key, residual, out, stream
 PyObject *dropout(PyObject *, PyObject *const *v, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -786,7 +989,7 @@ PyObject *dropout(PyObject *, PyObject *const *v, Py_ssize_t n) {
 // raises a status code.
 PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  constexpr int kFunctions = 11;
+  constexpr int kFunctions = 15;
   count(n, kFunctions + 1);
   void *f[kFunctions];
   for (int i = 0; i < kFunctions; ++i) {
@@ -803,7 +1006,11 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
   run_expert_gather = reinterpret_cast<decltype(run_expert_gather)>(f[7]);
   run_expert_combine = reinterpret_cast<decltype(run_expert_combine)>(f[8]);
   run_expert_combine_backward = reinterpret_cast<decltype(run_expert_combine_backward)>(f[9]);
-  run_dropout = reinterpret_cast<decltype(run_dropout)>(f[10]);
+  run_expert = reinterpret_cast<decltype(run_expert)>(f[10]);
+  run_expert_backward = reinterpret_cast<decltype(run_expert_backward)>(f[11]);
+  run_expert_gated = reinterpret_cast<decltype(run_expert_gated)>(f[12]);
+  run_expert_gated_backward = reinterpret_cast<decltype(run_expert_gated_backward)>(f[13]);
+  run_dropout = reinterpret_cast<decltype(run_dropout)>(f[14]);
   Py_INCREF(v[kFunctions]);
   Py_XDECREF(raise_status);
   raise_status = v[kFunctions];
@@ -816,7 +1023,9 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
 PyMethodDef methods[] = {FAST(init), FAST(matmul_epilogue), FAST(matmul_epilogue_backward),
                          FAST(gated), FAST(gated_backward), FAST(layer_norm),
                          FAST(layer_norm_backward), FAST(expert_sort), FAST(expert_gather),
-                         FAST(expert_combine), FAST(expert_combine_backward), FAST(dropout),
+                         FAST(expert_combine), FAST(expert_combine_backward), FAST(expert_matmul),
+                         FAST(expert_matmul_backward), FAST(expert_gated),
+                         FAST(expert_gated_backward), FAST(dropout),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gemm_gb300_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

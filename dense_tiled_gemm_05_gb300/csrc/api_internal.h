@@ -186,6 +186,11 @@ bool options_steer(gemm_handle_t h, const Problem &P);
 // launch.cu
 bool encode_2d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64_t outer,
                int64_t ld, uint32_t box_inner, uint32_t box_outer, bool atom32 = false);
+// 3D tensor map of `count` matrices `stride` elements apart, each `outer` lines of `inner`
+// elements with pitch ld: dims {inner, outer, count}, box {box_inner, box_outer, 1}, 128-byte
+// swizzle, zero fill outside each matrix.
+bool encode_3d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64_t outer,
+               int64_t count, int64_t ld, int64_t stride, uint32_t box_inner, uint32_t box_outer);
 cudaError_t stage_operand(const OperandPlan &o, void *dst, int es, cudaStream_t s);
 gemm_status_t launch_tc(const Problem &P, const Plan &pl, const void *a_ptr, int64_t a_ld,
                         const void *b_ptr, int64_t b_ld, int *status, uint64_t timeout_ns,

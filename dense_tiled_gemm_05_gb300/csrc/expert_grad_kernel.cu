@@ -1,0 +1,393 @@
+// expert_grad_kernel.cu -- the gradients of the experts' weights: for each expert e and the rows
+// r in [offsets[e], offsets[e + 1]),
+//
+//   D[e] = sum_r A[r]^T B[r]
+//
+// (A: rows x MA, B: rows x NB, D: experts x MA x NB). Both operands have the sum's axis outside
+// and are read in place, MN-major: a CTA pair's 256 x 256 tile takes 64 rows a K-block.
+//
+// An expert's rows end anywhere. TMA fills what lies outside the matrices with zeros, but the
+// rows after an expert's last are the next expert's (or nothing's: they may hold NaN), so they
+// have to leave both operands. The MMAs of the last K-block stop at the 16-row step that holds
+// the last row; of that step the up to 15 rows past it are set to zero in shared memory, by a
+// warp that the block's copies wait for instead of the MMA issuer (its own barrier), and that then
+// tells the issuer. All other blocks go from TMA to the MMAs as ever.
+//
+// The schedule is fixed, tile by tile through the experts, so that the clusters at work read the
+// same rows from L2. An expert without rows gets zeros. One accumulation a tile, in the rows'
+// order: the same call gives the same bits. Bound by the tensor cores for many rows an expert, by
+// the writing of D for few (256 rows of bf16: as long as its MMAs).
+#include "activation.cuh"
+#include "expert_kernels.h"
+#include "expert_tiles.cuh"
+#include "ff_boxes.cuh"
+
+namespace gemm_gb300 {
+namespace ff {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;                         // columns of A per CTA
+constexpr int BN = 256;
+constexpr int BK = 64;                          // rows a K-block
+constexpr int PANEL_BYTES = BK * kRowBytes;     // 64 columns of 64 rows
+constexpr int PANELS = 4;                       // two of A, two of B
+constexpr int STAGE_BYTES = PANELS * PANEL_BYTES;
+constexpr int STAGES = 5;
+constexpr int kEpi = 8;                         // epilogue warps
+constexpr int kMaskWarp = 2 + kEpi;
+constexpr int kGradThreads = 32 * (kMaskWarp + 1);
+constexpr int HALF = BN / 2;                    // accumulator columns of an epilogue warp
+constexpr int EPI_OFFSET = STAGES * STAGE_BYTES;
+constexpr int BAR_OFFSET = EPI_OFFSET + kEpi * 2 * kStoreBufBytes;
+constexpr int SMEM_BYTES = 232448;              // (all of it: see expert_pair_kernel.cu)
+static_assert(BAR_OFFSET + (4 * STAGES + 5) * 8 + (8 + 2 * STAGES) * 4 + 1024 <= SMEM_BYTES, "shared memory");
+
+// A tile of an expert: its rows and columns.
+struct Tile {
+  int e, lo, blocks, last;  // first row, K-blocks, rows of the last block
+  int m0, n0;
+  __device__ __forceinline__ Tile(const ExpertGradParams &p, int t) {
+    const int per = p.tiles_m * p.tiles_n;
+    e = t / per;
+    const int i = t - e * per;
+    m0 = i % p.tiles_m * (2 * BM);
+    n0 = i / p.tiles_m * BN;
+    lo = max(0, min(p.offsets[e], p.rows));
+    const int n = max(lo, min(p.offsets[e + 1], p.rows)) - lo;
+    blocks = (n + BK - 1) / BK;
+    last = n - (blocks - 1) * BK;
+  }
+  __device__ __forceinline__ bool ragged() const { return blocks > 0 && last % 16 != 0; }
+};
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src, int32_t x, int32_t y,
+                                             int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// This warp's 32 rows and 128 columns of the tile: by TMA through its two boxes, ...
+template <int OUT>
+__device__ __forceinline__ void store_boxes(const CUtensorMap *tmD, const ExpertGradParams &p, uint32_t t_row,
+                                            bool zero, uint8_t *boxes, int &next, int lane, int row0,
+                                            int n0, int e) {
+  if (row0 >= p.MA) return;
+#pragma unroll 1
+  for (int c = 0; c < HALF && n0 + c < p.NB; c += 64) {
+    float v[64];
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+    } else {
+      read_columns<64>(t_row + c, v);
+    }
+    uint8_t *box = boxes + next * kStoreBufBytes;
+    next ^= 1;
+    if (lane == 0) bulk_wait_group_read<1>();  // the store that last used this box has read it
+    __syncwarp();
+    write_box_row<OUT>(smem_u32(box) + lane * kRowBytes, lane, v);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(tmD, smem_u32(box), n0 + c, row0, e);
+      bulk_commit_group();
+    }
+  }
+}
+// ... or, where TMA cannot address D, each lane its row's elements.
+template <typename T>
+__device__ __forceinline__ void store_direct(const ExpertGradParams &p, uint32_t t_row, bool zero,
+                                             int row, int n0, int e) {
+#pragma unroll 1
+  for (int c = 0; c < HALF; c += 32) {
+    float v[32];
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    } else {
+      read_columns<32>(t_row + c, v);
+    }
+    if (row >= p.MA || n0 + c >= p.NB) continue;
+    T *d = static_cast<T *>(p.D) + e * p.stride_d + row * p.ldd + n0 + c;
+    const int n = min(32, p.NB - n0 - c);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) d[j] = from_f32<T>(v[j]);
+  }
+}
+
+__global__ void __launch_bounds__(kGradThreads, 1)
+    expert_grad_kernel(const __grid_constant__ ExpertGradMaps maps, const ExpertGradParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + BAR_OFFSET);
+  uint64_t *empty = full + STAGES;
+  uint64_t *tail = empty + STAGES;     // a ragged block's copies, this CTA's own
+  uint64_t *masked = tail + STAGES;    // (the leader's) both CTAs' surplus rows are zero
+  uint64_t *tmem_full = masked + STAGES;
+  uint64_t *tmem_empty = tmem_full + 2;
+  uint64_t *drain = tmem_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  // Teardown words, as in expert_pair_kernel.cu.
+  volatile uint32_t *xs = reinterpret_cast<volatile uint32_t *>(tmem_slot + 2);
+  volatile uint32_t *fill_bytes = xs + 4, *peer_bytes = fill_bytes + STAGES;
+  // stages whose own barriers were used for ragged blocks, and the parities of their last uses
+  volatile uint32_t *tails = peer_bytes + STAGES;
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
+      mbar_init(&masked[s], 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tmem_full[b], 1);
+      mbar_init(&tmem_empty[b], 2 * kEpi);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 6 + 2 * STAGES; ++i) xs[i] = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&maps.A);
+    prefetch_tensormap(&maps.B);
+    if (p.tma_out) prefetch_tensormap(&maps.D);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 2 * BN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  const int cluster_id = blockIdx.x / 2, clusters = gridDim.x / 2;
+  const int tiles = p.experts * p.tiles_m * p.tiles_n;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, issued = 0;
+      uint32_t tail_used = 0, tail_parity = 0;  // by stage: used at all, parity of the last use
+      bool ok = (p.debug_flags & kDebugStallProducer) == 0;
+      const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
+      const uint64_t keep = l2_policy_evict_last();
+      for (int t = cluster_id; ok && t < tiles; t += clusters) {
+        const Tile tile(p, t);
+        const int m0 = tile.m0 + static_cast<int>(rank) * BM, n0 = tile.n0 + static_cast<int>(rank) * BM;
+        for (int kb = 0; kb < tile.blocks; ++kb) {
+          if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
+            ok = false;  // test hook: this loader stops here, copies still in flight
+            break;
+          }
+          if (!mbar_wait(&empty[stage], phase ^ 1, wd)) {
+            ok = false;
+            break;
+          }
+          const bool own = kb == tile.blocks - 1 && tile.ragged();
+          uint32_t fb;
+          if (own) {
+            fb = mapa_shared(smem_u32(&tail[stage]), rank);
+            mbar_arrive_expect_tx(&tail[stage], STAGE_BYTES);
+            tail_parity = tail_used >> stage & 1 ? tail_parity ^ 1u << stage : tail_parity & ~(1u << stage);
+            tail_used |= 1u << stage;
+            if (leader) mbar_arrive(&full[stage]);
+          } else {
+            fb = mapa_shared(smem_u32(&full[stage]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2u * STAGE_BYTES);
+          }
+          fill_bytes[stage] = own ? 0 : STAGE_BYTES;
+          const uint32_t dst = smem_u32(smem + stage * STAGE_BYTES);
+          const int r0 = tile.lo + kb * BK;
+          tma_load_2d_pair_hint(dst, &maps.A, fb, m0, r0, keep);
+          tma_load_2d_pair_hint(dst + PANEL_BYTES, &maps.A, fb, m0 + 64, r0, keep);
+          tma_load_2d_pair_hint(dst + 2 * PANEL_BYTES, &maps.B, fb, n0, r0, keep);
+          tma_load_2d_pair_hint(dst + 3 * PANEL_BYTES, &maps.B, fb, n0 + 64, r0, keep);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      xs[0] = issued;
+      tails[0] = tail_used;
+      tails[1] = tail_parity;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer (leader)
+    if (leader && lane == 0) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0, masked_phase = 0;
+      bool ok = true;
+      for (int t = cluster_id; ok && t < tiles; t += clusters) {
+        const Tile tile(p, t);
+        if (tile.blocks == 0) continue;
+        if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < tile.blocks; ++kb) {
+          const bool end = kb == tile.blocks - 1;
+          ok = mbar_wait(&full[stage], phase, wd);
+          if (ok && end && tile.ragged()) {
+            ok = mbar_wait_cluster(&masked[stage], masked_phase >> stage & 1, wd);
+            masked_phase ^= 1u << stage;
+          }
+          if (!ok) break;
+          ++consumed;
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem + stage * STAGE_BYTES);
+          const uint32_t b_base = a_base + 2 * PANEL_BYTES;
+          const int steps = end ? (tile.last + 15) / 16 : BK / 16;
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint64_t ad = sdesc_sw128(a_base + kk * 16 * kRowBytes, PANEL_BYTES, 1024);
+            const uint64_t bd = sdesc_sw128(b_base + kk * 16 * kRowBytes, PANEL_BYTES, 1024);
+            mma_f16_pair(d_tmem, ad, bd, p.idesc, kb != 0 || kk != 0);
+          }
+          mma_commit_pair_multicast(&empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_multicast(&tmem_full[acc], 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      mma_commit_pair(drain);
+      drain_wait(drain, 0, p.timeout_ns);
+      xs[1] = consumed;
+    }
+    __syncwarp();
+  } else if (warp == kMaskWarp) {
+    // ------------------------- rows past an expert's last: zeros (both CTAs)
+    uint32_t fills = 0, phases = 0;
+    for (int t = cluster_id; t < tiles; t += clusters) {
+      const Tile tile(p, t);
+      fills += static_cast<uint32_t>(tile.blocks);
+      if (!tile.ragged()) continue;
+      const uint32_t stage = (fills - 1) % STAGES;
+      bool ok = mbar_wait(&tail[stage], phases >> stage & 1, wd);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      phases ^= 1u << stage;
+      const int first = tile.last, n = (tile.last + 15) / 16 * 16 - first;
+      // 8 pieces of 16 bytes a row and panel (a row is zero whatever its swizzle)
+      for (int i = lane; i < n * PANELS * 8; i += 32) {
+        const int piece = i % 8, panel = i / 8 % PANELS, row = first + i / (8 * PANELS);
+        *reinterpret_cast<uint4 *>(smem + stage * STAGE_BYTES + panel * PANEL_BYTES + row * kRowBytes +
+                                   piece * 16) = uint4{0, 0, 0, 0};
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&masked[stage]), 0));
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int e = warp - 2;
+    const int half = e / 4;
+    uint8_t *boxes = smem + EPI_OFFSET + e * 2 * kStoreBufBytes;
+    int next = 0;
+    uint32_t acc = 0, acc_phase = 0;
+    for (int t = cluster_id; t < tiles; t += clusters) {
+      const Tile tile(p, t);
+      const bool zero = tile.blocks == 0;
+      if (!zero) {
+        bool ok = mbar_wait_cluster(&tmem_full[acc], acc_phase, wd);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN + half * HALF;
+      const int row0 = tile.m0 + static_cast<int>(rank) * BM + quarter * 32, n0 = tile.n0 + half * HALF;
+      if (p.tma_out) {
+        if (p.dtype == GEMM_BF16)
+          store_boxes<GEMM_BF16>(&maps.D, p, t_row, zero, boxes, next, lane, row0, n0, tile.e);
+        else
+          store_boxes<GEMM_F16>(&maps.D, p, t_row, zero, boxes, next, lane, row0, n0, tile.e);
+      } else if (p.dtype == GEMM_BF16) {
+        store_direct<__nv_bfloat16>(p, t_row, zero, row0 + lane, n0, tile.e);
+      } else {
+        store_direct<__half>(p, t_row, zero, row0 + lane, n0, tile.e);
+      }
+      if (zero) continue;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(&xs[3])), rank ^ 1u),
+                          *abort_flag ? 1u : 0u);
+    if (!leader) {
+      st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(&xs[2])), 0), xs[0]);
+      for (int s = 0; s < STAGES; ++s)
+        st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(&peer_bytes[s])), 0),
+                              fill_bytes[s]);
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  if (*abort_flag || xs[3]) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < STAGES; ++i)
+        if (tails[0] >> i & 1) drain_wait(&tail[i], tails[1] >> i & 1, p.timeout_ns);
+    if (leader && threadIdx.x == 0)
+      drain_sized_fills<STAGES>(full, xs[1], xs[0], xs[2], fill_bytes, peer_bytes, p.timeout_ns);
+    cluster_sync();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * BN);
+  }
+}
+
+}  // namespace
+
+cudaError_t expert_grad_launch(const ExpertGradMaps &maps, const ExpertGradParams &p, int grid,
+                               cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(expert_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dependency_wait
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kGradThreads, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, expert_grad_kernel, maps, p);
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

@@ -38,6 +38,10 @@ cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int gra
                                            int in_dtype, void *dw, int64_t tokens, int64_t k,
                                            int64_t rows, int64_t N, int sm_count, cudaStream_t s);
 
+// Zeros in the rows of all experts (an empty sum).
+cudaError_t expert_zero_launch(void *y, int64_t ldy, int es, const int32_t *offsets, int64_t experts,
+                               int64_t rows, int64_t N, cudaStream_t s);
+
 // y = x * mask * scale + residual (null: 0); key: two 64-bit words on the device.
 cudaError_t dropout_launch(const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
                            int64_t ldy, int dtype, uint32_t threshold, float scale,

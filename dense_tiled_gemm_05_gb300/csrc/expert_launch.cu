@@ -1,0 +1,139 @@
+// expert_launch.cu -- host side of the experts' products (expert_pair_kernel.cu,
+// expert_grad_kernel.cu): copies of operands TMA cannot address, tensor maps, launch.
+#include <cstring>
+
+#include "expert_launch.h"
+
+using namespace gemm_gb300::api;
+
+namespace gemm_gb300 {
+namespace ff {
+
+namespace {
+
+constexpr int ES = 2;  // bytes an element: 16-bit types only
+
+bool addressable(const void *p, int64_t lines, int64_t ld, int64_t count, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (lines <= 1 || (ld * ES) % 16 == 0) &&
+         (count <= 1 || (stride * ES) % 16 == 0);
+}
+
+int64_t clusters_of(gemm_handle_t h, int64_t tiles) {
+  int64_t n = pair_slots(h->sm_count, h->max_ctas);
+  const int64_t fit = expert_max_clusters();
+  if (n > fit) n = fit;
+  return n > tiles ? tiles : n;
+}
+
+}  // namespace
+
+void ExpertOperand::plan(Carve *carve) {
+  staged = lines > 0 && len > 0 && !addressable(ptr, lines, ld, count, stride);
+  if (staged) offset = carve->take(count * lines * round_up(len, 8), ES);
+}
+
+gemm_status_t ExpertOperand::stage(gemm_handle_t h, char *buf, cudaStream_t s) {
+  if (!staged) return GEMM_OK;
+  const int64_t to_ld = round_up(len, 8);
+  char *to = buf + offset;
+  // matrices that follow one another are one with more lines
+  const bool one = count == 1 || stride == lines * ld;
+  for (int64_t e = 0; e < (one ? 1 : count); ++e) {
+    const cudaError_t err =
+        repack_launch(static_cast<const char *>(ptr) + e * stride * ES, ld, to + e * lines * to_ld * ES,
+                      to_ld, one ? count * lines : lines, len, ES, s);
+    if (err != cudaSuccess) return cuda_fail(err, "stage operand");
+    h->launches += 1;
+  }
+  ptr = to, ld = to_ld, stride = lines * to_ld;
+  staged = false;
+  return GEMM_OK;
+}
+
+ExpertOperand expert_weights(const void *W, int64_t ld, int64_t stride, int64_t experts, int64_t K,
+                             int64_t N, int layout) {
+  ExpertOperand o;
+  o.ptr = W, o.ld = ld, o.count = experts, o.stride = stride;
+  o.lines = layout == GEMM_ROW_MAJOR ? K : N;
+  o.len = layout == GEMM_ROW_MAJOR ? N : K;
+  return o;
+}
+
+ExpertOperand expert_rows(const void *X, int64_t ld, int64_t rows, int64_t cols) {
+  ExpertOperand o;
+  o.ptr = X, o.ld = ld, o.lines = rows, o.len = cols;
+  return o;
+}
+
+bool expert_tiles_fit(int64_t experts, int64_t rows, int64_t N, int64_t K) {
+  const int64_t n = (N + 127) / 128, k = (K + 127) / 128, t = rows / 128 + experts;
+  const int64_t most = INT32_MAX / 4;
+  return t <= most / n && t <= most / k && n <= most / k && experts <= most / (n * k);
+}
+
+gemm_status_t run_expert(gemm_handle_t h, const ExpertProduct &q, cudaStream_t s) {
+  ExpertMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  const bool two_x = q.second, two_w = q.second || q.gated;
+  // Boxes are one 128-byte row of K (or, with the features inside, of N) wide.
+  const uint32_t lines = q.w_mn ? 64u : 128u;
+  bool ok = encode_2d(&maps.X, q.dtype, q.X.ptr, q.X.len, q.X.lines, q.X.ld, 64, 32) &&
+            encode_3d(&maps.W, q.dtype, q.W.ptr, q.W.len, q.W.lines, q.W.count, q.W.ld, q.W.stride, 64, lines);
+  if (ok && two_x) ok = encode_2d(&maps.X2, q.dtype, q.X2.ptr, q.X2.len, q.X2.lines, q.X2.ld, 64, 32);
+  if (ok && two_w)
+    ok = encode_3d(&maps.W2, q.dtype, q.W2.ptr, q.W2.len, q.W2.lines, q.W2.count, q.W2.ld, q.W2.stride, 64, lines);
+  if (!ok) return GEMM_ERR_CUDA;
+  if (!two_x) maps.X2 = maps.X;  // never read
+  if (!two_w) maps.W2 = maps.W;
+  ExpertParams p{};
+  p.offsets = q.offsets;
+  p.experts = static_cast<int32_t>(q.experts), p.rows = static_cast<int32_t>(q.rows);
+  p.N = static_cast<int32_t>(q.N);
+  p.kb_first = static_cast<int32_t>((q.K + 63) / 64);
+  p.k_blocks = p.kb_first * (q.second ? 2 : 1);
+  p.idesc = make_idesc(q.dtype, q.w_mn, false, 0, 256);
+  p.dtype = q.dtype, p.act = q.act;
+  p.C = q.C, p.ldc = q.ldc;
+  p.pre = q.pre, p.ld_pre = q.ld_pre, p.pre2 = q.pre2, p.ld_pre2 = q.ld_pre2;
+  p.status = h->status;
+  p.timeout_ns = h->timeout_us * 1000ull;
+  p.debug_flags = stall_flags(h->stall_producer);
+  // at most one part tile an expert, and no more experts with rows than rows
+  const int64_t most = expert_tile_tokens(q.gated);
+  const int64_t tiles = (q.rows / most + (q.experts < q.rows ? q.experts : q.rows)) *
+                        ((q.N + kExpertFeatures - 1) / kExpertFeatures);
+  const cudaError_t e = expert_launch(q.gated, q.w_mn, maps, p, static_cast<int>(2 * clusters_of(h, tiles)), s);
+  if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
+  h->launches += 1;
+  return GEMM_OK;
+}
+
+gemm_status_t run_expert_grad(gemm_handle_t h, const ExpertGrad &q, cudaStream_t s) {
+  ExpertGradMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  ExpertGradParams p{};
+  p.offsets = q.offsets;
+  p.experts = static_cast<int32_t>(q.experts), p.rows = static_cast<int32_t>(q.rows);
+  p.MA = static_cast<int32_t>(q.A.len), p.NB = static_cast<int32_t>(q.B.len);
+  p.tiles_m = (p.MA + 255) / 256, p.tiles_n = (p.NB + 255) / 256;
+  p.idesc = make_idesc(q.dtype, true, true, 256, 256);
+  p.dtype = q.dtype;
+  p.D = q.D, p.ldd = q.ldd, p.stride_d = q.stride_d;
+  p.status = h->status;
+  p.timeout_ns = h->timeout_us * 1000ull;
+  p.debug_flags = stall_flags(h->stall_producer);
+  // TMA stores only where lines end on 16-byte boundaries (see the planner)
+  p.tma_out = (q.B.len * ES) % 16 == 0 && addressable(q.D, q.A.len, q.ldd, q.experts, q.stride_d);
+  if (!encode_2d(&maps.A, q.dtype, q.A.ptr, q.A.len, q.A.lines, q.A.ld, 64, 64) ||
+      !encode_2d(&maps.B, q.dtype, q.B.ptr, q.B.len, q.B.lines, q.B.ld, 64, 64) ||
+      (p.tma_out && !encode_3d(&maps.D, q.dtype, q.D, q.B.len, q.A.len, q.experts, q.ldd, q.stride_d, 64, 32)))
+    return GEMM_ERR_CUDA;
+  const int64_t tiles = q.experts * p.tiles_m * p.tiles_n;
+  const cudaError_t e = expert_grad_launch(maps, p, static_cast<int>(2 * clusters_of(h, tiles)), s);
+  if (e != cudaSuccess) return cuda_fail(e, "expert gradient launch");
+  h->launches += 1;
+  return GEMM_OK;
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

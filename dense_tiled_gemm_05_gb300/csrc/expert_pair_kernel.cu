@@ -1,0 +1,377 @@
+// expert_pair_kernel.cu -- the experts' products of rows sorted by expert:
+//
+//   Y[r] = X[r] W[e] (+ X2[r] W2[e])      or      H[r] = act(X[r] Wg[e]) * (X[r] Wu[e])
+//
+// for the rows r in [offsets[e], offsets[e + 1]) of each expert e.
+//
+// How many rows an expert has is known on the device only, from none to all of them, so tiles
+// have to fit any count. The weights are the MMA's M side, 256 output features on a pair of CTAs
+// (tcgen05.mma.cta_group::2), and the tokens its N side, whose width is set for every tile: an
+// expert's rows are shared evenly over tiles of at most 256 (gated: 128), each a multiple of 32
+// wide. 256-row tiles of tokens would waste half a tile an expert on average, an eighth of the
+// time at 1024 rows and a third at 256. The same layout serves few tokens: a 32-column MMA, and
+// the time is that of the weights' stream.
+//
+// Grid: one cluster of two CTAs for every two SMs, which walk the tiles of all experts; every
+// role reads the offsets from shared memory and finds its tiles by itself, so that no table is
+// made and no count goes to the host. Token tiles run fastest: the clusters at work share weights
+// through L2, and the next tile's loads and MMAs run under a tile's epilogue (two accumulators).
+//
+// The gated pair runs as two MMAs a K-step against the same tokens, g and u in the same lanes of
+// two column ranges of TMEM, so that each epilogue thread has both.
+//
+// The epilogue has one feature a lane and tokens along its registers: a warp's store of one
+// token is 32 neighbouring features. Rows past the expert's last are not stored (they are the
+// next expert's); bound: tensor cores for many rows an expert, HBM for few.
+#include <atomic>
+
+#include "activation.cuh"
+#include "expert_kernels.h"
+#include "expert_tiles.cuh"
+
+namespace gemm_gb300 {
+namespace ff {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;                         // features per CTA
+constexpr int BK = 64;
+constexpr int W_BYTES = BM * kRowBytes;         // one weight box (MN-major: two panels)
+constexpr int PANEL_BYTES = BK * kRowBytes;
+constexpr int BOX_TOKENS = 32;                  // tokens a TMA box
+constexpr int BOX_BYTES = BOX_TOKENS * kRowBytes;
+constexpr int kEpi = 8;                         // epilogue warps
+constexpr int kExpertThreads = 64 + 32 * kEpi;
+constexpr int ACC = 256;                        // TMEM columns of an accumulator (gated: 128 each)
+
+template <bool GATED>
+struct Shape {
+  static constexpr int TOKENS = GATED ? 128 : 256;
+  static constexpr int X_BYTES = TOKENS / 2 * kRowBytes;  // a CTA's half of the tokens
+  static constexpr int STAGE = (GATED ? 2 : 1) * W_BYTES + X_BYTES;
+  static constexpr int STAGES = GATED ? 5 : 6;
+  static constexpr int OFFSETS = STAGES * STAGE;
+  static constexpr int BARS = OFFSETS + (static_cast<int>(kMaxExperts) + 1) * 4 + 4;
+  static constexpr int END = BARS + (2 * STAGES + 5) * 8 + (6 + 2 * STAGES) * 4;
+};
+// All of an SM's shared memory, because the CTA takes all of its TMEM: no CTA that needs some
+// then shares the SM.
+constexpr int SMEM_BYTES = 232448;
+static_assert(Shape<false>::BARS % 8 == 0 && Shape<true>::BARS % 8 == 0, "barriers are aligned");
+static_assert(Shape<false>::END + 1024 <= SMEM_BYTES && Shape<true>::END + 1024 <= SMEM_BYTES, "shared memory");
+
+// The tokens' columns c0 .. c0 + 31 of this lane's feature, for `left` tokens from row on.
+template <typename T, bool GATED>
+__device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, int64_t row, int left,
+                                       int64_t f) {
+  uint32_t r[32], q[32];
+  __syncwarp();
+  tmem_ld_32x32b_x32(t_acc, r);
+  if (GATED) tmem_ld_32x32b_x32(t_acc + ACC / 2, q);
+  tmem_wait_ld();
+  if (f >= p.N) return;
+  float a[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(r[j]);
+  if (GATED) {
+    if (p.pre) {
+      T *g = static_cast<T *>(p.pre) + row * p.ld_pre + f;
+      T *u = static_cast<T *>(p.pre2) + row * p.ld_pre2 + f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < left) {
+          g[j * p.ld_pre] = from_f32<T>(a[j]);
+          u[j * p.ld_pre2] = from_f32<T>(__uint_as_float(q[j]));
+        }
+    }
+    activate_all<true>(a, p.act);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) a[j] *= __uint_as_float(q[j]);
+  }
+  T *y = static_cast<T *>(p.C) + row * p.ldc + f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < left) y[j * p.ldc] = from_f32<T>(a[j]);
+}
+
+template <bool GATED, bool W_MN>
+__global__ void __launch_bounds__(kExpertThreads, 1)
+    expert_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
+  using S = Shape<GATED>;
+  constexpr int STAGES = S::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  int32_t *offsets = reinterpret_cast<int32_t *>(smem + S::OFFSETS);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::BARS);
+  uint64_t *empty = full + STAGES;
+  uint64_t *tmem_full = empty + STAGES;
+  uint64_t *tmem_empty = tmem_full + 2;
+  uint64_t *drain = tmem_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  // Teardown words: fills this CTA's loader issued, fills the MMA issuer consumed, fills the
+  // peer's loader issued, whether the other CTA aborted; then the bytes of each stage's last
+  // fill, of this CTA and of the peer.
+  volatile uint32_t *xs = reinterpret_cast<volatile uint32_t *>(tmem_slot + 2);
+  volatile uint32_t *fill_bytes = xs + 4, *peer_bytes = fill_bytes + STAGES;
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tmem_full[b], 1);
+      mbar_init(&tmem_empty[b], 2 * kEpi);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 4 + 2 * STAGES; ++i) xs[i] = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&maps.X);
+    prefetch_tensormap(&maps.W);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 2 * ACC);
+    tmem_relinquish_pair();
+  }
+  // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
+  grid_dependency_wait();
+  load_offsets(offsets, p.offsets, p.experts, p.rows, kExpertThreads);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  grid_launch_dependents();
+  const uint32_t tmem_base = *tmem_slot;
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  const int cluster_id = blockIdx.x / 2, clusters = gridDim.x / 2;
+  ExpertWalk walk(offsets, p.experts, (p.N + kExpertFeatures - 1) / kExpertFeatures, S::TOKENS, 32);
+
+  if (warp == 0) {
+    // ------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, issued = 0;
+      bool ok = (p.debug_flags & kDebugStallProducer) == 0;
+      const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
+      const uint64_t keep = l2_policy_evict_last();
+      for (int t = cluster_id; ok && walk.seek(t); t += clusters) {
+        const int i = t - walk.begin;
+        const int row0 = walk.lo + i % walk.lines * walk.width;
+        const int f0 = i / walk.lines * kExpertFeatures + static_cast<int>(rank) * BM;
+        const int half = (min(walk.width, walk.hi - row0) + 31) / 32 * 16;  // a CTA's tokens
+        const int x_row = row0 + static_cast<int>(rank) * half;
+        const int boxes = (half + BOX_TOKENS - 1) / BOX_TOKENS;
+        const uint32_t bytes = static_cast<uint32_t>((GATED ? 2 : 1) * W_BYTES + boxes * BOX_BYTES);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
+            ok = false;  // test hook: this loader stops here, copies still in flight
+            break;
+          }
+          if (!mbar_wait(&empty[stage], phase ^ 1, wd)) {
+            ok = false;
+            break;
+          }
+          fill_bytes[stage] = bytes;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+          const uint32_t w_dst = smem_u32(smem + stage * S::STAGE);
+          const uint32_t x_dst = w_dst + (GATED ? 2 : 1) * W_BYTES;
+          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);  // the leader's barrier
+          const bool second = !GATED && kb >= p.kb_first;
+          const int k0 = (second ? kb - p.kb_first : kb) * BK;
+#pragma unroll
+          for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+            const CUtensorMap *w = (GATED ? m == 1 : second) ? &maps.W2 : &maps.W;
+            const uint32_t dst = w_dst + m * W_BYTES;
+            if (W_MN) {
+              tma_load_3d_pair(dst, w, fb, f0, k0, walk.e);
+              tma_load_3d_pair(dst + PANEL_BYTES, w, fb, f0 + 64, k0, walk.e);
+            } else {
+              tma_load_3d_pair(dst, w, fb, k0, f0, walk.e);
+            }
+          }
+          const CUtensorMap *x = second ? &maps.X2 : &maps.X;
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_pair_hint(x_dst + b * BOX_BYTES, x, fb, k0, x_row + b * BOX_TOKENS, keep);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      xs[0] = issued;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer (leader)
+    if (leader && lane == 0) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0;
+      bool ok = true;
+      for (int t = cluster_id; ok && walk.seek(t); t += clusters) {
+        const int row0 = walk.lo + (t - walk.begin) % walk.lines * walk.width;
+        const uint32_t n = static_cast<uint32_t>(min(walk.width, walk.hi - row0) + 31) / 32 * 32;
+        const uint32_t idesc = p.idesc | (n >> 3) << 17;
+        if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * ACC;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&full[stage], phase, wd)) {
+            ok = false;
+            break;
+          }
+          ++consumed;
+          tc_fence_after();
+          const uint32_t w_base = smem_u32(smem + stage * S::STAGE);
+          const uint32_t x_base = w_base + (GATED ? 2 : 1) * W_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t xd = sdesc_sw128(x_base + kk * 32, 16, 1024);
+#pragma unroll
+            for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+              const uint32_t w = w_base + m * W_BYTES;
+              const uint64_t wdesc = W_MN ? sdesc_sw128(w + kk * 16 * kRowBytes, PANEL_BYTES, 1024)
+                                          : sdesc_sw128(w + kk * 32, 16, 1024);
+              mma_f16_pair(d_tmem + m * (ACC / 2), wdesc, xd, idesc, kb != 0 || kk != 0);
+            }
+          }
+          mma_commit_pair_multicast(&empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_multicast(&tmem_full[acc], 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      mma_commit_pair(drain);
+      drain_wait(drain, 0, p.timeout_ns);
+      xs[1] = consumed;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int half = (warp - 2) / 4;  // takes every other 32 tokens
+    uint32_t acc = 0, acc_phase = 0;
+    for (int t = cluster_id; walk.seek(t); t += clusters) {
+      const int i = t - walk.begin;
+      const int row0 = walk.lo + i % walk.lines * walk.width;
+      const int tokens = min(walk.width, walk.hi - row0);
+      const int64_t f = i / walk.lines * kExpertFeatures + static_cast<int>(rank) * BM + quarter * 32 + lane;
+      bool ok = mbar_wait_cluster(&tmem_full[acc], acc_phase, wd);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC;
+      for (int c0 = half * 32; c0 < tokens; c0 += 64) {
+        if (p.dtype == GEMM_BF16)
+          finish<__nv_bfloat16, GATED>(p, t_row + c0, row0 + c0, tokens - c0, f);
+        else
+          finish<__half, GATED>(p, t_row + c0, row0 + c0, tokens - c0, f);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+    __syncwarp();
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(&xs[3])), rank ^ 1u),
+                          *abort_flag ? 1u : 0u);
+    if (!leader) {
+      st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(&xs[2])), 0), xs[0]);
+      for (int s = 0; s < STAGES; ++s)
+        st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t *>(&peer_bytes[s])), 0),
+                              fill_bytes[s]);
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  if (*abort_flag || xs[3]) {
+    if (leader && threadIdx.x == 0)
+      drain_sized_fills<STAGES>(full, xs[1], xs[0], xs[2], fill_bytes, peer_bytes, p.timeout_ns);
+    cluster_sync();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * ACC);
+  }
+}
+
+template <bool GATED, bool W_MN>
+cudaError_t launch_expert(const ExpertMaps &maps, const ExpertParams &p, int grid, cudaStream_t s) {
+  auto kernel = expert_kernel<GATED, W_MN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see grid_dependency_wait
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kExpertThreads, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+}
+
+}  // namespace
+
+cudaError_t expert_launch(bool gated, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
+                          int grid, cudaStream_t s) {
+  if (gated)
+    return w_mn ? launch_expert<true, true>(maps, p, grid, s) : launch_expert<true, false>(maps, p, grid, s);
+  return w_mn ? launch_expert<false, true>(maps, p, grid, s) : launch_expert<false, false>(maps, p, grid, s);
+}
+
+int expert_max_clusters() {
+  static std::atomic<int> cached[64];  // per device; 0 = not queried yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 1;
+  }
+  const int known = cached[dev].load(std::memory_order_relaxed);
+  if (known > 0) return known;
+  auto kernel = expert_kernel<false, false>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kExpertThreads, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int got = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess || got < 1) {
+    cudaGetLastError();
+    return 1;
+  }
+  cached[dev].store(got, std::memory_order_relaxed);
+  return got;
+}
+
+}  // namespace ff
+}  // namespace gemm_gb300

@@ -197,7 +197,32 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <typename E>
+__global__ void __launch_bounds__(kThreads)
+    zero_kernel(E *__restrict__ y, int64_t ldy, const int32_t *__restrict__ offsets, int experts,
+                int64_t rows, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t lo = max(offsets[0], 0), hi = min(static_cast<int64_t>(offsets[experts]), rows);
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (col >= N) return;
+  for (int64_t r = lo + blockIdx.y; r < hi; r += gridDim.y) y[r * ldy + col] = from_f32<E>(0.0f);
+}
+
 }  // namespace
+
+cudaError_t expert_zero_launch(void *y, int64_t ldy, int es, const int32_t *offsets, int64_t experts,
+                               int64_t rows, int64_t N, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((N + kThreads - 1) / kThreads),
+                  static_cast<unsigned>(std::min<int64_t>(rows, 1024)));
+  if (es == 4)
+    launch_pdl(zero_kernel<float>, grid, kThreads, 0, s, static_cast<float *>(y), ldy, offsets,
+               static_cast<int>(experts), rows, N);
+  else
+    launch_pdl(zero_kernel<__half>, grid, kThreads, 0, s, static_cast<__half *>(y), ldy, offsets,
+               static_cast<int>(experts), rows, N);
+  return cudaGetLastError();
+}
 
 cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *position, void *y,
                                  int64_t ldy, int es, int64_t tokens, int64_t k, int64_t rows,

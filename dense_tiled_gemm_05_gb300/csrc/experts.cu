@@ -1,19 +1,21 @@
 // experts.cu -- the C ABI of the operators of experts (the order of tokens by expert, rows into
-// that order and back) and of dropout: argument checks and launches.
+// that order and back, the experts' products) and of dropout: argument checks and launches.
 #include <cmath>
 
 #include "api_internal.h"
-#include "expert_internal.h"
+#include "expert_launch.h"
 #include "ff_checks.h"
 
 using namespace gemm_gb300;
 using namespace gemm_gb300::api;
 using ff::bad_matrix;
+using ff::Carve;
 using ff::disjoint;
 using ff::launched;
 using ff::matrix_span;
 using ff::misaligned;
 using ff::Span;
+using ff::valid_act;
 using ff::vector_span;
 
 namespace {
@@ -22,6 +24,70 @@ bool too_large(int64_t tokens, int64_t k, int64_t rows, int64_t N) {
   return tokens > INT32_MAX || k > INT32_MAX || rows > INT32_MAX || N > INT32_MAX ||
          tokens * k > INT32_MAX;
 }
+
+// Elements that the K x N weights of one expert span.
+int64_t weight_span(int64_t K, int64_t N, int64_t ld, int layout) {
+  return layout == GEMM_ROW_MAJOR ? (K - 1) * ld + N : (N - 1) * ld + K;
+}
+bool bad_weights(const void *W, int64_t experts, int64_t K, int64_t N, int64_t ld, int64_t stride,
+                 int layout) {
+  if (K == 0 || N == 0) return false;
+  return bad_matrix(W, K, N, ld, layout) || (experts > 1 && stride < weight_span(K, N, ld, layout));
+}
+// All experts' weights. (Two sets may be parts of one buffer, expert by expert.)
+Span weights_span(const void *W, int64_t experts, int64_t K, int64_t N, int64_t ld, int64_t stride,
+                  int layout, int es) {
+  if (K == 0 || N == 0) return Span{};
+  const int64_t one = weight_span(K, N, ld, layout);
+  return matrix_span(W, experts, one, experts > 1 ? stride : one, GEMM_ROW_MAJOR, es);
+}
+
+// What the experts' products share: sizes and offsets.
+gemm_status_t check_experts(gemm_handle_t h, int64_t experts, int64_t rows, int64_t N, int64_t K,
+                            const int32_t *offsets, int dtype, int layout) {
+  if (!h || experts < 1 || rows < 0 || N < 0 || K < 0 || !offsets || !valid_dtype(dtype) ||
+      !valid_layout(layout))
+    return GEMM_ERR_INVALID_ARG;
+  if (dtype == GEMM_F32 || experts > ff::kMaxExperts || too_large(rows, 1, N, K) || 2 * N > INT32_MAX ||
+      !ff::expert_tiles_fit(experts, rows, N > 0 ? N : 1, K > 0 ? K : 1))
+    return GEMM_ERR_UNSUPPORTED;
+  return misaligned(offsets, 4) ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+gemm_status_t zero_rows(gemm_handle_t h, void *Y, int64_t ld, int64_t rows, int64_t N,
+                        const int32_t *offsets, int64_t experts, cudaStream_t s) {
+  if (!Y || rows == 0 || N == 0) return GEMM_OK;
+  return launched(h, ff::expert_zero_launch(Y, ld, 2, offsets, experts, rows, N, s), "expert zero launch");
+}
+// The experts' weight gradients without any row.
+gemm_status_t zero_weights(gemm_handle_t h, void *D, int64_t experts, int64_t lines, int64_t len,
+                           int64_t ld, int64_t stride, int dtype, cudaStream_t s) {
+  const bool one = experts == 1 || stride == lines * ld;
+  for (int64_t e = 0; e < (one ? 1 : experts); ++e) {
+    const gemm_status_t st =
+        launched(h, zero_fill_launch(static_cast<char *>(D) + e * stride * 2, ld, one ? experts * lines : lines,
+                                     len, dtype, s), "zero fill");
+    if (st != GEMM_OK) return st;
+  }
+  return GEMM_OK;
+}
+
+// dW of one product from its operands' rows.
+gemm_status_t weight_gradient(gemm_handle_t h, const ff::ExpertOperand &X, const ff::ExpertOperand &dY,
+                              int64_t experts, const int32_t *offsets, void *dW, int64_t ld,
+                              int64_t stride, int dtype, int layout, cudaStream_t s) {
+  const ff::ExpertOperand &A = layout == GEMM_ROW_MAJOR ? X : dY, &B = layout == GEMM_ROW_MAJOR ? dY : X;
+  if (!dW || A.len == 0 || B.len == 0) return GEMM_OK;
+  if (X.lines == 0) return zero_weights(h, dW, experts, A.len, B.len, ld, stride, dtype, s);
+  ff::ExpertGrad q;
+  q.experts = experts, q.rows = X.lines, q.offsets = offsets;
+  q.A = A, q.B = B;
+  q.dtype = dtype;
+  q.D = dW, q.ldd = ld, q.stride_d = stride;
+  return ff::run_expert_grad(h, q, s);
+}
+
+int flip(int layout) { return layout == GEMM_ROW_MAJOR ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR; }
 
 }  // namespace
 
@@ -142,6 +208,238 @@ GEMM_API gemm_status_t gemm_expert_combine_backward(
                          weights || dweights ? weight_dtype : GEMM_F32, dZ, lddz, in_dtype, dweights,
                          tokens, k, rows, N, h->sm_count, static_cast<cudaStream_t>(cuda_stream)),
                   "expert combine backward launch");
+}
+
+GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t rows, int64_t N,
+                                       int64_t K, const void *X, int64_t ldx, const void *W,
+                                       int64_t ldw, int64_t stride_w, const int32_t *offsets,
+                                       void *Y, int64_t ldy, gemm_dtype_t dtype,
+                                       gemm_layout_t w_layout, void *cuda_stream) {
+  gemm_status_t st = check_experts(h, experts, rows, N, K, offsets, dtype, w_layout);
+  if (st != GEMM_OK) return st;
+  if (rows == 0 || N == 0) return GEMM_OK;
+  if (bad_matrix(X, rows, K, ldx, GEMM_ROW_MAJOR) || bad_matrix(Y, rows, N, ldy, GEMM_ROW_MAJOR) ||
+      bad_weights(W, experts, K, N, ldw, stride_w, w_layout))
+    return GEMM_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  if (misaligned(X, es) || misaligned(W, es) || misaligned(Y, es)) return GEMM_ERR_ALIGNMENT;
+  const Span outs[] = {matrix_span(Y, rows, N, ldy, GEMM_ROW_MAJOR, es)};
+  const Span ins[] = {matrix_span(X, rows, K, ldx, GEMM_ROW_MAJOR, es),
+                      weights_span(W, experts, K, N, ldw, stride_w, w_layout, es),
+                      vector_span(offsets, experts + 1, 4)};
+  if (!disjoint(outs, ins)) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (K == 0) return zero_rows(h, Y, ldy, rows, N, offsets, experts, s);
+  ff::ExpertProduct q;
+  q.experts = experts, q.rows = rows, q.N = N, q.K = K, q.offsets = offsets;
+  q.X = ff::expert_rows(X, ldx, rows, K);
+  q.W = ff::expert_weights(W, ldw, stride_w, experts, K, N, w_layout);
+  q.w_mn = w_layout == GEMM_ROW_MAJOR;
+  q.dtype = dtype;
+  q.C = Y, q.ldc = ldy;
+  Carve carve;
+  q.X.plan(&carve), q.W.plan(&carve);
+  st = reserve(h, h->ff, carve.bytes, s);
+  char *buf = static_cast<char *>(h->ff.ptr);
+  if (st == GEMM_OK) st = q.X.stage(h, buf, s);
+  if (st == GEMM_OK) st = q.W.stage(h, buf, s);
+  return st == GEMM_OK ? ff::run_expert(h, q, s) : st;
+}
+
+GEMM_API gemm_status_t gemm_run_expert_backward(
+    gemm_handle_t h, int64_t experts, int64_t rows, int64_t N, int64_t K, const void *dY,
+    int64_t lddy, const void *X, int64_t ldx, const void *W, int64_t ldw, int64_t stride_w,
+    const int32_t *offsets, void *dX, int64_t lddx, void *dW, int64_t lddw, int64_t stride_dw,
+    gemm_dtype_t dtype, gemm_layout_t w_layout, void *cuda_stream) {
+  gemm_status_t st = check_experts(h, experts, rows, N, K, offsets, dtype, w_layout);
+  if (st != GEMM_OK) return st;
+  if (bad_matrix(dY, rows, N, lddy, GEMM_ROW_MAJOR) ||
+      (dX && (bad_matrix(dX, rows, K, lddx, GEMM_ROW_MAJOR) ||
+              bad_weights(W, experts, K, N, ldw, stride_w, w_layout))) ||
+      (dW && (bad_matrix(X, rows, K, ldx, GEMM_ROW_MAJOR) ||
+              bad_weights(dW, experts, K, N, lddw, stride_dw, w_layout))))
+    return GEMM_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  if (misaligned(dY, es) || (dW && misaligned(X, es)) || (dX && misaligned(W, es)) ||
+      misaligned(dX, es) || misaligned(dW, es))
+    return GEMM_ERR_ALIGNMENT;
+  const Span outs[] = {matrix_span(dX, rows, K, lddx, GEMM_ROW_MAJOR, es),
+                       weights_span(dW, experts, K, N, lddw, stride_dw, w_layout, es)};
+  const Span ins[] = {matrix_span(dY, rows, N, lddy, GEMM_ROW_MAJOR, es),
+                      dW ? matrix_span(X, rows, K, ldx, GEMM_ROW_MAJOR, es) : Span{},
+                      dX ? weights_span(W, experts, K, N, ldw, stride_w, w_layout, es) : Span{},
+                      vector_span(offsets, experts + 1, 4)};
+  if (!disjoint(outs, ins)) return GEMM_ERR_INVALID_ARG;
+  if (!dX && !dW) return GEMM_OK;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool make_dx = dX && rows > 0 && K > 0 && N > 0;
+  ff::ExpertOperand xs = ff::expert_rows(X, ldx, rows, K), ys = ff::expert_rows(dY, lddy, rows, N);
+  ff::ExpertOperand ws = ff::expert_weights(W, ldw, stride_w, experts, K, N, w_layout);
+  Carve carve;
+  ys.plan(&carve);
+  if (dW) xs.plan(&carve);
+  if (make_dx) ws.plan(&carve);
+  st = reserve(h, h->ff, carve.bytes, s);
+  char *buf = static_cast<char *>(h->ff.ptr);
+  if (st == GEMM_OK) st = ys.stage(h, buf, s);
+  if (st == GEMM_OK) st = xs.stage(h, buf, s);
+  if (st == GEMM_OK) st = ws.stage(h, buf, s);
+  if (st != GEMM_OK) return st;
+  if (make_dx) {
+    ff::ExpertProduct q;
+    q.experts = experts, q.rows = rows, q.N = K, q.K = N, q.offsets = offsets;
+    q.X = ys, q.W = ws;
+    q.w_mn = flip(w_layout) == GEMM_ROW_MAJOR;
+    q.dtype = dtype;
+    q.C = dX, q.ldc = lddx;
+    st = ff::run_expert(h, q, s);
+  } else if (dX) {
+    st = zero_rows(h, dX, lddx, rows, K, offsets, experts, s);
+  }
+  if (st != GEMM_OK) return st;
+  return weight_gradient(h, xs, ys, experts, offsets, dW, lddw, stride_dw, dtype, w_layout, s);
+}
+
+GEMM_API gemm_status_t gemm_run_expert_gated(
+    gemm_handle_t h, int64_t experts, int64_t rows, int64_t F, int64_t K, const void *X,
+    int64_t ldx, const void *Wg, int64_t ldwg, int64_t stride_wg, const void *Wu, int64_t ldwu,
+    int64_t stride_wu, const int32_t *offsets, void *H, int64_t ldh, void *gate, int64_t ld_gate,
+    void *up, int64_t ld_up, gemm_dtype_t dtype, gemm_layout_t w_layout,
+    gemm_activation_t activation, void *cuda_stream) {
+  gemm_status_t st = check_experts(h, experts, rows, F, K, offsets, dtype, w_layout);
+  if (st != GEMM_OK) return st;
+  if (!valid_act(activation) || (gate == nullptr) != (up == nullptr)) return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 || F == 0) return GEMM_OK;
+  if (bad_matrix(X, rows, K, ldx, GEMM_ROW_MAJOR) || bad_matrix(H, rows, F, ldh, GEMM_ROW_MAJOR) ||
+      bad_weights(Wg, experts, K, F, ldwg, stride_wg, w_layout) ||
+      bad_weights(Wu, experts, K, F, ldwu, stride_wu, w_layout) || (gate && (ld_gate < F || ld_up < F)))
+    return GEMM_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  for (const void *p : {X, Wg, Wu, static_cast<const void *>(H), static_cast<const void *>(gate),
+                        static_cast<const void *>(up)})
+    if (misaligned(p, es)) return GEMM_ERR_ALIGNMENT;
+  const Span outs[] = {matrix_span(H, rows, F, ldh, GEMM_ROW_MAJOR, es),
+                       matrix_span(gate, rows, F, ld_gate, GEMM_ROW_MAJOR, es),
+                       matrix_span(up, rows, F, ld_up, GEMM_ROW_MAJOR, es)};
+  const Span ins[] = {matrix_span(X, rows, K, ldx, GEMM_ROW_MAJOR, es),
+                      weights_span(Wg, experts, K, F, ldwg, stride_wg, w_layout, es),
+                      weights_span(Wu, experts, K, F, ldwu, stride_wu, w_layout, es),
+                      vector_span(offsets, experts + 1, 4)};
+  if (!disjoint(outs, ins)) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (K == 0) {  // g = u = 0, and so h
+    st = zero_rows(h, H, ldh, rows, F, offsets, experts, s);
+    if (st == GEMM_OK) st = zero_rows(h, gate, ld_gate, rows, F, offsets, experts, s);
+    return st == GEMM_OK ? zero_rows(h, up, ld_up, rows, F, offsets, experts, s) : st;
+  }
+  ff::ExpertProduct q;
+  q.gated = true;
+  q.experts = experts, q.rows = rows, q.N = F, q.K = K, q.offsets = offsets;
+  q.X = ff::expert_rows(X, ldx, rows, K);
+  q.W = ff::expert_weights(Wg, ldwg, stride_wg, experts, K, F, w_layout);
+  q.W2 = ff::expert_weights(Wu, ldwu, stride_wu, experts, K, F, w_layout);
+  q.w_mn = w_layout == GEMM_ROW_MAJOR;
+  q.dtype = dtype, q.act = activation;
+  q.C = H, q.ldc = ldh;
+  q.pre = gate, q.ld_pre = ld_gate, q.pre2 = up, q.ld_pre2 = ld_up;
+  Carve carve;
+  q.X.plan(&carve), q.W.plan(&carve), q.W2.plan(&carve);
+  st = reserve(h, h->ff, carve.bytes, s);
+  char *buf = static_cast<char *>(h->ff.ptr);
+  if (st == GEMM_OK) st = q.X.stage(h, buf, s);
+  if (st == GEMM_OK) st = q.W.stage(h, buf, s);
+  if (st == GEMM_OK) st = q.W2.stage(h, buf, s);
+  return st == GEMM_OK ? ff::run_expert(h, q, s) : st;
+}
+
+GEMM_API gemm_status_t gemm_run_expert_gated_backward(
+    gemm_handle_t h, int64_t experts, int64_t rows, int64_t F, int64_t K, const void *dH,
+    int64_t lddh, const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, const void *X,
+    int64_t ldx, const void *Wg, int64_t ldwg, int64_t stride_wg, const void *Wu, int64_t ldwu,
+    int64_t stride_wu, const int32_t *offsets, void *dX, int64_t lddx, void *dWg, int64_t lddwg,
+    int64_t stride_dwg, void *dWu, int64_t lddwu, int64_t stride_dwu, gemm_dtype_t dtype,
+    gemm_layout_t w_layout, gemm_activation_t activation, void *cuda_stream) {
+  gemm_status_t st = check_experts(h, experts, rows, F, K, offsets, dtype, w_layout);
+  if (st != GEMM_OK) return st;
+  if (!valid_act(activation)) return GEMM_ERR_INVALID_ARG;
+  const bool weights = dWg || dWu;
+  if (bad_matrix(dH, rows, F, lddh, GEMM_ROW_MAJOR) || bad_matrix(gate, rows, F, ld_gate, GEMM_ROW_MAJOR) ||
+      bad_matrix(up, rows, F, ld_up, GEMM_ROW_MAJOR) ||
+      (weights && bad_matrix(X, rows, K, ldx, GEMM_ROW_MAJOR)) ||
+      (dWg && bad_weights(dWg, experts, K, F, lddwg, stride_dwg, w_layout)) ||
+      (dWu && bad_weights(dWu, experts, K, F, lddwu, stride_dwu, w_layout)) ||
+      (dX && (bad_matrix(dX, rows, K, lddx, GEMM_ROW_MAJOR) ||
+              bad_weights(Wg, experts, K, F, ldwg, stride_wg, w_layout) ||
+              bad_weights(Wu, experts, K, F, ldwu, stride_wu, w_layout))))
+    return GEMM_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  for (const void *p : {dH, gate, up, weights ? X : nullptr, dX ? Wg : nullptr, dX ? Wu : nullptr,
+                        static_cast<const void *>(dX), static_cast<const void *>(dWg),
+                        static_cast<const void *>(dWu)})
+    if (misaligned(p, es)) return GEMM_ERR_ALIGNMENT;
+  const Span outs[] = {matrix_span(dX, rows, K, lddx, GEMM_ROW_MAJOR, es),
+                       weights_span(dWg, experts, K, F, lddwg, stride_dwg, w_layout, es),
+                       weights_span(dWu, experts, K, F, lddwu, stride_dwu, w_layout, es)};
+  const Span ins[] = {matrix_span(dH, rows, F, lddh, GEMM_ROW_MAJOR, es),
+                      matrix_span(gate, rows, F, ld_gate, GEMM_ROW_MAJOR, es),
+                      matrix_span(up, rows, F, ld_up, GEMM_ROW_MAJOR, es),
+                      weights ? matrix_span(X, rows, K, ldx, GEMM_ROW_MAJOR, es) : Span{},
+                      dX ? weights_span(Wg, experts, K, F, ldwg, stride_wg, w_layout, es) : Span{},
+                      dX ? weights_span(Wu, experts, K, F, ldwu, stride_wu, w_layout, es) : Span{},
+                      vector_span(offsets, experts + 1, 4)};
+  if (!disjoint(outs, ins)) return GEMM_ERR_INVALID_ARG;
+  if (!dX && !weights) return GEMM_OK;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return GEMM_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool make_dx = dX && rows > 0 && K > 0 && F > 0;
+  // dg | du side by side, on 16-byte boundaries
+  const int64_t Fp = round_up(F, 8), ldd = 2 * Fp;
+  ff::ExpertOperand xs = ff::expert_rows(X, ldx, rows, K);
+  ff::ExpertOperand wg = ff::expert_weights(Wg, ldwg, stride_wg, experts, K, F, w_layout);
+  ff::ExpertOperand wu = ff::expert_weights(Wu, ldwu, stride_wu, experts, K, F, w_layout);
+  Carve carve;
+  const size_t d_off = carve.take(rows * ldd, es);
+  if (weights) xs.plan(&carve);
+  if (make_dx) wg.plan(&carve), wu.plan(&carve);
+  st = reserve(h, h->ff, carve.bytes, s);
+  if (st != GEMM_OK) return st;
+  char *buf = static_cast<char *>(h->ff.ptr);
+  char *dg = buf + d_off, *du = dg + Fp * es;
+  if (rows > 0 && F > 0) {
+    st = launched(h, ff::gated_slopes_launch(dH, lddh, gate, ld_gate, up, ld_up, dg, ldd, du, ldd,
+                                             dtype, activation, rows, F, s),
+                  "gated backward launch");
+    if (st != GEMM_OK) return st;
+  }
+  st = xs.stage(h, buf, s);
+  if (st == GEMM_OK) st = wg.stage(h, buf, s);
+  if (st == GEMM_OK) st = wu.stage(h, buf, s);
+  if (st != GEMM_OK) return st;
+  const ff::ExpertOperand gs = ff::expert_rows(dg, ldd, rows, F), us = ff::expert_rows(du, ldd, rows, F);
+  if (make_dx) {
+    ff::ExpertProduct q;
+    q.second = true;
+    q.experts = experts, q.rows = rows, q.N = K, q.K = F, q.offsets = offsets;
+    q.X = gs, q.W = wg, q.X2 = us, q.W2 = wu;
+    q.w_mn = flip(w_layout) == GEMM_ROW_MAJOR;
+    q.dtype = dtype;
+    q.C = dX, q.ldc = lddx;
+    st = ff::run_expert(h, q, s);
+  } else if (dX) {
+    st = zero_rows(h, dX, lddx, rows, K, offsets, experts, s);
+  }
+  if (st == GEMM_OK)
+    st = weight_gradient(h, xs, gs, experts, offsets, dWg, lddwg, stride_dwg, dtype, w_layout, s);
+  if (st == GEMM_OK)
+    st = weight_gradient(h, xs, us, experts, offsets, dWu, lddwu, stride_dwu, dtype, w_layout, s);
+  return st;
 }
 
 GEMM_API gemm_status_t gemm_dropout(gemm_handle_t h, int64_t M, int64_t N, const void *X,

@@ -108,6 +108,27 @@ bool encode_3d_panels(CUtensorMap *m, int dtype, const void *base, int64_t mn, i
   return r == CUDA_SUCCESS;
 }
 
+bool encode_3d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64_t outer,
+               int64_t count, int64_t ld, int64_t stride, uint32_t box_inner, uint32_t box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int es = esize_of(dtype);
+  int64_t pitch = ld * es, step = stride * es;
+  if (outer <= 1) pitch = round_up(inner * es, 16);  // a single line: any legal pitch
+  if (count <= 1) step = round_up(pitch * outer, 16);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(count)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(step)};
+  const cuuint32_t box[3] = {box_inner, box_outer, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, tmap_dtype(dtype), 3, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS && log_enabled())
+    std::fprintf(stderr, "[gemm] cuTensorMapEncodeTiled (3D) failed (%d)\n", static_cast<int>(r));
+  return r == CUDA_SUCCESS;
+}
+
 uint32_t make_idesc(int in_dtype, bool a_mn, bool b_mn, int n, int m) {
   const uint32_t fmt = in_dtype == GEMM_F16 ? 0u : in_dtype == GEMM_BF16 ? 1u : 2u;
   uint32_t d = 0;

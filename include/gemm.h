@@ -423,7 +423,7 @@ GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int6
 /* --------------------------------------------------------- operators of experts
  *
  * The parts of a feed-forward block that is split over experts: the order of its tokens by
- * expert, rows into that order and back, and dropout. Each of `tokens` tokens chooses `k` of
+ * expert, rows into that order and back, the experts' products, and dropout. Each of `tokens` tokens chooses `k` of
  * `experts` experts; pair (t, j) is token t's j-th choice. Rows, types, alignment, streams,
  * overlaps and errors are those of the feed-forward operators; sizes are at most INT32_MAX, and
  * so is tokens * k (else GEMM_ERR_UNSUPPORTED). */
@@ -473,6 +473,58 @@ GEMM_API gemm_status_t gemm_expert_combine_backward(
     const void *Z, int64_t ldz, int64_t rows, const int32_t *position, const void *weights,
     gemm_dtype_t weight_dtype, void *dZ, int64_t lddz, void *dweights, gemm_dtype_t in_dtype,
     gemm_dtype_t out_dtype, void *cuda_stream);
+
+/* The experts' products. X is rows x K, Y rows x N, row-major, in the order by expert; expert e has
+ * the rows offsets[e] .. offsets[e + 1] - 1 (experts + 1 values in DEVICE memory, read when the call
+ * runs: no count goes to the host) and the K x N weights at W + e * stride_w, each in w_layout with
+ * leading dimension ldw; stride_w is at least what one expert spans. For every row r of expert e
+ *     Y[r] = X[r] @ W[e],
+ * accumulated in fp32 and rounded once. Other rows of Y are left as they were, and other rows of X
+ * add nothing, whatever they hold. Offsets are expected in increasing order inside [0, rows]; they
+ * are taken as clamped to that range, and an expert whose end lies before its start has no rows.
+ * dtype: f16 or bf16 (GEMM_F32 is UNSUPPORTED). Operands TMA cannot address (a base, leading
+ * dimension or stride that is no multiple of 16 bytes) are copied first. experts in [1, 1024].
+ * GEMM_OPT_MAX_CTAS caps the CTAs; the other tile options have no effect. */
+GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t rows, int64_t N,
+                                       int64_t K, const void *X, int64_t ldx, const void *W,
+                                       int64_t ldw, int64_t stride_w, const int32_t *offsets,
+                                       void *Y, int64_t ldy, gemm_dtype_t dtype,
+                                       gemm_layout_t w_layout, void *cuda_stream);
+
+/* Backward pass of gemm_run_expert from dY (rows x N):
+ *     dX[r] = dY[r] @ W[e]^T   for the rows r of e (other rows are left as they were),
+ *     dW[e] = the sum over e's rows of X[r]^T dY[r]   (zeros for an expert without rows),
+ * dW in w_layout. Either of dX and dW may be NULL. The same call gives the same bits. */
+GEMM_API gemm_status_t gemm_run_expert_backward(
+    gemm_handle_t h, int64_t experts, int64_t rows, int64_t N, int64_t K, const void *dY,
+    int64_t lddy, const void *X, int64_t ldx, const void *W, int64_t ldw, int64_t stride_w,
+    const int32_t *offsets, void *dX, int64_t lddx, void *dW, int64_t lddw, int64_t stride_dw,
+    gemm_dtype_t dtype, gemm_layout_t w_layout, void *cuda_stream);
+
+/* The gated pair of projections of every expert: for every row r of expert e, with
+ * g = X[r] @ Wg[e] and u = X[r] @ Wu[e],
+ *     H[r] = act(g) * u        (H: rows x F),
+ * in one kernel that reads X once. `gate` and `up` (both or neither NULL) receive g and u for the
+ * backward pass. Rows, offsets, types and weights as gemm_run_expert. */
+GEMM_API gemm_status_t gemm_run_expert_gated(
+    gemm_handle_t h, int64_t experts, int64_t rows, int64_t F, int64_t K, const void *X,
+    int64_t ldx, const void *Wg, int64_t ldwg, int64_t stride_wg, const void *Wu, int64_t ldwu,
+    int64_t stride_wu, const int32_t *offsets, void *H, int64_t ldh, void *gate, int64_t ld_gate,
+    void *up, int64_t ld_up, gemm_dtype_t dtype, gemm_layout_t w_layout,
+    gemm_activation_t activation, void *cuda_stream);
+
+/* Backward pass of gemm_run_expert_gated from dH and the stored g and u (rows x F): with
+ * dg = dH * u * act'(g) and du = dH * act(g), rounded to the dtype,
+ *     dX[r] = dg[r] @ Wg[e]^T + du[r] @ Wu[e]^T   (one fp32 sum),
+ *     dWg[e] = sum_r X[r]^T dg[r],  dWu[e] = sum_r X[r]^T du[r].
+ * Any of dX, dWg, dWu may be NULL. Rows without an expert as in gemm_run_expert_backward. */
+GEMM_API gemm_status_t gemm_run_expert_gated_backward(
+    gemm_handle_t h, int64_t experts, int64_t rows, int64_t F, int64_t K, const void *dH,
+    int64_t lddh, const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, const void *X,
+    int64_t ldx, const void *Wg, int64_t ldwg, int64_t stride_wg, const void *Wu, int64_t ldwu,
+    int64_t stride_wu, const int32_t *offsets, void *dX, int64_t lddx, void *dWg, int64_t lddwg,
+    int64_t stride_dwg, void *dWu, int64_t lddwu, int64_t stride_dwu, gemm_dtype_t dtype,
+    gemm_layout_t w_layout, gemm_activation_t activation, void *cuda_stream);
 
 /* Dropout: with q = floor(65536 p + 1/2), every element of the M x N matrix X is dropped with
  * probability q / 65536, the others scaled by 65536 / (65536 - q),
