@@ -191,6 +191,18 @@ bool encode_2d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64
 // swizzle, zero fill outside each matrix.
 bool encode_3d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64_t outer,
                int64_t count, int64_t ld, int64_t stride, uint32_t box_inner, uint32_t box_outer);
+// 3D map over an MN-major operand's panels, and 4D over `count` of them `stride` apart: a CTA's slice
+// of a stage comes in one copy (see launch.cu). Only for MN extents of whole panels.
+bool encode_3d_panels(CUtensorMap *m, int dtype, const void *base, int64_t mn, int64_t k,
+                      int64_t ld, uint32_t k_rows, uint32_t panels, bool atom32);
+bool encode_4d_panels(CUtensorMap *m, int dtype, const void *base, int64_t mn, int64_t k, int64_t ld,
+                      int64_t count, int64_t stride, uint32_t k_rows, uint32_t panels);
+// 5D map over the lines of two K-major operands of one shape, `apart` bytes from each other, whose
+// boxes take 16 lines of the first, the same 16 of the second, the next 16 of the first and so on:
+// dims {inner, 16, 2, outer / 16, count}, box {box_inner, 16, 2, groups, 1}. outer is a multiple of 16.
+bool encode_mixed(CUtensorMap *m, int dtype, const void *base, int64_t apart, int64_t inner,
+                  int64_t outer, int64_t count, int64_t ld, int64_t stride, uint32_t box_inner,
+                  uint32_t groups);
 cudaError_t stage_operand(const OperandPlan &o, void *dst, int es, cudaStream_t s);
 gemm_status_t launch_tc(const Problem &P, const Plan &pl, const void *a_ptr, int64_t a_ld,
                         const void *b_ptr, int64_t b_ld, int *status, uint64_t timeout_ns,

@@ -47,6 +47,7 @@ static_assert(BAR_OFFSET + (4 * STAGES + 5) * 8 + (8 + 2 * STAGES) * 4 + 1024 <=
 // A tile of an expert: its rows and columns.
 struct Tile {
   int e, lo, blocks, last;  // first row, K-blocks, rows of the last block
+  int start;                // the K-block that the sum begins with; it wraps after the last one
   int m0, n0;
   __device__ __forceinline__ Tile(const ExpertGradParams &p, int t) {
     const int per = p.tiles_m * p.tiles_n;
@@ -58,6 +59,12 @@ struct Tile {
     const int n = max(lo, min(p.offsets[e + 1], p.rows)) - lo;
     blocks = (n + BK - 1) / BK;
     last = n - (blocks - 1) * BK;
+    // (neighbouring tiles start apart, at multiples of what a power of two below `blocks` allows)
+    start = blocks > 0 ? i & ((1 << (31 - __clz(blocks))) - 1) : 0;
+  }
+  // The K-block that comes i-th.
+  __device__ __forceinline__ int block(int i) const {
+    return i + start < blocks ? i + start : i + start - blocks;
   }
   __device__ __forceinline__ bool ragged() const { return blocks > 0 && last % 16 != 0; }
 };
@@ -68,6 +75,17 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src,
                    reinterpret_cast<uint64_t>(m)),
                "r"(src), "r"(x), "r"(y), "r"(z)
                : "memory");
+}
+
+// 128 columns of 64 rows of an operand, as two panels.
+__device__ __forceinline__ void load_panels(uint32_t dst, const CUtensorMap *m, int one, uint32_t bar,
+                                            int col, int row, uint64_t policy) {
+  if (one) {
+    tma_load_3d_pair_hint(dst, m, bar, 0, row, col / 64, policy);
+  } else {
+    tma_load_2d_pair_hint(dst, m, bar, col, row, policy);
+    tma_load_2d_pair_hint(dst + PANEL_BYTES, m, bar, col + 64, row, policy);
+  }
 }
 
 // This warp's 32 rows and 128 columns of the tile: by TMA through its two boxes, ...
@@ -190,7 +208,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int t = cluster_id; ok && t < tiles; t += clusters) {
         const Tile tile(p, t);
         const int m0 = tile.m0 + static_cast<int>(rank) * BM, n0 = tile.n0 + static_cast<int>(rank) * BM;
-        for (int kb = 0; kb < tile.blocks; ++kb) {
+        for (int ki = 0; ki < tile.blocks; ++ki) {
+          const int kb = tile.block(ki);
           if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
             ok = false;  // test hook: this loader stops here, copies still in flight
             break;
@@ -214,10 +233,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           fill_bytes[stage] = own ? 0 : STAGE_BYTES;
           const uint32_t dst = smem_u32(smem + stage * STAGE_BYTES);
           const int r0 = tile.lo + kb * BK;
-          tma_load_2d_pair_hint(dst, &maps.A, fb, m0, r0, keep);
-          tma_load_2d_pair_hint(dst + PANEL_BYTES, &maps.A, fb, m0 + 64, r0, keep);
-          tma_load_2d_pair_hint(dst + 2 * PANEL_BYTES, &maps.B, fb, n0, r0, keep);
-          tma_load_2d_pair_hint(dst + 3 * PANEL_BYTES, &maps.B, fb, n0 + 64, r0, keep);
+          load_panels(dst, &maps.A, p.panels_a, fb, m0, r0, keep);
+          load_panels(dst + 2 * PANEL_BYTES, &maps.B, p.panels_b, fb, n0, r0, keep);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -241,8 +258,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = 0; kb < tile.blocks; ++kb) {
-          const bool end = kb == tile.blocks - 1;
+        for (int ki = 0; ki < tile.blocks; ++ki) {
+          const bool end = tile.block(ki) == tile.blocks - 1;
           ok = mbar_wait(&full[stage], phase, wd);
           if (ok && end && tile.ragged()) {
             ok = mbar_wait_cluster(&masked[stage], masked_phase >> stage & 1, wd);
@@ -254,11 +271,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           const uint32_t a_base = smem_u32(smem + stage * STAGE_BYTES);
           const uint32_t b_base = a_base + 2 * PANEL_BYTES;
           const int steps = end ? (tile.last + 15) / 16 : BK / 16;
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint64_t ad = sdesc_sw128(a_base + kk * 16 * kRowBytes, PANEL_BYTES, 1024);
-            const uint64_t bd = sdesc_sw128(b_base + kk * 16 * kRowBytes, PANEL_BYTES, 1024);
-            mma_f16_pair(d_tmem, ad, bd, p.idesc, kb != 0 || kk != 0);
-          }
+          const uint64_t ad = sdesc_sw128(a_base, PANEL_BYTES, 1024), bd = sdesc_sw128(b_base, PANEL_BYTES, 1024);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)  // (16 rows on: 2048 bytes, in units of 16)
+            if (kk < steps)
+              mma_f16_pair(d_tmem, ad + kk * (16 * kRowBytes / 16), bd + kk * (16 * kRowBytes / 16), p.idesc,
+                           ki != 0 || kk != 0);
           mma_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
@@ -280,9 +298,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     uint32_t fills = 0, phases = 0;
     for (int t = cluster_id; t < tiles; t += clusters) {
       const Tile tile(p, t);
+      const uint32_t before = fills;
       fills += static_cast<uint32_t>(tile.blocks);
       if (!tile.ragged()) continue;
-      const uint32_t stage = (fills - 1) % STAGES;
+      const uint32_t stage = (before + static_cast<uint32_t>(tile.blocks - 1 - tile.start)) % STAGES;
       bool ok = mbar_wait(&tail[stage], phases >> stage & 1, wd);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;

@@ -22,6 +22,8 @@ struct ExpertParams {
   int32_t kb_first;        // those of the first pair
   uint32_t idesc;          // tcgen05 instruction descriptor without its N
   int32_t dtype, act;
+  int32_t panels;          // w_mn: a stage's weights come in one copy
+  int32_t up_first;        // interleaved pair: the up projection's 16 rows come before the gate's
   void *C;
   int64_t ldc;
   void *pre, *pre2;        // gated: receive the two products, or null
@@ -30,14 +32,19 @@ struct ExpertParams {
   uint64_t timeout_ns;
   int32_t debug_flags;
 };
-// X, X2: {K, rows} in boxes of 64 x 32. W, W2: {K, N, experts} in boxes of 64 x 128 or (w_mn)
-// {N, K, experts} in boxes of 64 x 64.
+// X, X2: {K, rows} in boxes of 64 x 32, 64 and 128. W, W2: {K, N, experts} in boxes of 64 x 128, or
+// (w_mn) {64, K, N / 64, experts} in boxes of 64 x 64 x 2 where N allows it (p.panels), else
+// {N, K, experts} in boxes of 64 x 64; an interleaved pair {K, 16, 2, N / 16, experts} in boxes of
+// 64 x 16 x 2 x 4, the third axis leading from one matrix to the other.
 struct ExpertMaps {
-  CUtensorMap X, X2, W, W2;
+  CUtensorMap X[3], X2[3], W, W2;
 };
-constexpr int kExpertFeatures = 256;  // features a tile
-inline int expert_tile_tokens(bool gated) { return gated ? 128 : 256; }  // tokens a tile, at most
-cudaError_t expert_launch(bool gated, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
+// How a call runs: one product; a gated pair whose weights come interleaved, 16 rows of each in
+// turn (K-contiguous weights); or a gated pair in two accumulators.
+enum ExpertMode { kExpertPlain, kExpertMixed, kExpertTwo };
+__host__ __device__ constexpr int expert_features(int mode) { return mode == kExpertMixed ? 128 : 256; }
+__host__ __device__ constexpr int expert_tokens(int mode) { return mode == kExpertTwo ? 128 : 256; }
+cudaError_t expert_launch(ExpertMode mode, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
                           int grid, cudaStream_t s);
 // Clusters of two CTAs of these kernels that fit on the current device at once.
 int expert_max_clusters();
@@ -51,13 +58,15 @@ struct ExpertGradParams {
   uint32_t idesc;
   int32_t dtype;
   int32_t tma_out;         // D is TMA-addressable
+  int32_t panels_a, panels_b;  // a stage's operand comes in one copy
   void *D;
   int64_t ldd, stride_d;
   int *status;
   uint64_t timeout_ns;
   int32_t debug_flags;
 };
-// A: {MA, rows}, B: {NB, rows} in boxes of 64 x 64; D: {NB, MA, experts} in boxes of 64 x 32.
+// A: {64, rows, MA / 64} in boxes of 64 x 64 x 2 where MA allows it (panels_a), else {MA, rows} in
+// boxes of 64 x 64; B likewise; D: {NB, MA, experts} in boxes of 64 x 32.
 struct ExpertGradMaps {
   CUtensorMap A, B, D;
 };

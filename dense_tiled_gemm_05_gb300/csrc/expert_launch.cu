@@ -18,6 +18,23 @@ bool addressable(const void *p, int64_t lines, int64_t ld, int64_t count, int64_
          (count <= 1 || (stride * ES) % 16 == 0);
 }
 
+// Boxes are one 128-byte row of K (or, with the features inside, of N) wide.
+bool encode_rows(CUtensorMap (&m)[3], const ExpertOperand &x, int dtype) {
+  return encode_2d(&m[0], dtype, x.ptr, x.len, x.lines, x.ld, 64, 32) &&
+         encode_2d(&m[1], dtype, x.ptr, x.len, x.lines, x.ld, 64, 64) &&
+         encode_2d(&m[2], dtype, x.ptr, x.len, x.lines, x.ld, 64, 128);
+}
+bool encode_weights(CUtensorMap *m, const ExpertOperand &w, bool mn, bool panels, int dtype) {
+  if (panels) return encode_4d_panels(m, dtype, w.ptr, w.len, w.lines, w.ld, w.count, w.stride, 64, 2);
+  return encode_3d(m, dtype, w.ptr, w.len, w.lines, w.count, w.ld, w.stride, 64, mn ? 64 : 128);
+}
+// Rows as an operand whose sum runs over them.
+bool encode_outer(CUtensorMap *m, const ExpertOperand &x, int dtype, int32_t *panels) {
+  *panels = x.len % 64 == 0 && x.lines > 1;
+  return *panels ? encode_3d_panels(m, dtype, x.ptr, x.len, x.lines, x.ld, 64, 2, false)
+                 : encode_2d(m, dtype, x.ptr, x.len, x.lines, x.ld, 64, 64);
+}
+
 int64_t clusters_of(gemm_handle_t h, int64_t tiles) {
   int64_t n = pair_slots(h->sm_count, h->max_ctas);
   const int64_t fit = expert_max_clusters();
@@ -75,16 +92,26 @@ gemm_status_t run_expert(gemm_handle_t h, const ExpertProduct &q, cudaStream_t s
   ExpertMaps maps;
   std::memset(&maps, 0, sizeof maps);
   const bool two_x = q.second, two_w = q.second || q.gated;
-  // Boxes are one 128-byte row of K (or, with the features inside, of N) wide.
-  const uint32_t lines = q.w_mn ? 64u : 128u;
-  bool ok = encode_2d(&maps.X, q.dtype, q.X.ptr, q.X.len, q.X.lines, q.X.ld, 64, 32) &&
-            encode_3d(&maps.W, q.dtype, q.W.ptr, q.W.len, q.W.lines, q.W.count, q.W.ld, q.W.stride, 64, lines);
-  if (ok && two_x) ok = encode_2d(&maps.X2, q.dtype, q.X2.ptr, q.X2.len, q.X2.lines, q.X2.ld, 64, 32);
-  if (ok && two_w)
-    ok = encode_3d(&maps.W2, q.dtype, q.W2.ptr, q.W2.len, q.W2.lines, q.W2.count, q.W2.ld, q.W2.stride, 64, lines);
+  const bool panels = q.w_mn && q.N % 64 == 0 && q.W.lines > 1;
+  // The interleaved pair's map leads from one matrix to the other: less than 2^40 bytes, the limit
+  // of a tensor map's strides, and the same steps in both.
+  const intptr_t apart = reinterpret_cast<intptr_t>(q.W2.ptr) - reinterpret_cast<intptr_t>(q.W.ptr);
+  const ExpertMode mode = !q.gated ? kExpertPlain
+                          : !q.w_mn && q.N % 16 == 0 && q.W.ld == q.W2.ld &&
+                                  (q.experts == 1 || q.W.stride == q.W2.stride) && apart != 0 &&
+                                  apart > -(intptr_t{1} << 40) && apart < (intptr_t{1} << 40)
+                              ? kExpertMixed
+                              : kExpertTwo;
+  bool ok = encode_rows(maps.X, q.X, q.dtype) && (!two_x || encode_rows(maps.X2, q.X2, q.dtype));
+  if (ok && mode == kExpertMixed)
+    ok = encode_mixed(&maps.W, q.dtype, apart > 0 ? q.W.ptr : q.W2.ptr, apart > 0 ? apart : -apart, q.W.len,
+                      q.W.lines, q.W.count, q.W.ld, q.W.stride, 64, 4);
+  else if (ok)
+    ok = encode_weights(&maps.W, q.W, q.w_mn, panels, q.dtype) &&
+         (!two_w || encode_weights(&maps.W2, q.W2, q.w_mn, panels, q.dtype));
   if (!ok) return GEMM_ERR_CUDA;
-  if (!two_x) maps.X2 = maps.X;  // never read
-  if (!two_w) maps.W2 = maps.W;
+  if (!two_x) std::memcpy(maps.X2, maps.X, sizeof maps.X);  // never read
+  if (!two_w || mode == kExpertMixed) maps.W2 = maps.W;
   ExpertParams p{};
   p.offsets = q.offsets;
   p.experts = static_cast<int32_t>(q.experts), p.rows = static_cast<int32_t>(q.rows);
@@ -92,17 +119,16 @@ gemm_status_t run_expert(gemm_handle_t h, const ExpertProduct &q, cudaStream_t s
   p.kb_first = static_cast<int32_t>((q.K + 63) / 64);
   p.k_blocks = p.kb_first * (q.second ? 2 : 1);
   p.idesc = make_idesc(q.dtype, q.w_mn, false, 0, 256);
-  p.dtype = q.dtype, p.act = q.act;
+  p.dtype = q.dtype, p.act = q.act, p.panels = panels, p.up_first = apart < 0;
   p.C = q.C, p.ldc = q.ldc;
   p.pre = q.pre, p.ld_pre = q.ld_pre, p.pre2 = q.pre2, p.ld_pre2 = q.ld_pre2;
   p.status = h->status;
   p.timeout_ns = h->timeout_us * 1000ull;
   p.debug_flags = stall_flags(h->stall_producer);
   // at most one part tile an expert, and no more experts with rows than rows
-  const int64_t most = expert_tile_tokens(q.gated);
-  const int64_t tiles = (q.rows / most + (q.experts < q.rows ? q.experts : q.rows)) *
-                        ((q.N + kExpertFeatures - 1) / kExpertFeatures);
-  const cudaError_t e = expert_launch(q.gated, q.w_mn, maps, p, static_cast<int>(2 * clusters_of(h, tiles)), s);
+  const int64_t tiles = (q.rows / expert_tokens(mode) + (q.experts < q.rows ? q.experts : q.rows)) *
+                        ((q.N + expert_features(mode) - 1) / expert_features(mode));
+  const cudaError_t e = expert_launch(mode, q.w_mn, maps, p, static_cast<int>(2 * clusters_of(h, tiles)), s);
   if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
   h->launches += 1;
   return GEMM_OK;
@@ -124,8 +150,7 @@ gemm_status_t run_expert_grad(gemm_handle_t h, const ExpertGrad &q, cudaStream_t
   p.debug_flags = stall_flags(h->stall_producer);
   // TMA stores only where lines end on 16-byte boundaries (see the planner)
   p.tma_out = (q.B.len * ES) % 16 == 0 && addressable(q.D, q.A.len, q.ldd, q.experts, q.stride_d);
-  if (!encode_2d(&maps.A, q.dtype, q.A.ptr, q.A.len, q.A.lines, q.A.ld, 64, 64) ||
-      !encode_2d(&maps.B, q.dtype, q.B.ptr, q.B.len, q.B.lines, q.B.ld, 64, 64) ||
+  if (!encode_outer(&maps.A, q.A, q.dtype, &p.panels_a) || !encode_outer(&maps.B, q.B, q.dtype, &p.panels_b) ||
       (p.tma_out && !encode_3d(&maps.D, q.dtype, q.D, q.B.len, q.A.len, q.experts, q.ldd, q.stride_d, 64, 32)))
     return GEMM_ERR_CUDA;
   const int64_t tiles = q.experts * p.tiles_m * p.tiles_n;

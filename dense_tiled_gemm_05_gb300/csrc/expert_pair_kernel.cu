@@ -17,8 +17,14 @@
 // made and no count goes to the host. Token tiles run fastest: the clusters at work share weights
 // through L2, and the next tile's loads and MMAs run under a tile's epilogue (two accumulators).
 //
-// The gated pair runs as two MMAs a K-step against the same tokens, g and u in the same lanes of
-// two column ranges of TMEM, so that each epilogue thread has both.
+// The gated pair of K-contiguous weights: one TMA copy brings 16 rows of the gate's weights, the
+// same 16 of the up projection's, the next 16 of the gate's and so on (a 5D map whose third axis
+// leads from one matrix to the other), so that a warp's 32 TMEM lanes are g and u of 16 features
+// and a shuffle brings them together: 128 features a tile, one MMA a K-step. Other weights (other
+// layouts, feature counts that are no multiple of 16) run as two MMAs a K-step against the same
+// 128 tokens, g and u in the same lanes of two column ranges: those narrower MMAs read a third more
+// shared memory an operation and reached 1340 TFLOP/s where 256 columns reach 1660 (16384 rows,
+// 2048 x 4096).
 //
 // The epilogue has one feature a lane and tokens along its registers: a warp's store of one
 // token is 32 neighbouring features. Rows past the expert's last are not stored (they are the
@@ -39,18 +45,18 @@ constexpr int BM = 128;                         // features per CTA
 constexpr int BK = 64;
 constexpr int W_BYTES = BM * kRowBytes;         // one weight box (MN-major: two panels)
 constexpr int PANEL_BYTES = BK * kRowBytes;
-constexpr int BOX_TOKENS = 32;                  // tokens a TMA box
-constexpr int BOX_BYTES = BOX_TOKENS * kRowBytes;
 constexpr int kEpi = 8;                         // epilogue warps
 constexpr int kExpertThreads = 64 + 32 * kEpi;
 constexpr int ACC = 256;                        // TMEM columns of an accumulator (gated: 128 each)
 
-template <bool GATED>
+template <int MODE>
 struct Shape {
-  static constexpr int TOKENS = GATED ? 128 : 256;
-  static constexpr int X_BYTES = TOKENS / 2 * kRowBytes;  // a CTA's half of the tokens
-  static constexpr int STAGE = (GATED ? 2 : 1) * W_BYTES + X_BYTES;
-  static constexpr int STAGES = GATED ? 5 : 6;
+  static constexpr bool TWO = MODE == kExpertTwo;             // weight boxes, accumulators
+  static constexpr int FEATURES = expert_features(MODE) / 2;  // a CTA's
+  static constexpr int TOKENS = expert_tokens(MODE);
+  static constexpr int W_ALL = (TWO ? 2 : 1) * W_BYTES;
+  static constexpr int STAGE = W_ALL + TOKENS / 2 * kRowBytes;  // (a CTA's half of the tokens)
+  static constexpr int STAGES = TWO ? 5 : 6;
   static constexpr int OFFSETS = STAGES * STAGE;
   static constexpr int BARS = OFFSETS + (static_cast<int>(kMaxExperts) + 1) * 4 + 4;
   static constexpr int END = BARS + (2 * STAGES + 5) * 8 + (6 + 2 * STAGES) * 4;
@@ -58,10 +64,10 @@ struct Shape {
 // All of an SM's shared memory, because the CTA takes all of its TMEM: no CTA that needs some
 // then shares the SM.
 constexpr int SMEM_BYTES = 232448;
-static_assert(Shape<false>::BARS % 8 == 0 && Shape<true>::BARS % 8 == 0, "barriers are aligned");
-static_assert(Shape<false>::END + 1024 <= SMEM_BYTES && Shape<true>::END + 1024 <= SMEM_BYTES, "shared memory");
+static_assert(Shape<kExpertPlain>::BARS % 8 == 0 && Shape<kExpertTwo>::BARS % 8 == 0, "barriers are aligned");
+static_assert(Shape<kExpertPlain>::END + 1024 <= SMEM_BYTES && Shape<kExpertTwo>::END + 1024 <= SMEM_BYTES, "shared memory");
 
-// The tokens' columns c0 .. c0 + 31 of this lane's feature, for `left` tokens from row on.
+// 32 tokens' columns of this lane, the `left` first of them stored from `row` on: one feature f, ...
 template <typename T, bool GATED>
 __device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, int64_t row, int left,
                                        int64_t f) {
@@ -95,10 +101,50 @@ __device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, in
     if (j < left) y[j * p.ldc] = from_f32<T>(a[j]);
 }
 
-template <bool GATED, bool W_MN>
+// ... or g or u of one (the other 16 lanes have the other): the lower half of the warp finishes the
+// even tokens, the upper half the odd ones.
+template <typename T>
+__device__ __forceinline__ void finish_mixed(const ExpertParams &p, uint32_t t_acc, int64_t row, int left,
+                                             int64_t f, int lane) {
+  uint32_t r[32];
+  __syncwarp();
+  tmem_ld_32x32b_x32(t_acc, r);
+  tmem_wait_ld();
+  const bool odd = lane >= 16, gate = odd == (p.up_first != 0);
+  float a[16], u[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float mine = __uint_as_float(odd ? r[2 * j + 1] : r[2 * j]);
+    const float other =
+        __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? r[2 * j] : r[2 * j + 1], 16));
+    a[j] = gate ? mine : other;
+    u[j] = gate ? other : mine;
+  }
+  if (f >= p.N) return;
+  row += odd;
+  left -= odd;
+  if (p.pre) {
+    T *g = static_cast<T *>(p.pre) + row * p.ld_pre + f;
+    T *v = static_cast<T *>(p.pre2) + row * p.ld_pre2 + f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (2 * j < left) {
+        g[2 * j * p.ld_pre] = from_f32<T>(a[j]);
+        v[2 * j * p.ld_pre2] = from_f32<T>(u[j]);
+      }
+  }
+  activate_all<true>(a, p.act);
+  T *y = static_cast<T *>(p.C) + row * p.ldc + f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (2 * j < left) y[2 * j * p.ldc] = from_f32<T>(a[j] * u[j]);
+}
+
+template <int MODE, bool W_MN>
 __global__ void __launch_bounds__(kExpertThreads, 1)
     expert_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
-  using S = Shape<GATED>;
+  using S = Shape<MODE>;
+  constexpr bool TWO = S::TWO;
   constexpr int STAGES = S::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -135,7 +181,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < 4 + 2 * STAGES; ++i) xs[i] = 0;
     fence_barrier_init();
-    prefetch_tensormap(&maps.X);
+    prefetch_tensormap(&maps.X[2]);
     prefetch_tensormap(&maps.W);
   }
   if (warp == 1) {
@@ -152,7 +198,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
   const int cluster_id = blockIdx.x / 2, clusters = gridDim.x / 2;
-  ExpertWalk walk(offsets, p.experts, (p.N + kExpertFeatures - 1) / kExpertFeatures, S::TOKENS, 32);
+  ExpertWalk walk(offsets, p.experts, (p.N + 2 * S::FEATURES - 1) / (2 * S::FEATURES), S::TOKENS, 32);
+  int line, column;
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
@@ -162,13 +209,15 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
       const uint64_t keep = l2_policy_evict_last();
       for (int t = cluster_id; ok && walk.seek(t); t += clusters) {
-        const int i = t - walk.begin;
-        const int row0 = walk.lo + i % walk.lines * walk.width;
-        const int f0 = i / walk.lines * kExpertFeatures + static_cast<int>(rank) * BM;
+        walk.place(t, line, column);
+        const int row0 = walk.lo + line * walk.width;
+        const int f0 = (2 * column + static_cast<int>(rank)) * S::FEATURES;
         const int half = (min(walk.width, walk.hi - row0) + 31) / 32 * 16;  // a CTA's tokens
         const int x_row = row0 + static_cast<int>(rank) * half;
-        const int boxes = (half + BOX_TOKENS - 1) / BOX_TOKENS;
-        const uint32_t bytes = static_cast<uint32_t>((GATED ? 2 : 1) * W_BYTES + boxes * BOX_BYTES);
+        // the smallest box that holds them: one copy a stage (a copy's issue takes the loader some
+        // 150 cycles, so five 32-token ones made it the slowest part)
+        const int box = half <= 32 ? 0 : half <= 64 ? 1 : 2;
+        const uint32_t bytes = static_cast<uint32_t>(S::W_ALL + (kRowBytes * 32 << box));
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
             ok = false;  // test hook: this loader stops here, copies still in flight
@@ -181,24 +230,26 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           fill_bytes[stage] = bytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
           const uint32_t w_dst = smem_u32(smem + stage * S::STAGE);
-          const uint32_t x_dst = w_dst + (GATED ? 2 : 1) * W_BYTES;
+          const uint32_t x_dst = w_dst + S::W_ALL;
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);  // the leader's barrier
-          const bool second = !GATED && kb >= p.kb_first;
+          const bool second = MODE == kExpertPlain && kb >= p.kb_first;
           const int k0 = (second ? kb - p.kb_first : kb) * BK;
 #pragma unroll
-          for (int m = 0; m < (GATED ? 2 : 1); ++m) {
-            const CUtensorMap *w = (GATED ? m == 1 : second) ? &maps.W2 : &maps.W;
+          for (int m = 0; m < (TWO ? 2 : 1); ++m) {
+            const CUtensorMap *w = (TWO ? m == 1 : second) ? &maps.W2 : &maps.W;
             const uint32_t dst = w_dst + m * W_BYTES;
-            if (W_MN) {
+            if (MODE == kExpertMixed) {
+              tma_load_5d_pair(dst, w, fb, k0, 0, 0, f0 / 16, walk.e);
+            } else if (W_MN && p.panels) {
+              tma_load_4d_pair(dst, w, fb, 0, k0, f0 / 64, walk.e);
+            } else if (W_MN) {
               tma_load_3d_pair(dst, w, fb, f0, k0, walk.e);
               tma_load_3d_pair(dst + PANEL_BYTES, w, fb, f0 + 64, k0, walk.e);
             } else {
               tma_load_3d_pair(dst, w, fb, k0, f0, walk.e);
             }
           }
-          const CUtensorMap *x = second ? &maps.X2 : &maps.X;
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_pair_hint(x_dst + b * BOX_BYTES, x, fb, k0, x_row + b * BOX_TOKENS, keep);
+          tma_load_2d_pair_hint(x_dst, second ? &maps.X2[box] : &maps.X[box], fb, k0, x_row, keep);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -215,7 +266,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0;
       bool ok = true;
       for (int t = cluster_id; ok && walk.seek(t); t += clusters) {
-        const int row0 = walk.lo + (t - walk.begin) % walk.lines * walk.width;
+        walk.place(t, line, column);
+        const int row0 = walk.lo + line * walk.width;
         const uint32_t n = static_cast<uint32_t>(min(walk.width, walk.hi - row0) + 31) / 32 * 32;
         const uint32_t idesc = p.idesc | (n >> 3) << 17;
         if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
@@ -229,18 +281,15 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           ++consumed;
           tc_fence_after();
           const uint32_t w_base = smem_u32(smem + stage * S::STAGE);
-          const uint32_t x_base = w_base + (GATED ? 2 : 1) * W_BYTES;
+          const uint64_t xd = sdesc_sw128(w_base + S::W_ALL, 16, 1024);
+          const uint64_t wd = W_MN ? sdesc_sw128(w_base, PANEL_BYTES, 1024) : sdesc_sw128(w_base, 16, 1024);
+          constexpr int W_STEP = W_MN ? 16 * kRowBytes / 16 : 32 / 16;  // 16 of K, in units of 16 bytes
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t xd = sdesc_sw128(x_base + kk * 32, 16, 1024);
+          for (int kk = 0; kk < BK / 16; ++kk)
 #pragma unroll
-            for (int m = 0; m < (GATED ? 2 : 1); ++m) {
-              const uint32_t w = w_base + m * W_BYTES;
-              const uint64_t wdesc = W_MN ? sdesc_sw128(w + kk * 16 * kRowBytes, PANEL_BYTES, 1024)
-                                          : sdesc_sw128(w + kk * 32, 16, 1024);
-              mma_f16_pair(d_tmem + m * (ACC / 2), wdesc, xd, idesc, kb != 0 || kk != 0);
-            }
-          }
+            for (int m = 0; m < (TWO ? 2 : 1); ++m)
+              mma_f16_pair(d_tmem + m * (ACC / 2), wd + m * (W_BYTES / 16) + kk * W_STEP, xd + kk * (32 / 16),
+                           idesc, kb != 0 || kk != 0);
           mma_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
@@ -263,20 +312,27 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     const int half = (warp - 2) / 4;  // takes every other 32 tokens
     uint32_t acc = 0, acc_phase = 0;
     for (int t = cluster_id; walk.seek(t); t += clusters) {
-      const int i = t - walk.begin;
-      const int row0 = walk.lo + i % walk.lines * walk.width;
+      walk.place(t, line, column);
+      const int row0 = walk.lo + line * walk.width;
       const int tokens = min(walk.width, walk.hi - row0);
-      const int64_t f = i / walk.lines * kExpertFeatures + static_cast<int>(rank) * BM + quarter * 32 + lane;
+      const int64_t f = (2 * column + static_cast<int>(rank)) * S::FEATURES +
+                        (MODE == kExpertMixed ? quarter * 16 + lane % 16 : quarter * 32 + lane);
       bool ok = mbar_wait_cluster(&tmem_full[acc], acc_phase, wd);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC;
       for (int c0 = half * 32; c0 < tokens; c0 += 64) {
-        if (p.dtype == GEMM_BF16)
-          finish<__nv_bfloat16, GATED>(p, t_row + c0, row0 + c0, tokens - c0, f);
-        else
-          finish<__half, GATED>(p, t_row + c0, row0 + c0, tokens - c0, f);
+        if (MODE == kExpertMixed) {
+          if (p.dtype == GEMM_BF16)
+            finish_mixed<__nv_bfloat16>(p, t_row + c0, row0 + c0, tokens - c0, f, lane);
+          else
+            finish_mixed<__half>(p, t_row + c0, row0 + c0, tokens - c0, f, lane);
+        } else if (p.dtype == GEMM_BF16) {
+          finish<__nv_bfloat16, TWO>(p, t_row + c0, row0 + c0, tokens - c0, f);
+        } else {
+          finish<__half, TWO>(p, t_row + c0, row0 + c0, tokens - c0, f);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -311,9 +367,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   }
 }
 
-template <bool GATED, bool W_MN>
+template <int MODE, bool W_MN>
 cudaError_t launch_expert(const ExpertMaps &maps, const ExpertParams &p, int grid, cudaStream_t s) {
-  auto kernel = expert_kernel<GATED, W_MN>;
+  auto kernel = expert_kernel<MODE, W_MN>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -335,11 +391,12 @@ cudaError_t launch_expert(const ExpertMaps &maps, const ExpertParams &p, int gri
 
 }  // namespace
 
-cudaError_t expert_launch(bool gated, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
+cudaError_t expert_launch(ExpertMode mode, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
                           int grid, cudaStream_t s) {
-  if (gated)
-    return w_mn ? launch_expert<true, true>(maps, p, grid, s) : launch_expert<true, false>(maps, p, grid, s);
-  return w_mn ? launch_expert<false, true>(maps, p, grid, s) : launch_expert<false, false>(maps, p, grid, s);
+  if (mode == kExpertMixed) return w_mn ? cudaErrorInvalidValue : launch_expert<kExpertMixed, false>(maps, p, grid, s);
+  if (mode == kExpertTwo)
+    return w_mn ? launch_expert<kExpertTwo, true>(maps, p, grid, s) : launch_expert<kExpertTwo, false>(maps, p, grid, s);
+  return w_mn ? launch_expert<kExpertPlain, true>(maps, p, grid, s) : launch_expert<kExpertPlain, false>(maps, p, grid, s);
 }
 
 int expert_max_clusters() {
@@ -351,7 +408,7 @@ int expert_max_clusters() {
   }
   const int known = cached[dev].load(std::memory_order_relaxed);
   if (known > 0) return known;
-  auto kernel = expert_kernel<false, false>;
+  auto kernel = expert_kernel<kExpertPlain, false>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -108,6 +108,47 @@ bool encode_3d_panels(CUtensorMap *m, int dtype, const void *base, int64_t mn, i
   return r == CUDA_SUCCESS;
 }
 
+bool encode_4d_panels(CUtensorMap *m, int dtype, const void *base, int64_t mn, int64_t k, int64_t ld,
+                      int64_t count, int64_t stride, uint32_t k_rows, uint32_t panels) {
+  EncodeTiledFn fn = encode_fn();
+  const int es = esize_of(dtype);
+  const int64_t panel = 128 / es;
+  if (!fn || mn % panel != 0 || k <= 1) return false;
+  const int64_t step = count > 1 ? stride * es : round_up(k * ld * es, 16);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(panel), static_cast<cuuint64_t>(k),
+                              static_cast<cuuint64_t>(mn / panel), static_cast<cuuint64_t>(count)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld * es), 128, static_cast<cuuint64_t>(step)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(panel), k_rows, panels, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, tmap_dtype(dtype), 4, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS && log_enabled())
+    std::fprintf(stderr, "[gemm] cuTensorMapEncodeTiled (4D panels) failed (%d)\n", static_cast<int>(r));
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_mixed(CUtensorMap *m, int dtype, const void *base, int64_t apart, int64_t inner,
+                  int64_t outer, int64_t count, int64_t ld, int64_t stride, uint32_t box_inner,
+                  uint32_t groups) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || outer % 16 != 0) return false;
+  const int es = esize_of(dtype);
+  const int64_t step = count > 1 ? stride * es : round_up(outer * ld * es, 16);
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(inner), 16, 2, static_cast<cuuint64_t>(outer / 16),
+                              static_cast<cuuint64_t>(count)};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(ld * es), static_cast<cuuint64_t>(apart),
+                                 static_cast<cuuint64_t>(16 * ld * es), static_cast<cuuint64_t>(step)};
+  const cuuint32_t box[5] = {box_inner, 16, 2, groups, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(m, tmap_dtype(dtype), 5, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS && log_enabled())
+    std::fprintf(stderr, "[gemm] cuTensorMapEncodeTiled (5D) failed (%d)\n", static_cast<int>(r));
+  return r == CUDA_SUCCESS;
+}
+
 bool encode_3d(CUtensorMap *m, int dtype, const void *base, int64_t inner, int64_t outer,
                int64_t count, int64_t ld, int64_t stride, uint32_t box_inner, uint32_t box_outer) {
   EncodeTiledFn fn = encode_fn();
