@@ -56,6 +56,8 @@ struct gemm_handle_s {
   int host_panel = 0;  // gemm_run_host panel width (rows of A, columns of B), 0 auto
   // split-K workspace of the CTA-pair kernel: partial tiles and flags
   Workspace split;
+  // sums and flags of the experts' products' split tiles
+  Workspace expert_split;
   // host-buffer pipeline (gemm_run_host): device copies of A, B, C, streams and events
   static constexpr int kMaxPanels = 48;  // per operand; steps <= 2 * kMaxPanels
   Workspace host;

@@ -28,26 +28,37 @@ struct ExpertParams {
   int64_t ldc;
   void *pre, *pre2;        // gated: receive the two products, or null
   int64_t ld_pre, ld_pre2;
+  // sums of split tiles: [cluster][CTA][column][128], flags and epoch as in TcParams
+  // (stream_k: GEMM_OPT_STREAM_K)
+  int32_t stream_k;
+  float *sk_partials;
+  int *sk_flags;
+  int *sk_epoch_word;
   int *status;
   uint64_t timeout_ns;
   int32_t debug_flags;
 };
-// X, X2: {K, rows} in boxes of 64 x 32, 64 and 128. W, W2: {K, N, experts} in boxes of 64 x 128, or
+// X, X2: {K, rows} in boxes of 64 x 32, 64, 96 and 128. W, W2: {K, N, experts} in boxes of 64 x 128, or
 // (w_mn) {64, K, N / 64, experts} in boxes of 64 x 64 x 2 where N allows it (p.panels), else
 // {N, K, experts} in boxes of 64 x 64; an interleaved pair {K, 16, 2, N / 16, experts} in boxes of
 // 64 x 16 x 2 x 4, the third axis leading from one matrix to the other.
 struct ExpertMaps {
-  CUtensorMap X[3], X2[3], W, W2;
+  CUtensorMap X[4], X2[4], W, W2;
 };
 // How a call runs: one product; a gated pair whose weights come interleaved, 16 rows of each in
 // turn (K-contiguous weights); or a gated pair in two accumulators.
 enum ExpertMode { kExpertPlain, kExpertMixed, kExpertTwo };
 __host__ __device__ constexpr int expert_features(int mode) { return mode == kExpertMixed ? 128 : 256; }
-__host__ __device__ constexpr int expert_tokens(int mode) { return mode == kExpertTwo ? 128 : 256; }
-cudaError_t expert_launch(ExpertMode mode, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
-                          int grid, cudaStream_t s);
-// Clusters of two CTAs of these kernels that fit on the current device at once.
+__host__ __device__ constexpr int expert_tokens(int mode, bool narrow) {
+  return narrow ? 64 : mode == kExpertTwo ? 128 : 256;
+}
+// narrow: for few rows an expert (not with kExpertTwo).
+cudaError_t expert_launch(ExpertMode mode, bool w_mn, bool narrow, const ExpertMaps &maps,
+                          const ExpertParams &p, int grid, cudaStream_t s);
+// Clusters of two CTAs of these kernels, one an SM, that fit on the current device at once.
 int expert_max_clusters();
+// Floats of a cluster's sums of split tiles.
+inline int64_t expert_share_floats(bool narrow) { return 2 * 128 * (narrow ? 64 : 256); }
 
 // D[e] = sum over the rows r of expert e of A[r]^T B[r].
 struct ExpertGradParams {

@@ -12,6 +12,8 @@ namespace ff {
 namespace {
 
 constexpr int ES = 2;  // bytes an element: 16-bit types only
+// Rows an expert with rows, on average, up to which its products run in narrow tiles.
+constexpr int64_t kNarrowRows = 32;
 
 bool addressable(const void *p, int64_t lines, int64_t ld, int64_t count, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (lines <= 1 || (ld * ES) % 16 == 0) &&
@@ -19,10 +21,10 @@ bool addressable(const void *p, int64_t lines, int64_t ld, int64_t count, int64_
 }
 
 // Boxes are one 128-byte row of K (or, with the features inside, of N) wide.
-bool encode_rows(CUtensorMap (&m)[3], const ExpertOperand &x, int dtype) {
-  return encode_2d(&m[0], dtype, x.ptr, x.len, x.lines, x.ld, 64, 32) &&
-         encode_2d(&m[1], dtype, x.ptr, x.len, x.lines, x.ld, 64, 64) &&
-         encode_2d(&m[2], dtype, x.ptr, x.len, x.lines, x.ld, 64, 128);
+bool encode_rows(CUtensorMap (&m)[4], const ExpertOperand &x, int dtype) {
+  for (uint32_t i = 0; i < 4; ++i)
+    if (!encode_2d(&m[i], dtype, x.ptr, x.len, x.lines, x.ld, 64, 32 * (i + 1))) return false;
+  return true;
 }
 bool encode_weights(CUtensorMap *m, const ExpertOperand &w, bool mn, bool panels, int dtype) {
   if (panels) return encode_4d_panels(m, dtype, w.ptr, w.len, w.lines, w.ld, w.count, w.stride, 64, 2);
@@ -35,10 +37,28 @@ bool encode_outer(CUtensorMap *m, const ExpertOperand &x, int dtype, int32_t *pa
                  : encode_2d(m, dtype, x.ptr, x.len, x.lines, x.ld, 64, 64);
 }
 
-int64_t clusters_of(gemm_handle_t h, int64_t tiles) {
+// The handle's workspace of split tiles: [epoch word, arrival count | eight flags a CTA of the largest
+// grid | sums of `clusters`]. The region of the flags has one size for all grids, so that none finds
+// sums where it expects flags.
+gemm_status_t share_workspace(gemm_handle_t h, ExpertParams *p, int64_t clusters, bool narrow, cudaStream_t s) {
+  const int64_t ctas = 2 * static_cast<int64_t>(h->sm_count);
+  const size_t flags = static_cast<size_t>(round_up(static_cast<int64_t>((2 + 8 * ctas) * sizeof(int)), 256));
+  const size_t sums = static_cast<size_t>(clusters * expert_share_floats(narrow)) * sizeof(float);
+  const gemm_status_t st = reserve(h, h->expert_split, flags + sums, s, flags);
+  if (st != GEMM_OK) return st;
+  p->sk_epoch_word = static_cast<int *>(h->expert_split.ptr);
+  p->sk_flags = p->sk_epoch_word + 2;
+  p->sk_partials = reinterpret_cast<float *>(static_cast<char *>(h->expert_split.ptr) + flags);
+  return GEMM_OK;
+}
+
+// Narrow tiles run two CTAs an SM. (The occupancy query counts one; were a cluster to wait for its
+// place, those that run do not wait for it: sums come from lower-numbered clusters.)
+int64_t clusters_of(gemm_handle_t h, int64_t tiles, bool narrow) {
   int64_t n = pair_slots(h->sm_count, h->max_ctas);
   const int64_t fit = expert_max_clusters();
   if (n > fit) n = fit;
+  if (narrow && h->max_ctas == 0) n *= 2;
   return n > tiles ? tiles : n;
 }
 
@@ -126,9 +146,17 @@ gemm_status_t run_expert(gemm_handle_t h, const ExpertProduct &q, cudaStream_t s
   p.timeout_ns = h->timeout_us * 1000ull;
   p.debug_flags = stall_flags(h->stall_producer);
   // at most one part tile an expert, and no more experts with rows than rows
-  const int64_t tiles = (q.rows / expert_tokens(mode) + (q.experts < q.rows ? q.experts : q.rows)) *
+  const int64_t used = q.experts < q.rows ? q.experts : q.rows;
+  const bool narrow = mode != kExpertTwo && q.rows <= kNarrowRows * used;
+  const int64_t tiles = (q.rows / expert_tokens(mode, narrow) + used) *
                         ((q.N + expert_features(mode) - 1) / expert_features(mode));
-  const cudaError_t e = expert_launch(mode, q.w_mn, maps, p, static_cast<int>(2 * clusters_of(h, tiles)), s);
+  // as many clusters as run at once: how many tiles there are, and whether they are shared, shows
+  // on the device
+  const int64_t clusters = clusters_of(h, tiles * ((p.k_blocks + 3) / 4), narrow);
+  p.stream_k = h->stream_k;
+  const gemm_status_t st = share_workspace(h, &p, clusters, narrow, s);
+  if (st != GEMM_OK) return st;
+  const cudaError_t e = expert_launch(mode, q.w_mn, narrow, maps, p, static_cast<int>(2 * clusters), s);
   if (e != cudaSuccess) return cuda_fail(e, "expert product launch");
   h->launches += 1;
   return GEMM_OK;
@@ -154,7 +182,7 @@ gemm_status_t run_expert_grad(gemm_handle_t h, const ExpertGrad &q, cudaStream_t
       (p.tma_out && !encode_3d(&maps.D, q.dtype, q.D, q.B.len, q.A.len, q.experts, q.ldd, q.stride_d, 64, 32)))
     return GEMM_ERR_CUDA;
   const int64_t tiles = q.experts * p.tiles_m * p.tiles_n;
-  const cudaError_t e = expert_grad_launch(maps, p, static_cast<int>(2 * clusters_of(h, tiles)), s);
+  const cudaError_t e = expert_grad_launch(maps, p, static_cast<int>(2 * clusters_of(h, tiles, false)), s);
   if (e != cudaSuccess) return cuda_fail(e, "expert gradient launch");
   h->launches += 1;
   return GEMM_OK;

@@ -12,10 +12,14 @@
 // time at 1024 rows and a third at 256. The same layout serves few tokens: a 32-column MMA, and
 // the time is that of the weights' stream.
 //
-// Grid: one cluster of two CTAs for every two SMs, which walk the tiles of all experts; every
-// role reads the offsets from shared memory and finds its tiles by itself, so that no table is
-// made and no count goes to the host. Token tiles run fastest: the clusters at work share weights
+// Grid: one cluster of two CTAs for every two SMs, which walk the tiles of all experts; every CTA
+// makes the table of tiles in its shared memory from the offsets, so that no count goes to the host
+// and no other launch is needed. Token tiles run fastest: the clusters at work share weights
 // through L2, and the next tile's loads and MMAs run under a tile's epilogue (two accumulators).
+// Where the last round of tiles would leave clusters idle for long, or there are fewer tiles than
+// clusters, the last tiles' K-blocks are shared equally (sk_schedule.h): a cluster that lacks a
+// tile's end writes its fp32 sums, one 128-byte line a column and warp, and the cluster that has
+// the end adds them in their order.
 //
 // The gated pair of K-contiguous weights: one TMA copy brings 16 rows of the gate's weights, the
 // same 16 of the up projection's, the next 16 of the gate's and so on (a 5D map whose third axis
@@ -47,35 +51,68 @@ constexpr int W_BYTES = BM * kRowBytes;         // one weight box (MN-major: two
 constexpr int PANEL_BYTES = BK * kRowBytes;
 constexpr int kEpi = 8;                         // epilogue warps
 constexpr int kExpertThreads = 64 + 32 * kEpi;
-constexpr int ACC = 256;                        // TMEM columns of an accumulator (gated: 128 each)
-
-template <int MODE>
+// A kernel's tiles and shared memory. Narrow: for few rows an expert, tiles of at most 64 tokens, so
+// that two CTAs fit an SM: twice as many, smaller shares of the weights' stream, and a kernel's start
+// (the table, the first loads) runs under the end of the one before it. One GB300, us, calls one
+// after another, narrow and wide: 4 rows gated 2048 x 4096 NARROW_A, 256 rows of 32 experts
+// 4096 x 2048 NARROW_B.
+template <int MODE, bool NARROW>
 struct Shape {
   static constexpr bool TWO = MODE == kExpertTwo;             // weight boxes, accumulators
   static constexpr int FEATURES = expert_features(MODE) / 2;  // a CTA's
-  static constexpr int TOKENS = expert_tokens(MODE);
+  static constexpr int TOKENS = expert_tokens(MODE, NARROW);
+  static constexpr int ACC = NARROW ? 64 : 256;               // TMEM columns of a tile (two: half each)
   static constexpr int W_ALL = (TWO ? 2 : 1) * W_BYTES;
   static constexpr int STAGE = W_ALL + TOKENS / 2 * kRowBytes;  // (a CTA's half of the tokens)
-  static constexpr int STAGES = TWO ? 5 : 6;
+  static constexpr int STAGES = TWO || NARROW ? 5 : 6;
   static constexpr int OFFSETS = STAGES * STAGE;
-  static constexpr int BARS = OFFSETS + (static_cast<int>(kMaxExperts) + 1) * 4 + 4;
-  static constexpr int END = BARS + (2 * STAGES + 5) * 8 + (6 + 2 * STAGES) * 4;
+  static constexpr int BARS = OFFSETS + 2 * (static_cast<int>(kMaxExperts) + 1) * 4;
+  static constexpr int END = BARS + (2 * STAGES + 5) * 8 + (6 + 2 * STAGES) * 4 + 1024;
+  // A wide CTA takes all of an SM's TMEM and so all of its shared memory, which keeps CTAs away that
+  // would wait for the first with the second in hand; narrow ones take a quarter and a half.
+  static constexpr int SMEM = NARROW ? 114688 : 232448;
+  static constexpr int SHARE = ACC * BM;                      // floats of a CTA's share of a split tile
+  static_assert(BARS % 8 == 0 && END <= SMEM, "shared memory");
 };
-// All of an SM's shared memory, because the CTA takes all of its TMEM: no CTA that needs some
-// then shares the SM.
-constexpr int SMEM_BYTES = 232448;
-static_assert(Shape<kExpertPlain>::BARS % 8 == 0 && Shape<kExpertTwo>::BARS % 8 == 0, "barriers are aligned");
-static_assert(Shape<kExpertPlain>::END + 1024 <= SMEM_BYTES && Shape<kExpertTwo>::END + 1024 <= SMEM_BYTES, "shared memory");
 
-// 32 tokens' columns of this lane, the `left` first of them stored from `row` on: one feature f, ...
-template <typename T, bool GATED>
-__device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, int64_t row, int left,
-                                       int64_t f) {
-  uint32_t r[32], q[32];
+// Split tiles: the sums of `n` clusters before this one, at this lane's place of column 0.
+struct Shares {
+  const float *first;
+  int n, step;
+};
+// 32 columns from c0 on: the accumulator and what other clusters summed before it.
+__device__ __forceinline__ void add_shares(const Shares &sh, int c0, uint32_t (&r)[32]) {
+  const float *from = sh.first + c0 * BM;
+  for (int i = 0; i < sh.n; ++i, from += sh.step) {
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __ldcg(from + j * BM);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + v[j]);
+  }
+}
+__device__ __forceinline__ void read_sums(uint32_t t_acc, int c0, const Shares &sh, uint32_t (&r)[32]) {
   __syncwarp();
-  tmem_ld_32x32b_x32(t_acc, r);
-  if (GATED) tmem_ld_32x32b_x32(t_acc + ACC / 2, q);
+  tmem_ld_32x32b_x32(t_acc + c0, r);
   tmem_wait_ld();
+  if (sh.n > 0) add_shares(sh, c0, r);
+}
+// This lane's 32 columns from c0 on for the cluster that finishes the tile.
+__device__ __forceinline__ void write_share(float *to, uint32_t t_acc, int c0) {
+  uint32_t r[32];
+  read_sums(t_acc, c0, Shares{nullptr, 0, 0}, r);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) __stcg(to + (c0 + j) * BM, __uint_as_float(r[j]));
+}
+
+// 32 tokens' columns from c0 on of this lane, the `left` first of them stored from `row` on: one
+// feature f, ...
+template <typename T, bool GATED, int ACC>
+__device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, int c0, const Shares &sh,
+                                       int64_t row, int left, int64_t f) {
+  uint32_t r[32], q[32];
+  read_sums(t_acc, c0, sh, r);
+  if (GATED) read_sums(t_acc, ACC / 2 + c0, sh, q);
   if (f >= p.N) return;
   float a[32];
 #pragma unroll
@@ -104,12 +141,10 @@ __device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, in
 // ... or g or u of one (the other 16 lanes have the other): the lower half of the warp finishes the
 // even tokens, the upper half the odd ones.
 template <typename T>
-__device__ __forceinline__ void finish_mixed(const ExpertParams &p, uint32_t t_acc, int64_t row, int left,
-                                             int64_t f, int lane) {
+__device__ __forceinline__ void finish_mixed(const ExpertParams &p, uint32_t t_acc, int c0, const Shares &sh,
+                                             int64_t row, int left, int64_t f, int lane) {
   uint32_t r[32];
-  __syncwarp();
-  tmem_ld_32x32b_x32(t_acc, r);
-  tmem_wait_ld();
+  read_sums(t_acc, c0, sh, r);
   const bool odd = lane >= 16, gate = odd == (p.up_first != 0);
   float a[16], u[16];
 #pragma unroll
@@ -140,16 +175,48 @@ __device__ __forceinline__ void finish_mixed(const ExpertParams &p, uint32_t t_a
     if (2 * j < left) y[2 * j * p.ldc] = from_f32<T>(a[j] * u[j]);
 }
 
-template <int MODE, bool W_MN>
-__global__ void __launch_bounds__(kExpertThreads, 1)
+// How the tiles are shared: whole ones round-robin, or the last rounds by K-blocks. Sharing costs
+// the writing and adding of sums, about `cost` K-blocks' time, and pays when it shortens the last
+// round by more. With fewer tiles than clusters a tile is cut into at most sqrt(k_blocks / 4) shares,
+// since their sums are added one after another.
+__device__ __forceinline__ SkSchedule share_out(int tiles, int kb, int clusters, int mode, int cost, bool narrow) {
+  int slots = clusters;
+  if (tiles < clusters) {
+    int most = 1;
+    while (most < clusters && 4 * (most + 1) * (most + 1) <= kb) ++most;
+    slots = min(clusters, tiles * most);
+  }
+  const int rest = slots > 0 ? tiles % slots : 0;
+  // K-blocks of the last round that a cluster is spared
+  const int64_t shared = static_cast<int64_t>(tiles < slots ? tiles : rest) * kb;
+  const int64_t saved = slots > 0 ? kb - (shared + slots - 1) / slots : 0;
+  const bool split = mode != 1 && shared > 0 && kb > 1 && (mode == 2 || (saved > cost && !(narrow && 2 * tiles > clusters)));
+  if (!split) return sk_make(tiles, kb, clusters, tiles);
+  return sk_make(tiles, kb, slots, sk_dp_tiles(tiles, kb, slots, true));
+}
+
+// A cluster's pieces of work, in its order.
+struct ExpertWork {
+  WorkIter it;
+  bool idle;
+  __device__ __forceinline__ ExpertWork(const SkSchedule &s, int cluster)
+      : it(s, cluster < s.slots ? cluster : 0), idle(cluster >= s.slots) {}
+  __device__ __forceinline__ bool next(SkSegment &seg) { return !idle && it.next(seg); }
+};
+
+template <int MODE, bool W_MN, bool NARROW>
+__global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
     expert_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
-  using S = Shape<MODE>;
+  using S = Shape<MODE, NARROW>;
   constexpr bool TWO = S::TWO;
+  constexpr int ACC = S::ACC;
   constexpr int STAGES = S::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  int32_t *offsets = reinterpret_cast<int32_t *>(smem + S::OFFSETS);
+  const ExpertTiles table{reinterpret_cast<int32_t *>(smem + S::OFFSETS),
+                          reinterpret_cast<int32_t *>(smem + S::OFFSETS) + kMaxExperts + 1, p.experts,
+                          (p.N + 2 * S::FEATURES - 1) / (2 * S::FEATURES), S::TOKENS};
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::BARS);
   uint64_t *empty = full + STAGES;
   uint64_t *tmem_full = empty + STAGES;
@@ -181,7 +248,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < 4 + 2 * STAGES; ++i) xs[i] = 0;
     fence_barrier_init();
-    prefetch_tensormap(&maps.X[2]);
+    prefetch_tensormap(&maps.X[NARROW ? 0 : 3]);
     prefetch_tensormap(&maps.W);
   }
   if (warp == 1) {
@@ -190,16 +257,25 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   }
   // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
   grid_dependency_wait();
-  load_offsets(offsets, p.offsets, p.experts, p.rows, kExpertThreads);
+  const int epoch = sk_epoch_begin(p.sk_epoch_word);
+  table.fill(p.offsets, p.rows, kExpertThreads);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   grid_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
-  const int cluster_id = blockIdx.x / 2, clusters = gridDim.x / 2;
-  ExpertWalk walk(offsets, p.experts, (p.N + 2 * S::FEATURES - 1) / (2 * S::FEATURES), S::TOKENS, 32);
-  int line, column;
+  const int cluster_id = blockIdx.x / 2;
+  const int tiles = table.count();
+  // (sums of wider tiles cost more; of the average width)
+  const int width = tiles > 0 ? (table.offsets[p.experts] - table.offsets[0]) / max(tiles / table.across, 1) : 0;
+  const SkSchedule sched = share_out(tiles, p.k_blocks, gridDim.x / 2, p.stream_k, 4 + width / 8, NARROW);
+  const bool split = sched.dp_tiles < sched.tiles;
+  // Every CTA has read the epoch word before it arrives here, and the next launch reads it after
+  // this one: the last to arrive may advance it at once.
+  if (split && threadIdx.x == 32 + 1) sk_epoch_end(p.sk_epoch_word, epoch);
+  ExpertWork work(sched, cluster_id);
+  SkSegment seg;
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
@@ -208,17 +284,16 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       bool ok = (p.debug_flags & kDebugStallProducer) == 0;
       const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
       const uint64_t keep = l2_policy_evict_last();
-      for (int t = cluster_id; ok && walk.seek(t); t += clusters) {
-        walk.place(t, line, column);
-        const int row0 = walk.lo + line * walk.width;
-        const int f0 = (2 * column + static_cast<int>(rank)) * S::FEATURES;
-        const int half = (min(walk.width, walk.hi - row0) + 31) / 32 * 16;  // a CTA's tokens
-        const int x_row = row0 + static_cast<int>(rank) * half;
+      while (ok && work.next(seg)) {
+        const ExpertTiles::Tile tile = table.at(seg.tile);
+        const int f0 = (2 * tile.column + static_cast<int>(rank)) * S::FEATURES;
+        const int half = (tile.rows + 31) / 32 * 16;  // a CTA's tokens
+        const int x_row = tile.row0 + static_cast<int>(rank) * half;
         // the smallest box that holds them: one copy a stage (a copy's issue takes the loader some
         // 150 cycles, so five 32-token ones made it the slowest part)
-        const int box = half <= 32 ? 0 : half <= 64 ? 1 : 2;
-        const uint32_t bytes = static_cast<uint32_t>(S::W_ALL + (kRowBytes * 32 << box));
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        const int box = NARROW ? 0 : (half - 1) / 32;
+        const uint32_t bytes = static_cast<uint32_t>(S::W_ALL + kRowBytes * 32 * (box + 1));
+        for (int kb = seg.kb_begin; kb < seg.kb_end; ++kb) {
           if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
             ok = false;  // test hook: this loader stops here, copies still in flight
             break;
@@ -239,14 +314,14 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             const CUtensorMap *w = (TWO ? m == 1 : second) ? &maps.W2 : &maps.W;
             const uint32_t dst = w_dst + m * W_BYTES;
             if (MODE == kExpertMixed) {
-              tma_load_5d_pair(dst, w, fb, k0, 0, 0, f0 / 16, walk.e);
+              tma_load_5d_pair(dst, w, fb, k0, 0, 0, f0 / 16, tile.e);
             } else if (W_MN && p.panels) {
-              tma_load_4d_pair(dst, w, fb, 0, k0, f0 / 64, walk.e);
+              tma_load_4d_pair(dst, w, fb, 0, k0, f0 / 64, tile.e);
             } else if (W_MN) {
-              tma_load_3d_pair(dst, w, fb, f0, k0, walk.e);
-              tma_load_3d_pair(dst + PANEL_BYTES, w, fb, f0 + 64, k0, walk.e);
+              tma_load_3d_pair(dst, w, fb, f0, k0, tile.e);
+              tma_load_3d_pair(dst + PANEL_BYTES, w, fb, f0 + 64, k0, tile.e);
             } else {
-              tma_load_3d_pair(dst, w, fb, k0, f0, walk.e);
+              tma_load_3d_pair(dst, w, fb, k0, f0, tile.e);
             }
           }
           tma_load_2d_pair_hint(x_dst, second ? &maps.X2[box] : &maps.X[box], fb, k0, x_row, keep);
@@ -265,15 +340,13 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     if (leader && lane == 0) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0;
       bool ok = true;
-      for (int t = cluster_id; ok && walk.seek(t); t += clusters) {
-        walk.place(t, line, column);
-        const int row0 = walk.lo + line * walk.width;
-        const uint32_t n = static_cast<uint32_t>(min(walk.width, walk.hi - row0) + 31) / 32 * 32;
+      while (ok && work.next(seg)) {
+        const uint32_t n = static_cast<uint32_t>(table.at(seg.tile).rows + 31) / 32 * 32;
         const uint32_t idesc = p.idesc | (n >> 3) << 17;
         if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * ACC;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = seg.kb_begin; kb < seg.kb_end; ++kb) {
           if (!mbar_wait(&full[stage], phase, wd)) {
             ok = false;
             break;
@@ -289,7 +362,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
 #pragma unroll
             for (int m = 0; m < (TWO ? 2 : 1); ++m)
               mma_f16_pair(d_tmem + m * (ACC / 2), wd + m * (W_BYTES / 16) + kk * W_STEP, xd + kk * (32 / 16),
-                           idesc, kb != 0 || kk != 0);
+                           idesc, kb != seg.kb_begin || kk != 0);
           mma_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
@@ -311,27 +384,49 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     const int quarter = warp & 3;
     const int half = (warp - 2) / 4;  // takes every other 32 tokens
     uint32_t acc = 0, acc_phase = 0;
-    for (int t = cluster_id; walk.seek(t); t += clusters) {
-      walk.place(t, line, column);
-      const int row0 = walk.lo + line * walk.width;
-      const int tokens = min(walk.width, walk.hi - row0);
-      const int64_t f = (2 * column + static_cast<int>(rank)) * S::FEATURES +
+    const int e = warp - 2;
+    // this lane's place in a CTA's shares
+    float *const place = split ? p.sk_partials + quarter * 32 + lane : nullptr;
+    while (work.next(seg)) {
+      const ExpertTiles::Tile tile = table.at(seg.tile);
+      const int64_t f = (2 * tile.column + static_cast<int>(rank)) * S::FEATURES +
                         (MODE == kExpertMixed ? quarter * 16 + lane % 16 : quarter * 32 + lane);
-      bool ok = mbar_wait_cluster(&tmem_full[acc], acc_phase, wd);
+      Shares sh{nullptr, 0, 2 * S::SHARE};
+      bool ok = true;
+      if (seg.role == kSegOwner) {
+        // the clusters first_src..last_src computed the start of this tile
+        for (int w = seg.first_src; ok && w <= seg.last_src; ++w)
+          ok = wait_flag(p.sk_flags + (w * 2 + rank) * kEpi + e, epoch, wd);
+        sh.first = place + static_cast<int64_t>(seg.first_src * 2 + static_cast<int>(rank)) * S::SHARE;
+        sh.n = seg.last_src - seg.first_src + 1;
+      }
+      ok = ok && mbar_wait_cluster(&tmem_full[acc], acc_phase, wd);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC;
-      for (int c0 = half * 32; c0 < tokens; c0 += 64) {
-        if (MODE == kExpertMixed) {
-          if (p.dtype == GEMM_BF16)
-            finish_mixed<__nv_bfloat16>(p, t_row + c0, row0 + c0, tokens - c0, f, lane);
-          else
-            finish_mixed<__half>(p, t_row + c0, row0 + c0, tokens - c0, f, lane);
-        } else if (p.dtype == GEMM_BF16) {
-          finish<__nv_bfloat16, TWO>(p, t_row + c0, row0 + c0, tokens - c0, f);
-        } else {
-          finish<__half, TWO>(p, t_row + c0, row0 + c0, tokens - c0, f);
+      if (seg.role == kSegPartial) {
+        float *to = place + static_cast<int64_t>(cluster_id * 2 + static_cast<int>(rank)) * S::SHARE;
+        for (int c0 = half * 32; c0 < tile.rows; c0 += 64) {
+          write_share(to, t_row, c0);
+          if (TWO) write_share(to, t_row, ACC / 2 + c0);
+        }
+        __syncwarp();  // (every lane's stores come before the flag)
+        if (lane == 0) st_release_gpu(p.sk_flags + (cluster_id * 2 + rank) * kEpi + e, epoch);
+      } else {
+        for (int c0 = half * 32; c0 < tile.rows; c0 += 64) {
+          const int64_t row = tile.row0 + c0;
+          const int left = tile.rows - c0;
+          if (MODE == kExpertMixed) {
+            if (p.dtype == GEMM_BF16)
+              finish_mixed<__nv_bfloat16>(p, t_row, c0, sh, row, left, f, lane);
+            else
+              finish_mixed<__half>(p, t_row, c0, sh, row, left, f, lane);
+          } else if (p.dtype == GEMM_BF16) {
+            finish<__nv_bfloat16, TWO, S::ACC>(p, t_row, c0, sh, row, left, f);
+          } else {
+            finish<__half, TWO, S::ACC>(p, t_row, c0, sh, row, left, f);
+          }
         }
       }
       tc_fence_before();
@@ -367,10 +462,11 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   }
 }
 
-template <int MODE, bool W_MN>
+template <int MODE, bool W_MN, bool NARROW>
 cudaError_t launch_expert(const ExpertMaps &maps, const ExpertParams &p, int grid, cudaStream_t s) {
-  auto kernel = expert_kernel<MODE, W_MN>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  auto kernel = expert_kernel<MODE, W_MN, NARROW>;
+  constexpr int SMEM = Shape<MODE, NARROW>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -382,7 +478,7 @@ cudaError_t launch_expert(const ExpertMaps &maps, const ExpertParams &p, int gri
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kExpertThreads, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -391,12 +487,20 @@ cudaError_t launch_expert(const ExpertMaps &maps, const ExpertParams &p, int gri
 
 }  // namespace
 
-cudaError_t expert_launch(ExpertMode mode, bool w_mn, const ExpertMaps &maps, const ExpertParams &p,
-                          int grid, cudaStream_t s) {
-  if (mode == kExpertMixed) return w_mn ? cudaErrorInvalidValue : launch_expert<kExpertMixed, false>(maps, p, grid, s);
-  if (mode == kExpertTwo)
-    return w_mn ? launch_expert<kExpertTwo, true>(maps, p, grid, s) : launch_expert<kExpertTwo, false>(maps, p, grid, s);
-  return w_mn ? launch_expert<kExpertPlain, true>(maps, p, grid, s) : launch_expert<kExpertPlain, false>(maps, p, grid, s);
+cudaError_t expert_launch(ExpertMode mode, bool w_mn, bool narrow, const ExpertMaps &maps,
+                          const ExpertParams &p, int grid, cudaStream_t s) {
+  if (mode == kExpertTwo && !narrow)
+    return w_mn ? launch_expert<kExpertTwo, true, false>(maps, p, grid, s)
+                : launch_expert<kExpertTwo, false, false>(maps, p, grid, s);
+  if (mode == kExpertMixed && !w_mn)
+    return narrow ? launch_expert<kExpertMixed, false, true>(maps, p, grid, s)
+                  : launch_expert<kExpertMixed, false, false>(maps, p, grid, s);
+  if (mode != kExpertPlain) return cudaErrorInvalidValue;
+  if (narrow)
+    return w_mn ? launch_expert<kExpertPlain, true, true>(maps, p, grid, s)
+                : launch_expert<kExpertPlain, false, true>(maps, p, grid, s);
+  return w_mn ? launch_expert<kExpertPlain, true, false>(maps, p, grid, s)
+              : launch_expert<kExpertPlain, false, false>(maps, p, grid, s);
 }
 
 int expert_max_clusters() {
@@ -408,7 +512,8 @@ int expert_max_clusters() {
   }
   const int known = cached[dev].load(std::memory_order_relaxed);
   if (known > 0) return known;
-  auto kernel = expert_kernel<kExpertPlain, false>;
+  auto kernel = expert_kernel<kExpertPlain, false, false>;
+  constexpr int smem = Shape<kExpertPlain, false>::SMEM;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -417,11 +522,11 @@ int expert_max_clusters() {
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kExpertThreads, 1, 1);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int got = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess || got < 1) {
     cudaGetLastError();
     return 1;

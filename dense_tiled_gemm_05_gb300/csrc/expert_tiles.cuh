@@ -8,50 +8,83 @@
 namespace gemm_gb300 {
 namespace ff {
 
-// Copies offsets (at most kMaxExperts + 1) to shared memory, kept inside [0, rows]. A walk takes
-// them in order and never back, so that offsets that decrease leave an expert without rows
-// instead of sending it outside.
-__device__ __forceinline__ void load_offsets(int32_t *to, const int32_t *offsets, int experts,
-                                             int rows, int threads) {
-  for (int e = threadIdx.x; e <= experts; e += threads) to[e] = max(0, min(offsets[e], rows));
-}
+// The tiles of all experts, numbered through: an expert with n rows has ceil(n / most) tiles along
+// its rows times `across` the other way. Both tables live in shared memory: the experts' first rows
+// (experts + 1) and first tiles (experts + 1; the last one is the number of tiles).
+struct ExpertTiles {
+  int32_t *offsets, *begins;
+  int experts, across;
+  int most;  // rows a tile, at most: a power of two
 
-// Experts in order with their tiles: `lines` tiles along the rows (of `width` rows each, the last
-// one shorter) times `across` tiles the other way. Tiles are numbered through all experts.
-struct ExpertWalk {
-  const int32_t *offsets;
-  int experts, across, most, step;  // most: rows a tile, at most; step: width's granularity
-  int e, lo, hi, begin, count, lines, width;
-  __device__ __forceinline__ ExpertWalk(const int32_t *o, int n, int a, int m, int s)
-      : offsets(o), experts(n), across(a), most(m), step(s), e(-1), lo(0), hi(o[0]), begin(0), count(0),
-        lines(0), width(0) {}
-  // Advances to the expert of tile t (t grows from call to call); false past the last one.
-  __device__ __forceinline__ bool seek(int t) {
-    while (t >= begin + count) {
-      if (++e >= experts) return false;
-      begin += count;
-      lo = hi;
-      hi = max(lo, offsets[e + 1]);
-      const int n = hi - lo;
-      lines = (n + most - 1) / most;
-      // rows shared evenly: 300 rows of 256 at most are 160 and 140, not 256 and 44
-      width = lines > 0 ? ((n + lines - 1) / lines + step - 1) / step * step : 0;
-      count = lines * across;
+  // Fills the tables from the caller's offsets, by all threads; a barrier has to follow. Offsets are
+  // kept inside [0, rows] and never decrease, so that no row has two experts and none lies outside.
+  __device__ __forceinline__ void fill(const int32_t *from, int rows, int threads) const {
+    for (int e = threadIdx.x; e <= experts; e += threads) offsets[e] = max(0, min(from[e], rows));
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    int high = offsets[0], sum = 0;
+    __syncwarp();
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+      const int e = e0 + static_cast<int>(threadIdx.x);
+      int end = e < experts ? offsets[e + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, end, d);
+        if (static_cast<int>(threadIdx.x) >= d) end = max(end, v);
+      }
+      end = max(end, high);
+      int start = __shfl_up_sync(0xffffffffu, end, 1);
+      if (threadIdx.x == 0) start = high;
+      const int mine = e < experts ? (end - start + most - 1) / most * across : 0;
+      int through = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, through, d);
+        if (static_cast<int>(threadIdx.x) >= d) through += v;
+      }
+      if (e < experts) {
+        offsets[e + 1] = end;
+        begins[e] = sum + through - mine;
+        if (e == experts - 1) begins[experts] = sum + through;
+      }
+      high = __shfl_sync(0xffffffffu, end, 31);
+      sum += __shfl_sync(0xffffffffu, through, 31);
     }
-    return true;
   }
-  // Line and column of tile t of the expert found: lines run fastest, in groups of eight, so that
-  // neighbouring tiles share both operands through L2.
-  __device__ __forceinline__ void place(int t, int &line, int &column) const {
-    int i = t - begin, first = 0, n = lines;
-    if (lines > 8) {
-      const int group = i / (8 * across);
-      first = group * 8;
-      i -= group * 8 * across;
-      n = min(lines - first, 8);
+  __device__ __forceinline__ int count() const { return begins[experts]; }
+
+  struct Tile {
+    int e, row0, rows, column;
+  };
+  // Tile t: its rows are an even share of the expert's, in steps of 32 (300 rows of 256 at most are
+  // 160 and 140, not 256 and 44). Tiles along the rows run fastest, in groups of eight, so that
+  // neighbours share both operands through L2.
+  __device__ __forceinline__ Tile at(int t) const {
+    int lo = 0, hi = experts;  // begins[lo] <= t < begins[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (begins[mid] <= t)
+        lo = mid;
+      else
+        hi = mid;
     }
-    column = i / n;
-    line = first + (i - column * n);
+    const int first_row = offsets[lo], n = offsets[lo + 1] - first_row;
+    const int lines = (n + most - 1) / most;
+    const int width = lines == 1 ? n : ((n + lines - 1) / lines + 31) / 32 * 32;
+    int i = t - begins[lo], first = 0, group = lines;
+    if (lines > 8) {
+      const int g = i / (8 * across);
+      first = g * 8;
+      i -= g * 8 * across;
+      group = min(lines - first, 8);
+    }
+    Tile tile;
+    tile.e = lo;
+    tile.column = group == 1 ? i : i / group;
+    const int line = first + (i - tile.column * group);
+    tile.row0 = first_row + line * width;
+    tile.rows = min(width, n - line * width);
+    return tile;
   }
 };
 

@@ -86,7 +86,7 @@ GEMM_API void gemm_destroy(gemm_handle_t h) {
   if (!h) return;
   DeviceGuard g(h->device);
   cudaDeviceSynchronize();
-  for (const Workspace *w : {&h->staging, &h->split, &h->host, &h->strided, &h->ff})
+  for (const Workspace *w : {&h->staging, &h->split, &h->host, &h->strided, &h->ff, &h->expert_split})
     if (w->ptr) cudaFree(w->ptr);
   while (RetiredBuffer *r = h->retired) {
     h->retired = r->next;
