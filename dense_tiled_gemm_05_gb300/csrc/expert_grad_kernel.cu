@@ -62,10 +62,6 @@ struct Tile {
     // (neighbouring tiles start apart, at multiples of what a power of two below `blocks` allows)
     start = blocks > 0 ? i & ((1 << (31 - __clz(blocks))) - 1) : 0;
   }
-  // The K-block that comes i-th.
-  __device__ __forceinline__ int block(int i) const {
-    return i + start < blocks ? i + start : i + start - blocks;
-  }
   __device__ __forceinline__ bool ragged() const { return blocks > 0 && last % 16 != 0; }
 };
 
@@ -158,7 +154,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   // stages whose own barriers were used for ragged blocks, and the parities of their last uses
   volatile uint32_t *tails = peer_bytes + STAGES;
 
-  const int warp = threadIdx.x / 32;
+  const int warp = uniform(static_cast<int>(threadIdx.x / 32));
   const int lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -189,7 +185,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
+  const uint32_t smem_base = smem_u32(smem);
   // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
   grid_dependency_wait();
   grid_launch_dependents();
@@ -199,49 +196,55 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, issued = 0;
-      uint32_t tail_used = 0, tail_parity = 0;  // by stage: used at all, parity of the last use
-      bool ok = (p.debug_flags & kDebugStallProducer) == 0;
-      const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
-      const uint64_t keep = l2_policy_evict_last();
-      for (int t = cluster_id; ok && t < tiles; t += clusters) {
-        const Tile tile(p, t);
-        const int m0 = tile.m0 + static_cast<int>(rank) * BM, n0 = tile.n0 + static_cast<int>(rank) * BM;
-        for (int ki = 0; ki < tile.blocks; ++ki) {
-          const int kb = tile.block(ki);
-          if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
-            ok = false;  // test hook: this loader stops here, copies still in flight
-            break;
-          }
-          if (!mbar_wait(&empty[stage], phase ^ 1, wd)) {
-            ok = false;
-            break;
-          }
-          const bool own = kb == tile.blocks - 1 && tile.ragged();
-          uint32_t fb;
+    // (the whole warp walks, one lane issues)
+    const bool issuer = elect_one();
+    uint32_t stage = 0, phase = 0, issued = 0;
+    uint32_t tail_used = 0, tail_parity = 0;  // by stage: used at all, parity of the last use
+    bool ok = (p.debug_flags & kDebugStallProducer) == 0;
+    const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
+    const uint64_t keep = l2_policy_evict_last();
+    for (int t = cluster_id; ok && t < tiles; t += clusters) {
+      const Tile tile(p, t);
+      const int m0 = tile.m0 + static_cast<int>(rank) * BM, n0 = tile.n0 + static_cast<int>(rank) * BM;
+      const int blocks = uniform(tile.blocks), first = uniform(tile.lo);
+      const int own_block = uniform(tile.ragged() ? tile.blocks - 1 : -1);
+      int kb = uniform(tile.start);
+      for (int i = 0; i < blocks; ++i) {
+        if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
+          ok = false;  // test hook: this loader stops here, copies still in flight
+          break;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, wd));
+        if (!ok) break;
+        const bool own = kb == own_block;
+        if (own) {
+          tail_parity = tail_used >> stage & 1 ? tail_parity ^ 1u << stage : tail_parity & ~(1u << stage);
+          tail_used |= 1u << stage;
+        }
+        if (issuer) {
+          const uint32_t fb = own ? mapa_shared(smem_u32(&tail[stage]), rank)
+                                  : mapa_shared(smem_u32(&full[stage]), 0);  // the leader's barrier
           if (own) {
-            fb = mapa_shared(smem_u32(&tail[stage]), rank);
             mbar_arrive_expect_tx(&tail[stage], STAGE_BYTES);
-            tail_parity = tail_used >> stage & 1 ? tail_parity ^ 1u << stage : tail_parity & ~(1u << stage);
-            tail_used |= 1u << stage;
             if (leader) mbar_arrive(&full[stage]);
-          } else {
-            fb = mapa_shared(smem_u32(&full[stage]), 0);
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2u * STAGE_BYTES);
+          } else if (leader) {
+            mbar_arrive_expect_tx(&full[stage], 2u * STAGE_BYTES);
           }
           fill_bytes[stage] = own ? 0 : STAGE_BYTES;
-          const uint32_t dst = smem_u32(smem + stage * STAGE_BYTES);
-          const int r0 = tile.lo + kb * BK;
-          load_panels(dst, &maps.A, p.panels_a, fb, m0, r0, keep);
-          load_panels(dst + 2 * PANEL_BYTES, &maps.B, p.panels_b, fb, n0, r0, keep);
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+          const uint32_t dst = smem_base + stage * STAGE_BYTES;
+          load_panels(dst, &maps.A, p.panels_a, fb, m0, first + kb * BK, keep);
+          load_panels(dst + 2 * PANEL_BYTES, &maps.B, p.panels_b, fb, n0, first + kb * BK, keep);
+        }
+        __syncwarp();
+        ++issued;
+        if (++kb == blocks) kb = 0;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
+    }
+    if (lane == 0) {
       xs[0] = issued;
       tails[0] = tail_used;
       tails[1] = tail_parity;
@@ -249,48 +252,62 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer (leader)
-    if (leader && lane == 0) {
+    if (leader) {  // (the whole warp walks, one lane issues)
+      const bool issuer = elect_one();
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0, masked_phase = 0;
       bool ok = true;
       for (int t = cluster_id; ok && t < tiles; t += clusters) {
         const Tile tile(p, t);
-        if (tile.blocks == 0) continue;
-        if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
+        const int blocks = uniform(tile.blocks);
+        if (blocks == 0) continue;
+        const int last = uniform(tile.last);
+        const bool ragged = last % 16 != 0;
+        int kb = uniform(tile.start);
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int ki = 0; ki < tile.blocks; ++ki) {
-          const bool end = tile.block(ki) == tile.blocks - 1;
+        for (int i = 0; i < blocks; ++i) {
+          const bool end = kb == blocks - 1;
           ok = mbar_wait(&full[stage], phase, wd);
-          if (ok && end && tile.ragged()) {
-            ok = mbar_wait_cluster(&masked[stage], masked_phase >> stage & 1, wd);
+          if (end && ragged) {
+            ok = ok && mbar_wait_cluster(&masked[stage], masked_phase >> stage & 1, wd);
             masked_phase ^= 1u << stage;
           }
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++consumed;
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + stage * STAGE_BYTES);
-          const uint32_t b_base = a_base + 2 * PANEL_BYTES;
-          const int steps = end ? (tile.last + 15) / 16 : BK / 16;
-          const uint64_t ad = sdesc_sw128(a_base, PANEL_BYTES, 1024), bd = sdesc_sw128(b_base, PANEL_BYTES, 1024);
+          const uint32_t a_base = smem_base + stage * STAGE_BYTES;
+          const uint64_t ad = sdesc_sw128(a_base, PANEL_BYTES, 1024);
+          const uint64_t bd = sdesc_sw128(a_base + 2 * PANEL_BYTES, PANEL_BYTES, 1024);
+          const int steps = end ? (last + 15) / 16 : BK / 16;
+          if (issuer) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)  // (16 rows on: 2048 bytes, in units of 16)
-            if (kk < steps)
-              mma_f16_pair(d_tmem, ad + kk * (16 * kRowBytes / 16), bd + kk * (16 * kRowBytes / 16), p.idesc,
-                           ki != 0 || kk != 0);
-          mma_commit_pair_multicast(&empty[stage], 0x3);
+            for (int kk = 0; kk < BK / 16; ++kk)  // (16 rows on: 2048 bytes, in units of 16)
+              if (kk < steps)
+                mma_f16_pair(d_tmem, ad + kk * (16 * kRowBytes / 16), bd + kk * (16 * kRowBytes / 16), p.idesc,
+                             i != 0 || kk != 0);
+            mma_commit_pair_multicast(&empty[stage], 0x3);
+          }
+          __syncwarp();
+          if (++kb == blocks) kb = 0;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit_pair_multicast(&tmem_full[acc], 0x3);
+        if (issuer) mma_commit_pair_multicast(&tmem_full[acc], 0x3);
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
-      mma_commit_pair(drain);
-      drain_wait(drain, 0, p.timeout_ns);
-      xs[1] = consumed;
+      if (issuer) {
+        mma_commit_pair(drain);
+        drain_wait(drain, 0, p.timeout_ns);
+        xs[1] = consumed;
+      }
     }
     __syncwarp();
   } else if (warp == kMaskWarp) {

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
   volatile uint32_t *xs = reinterpret_cast<volatile uint32_t *>(tmem_slot + 2);
   volatile uint32_t *fill_bytes = xs + 4, *peer_bytes = fill_bytes + STAGES;
 
-  const int warp = threadIdx.x / 32;
+  const int warp = uniform(static_cast<int>(threadIdx.x / 32));
   const int lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
   cluster_sync();
   tc_fence_after();
   grid_launch_dependents();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
+  const uint32_t smem_base = smem_u32(smem);
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
   const int cluster_id = blockIdx.x / 2;
   const int tiles = table.count();
@@ -279,33 +280,34 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, issued = 0;
-      bool ok = (p.debug_flags & kDebugStallProducer) == 0;
-      const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
-      const uint64_t keep = l2_policy_evict_last();
-      while (ok && work.next(seg)) {
-        const ExpertTiles::Tile tile = table.at(seg.tile);
-        const int f0 = (2 * tile.column + static_cast<int>(rank)) * S::FEATURES;
-        const int half = (tile.rows + 31) / 32 * 16;  // a CTA's tokens
-        const int x_row = tile.row0 + static_cast<int>(rank) * half;
-        // the smallest box that holds them: one copy a stage (a copy's issue takes the loader some
-        // 150 cycles, so five 32-token ones made it the slowest part)
-        const int box = NARROW ? 0 : (half - 1) / 32;
-        const uint32_t bytes = static_cast<uint32_t>(S::W_ALL + kRowBytes * 32 * (box + 1));
-        for (int kb = seg.kb_begin; kb < seg.kb_end; ++kb) {
-          if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
-            ok = false;  // test hook: this loader stops here, copies still in flight
-            break;
-          }
-          if (!mbar_wait(&empty[stage], phase ^ 1, wd)) {
-            ok = false;
-            break;
-          }
+    // (the whole warp walks, one lane issues)
+    const bool issuer = elect_one();
+    uint32_t stage = 0, phase = 0, issued = 0;
+    bool ok = (p.debug_flags & kDebugStallProducer) == 0;
+    const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
+    const uint64_t keep = l2_policy_evict_last();
+    while (ok && work.next(seg)) {
+      const ExpertTiles::Tile tile = table.at(seg.tile);
+      const int expert = uniform(tile.e);
+      const int f0 = uniform(2 * tile.column + static_cast<int>(rank)) * S::FEATURES;
+      const int half = uniform((tile.rows + 31) / 32 * 16);  // a CTA's tokens
+      const int x_row = uniform(tile.row0) + static_cast<int>(rank) * half;
+      // the smallest box that holds them: one copy a stage (a copy's issue takes the loader some
+      // 50 cycles, and its loop ran as long as four MMAs with five 32-token ones)
+      const int box = NARROW ? 0 : (half - 1) / 32;
+      const uint32_t bytes = static_cast<uint32_t>(S::W_ALL + kRowBytes * 32 * (box + 1));
+      const int kb_end = uniform(seg.kb_end);
+      for (int kb = uniform(seg.kb_begin); kb < kb_end; ++kb) {
+        if (stop_after >= 0 && issued >= static_cast<uint32_t>(stop_after)) {
+          ok = false;  // test hook: this loader stops here, copies still in flight
+          break;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1, wd));
+        if (!ok) break;
+        if (issuer) {
           fill_bytes[stage] = bytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
-          const uint32_t w_dst = smem_u32(smem + stage * S::STAGE);
-          const uint32_t x_dst = w_dst + S::W_ALL;
+          const uint32_t w_dst = smem_base + stage * S::STAGE;
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);  // the leader's barrier
           const bool second = MODE == kExpertPlain && kb >= p.kb_first;
           const int k0 = (second ? kb - p.kb_first : kb) * BK;
@@ -314,69 +316,77 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
             const CUtensorMap *w = (TWO ? m == 1 : second) ? &maps.W2 : &maps.W;
             const uint32_t dst = w_dst + m * W_BYTES;
             if (MODE == kExpertMixed) {
-              tma_load_5d_pair(dst, w, fb, k0, 0, 0, f0 / 16, tile.e);
+              tma_load_5d_pair(dst, w, fb, k0, 0, 0, f0 / 16, expert);
             } else if (W_MN && p.panels) {
-              tma_load_4d_pair(dst, w, fb, 0, k0, f0 / 64, tile.e);
+              tma_load_4d_pair(dst, w, fb, 0, k0, f0 / 64, expert);
             } else if (W_MN) {
-              tma_load_3d_pair(dst, w, fb, f0, k0, tile.e);
-              tma_load_3d_pair(dst + PANEL_BYTES, w, fb, f0 + 64, k0, tile.e);
+              tma_load_3d_pair(dst, w, fb, f0, k0, expert);
+              tma_load_3d_pair(dst + PANEL_BYTES, w, fb, f0 + 64, k0, expert);
             } else {
-              tma_load_3d_pair(dst, w, fb, k0, f0, tile.e);
+              tma_load_3d_pair(dst, w, fb, k0, f0, expert);
             }
           }
-          tma_load_2d_pair_hint(x_dst, second ? &maps.X2[box] : &maps.X[box], fb, k0, x_row, keep);
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+          tma_load_2d_pair_hint(w_dst + S::W_ALL, second ? &maps.X2[box] : &maps.X[box], fb, k0, x_row, keep);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      xs[0] = issued;
     }
+    if (lane == 0) xs[0] = issued;
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer (leader)
-    if (leader && lane == 0) {
+    if (leader) {  // (the whole warp walks, one lane issues)
+      const bool issuer = elect_one();
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0;
       bool ok = true;
       while (ok && work.next(seg)) {
-        const uint32_t n = static_cast<uint32_t>(table.at(seg.tile).rows + 31) / 32 * 32;
+        const uint32_t n = static_cast<uint32_t>(uniform(table.at(seg.tile).rows) + 31) / 32 * 32;
         const uint32_t idesc = p.idesc | (n >> 3) << 17;
-        if (!mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd)) break;
+        const int blocks = uniform(seg.kb_end - seg.kb_begin);
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1, wd));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * ACC;
-        for (int kb = seg.kb_begin; kb < seg.kb_end; ++kb) {
-          if (!mbar_wait(&full[stage], phase, wd)) {
-            ok = false;
-            break;
-          }
+        for (int i = 0; i < blocks; ++i) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, wd));
+          if (!ok) break;
           ++consumed;
           tc_fence_after();
-          const uint32_t w_base = smem_u32(smem + stage * S::STAGE);
+          const uint32_t w_base = smem_base + stage * S::STAGE;
           const uint64_t xd = sdesc_sw128(w_base + S::W_ALL, 16, 1024);
-          const uint64_t wd = W_MN ? sdesc_sw128(w_base, PANEL_BYTES, 1024) : sdesc_sw128(w_base, 16, 1024);
+          const uint64_t wd_ = W_MN ? sdesc_sw128(w_base, PANEL_BYTES, 1024) : sdesc_sw128(w_base, 16, 1024);
           constexpr int W_STEP = W_MN ? 16 * kRowBytes / 16 : 32 / 16;  // 16 of K, in units of 16 bytes
+          if (issuer) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
+            for (int kk = 0; kk < BK / 16; ++kk)
 #pragma unroll
-            for (int m = 0; m < (TWO ? 2 : 1); ++m)
-              mma_f16_pair(d_tmem + m * (ACC / 2), wd + m * (W_BYTES / 16) + kk * W_STEP, xd + kk * (32 / 16),
-                           idesc, kb != seg.kb_begin || kk != 0);
-          mma_commit_pair_multicast(&empty[stage], 0x3);
+              for (int m = 0; m < (TWO ? 2 : 1); ++m)
+                mma_f16_pair(d_tmem + m * (ACC / 2), wd_ + m * (W_BYTES / 16) + kk * W_STEP,
+                             xd + kk * (32 / 16), idesc, i != 0 || kk != 0);
+            mma_commit_pair_multicast(&empty[stage], 0x3);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit_pair_multicast(&tmem_full[acc], 0x3);
+        if (issuer) mma_commit_pair_multicast(&tmem_full[acc], 0x3);
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
-      mma_commit_pair(drain);
-      drain_wait(drain, 0, p.timeout_ns);
-      xs[1] = consumed;
+      if (issuer) {
+        mma_commit_pair(drain);
+        drain_wait(drain, 0, p.timeout_ns);
+        xs[1] = consumed;
+      }
     }
     __syncwarp();
   } else {
