@@ -14,7 +14,10 @@
 // tells the issuer. All other blocks go from TMA to the MMAs as ever.
 //
 // The schedule is fixed, tile by tile through the experts, so that the clusters at work read the
-// same rows from L2. An expert without rows gets zeros. One accumulation a tile, in the rows'
+// same rows from L2. Tiles of an expert with many rows run long: the experts come in the order of
+// their rows, most first, and every other round of clusters runs backwards, so that the shares even
+// out (16 experts of 46 to 4407 rows, 2048 x 4096: SORT_A us, SORT_B in their own order). An expert
+// without rows gets zeros. One accumulation a tile, in the rows'
 // order: the same call gives the same bits. Bound by the tensor cores for many rows an expert, by
 // the writing of D for few (256 rows of bf16: as long as its MMAs).
 #include "activation.cuh"
@@ -42,27 +45,68 @@ constexpr int HALF = BN / 2;                    // accumulator columns of an epi
 constexpr int EPI_OFFSET = STAGES * STAGE_BYTES;
 constexpr int BAR_OFFSET = EPI_OFFSET + kEpi * 2 * kStoreBufBytes;
 constexpr int SMEM_BYTES = 232448;              // (all of it: see expert_pair_kernel.cu)
-static_assert(BAR_OFFSET + (4 * STAGES + 5) * 8 + (8 + 2 * STAGES) * 4 + 1024 <= SMEM_BYTES, "shared memory");
+constexpr int ORDER_OFFSET = BAR_OFFSET + (4 * STAGES + 5) * 8 + (8 + 2 * STAGES) * 4;
+constexpr int kOrdered = 256;                   // experts that are put in order, at most
+static_assert(ORDER_OFFSET + kOrdered * 6 + 1024 <= SMEM_BYTES, "shared memory");
+
+__device__ __forceinline__ int first_row(const ExpertGradParams &p, int e) {
+  return max(0, min(p.offsets[e], p.rows));
+}
+__device__ __forceinline__ int row_count(const ExpertGradParams &p, int e) {
+  const int lo = first_row(p, e);
+  return max(lo, min(p.offsets[e + 1], p.rows)) - lo;
+}
+
+// Experts by their rows, most first (equal ones by number), in shared memory; a barrier has to follow.
+struct ExpertOrder {
+  int32_t *rows;    // [kOrdered]
+  uint16_t *order;  // [kOrdered]
+  __device__ __forceinline__ void fill(const ExpertGradParams &p) const {
+    if (p.experts > kOrdered) return;
+    for (int e = threadIdx.x; e < p.experts; e += kGradThreads) rows[e] = row_count(p, e);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.experts; e += kGradThreads) {
+      const int n = rows[e];
+      int rank = 0;
+      for (int i = 0; i < p.experts; ++i) rank += rows[i] > n || (rows[i] == n && i < e);
+      order[rank] = static_cast<uint16_t>(e);
+    }
+  }
+  __device__ __forceinline__ int at(const ExpertGradParams &p, int i) const {
+    return p.experts > kOrdered ? i : order[i];
+  }
+};
 
 // A tile of an expert: its rows and columns.
 struct Tile {
   int e, lo, blocks, last;  // first row, K-blocks, rows of the last block
   int start;                // the K-block that the sum begins with; it wraps after the last one
   int m0, n0;
-  __device__ __forceinline__ Tile(const ExpertGradParams &p, int t) {
+  __device__ __forceinline__ Tile(const ExpertGradParams &p, const ExpertOrder &order, int t) {
     const int per = p.tiles_m * p.tiles_n;
-    e = t / per;
-    const int i = t - e * per;
-    m0 = i % p.tiles_m * (2 * BM);
-    n0 = i / p.tiles_m * BN;
-    lo = max(0, min(p.offsets[e], p.rows));
-    const int n = max(lo, min(p.offsets[e + 1], p.rows)) - lo;
+    const int place = t / per, i = t - place * per;
+    e = order.at(p, place);
+    n0 = i / p.tiles_m;
+    m0 = (i - n0 * p.tiles_m) * (2 * BM);
+    n0 *= BN;
+    lo = first_row(p, e);
+    const int n = row_count(p, e);
     blocks = (n + BK - 1) / BK;
     last = n - (blocks - 1) * BK;
     // (neighbouring tiles start apart, at multiples of what a power of two below `blocks` allows)
     start = blocks > 0 ? i & ((1 << (31 - __clz(blocks))) - 1) : 0;
   }
   __device__ __forceinline__ bool ragged() const { return blocks > 0 && last % 16 != 0; }
+};
+
+// A cluster's tiles: one of every round, forwards and backwards in turn.
+struct Rounds {
+  int cluster, clusters, tiles, i;
+  __device__ __forceinline__ bool next(int &t) {
+    t = i * clusters + (i & 1 ? clusters - 1 - cluster : cluster);
+    ++i;
+    return t < tiles;
+  }
 };
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src, int32_t x, int32_t y,
@@ -190,9 +234,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
   grid_dependency_wait();
   grid_launch_dependents();
+  const ExpertOrder order{reinterpret_cast<int32_t *>(smem + ORDER_OFFSET),
+                          reinterpret_cast<uint16_t *>(smem + ORDER_OFFSET + kOrdered * 4)};
+  order.fill(p);
+  __syncthreads();
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
-  const int cluster_id = blockIdx.x / 2, clusters = gridDim.x / 2;
-  const int tiles = p.experts * p.tiles_m * p.tiles_n;
+  Rounds rounds{static_cast<int>(blockIdx.x / 2), static_cast<int>(gridDim.x / 2),
+                p.experts * p.tiles_m * p.tiles_n, 0};
+  int t;
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
@@ -203,8 +252,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     bool ok = (p.debug_flags & kDebugStallProducer) == 0;
     const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
     const uint64_t keep = l2_policy_evict_last();
-    for (int t = cluster_id; ok && t < tiles; t += clusters) {
-      const Tile tile(p, t);
+    while (ok && rounds.next(t)) {
+      const Tile tile(p, order, t);
       const int m0 = tile.m0 + static_cast<int>(rank) * BM, n0 = tile.n0 + static_cast<int>(rank) * BM;
       const int blocks = uniform(tile.blocks), first = uniform(tile.lo);
       const int own_block = uniform(tile.ragged() ? tile.blocks - 1 : -1);
@@ -256,8 +305,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const bool issuer = elect_one();
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, consumed = 0, masked_phase = 0;
       bool ok = true;
-      for (int t = cluster_id; ok && t < tiles; t += clusters) {
-        const Tile tile(p, t);
+      while (ok && rounds.next(t)) {
+        const Tile tile(p, order, t);
         const int blocks = uniform(tile.blocks);
         if (blocks == 0) continue;
         const int last = uniform(tile.last);
@@ -313,8 +362,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   } else if (warp == kMaskWarp) {
     // ------------------------- rows past an expert's last: zeros (both CTAs)
     uint32_t fills = 0, phases = 0;
-    for (int t = cluster_id; t < tiles; t += clusters) {
-      const Tile tile(p, t);
+    while (rounds.next(t)) {
+      const Tile tile(p, order, t);
       const uint32_t before = fills;
       fills += static_cast<uint32_t>(tile.blocks);
       if (!tile.ragged()) continue;
@@ -343,8 +392,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     uint8_t *boxes = smem + EPI_OFFSET + e * 2 * kStoreBufBytes;
     int next = 0;
     uint32_t acc = 0, acc_phase = 0;
-    for (int t = cluster_id; t < tiles; t += clusters) {
-      const Tile tile(p, t);
+    while (rounds.next(t)) {
+      const Tile tile(p, order, t);
       const bool zero = tile.blocks == 0;
       if (!zero) {
         bool ok = mbar_wait_cluster(&tmem_full[acc], acc_phase, wd);

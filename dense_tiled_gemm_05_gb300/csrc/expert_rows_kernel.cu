@@ -24,20 +24,22 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 32 * VEC;  // columns a warp covers at a time
+constexpr int64_t kWalkCtas = 1520;
 
 bool aligned16(const void *p, int64_t ld, int es) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0);
 }
 int esize(int dt) { return dt == GEMM_F32 ? 4 : 2; }
 
-// Column blocks along x; along y as many CTAs as keep 152 SMs busy, each warp walking tokens.
-dim3 token_grid(int64_t tokens, int64_t N) {
+// Column blocks along x, tokens along y: one a warp where rows are mostly written, since CTAs then
+// start in the order of memory, which HBM writes faster than grids that stay and stride through it
+// (65536 rows of 4 KB from 16384: 54 us against 63 with 608 CTAs that loop); about ten CTAs an SM,
+// whose warps walk tokens, where they are mostly read.
+dim3 token_grid(int64_t tokens, int64_t N, bool walk) {
   const int64_t gx = (N + kCols - 1) / kCols;
-  const int64_t all = (tokens + kWarps - 1) / kWarps;
-  int64_t gy = (3040 + gx - 1) / gx;
-  if (gy > all) gy = all;
-  if (gy > 65535) gy = 65535;
-  return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  int64_t gy = (tokens + kWarps - 1) / kWarps;
+  if (walk) gy = std::min(gy, (kWalkCtas + gx - 1) / gx);
+  return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(gy, 65535)));
 }
 
 #define FF_TOKENS(t, tokens)                                                              \
@@ -72,7 +74,6 @@ __global__ void __launch_bounds__(kThreads)
   grid_launch_dependents();
   const int lane = threadIdx.x % 32;
   const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
-#pragma unroll 2
   FF_TOKENS(t, tokens) {
     alignas(16) E e[VEC];
     cols.load(x + t * ldx, e);
@@ -97,16 +98,28 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x % 32;
   const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
   constexpr int BATCH = sizeof(TI) == 4 ? 2 : 4;  // rows on the way at once
-  FF_TOKENS(t, tokens) {
+  const int64_t step = static_cast<int64_t>(gridDim.y) * kWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32;
+  // a token's first 32 positions and weights are asked for while the token before it is added up
+  auto position_of = [&](int64_t i, int j) { return j < k && i < tokens ? position[i * k + j] : -1; };
+  auto weight_of = [&](int64_t i, int j) {
+    return !w ? 1.0f : j < k && i < tokens ? load_any(w, w_dtype, i * k + j) : 0.0f;
+  };
+  int32_t next_p = position_of(t, lane);
+  float next_f = weight_of(t, lane);
+  for (; t < tokens; t += step) {
     float sum[VEC];
     alignas(16) TO res[VEC];  // (y may be the residual: a lane reads its columns before it writes them)
     if (residual) cols.load(residual + t * ldr, res);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) sum[c] = 0.0f;
+    int32_t p = next_p;
+    float f = next_f;
+    next_p = position_of(t + step, lane);
+    next_f = weight_of(t + step, lane);
     for (int j0 = 0; j0 < k; j0 += 32) {
       const int n = min(32, k - j0);
-      const int32_t p = lane < n ? position[t * k + j0 + lane] : -1;
-      const float f = !w ? 1.0f : lane < n ? load_any(w, w_dtype, t * k + j0 + lane) : 0.0f;
+      if (j0 > 0) p = position_of(t, j0 + lane), f = weight_of(t, j0 + lane);
       for (int j = 0; j < n; j += BATCH) {
         alignas(16) TI e[BATCH][VEC];
         float wj[BATCH];
@@ -230,7 +243,7 @@ cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *posi
   const bool vector = aligned16(x, ldx, es) && aligned16(y, ldy, es) && N % VEC == 0;
   auto go = [&](auto *type, auto vec) {
     using E = std::remove_pointer_t<decltype(type)>;
-    launch_pdl(gather_kernel<E, decltype(vec)::value>, token_grid(tokens, N), kThreads, 0, s,
+    launch_pdl(gather_kernel<E, decltype(vec)::value>, token_grid(tokens, N, false), kThreads, 0, s,
                static_cast<const E *>(x), ldx, position, static_cast<E *>(y), ldy, tokens,
                static_cast<int>(k), rows, N);
   };
@@ -250,7 +263,7 @@ cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, cons
   FF_TYPED(in_dtype, TI, {
     FF_TYPED(out_dtype, TO, {
       auto go = [&](auto kernel) {
-        launch_pdl(kernel, token_grid(tokens, N), kThreads, 0, s, static_cast<const TI *>(z), ldz,
+        launch_pdl(kernel, token_grid(tokens, N, true), kThreads, 0, s, static_cast<const TI *>(z), ldz,
                    position, w, w_dtype, static_cast<const TO *>(residual), ldr,
                    static_cast<TO *>(y), ldy, tokens, static_cast<int>(k), rows, N);
       };
@@ -273,7 +286,7 @@ cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int gra
   int share = 1;
   while (share < kWarps && pairs * share < target && N > static_cast<int64_t>(share) * kCols) share *= 2;
   const int per_cta = kWarps / share;
-  const int64_t ctas = std::min<int64_t>((pairs + per_cta - 1) / per_cta, int64_t{152} * 64);
+  const int64_t ctas = std::min<int64_t>((pairs + per_cta - 1) / per_cta, int64_t{1} << 20);
   FF_TYPED(grad_dtype, TG, {
     FF_TYPED(in_dtype, TZ, {
       auto go = [&](auto kernel) {

@@ -4,14 +4,16 @@
 //   position[i] = offsets[id_i] + number of entries before i with the same id,
 //
 // a stable counting sort (-1 for an id outside [0, experts)). The entries are cut into chunks, a
-// CTA each, and a chunk into one run of neighbours a warp. One kernel counts every chunk's ids;
-// the next adds up the counts of the chunks before its own and of the experts before each (every
-// CTA for itself: at most 128 chunks, so up to half a megabyte from L2), then of its own warps
-// before each, and gives out positions 32 entries at a time: lanes with one id find each other
-// by a warp match and are ranked by lane. All counts are integers: the same ids give the same
-// order. Up to kChunk entries take one launch.
+// CTA each, and a chunk into one run of neighbours a warp, ITEMS a lane in registers. One kernel
+// counts every chunk's ids; the next ranks its own entries 32 at a time -- lanes with one id find
+// each other by a warp match, and the warp's running count of that id gives their places in its
+// run -- and meanwhile adds up the counts of the chunks before its own and of the experts before
+// each (every CTA for itself, from L2: at most 128 chunks until a lane's entries no longer fit its
+// registers), then of its warps. All counts are integers: the same ids give the same order. Up to
+// 2048 entries take one launch.
 //
-// Bound by latency: a chain of loads, counts, prefix sums and stores.
+// Bound by latency, a chain of loads, matches, prefix sums and stores (one GB300: 256 entries
+// SORT_A us, 65536 SORT_B, calls one after another).
 #include <algorithm>
 
 #include "expert_internal.h"
@@ -24,22 +26,25 @@ namespace {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int64_t kChunk = 2048;     // least entries a CTA
-constexpr int64_t kMaxChunks = 128;
+constexpr int64_t kMaxChunks = 128;  // of up to 16 entries a thread
 
 struct SortParams {
   const void *ids;
   int64_t ld_ids;
   int64_t n;
   int32_t k, experts, chunk, chunks;
-  int32_t wide;
+  int32_t wide, flat;  // 8-byte ids; rows of ids follow one another
   int32_t *position, *offsets;
   int32_t *counts;  // [chunks][experts]
 };
 
 // Expert of entry i, or -1.
 __device__ __forceinline__ int id_at(const SortParams &p, int64_t i) {
-  const int64_t t = i / p.k, at = t * p.ld_ids + (i - t * p.k);
+  int64_t at = i;
+  if (!p.flat) {
+    const uint32_t t = static_cast<uint32_t>(i) / static_cast<uint32_t>(p.k);
+    at = t * p.ld_ids + (static_cast<uint32_t>(i) - t * static_cast<uint32_t>(p.k));
+  }
   const int64_t id = p.wide ? static_cast<const int64_t *>(p.ids)[at]
                             : static_cast<int64_t>(static_cast<const int32_t *>(p.ids)[at]);
   return id >= 0 && id < p.experts ? static_cast<int>(id) : -1;
@@ -62,6 +67,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const SortPa
     p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = count[e];
 }
 
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const SortParams p) {
   extern __shared__ int32_t smem[];
   const int E = p.experts;
@@ -75,22 +81,42 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const SortPa
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // This warp's run of the chunk.
-  const int64_t run = (p.chunk + kSortWarps - 1) / kSortWarps;
-  const int64_t end = min(static_cast<int64_t>(blockIdx.x + 1) * p.chunk, p.n);
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * p.chunk + warp * run;
-  const int64_t hi = min(lo + run, end);
+  // This warp's run of the chunk: every lane's entries, and their places among the run's entries
+  // of the same expert.
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * p.chunk + warp * (32 * ITEMS);
+  int id[ITEMS], place[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int64_t at = lo + i * 32 + lane;
+    id[i] = at < p.n ? id_at(p, at) : -1;
+  }
   int32_t *mine = cursor + warp * E;
-  for (int64_t i = lo + lane; i < hi; i += 32) {
-    const int id = id_at(p, i);
-    if (id >= 0) atomicAdd(&mine[id], 1);
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    if (lo + i * 32 >= p.n) break;
+    const unsigned same = __match_any_sync(0xffffffffu, id[i]);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    const int at = id[i] >= 0 ? mine[id[i]] : 0;
+    __syncwarp();  // every lane has read its count
+    if (id[i] >= 0 && rank == 0) mine[id[i]] = at + __popc(same);
+    __syncwarp();
+    place[i] = at + rank;
   }
   if (p.chunks > 1) {
-    for (int c = warp; c < p.chunks; c += kSortWarps)
-      for (int e = lane; e < E; e += 32) {
-        const int v = p.counts[static_cast<int64_t>(c) * E + e];
-        if (v) atomicAdd(&total[e], v);
-        if (v && c < static_cast<int>(blockIdx.x)) atomicAdd(&before[e], v);
+    // groups of threads take every so many-th chunk, a thread one expert
+    const int width = (E + 31) / 32 * 32, groups = max(1, kSortThreads / width);
+    const int g = static_cast<int>(threadIdx.x) / width;
+    if (g < groups)
+      for (int e = static_cast<int>(threadIdx.x) - g * width; e < E; e += kSortThreads) {
+        int all = 0, earlier = 0;
+#pragma unroll 8
+        for (int c = g; c < p.chunks; c += groups) {
+          const int v = p.counts[static_cast<int64_t>(c) * E + e];
+          all += v;
+          earlier += c < static_cast<int>(blockIdx.x) ? v : 0;
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], earlier);
       }
   }
   __syncthreads();
@@ -139,28 +165,36 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const SortPa
     }
   }
   __syncthreads();
-  for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int id = i < hi ? id_at(p, i) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, id);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    const int at = id >= 0 ? mine[id] : 0;
-    __syncwarp();  // every lane has read its cursor
-    if (id >= 0 && rank == 0) mine[id] = at + __popc(same);
-    __syncwarp();
-    if (i < hi) p.position[i] = id >= 0 ? at + rank : -1;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int64_t at = lo + i * 32 + lane;
+    if (at < p.n) p.position[at] = id[i] >= 0 ? mine[id[i]] + place[i] : -1;
   }
 }
 
-int64_t chunk_of(int64_t n) {
-  const int64_t even = (n + kMaxChunks - 1) / kMaxChunks;
-  return even > kChunk ? (even + 511) / 512 * 512 : kChunk;
+// Entries a lane holds: 4, 8 or 16, and 16 for any longer list.
+int items_of(int64_t n) {
+  int items = 4;
+  while (items < 16 && n > kMaxChunks * kSortThreads * items) items *= 2;
+  return items;
+}
+
+template <int ITEMS>
+cudaError_t place_launch(const SortParams &p, dim3 grid, size_t smem, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        expert_place_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>((2 + kSortWarps) * kMaxExperts * sizeof(int32_t)));
+    if (e != cudaSuccess) return e;
+  }
+  launch_pdl(expert_place_kernel<ITEMS>, grid, kSortThreads, smem, s, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t expert_sort_bytes(int64_t n, int64_t experts) {
-  const int64_t chunk = chunk_of(n), chunks = (n + chunk - 1) / chunk;
+  const int64_t chunk = static_cast<int64_t>(kSortThreads) * items_of(n), chunks = (n + chunk - 1) / chunk;
   return chunks > 1 ? static_cast<size_t>(chunks * experts) * sizeof(int32_t) : 0;
 }
 
@@ -169,30 +203,25 @@ cudaError_t expert_sort_launch(const void *ids, int64_t ld_ids, bool wide, int64
                                void *workspace, int *launches, cudaStream_t s) {
   SortParams p{};
   p.ids = ids, p.ld_ids = ld_ids, p.wide = wide;
+  p.flat = tokens <= 1 || ld_ids == k;
   p.n = tokens * k;
   p.k = static_cast<int32_t>(std::max<int64_t>(k, 1));
   p.experts = static_cast<int32_t>(experts);
-  const int64_t chunk = chunk_of(p.n);
+  const int items = items_of(p.n);
+  const int64_t chunk = static_cast<int64_t>(kSortThreads) * items;
   const int64_t chunks = std::max<int64_t>((p.n + chunk - 1) / chunk, 1);
   p.chunk = static_cast<int32_t>(chunk), p.chunks = static_cast<int32_t>(chunks);
   p.position = position, p.offsets = offsets;
   p.counts = static_cast<int32_t *>(workspace);
   const dim3 grid(static_cast<unsigned>(chunks));
-  *launches = 0;
-  if (chunks > 1) {
-    launch_pdl(expert_count_kernel, grid, kSortThreads, experts * sizeof(int32_t), s, p);
-    *launches += 1;
-  }
+  *launches = chunks > 1 ? 2 : 1;
+  if (chunks > 1) launch_pdl(expert_count_kernel, grid, kSortThreads, experts * sizeof(int32_t), s, p);
   const size_t smem = static_cast<size_t>(2 + kSortWarps) * experts * sizeof(int32_t);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        static_cast<int>((2 + kSortWarps) * kMaxExperts * sizeof(int32_t)));
-    if (e != cudaSuccess) return e;
+  switch (items) {
+    case 4: return place_launch<4>(p, grid, smem, s);
+    case 8: return place_launch<8>(p, grid, smem, s);
+    default: return place_launch<16>(p, grid, smem, s);
   }
-  launch_pdl(expert_place_kernel, grid, kSortThreads, smem, s, p);
-  *launches += 1;
-  return cudaGetLastError();
 }
 
 }  // namespace ff
