@@ -29,7 +29,7 @@ cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *posi
 cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
                                   const void *w, int w_dtype, const void *residual, int64_t ldr,
                                   void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
-                                  int64_t rows, int64_t N, cudaStream_t s);
+                                  int64_t rows, int64_t N, int sm_count, cudaStream_t s);
 
 // dz[position[t, j]] = w[t, j] dy[t] (or null), dw[t, j] = dy[t] . z[position[t, j]] (or null).
 cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int grad_dtype,

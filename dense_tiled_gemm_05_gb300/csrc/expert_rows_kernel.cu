@@ -24,22 +24,26 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 32 * VEC;  // columns a warp covers at a time
-constexpr int64_t kWalkCtas = 1520;
+constexpr int kWalkers = 4;      // CTAs an SM of kernels whose warps walk tokens
 
 bool aligned16(const void *p, int64_t ld, int es) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0);
 }
 int esize(int dt) { return dt == GEMM_F32 ? 4 : 2; }
 
-// Column blocks along x, tokens along y: one a warp where rows are mostly written, since CTAs then
+// Column blocks along x, tokens along y. Where rows are mostly written, one token a warp: CTAs then
 // start in the order of memory, which HBM writes faster than grids that stay and stride through it
-// (65536 rows of 4 KB from 16384: 54 us against 63 with 608 CTAs that loop); about ten CTAs an SM,
-// whose warps walk tokens, where they are mostly read.
-dim3 token_grid(int64_t tokens, int64_t N, bool walk) {
-  const int64_t gx = (N + kCols - 1) / kCols;
-  int64_t gy = (tokens + kWarps - 1) / kWarps;
-  if (walk) gy = std::min(gy, (kWalkCtas + gx - 1) / gx);
+// (65536 rows of 4 KB from 16384: 54 us against 63 with 608 CTAs that loop).
+dim3 token_grid(int64_t tokens, int64_t N) {
+  const int64_t gx = (N + kCols - 1) / kCols, gy = (tokens + kWarps - 1) / kWarps;
   return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(gy, 65535)));
+}
+// Where they are mostly read, exactly as many CTAs as stay (16384 tokens of 4 x 4 KB: 66 us; with
+// two and a half times as many 72, with a quarter more than fit 71), whose warps walk tokens.
+dim3 walk_grid(int64_t tokens, int64_t N, int sm_count) {
+  const int64_t all = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * kWalkers;
+  const int64_t gx = (N + kCols - 1) / kCols, gy = (tokens + kWarps - 1) / kWarps;
+  return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(std::max<int64_t>(std::min(gy, all / gx), 1)));
 }
 
 #define FF_TOKENS(t, tokens)                                                              \
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename TI, typename TO, bool VECTOR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kWalkers)
     combine_kernel(const TI *__restrict__ z, int64_t ldz, const int32_t *__restrict__ position,
                    const void *__restrict__ w, int w_dtype, const TO *residual, int64_t ldr, TO *y,
                    int64_t ldy, int64_t tokens, int k, int64_t rows, int64_t N) {
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
   grid_launch_dependents();
   const int lane = threadIdx.x % 32;
   const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
-  constexpr int BATCH = sizeof(TI) == 4 ? 2 : 4;  // rows on the way at once
+  constexpr int BATCH = sizeof(TI) == 4 || !VECTOR ? 2 : 4;  // rows on the way at once
   const int64_t step = static_cast<int64_t>(gridDim.y) * kWarps;
   int64_t t = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32;
   // a token's first 32 positions and weights are asked for while the token before it is added up
@@ -243,7 +247,7 @@ cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *posi
   const bool vector = aligned16(x, ldx, es) && aligned16(y, ldy, es) && N % VEC == 0;
   auto go = [&](auto *type, auto vec) {
     using E = std::remove_pointer_t<decltype(type)>;
-    launch_pdl(gather_kernel<E, decltype(vec)::value>, token_grid(tokens, N, false), kThreads, 0, s,
+    launch_pdl(gather_kernel<E, decltype(vec)::value>, token_grid(tokens, N), kThreads, 0, s,
                static_cast<const E *>(x), ldx, position, static_cast<E *>(y), ldy, tokens,
                static_cast<int>(k), rows, N);
   };
@@ -257,13 +261,13 @@ cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *posi
 cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
                                   const void *w, int w_dtype, const void *residual, int64_t ldr,
                                   void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
-                                  int64_t rows, int64_t N, cudaStream_t s) {
+                                  int64_t rows, int64_t N, int sm_count, cudaStream_t s) {
   const bool vector = aligned16(z, ldz, esize(in_dtype)) && aligned16(y, ldy, esize(out_dtype)) &&
                       aligned16(residual, ldr, esize(out_dtype)) && N % VEC == 0;
   FF_TYPED(in_dtype, TI, {
     FF_TYPED(out_dtype, TO, {
       auto go = [&](auto kernel) {
-        launch_pdl(kernel, token_grid(tokens, N, true), kThreads, 0, s, static_cast<const TI *>(z), ldz,
+        launch_pdl(kernel, walk_grid(tokens, N, sm_count), kThreads, 0, s, static_cast<const TI *>(z), ldz,
                    position, w, w_dtype, static_cast<const TO *>(residual), ldr,
                    static_cast<TO *>(y), ldy, tokens, static_cast<int>(k), rows, N);
       };
