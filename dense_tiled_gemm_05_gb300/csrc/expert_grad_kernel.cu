@@ -47,33 +47,37 @@ constexpr int BAR_OFFSET = EPI_OFFSET + kEpi * 2 * kStoreBufBytes;
 constexpr int SMEM_BYTES = 232448;              // (all of it: see expert_pair_kernel.cu)
 constexpr int ORDER_OFFSET = BAR_OFFSET + (4 * STAGES + 5) * 8 + (8 + 2 * STAGES) * 4;
 constexpr int kOrdered = 256;                   // experts that are put in order, at most
-static_assert(ORDER_OFFSET + kOrdered * 6 + 1024 <= SMEM_BYTES, "shared memory");
+static_assert(ORDER_OFFSET + (kOrdered + 1) * 4 + kOrdered + 1024 <= SMEM_BYTES, "shared memory");
 
-__device__ __forceinline__ int first_row(const ExpertGradParams &p, int e) {
-  return max(0, min(p.offsets[e], p.rows));
-}
-__device__ __forceinline__ int row_count(const ExpertGradParams &p, int e) {
-  const int lo = first_row(p, e);
-  return max(lo, min(p.offsets[e + 1], p.rows)) - lo;
-}
-
-// Experts by their rows, most first (equal ones by number), in shared memory; a barrier has to follow.
+// Experts by their rows, most first (equal ones by number), and their first rows, in shared memory:
+// read from there, a tile's place costs each role some hundred cycles, from global memory (there is
+// no room for an L1) 3700. More experts than kOrdered come in their own order, from global memory.
+// Offsets are kept inside [0, rows], and an expert whose end lies before its start has no rows.
 struct ExpertOrder {
-  int32_t *rows;    // [kOrdered]
-  uint16_t *order;  // [kOrdered]
+  int32_t *offsets;  // [kOrdered + 1]
+  uint8_t *order;    // [kOrdered]
+  bool here;
+  // by all threads; a barrier has to follow
   __device__ __forceinline__ void fill(const ExpertGradParams &p) const {
-    if (p.experts > kOrdered) return;
-    for (int e = threadIdx.x; e < p.experts; e += kGradThreads) rows[e] = row_count(p, e);
+    if (!here) return;
+    for (int e = threadIdx.x; e <= p.experts; e += kGradThreads)
+      offsets[e] = max(0, min(p.offsets[e], p.rows));
     __syncthreads();
     for (int e = threadIdx.x; e < p.experts; e += kGradThreads) {
-      const int n = rows[e];
+      const int n = offsets[e + 1] - offsets[e];
       int rank = 0;
-      for (int i = 0; i < p.experts; ++i) rank += rows[i] > n || (rows[i] == n && i < e);
-      order[rank] = static_cast<uint16_t>(e);
+      for (int i = 0; i < p.experts; ++i) {
+        const int m = offsets[i + 1] - offsets[i];
+        rank += m > n || (m == n && i < e);
+      }
+      order[rank] = static_cast<uint8_t>(e);
     }
   }
-  __device__ __forceinline__ int at(const ExpertGradParams &p, int i) const {
-    return p.experts > kOrdered ? i : order[i];
+  __device__ __forceinline__ int at(int i) const { return here ? order[i] : i; }
+  __device__ __forceinline__ void rows_of(const ExpertGradParams &p, int e, int &lo, int &n) const {
+    lo = here ? offsets[e] : max(0, min(p.offsets[e], p.rows));
+    const int hi = here ? offsets[e + 1] : max(0, min(p.offsets[e + 1], p.rows));
+    n = max(hi - lo, 0);
   }
 };
 
@@ -84,13 +88,13 @@ struct Tile {
   int m0, n0;
   __device__ __forceinline__ Tile(const ExpertGradParams &p, const ExpertOrder &order, int t) {
     const int per = p.tiles_m * p.tiles_n;
-    const int place = t / per, i = t - place * per;
-    e = order.at(p, place);
-    n0 = i / p.tiles_m;
+    const int place = static_cast<uint32_t>(t) / static_cast<uint32_t>(per), i = t - place * per;
+    e = order.at(place);
+    n0 = static_cast<uint32_t>(i) / static_cast<uint32_t>(p.tiles_m);
     m0 = (i - n0 * p.tiles_m) * (2 * BM);
     n0 *= BN;
-    lo = first_row(p, e);
-    const int n = row_count(p, e);
+    int n;
+    order.rows_of(p, e, lo, n);
     blocks = (n + BK - 1) / BK;
     last = n - (blocks - 1) * BK;
     // (neighbouring tiles start apart, at multiples of what a power of two below `blocks` allows)
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
   const ExpertOrder order{reinterpret_cast<int32_t *>(smem + ORDER_OFFSET),
-                          reinterpret_cast<uint16_t *>(smem + ORDER_OFFSET + kOrdered * 4)};
+                          smem + ORDER_OFFSET + (kOrdered + 1) * 4, p.experts <= kOrdered};
   order.fill(p);
   __syncthreads();
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (zero) continue;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      if (lane == 0) arrive_read(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }

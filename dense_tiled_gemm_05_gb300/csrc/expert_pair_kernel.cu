@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
+      if (lane == 0) arrive_read(mapa_shared(smem_u32(&tmem_empty[acc]), 0));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }

@@ -104,6 +104,15 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
+// Tells the MMA issuer of the pair that this warp has read an accumulator. The reads are complete
+// (tcgen05.wait::ld) and no other memory is handed over, so that nothing has to be released: at
+// cluster scope a release waits for the warp's stores of the tile, some 3000 cycles when memory is
+// busy, and held up the next tile's MMAs (256 rows an expert: NOREL_A us of weight gradients against
+// NOREL_B).
+__device__ __forceinline__ void arrive_read(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // tc::drain_pair_fills for fills of different sizes: bytes[s] and peer_bytes[s] are those of the
 // last fill of stage s that this CTA and the peer issued.
 template <int STAGES>
