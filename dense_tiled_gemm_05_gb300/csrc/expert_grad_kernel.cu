@@ -256,9 +256,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     bool ok = (p.debug_flags & kDebugStallProducer) == 0;
     const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
     const uint64_t keep = l2_policy_evict_last();
+    const uint32_t full_bars = mapa_shared(smem_u32(full), 0);  // the leader's
+    const uint32_t tail_bars = mapa_shared(smem_u32(tail), rank);
     while (ok && rounds.next(t)) {
       const Tile tile(p, order, t);
-      const int m0 = tile.m0 + static_cast<int>(rank) * BM, n0 = tile.n0 + static_cast<int>(rank) * BM;
+      const int m0 = uniform(tile.m0) + static_cast<int>(rank) * BM;
+      const int n0 = uniform(tile.n0) + static_cast<int>(rank) * BM;
       const int blocks = uniform(tile.blocks), first = uniform(tile.lo);
       const int own_block = uniform(tile.ragged() ? tile.blocks - 1 : -1);
       int kb = uniform(tile.start);
@@ -275,8 +278,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           tail_used |= 1u << stage;
         }
         if (issuer) {
-          const uint32_t fb = own ? mapa_shared(smem_u32(&tail[stage]), rank)
-                                  : mapa_shared(smem_u32(&full[stage]), 0);  // the leader's barrier
+          const uint32_t fb = (own ? tail_bars : full_bars) + stage * 8;
           if (own) {
             mbar_arrive_expect_tx(&tail[stage], STAGE_BYTES);
             if (leader) mbar_arrive(&full[stage]);

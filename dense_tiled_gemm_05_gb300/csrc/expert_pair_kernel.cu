@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
     bool ok = (p.debug_flags & kDebugStallProducer) == 0;
     const int stop_after = stall_after_fills(p.debug_flags, static_cast<int>(rank));
     const uint64_t keep = l2_policy_evict_last();
+    const uint32_t full_bars = mapa_shared(smem_u32(full), 0);  // the leader's
     while (ok && work.next(seg)) {
       const ExpertTiles::Tile tile = table.at(seg.tile);
       const int expert = uniform(tile.e);
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
           fill_bytes[stage] = bytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
           const uint32_t w_dst = smem_base + stage * S::STAGE;
-          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);  // the leader's barrier
+          const uint32_t fb = full_bars + stage * 8;
           const bool second = MODE == kExpertPlain && kb >= p.kb_first;
           const int k0 = (second ? kb - p.kb_first : kb) * BK;
 #pragma unroll
