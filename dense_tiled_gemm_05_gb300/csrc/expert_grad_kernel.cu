@@ -160,12 +160,18 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap *tmD, const Expert
     }
   }
 }
-// ... or, where TMA cannot address D, each lane its row's elements.
+// ... or, where TMA cannot address D, by rows: a warp's 32 x 32 values turn in shared memory, so that
+// the lanes of a store are neighbours (2048 x 1001 of 32 experts: DIRECT_A us, DIRECT_B with a row a
+// lane).
 template <typename T>
-__device__ __forceinline__ void store_direct(const ExpertGradParams &p, uint32_t t_row, bool zero,
-                                             int row, int n0, int e) {
+__device__ __forceinline__ void store_direct(const ExpertGradParams &p, uint32_t t_row, bool zero, uint8_t *box,
+                                             int lane, int row0, int n0, int e) {
+  constexpr int PITCH = 34;  // 17 words a row: neither side meets a bank twice
+  T *turn = reinterpret_cast<T *>(box);
+  const int rows = min(32, p.MA - row0);
+  if (rows <= 0) return;
 #pragma unroll 1
-  for (int c = 0; c < HALF; c += 32) {
+  for (int c = 0; c < HALF && n0 + c < p.NB; c += 32) {
     float v[32];
     if (zero) {
 #pragma unroll
@@ -173,12 +179,13 @@ __device__ __forceinline__ void store_direct(const ExpertGradParams &p, uint32_t
     } else {
       read_columns<32>(t_row + c, v);
     }
-    if (row >= p.MA || n0 + c >= p.NB) continue;
-    T *d = static_cast<T *>(p.D) + e * p.stride_d + row * p.ldd + n0 + c;
-    const int n = min(32, p.NB - n0 - c);
+    __syncwarp();  // the previous columns have been read
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) d[j] = from_f32<T>(v[j]);
+    for (int i = 0; i < 32; ++i) turn[lane * PITCH + i] = from_f32<T>(v[i]);
+    __syncwarp();
+    T *d = static_cast<T *>(p.D) + e * p.stride_d + row0 * p.ldd + n0 + c + lane;
+    if (n0 + c + lane < p.NB)
+      for (int r = 0; r < rows; ++r) d[r * p.ldd] = turn[r * PITCH + lane];
   }
 }
 
@@ -415,9 +422,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         else
           store_boxes<GEMM_F16>(&maps.D, p, t_row, zero, boxes, next, lane, row0, n0, tile.e);
       } else if (p.dtype == GEMM_BF16) {
-        store_direct<__nv_bfloat16>(p, t_row, zero, row0 + lane, n0, tile.e);
+        store_direct<__nv_bfloat16>(p, t_row, zero, boxes, lane, row0, n0, tile.e);
       } else {
-        store_direct<__half>(p, t_row, zero, row0 + lane, n0, tile.e);
+        store_direct<__half>(p, t_row, zero, boxes, lane, row0, n0, tile.e);
       }
       if (zero) continue;
       tc_fence_before();

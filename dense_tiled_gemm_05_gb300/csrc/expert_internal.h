@@ -42,6 +42,12 @@ cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int gra
 cudaError_t expert_zero_launch(void *y, int64_t ldy, int es, const int32_t *offsets, int64_t experts,
                                int64_t rows, int64_t N, cudaStream_t s);
 
+// Copies `count` matrices of `lines` lines of `len` 16-bit elements (lines ld apart, matrices stride
+// apart, of any alignment) to lines to_ld apart that follow one another from a 16-byte boundary
+// (to_ld: a multiple of 8, at least len).
+cudaError_t expert_stage_launch(const void *src, int64_t ld, int64_t stride, int64_t lines, int64_t count,
+                                int64_t len, void *dst, int64_t to_ld, cudaStream_t s);
+
 // y = x * mask * scale + residual (null: 0); key: two 64-bit words on the device.
 cudaError_t dropout_launch(const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
                            int64_t ldy, int dtype, uint32_t threshold, float scale,

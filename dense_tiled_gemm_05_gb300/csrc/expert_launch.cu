@@ -73,15 +73,9 @@ gemm_status_t ExpertOperand::stage(gemm_handle_t h, char *buf, cudaStream_t s) {
   if (!staged) return GEMM_OK;
   const int64_t to_ld = round_up(len, 8);
   char *to = buf + offset;
-  // matrices that follow one another are one with more lines
-  const bool one = count == 1 || stride == lines * ld;
-  for (int64_t e = 0; e < (one ? 1 : count); ++e) {
-    const cudaError_t err =
-        repack_launch(static_cast<const char *>(ptr) + e * stride * ES, ld, to + e * lines * to_ld * ES,
-                      to_ld, one ? count * lines : lines, len, ES, s);
-    if (err != cudaSuccess) return cuda_fail(err, "stage operand");
-    h->launches += 1;
-  }
+  const cudaError_t err = expert_stage_launch(ptr, ld, stride, lines, count, len, to, to_ld, s);
+  if (err != cudaSuccess) return cuda_fail(err, "stage operand");
+  h->launches += 1;
   ptr = to, ld = to_ld, stride = lines * to_ld;
   staged = false;
   return GEMM_OK;

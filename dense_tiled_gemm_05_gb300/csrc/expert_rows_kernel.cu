@@ -4,6 +4,8 @@
 //   y[t]  = sum_j w[t, j] z[position[t, j]] + residual[t]             (combine)
 //   dz[position[t, j]] = w[t, j] dy[t],  dw[t, j] = dy[t] . z[position[t, j]]
 //
+// and the copies of operands that TMA cannot address.
+//
 // All are bound by the bytes they move. A warp covers 256 columns, eight a lane, in 16-byte
 // accesses where the rows allow it. It reads a token's positions (and weights) with one load,
 // lane j the j-th, and hands them round by shuffles, so that all of a token's rows are on the
@@ -226,7 +228,45 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t r = lo + blockIdx.y; r < hi; r += gridDim.y) y[r * ldy + col] = from_f32<E>(0.0f);
 }
 
+// A warp copies 256 elements of a line, a lane eight: their 4-byte words, shifted by half a word
+// where the line starts on an odd element, as one 16-byte store. Every word that is read holds an
+// element of the line. (32 matrices of 2048 x 1001: STAGE_A us; two-byte accesses took 230.)
+__global__ void __launch_bounds__(kThreads)
+    stage_kernel(const uint16_t *__restrict__ src, int64_t ld, int64_t stride, int64_t lines, int64_t all,
+                 int64_t len, int64_t chunks, uint16_t *__restrict__ dst, int64_t to_ld) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x % 32;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; i < all * chunks;
+       i += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t line = i / chunks, e = line / lines;
+    const int64_t j0 = (i - line * chunks) * kCols + lane * VEC;
+    if (j0 >= len) continue;
+    const uint16_t *from = src + e * stride + (line - e * lines) * ld + j0;
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(from) / 2 % 2);
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(from - odd);
+    uint32_t w[5];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) w[q] = j0 - odd + 2 * q < len && (q < 4 || odd) ? words[q] : 0u;
+    uint4 out;
+    out.x = odd ? __funnelshift_r(w[0], w[1], 16) : w[0];
+    out.y = odd ? __funnelshift_r(w[1], w[2], 16) : w[1];
+    out.z = odd ? __funnelshift_r(w[2], w[3], 16) : w[2];
+    out.w = odd ? __funnelshift_r(w[3], w[4], 16) : w[3];
+    *reinterpret_cast<uint4 *>(dst + line * to_ld + j0) = out;
+  }
+}
+
 }  // namespace
+
+cudaError_t expert_stage_launch(const void *src, int64_t ld, int64_t stride, int64_t lines, int64_t count,
+                                int64_t len, void *dst, int64_t to_ld, cudaStream_t s) {
+  const int64_t chunks = (len + kCols - 1) / kCols, all = lines * count;
+  const int64_t ctas = std::min<int64_t>((all * chunks + kWarps - 1) / kWarps, int64_t{1} << 20);
+  launch_pdl(stage_kernel, dim3(static_cast<unsigned>(ctas)), kThreads, 0, s, static_cast<const uint16_t *>(src),
+             ld, stride, lines, all, len, chunks, static_cast<uint16_t *>(dst), to_ld);
+  return cudaGetLastError();
+}
 
 cudaError_t expert_zero_launch(void *y, int64_t ldy, int es, const int32_t *offsets, int64_t experts,
                                int64_t rows, int64_t N, cudaStream_t s) {

@@ -56,8 +56,8 @@ struct ExpertTiles {
   struct Tile {
     int e, row0, rows, column;
   };
-  // Tile t: its rows are an even share of the expert's, in steps of 32 (300 rows of 256 at most are
-  // 160 and 140, not 256 and 44). Tiles along the rows run fastest, in groups of eight, so that
+  // Tile t: its rows are an even share of the expert's, in steps of 32 (594 rows of 256 at most are
+  // 224, 192 and 178, not 256, 256 and 82). Tiles along the rows run fastest, in groups of eight, so that
   // neighbours share both operands through L2.
   __device__ __forceinline__ Tile at(int t) const {
     int lo = 0, hi = experts;  // begins[lo] <= t < begins[hi]
@@ -70,7 +70,7 @@ struct ExpertTiles {
     }
     const int first_row = offsets[lo], n = offsets[lo + 1] - first_row;
     const int lines = (n + most - 1) / most;
-    const int width = lines == 1 ? n : ((n + lines - 1) / lines + 31) / 32 * 32;
+    const int steps = (n + 31) / 32, share = lines == 1 ? steps : steps / lines, extra = steps - share * lines;
     int i = t - begins[lo], first = 0, group = lines;
     if (lines > 8) {
       const int g = i / (8 * across);
@@ -82,8 +82,9 @@ struct ExpertTiles {
     tile.e = lo;
     tile.column = group == 1 ? i : i / group;
     const int line = first + (i - tile.column * group);
-    tile.row0 = first_row + line * width;
-    tile.rows = min(width, n - line * width);
+    const int row = 32 * (line * share + min(line, extra));
+    tile.row0 = first_row + row;
+    tile.rows = min(32 * (share + (line < extra ? 1 : 0)), n - row);
     return tile;
   }
 };
