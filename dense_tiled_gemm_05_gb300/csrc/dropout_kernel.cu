@@ -19,6 +19,7 @@
 #include "expert_internal.h"
 #include "pdl.h"
 #include "ptx.cuh"
+#include "row_piece.cuh"
 
 namespace gemm_gb300 {
 namespace ff {
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(kThreads)
   grid_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint64_t seed = key[0], offset = key[1];
-  const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
+  const RowPiece<VECTOR> cols(static_cast<int64_t>(blockIdx.x) * kCols, N, lane);
   const uint32_t block = static_cast<uint32_t>(blockIdx.x) * 32 + lane;
   const uint32_t row_step = gridDim.y * kWarps;
 #pragma unroll 2

@@ -12,6 +12,7 @@ namespace gemm_gb300 {
 namespace ff {
 
 constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxSorted = int64_t{1} << 26;  // ids of a call (the work grows with their square)
 
 // Workspace of expert_sort_launch (0 when one CTA takes all ids).
 size_t expert_sort_bytes(int64_t n, int64_t experts);

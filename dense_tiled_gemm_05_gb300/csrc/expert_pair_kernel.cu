@@ -54,8 +54,8 @@ constexpr int kExpertThreads = 64 + 32 * kEpi;
 // A kernel's tiles and shared memory. Narrow: for few rows an expert, tiles of at most 64 tokens, so
 // that two CTAs fit an SM: twice as many, smaller shares of the weights' stream, and a kernel's start
 // (the table, the first loads) runs under the end of the one before it. One GB300, us, calls one
-// after another, narrow and wide: 4 rows gated 2048 x 4096 NARROW_A, 256 rows of 32 experts
-// 4096 x 2048 NARROW_B.
+// after another, narrow and wide: 4 rows gated 2048 x 4096 26.9 and 29.7, 256 rows of 32
+// experts 4096 x 2048 81.8 and 86.0.
 template <int MODE, bool NARROW>
 struct Shape {
   static constexpr bool TWO = MODE == kExpertTwo;             // weight boxes, accumulators

@@ -18,6 +18,7 @@
 #include "expert_internal.h"
 #include "pdl.h"
 #include "ptx.cuh"
+#include "row_piece.cuh"
 
 namespace gemm_gb300 {
 namespace ff {
@@ -40,8 +41,8 @@ dim3 token_grid(int64_t tokens, int64_t N) {
   const int64_t gx = (N + kCols - 1) / kCols, gy = (tokens + kWarps - 1) / kWarps;
   return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(gy, 65535)));
 }
-// Where they are mostly read, exactly as many CTAs as stay (16384 tokens of 4 x 4 KB: 66 us; with
-// two and a half times as many 72, with a quarter more than fit 71), whose warps walk tokens.
+// Where they are mostly read, exactly as many CTAs as stay (16384 tokens of 4 x 4 KB and a residual:
+// 64 us; with two and a half times as many 72), whose warps walk tokens.
 dim3 walk_grid(int64_t tokens, int64_t N, int sm_count) {
   const int64_t all = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * kWalkers;
   const int64_t gx = (N + kCols - 1) / kCols, gy = (tokens + kWarps - 1) / kWarps;
@@ -57,21 +58,6 @@ __device__ __forceinline__ int64_t row_of(int32_t position, int64_t rows) {
   return position >= 0 && position < rows ? position : -1;
 }
 
-// The bits of a row's eight columns a lane (E: any type of their size).
-template <typename E, bool VECTOR>
-__device__ __forceinline__ void store_raw(const Columns<32, VECTOR> &cols, E *row, const E (&e)[VEC]) {
-  if (VECTOR) {
-    if (!cols.in(0)) return;
-#pragma unroll
-    for (int w = 0; w < VEC * static_cast<int>(sizeof(E)) / 16; ++w)
-      reinterpret_cast<uint4 *>(row + cols.at(0))[w] = reinterpret_cast<const uint4 *>(e)[w];
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      if (cols.in(i)) row[cols.at(i)] = e[i];
-  }
-}
-
 template <typename E, bool VECTOR>
 __global__ void __launch_bounds__(kThreads)
     gather_kernel(const E *__restrict__ x, int64_t ldx, const int32_t *__restrict__ position,
@@ -79,7 +65,7 @@ __global__ void __launch_bounds__(kThreads)
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x % 32;
-  const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
+  const RowPiece<VECTOR> cols(static_cast<int64_t>(blockIdx.x) * kCols, N, lane);
   FF_TOKENS(t, tokens) {
     alignas(16) E e[VEC];
     cols.load(x + t * ldx, e);
@@ -88,7 +74,7 @@ __global__ void __launch_bounds__(kThreads)
       const int32_t p = lane < n ? position[t * k + j0 + lane] : -1;
       for (int j = 0; j < n; ++j) {
         const int64_t r = row_of(__shfl_sync(0xffffffffu, p, j), rows);
-        if (r >= 0) store_raw(cols, y + r * ldy, e);
+        if (r >= 0) cols.store_raw(y + r * ldy, e);
       }
     }
   }
@@ -102,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, kWalkers)
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x % 32;
-  const Columns<32, VECTOR> cols{static_cast<int64_t>(blockIdx.x) * kCols, N, lane};
+  const RowPiece<VECTOR> cols(static_cast<int64_t>(blockIdx.x) * kCols, N, lane);
   constexpr int BATCH = sizeof(TI) == 4 || !VECTOR ? 2 : 4;  // rows on the way at once
   const int64_t step = static_cast<int64_t>(gridDim.y) * kWarps;
   int64_t t = static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32;
@@ -229,8 +215,9 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // A warp copies 256 elements of a line, a lane eight: their 4-byte words, shifted by half a word
-// where the line starts on an odd element, as one 16-byte store. Every word that is read holds an
-// element of the line. (32 matrices of 2048 x 1001: STAGE_A us; two-byte accesses took 230.)
+// where the line starts on an odd element, as one 16-byte store. At a line's ends its own half of a
+// word is read. (32 matrices of 2048 x 1001, a
+// quarter of a gigabyte read and written: about 60 us; with two-byte accesses 230.)
 __global__ void __launch_bounds__(kThreads)
     stage_kernel(const uint16_t *__restrict__ src, int64_t ld, int64_t stride, int64_t lines, int64_t all,
                  int64_t len, int64_t chunks, uint16_t *__restrict__ dst, int64_t to_ld) {
@@ -245,9 +232,20 @@ __global__ void __launch_bounds__(kThreads)
     const uint16_t *from = src + e * stride + (line - e * lines) * ld + j0;
     const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(from) / 2 % 2);
     const uint32_t *words = reinterpret_cast<const uint32_t *>(from - odd);
+    const uint16_t *halves = from - odd;
     uint32_t w[5];
 #pragma unroll
-    for (int q = 0; q < 5; ++q) w[q] = j0 - odd + 2 * q < len && (q < 4 || odd) ? words[q] : 0u;
+    for (int q = 0; q < 5; ++q) {
+      const int64_t j = j0 - odd + 2 * q;  // the word's first element
+      w[q] = 0u;
+      if (q == 4 && !odd) break;
+      if (j >= 0 && j + 1 < len)
+        w[q] = words[q];
+      else if (j < 0)
+        w[q] = static_cast<uint32_t>(halves[2 * q + 1]) << 16;
+      else if (j < len)
+        w[q] = halves[2 * q];
+    }
     uint4 out;
     out.x = odd ? __funnelshift_r(w[0], w[1], 16) : w[0];
     out.y = odd ? __funnelshift_r(w[1], w[2], 16) : w[1];

@@ -13,7 +13,7 @@
 // 2048 entries take one launch.
 //
 // Bound by latency, a chain of loads, matches, prefix sums and stores (one GB300: 256 entries
-// SORT_A us, 65536 SORT_B, calls one after another).
+// 2.9 us, 65536 6.6, calls one after another).
 #include <algorithm>
 
 #include "expert_internal.h"

@@ -108,8 +108,8 @@ __device__ __forceinline__ bool elect_one() {
 // Tells the MMA issuer of the pair that this warp has read an accumulator. The reads are complete
 // (tcgen05.wait::ld) and no other memory is handed over, so that nothing has to be released: at
 // cluster scope a release waits for the warp's stores of the tile, some 3000 cycles when memory is
-// busy, and held up the next tile's MMAs (256 rows an expert: NOREL_A us of weight gradients against
-// NOREL_B).
+// busy, and held up the next tile's MMAs (weight gradients of 256 rows an expert, 4096 x 2048: 252 us
+// against 307).
 __device__ __forceinline__ void arrive_read(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -101,7 +101,8 @@ GEMM_API gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t
     return GEMM_ERR_INVALID_ARG;
   if (bad_matrix(ids, tokens, k, ld_ids, GEMM_ROW_MAJOR) || (tokens > 0 && k > 0 && !position))
     return GEMM_ERR_INVALID_ARG;
-  if (experts > ff::kMaxExperts || too_large(tokens, k, 0, 0)) return GEMM_ERR_UNSUPPORTED;
+  if (experts > ff::kMaxExperts || too_large(tokens, k, 0, 0) || tokens * k > ff::kMaxSorted)
+    return GEMM_ERR_UNSUPPORTED;
   if (misaligned(ids, id_bytes) || misaligned(position, 4) || misaligned(offsets, 4))
     return GEMM_ERR_ALIGNMENT;
   const Span outs[] = {vector_span(position, tokens * k, 4), vector_span(offsets, experts + 1, 4)};

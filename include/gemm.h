@@ -434,8 +434,8 @@ GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int6
  *     position[t * k + j] = offsets[id] + number of pairs before (t, j), row by row, with its id,
  * and -1 for an id outside [0, experts): a pair without an expert, such as the padding of a batch.
  * The pairs of expert e then have the rows offsets[e] .. offsets[e + 1] - 1. offsets has
- * experts + 1 values. experts in [1, 1024] (more: UNSUPPORTED). tokens == 0 or k == 0 writes the
- * offsets (zeros). */
+ * experts + 1 values. experts in [1, 1024] and tokens * k up to 2^26 (more: UNSUPPORTED).
+ * tokens == 0 or k == 0 writes the offsets (zeros). */
 GEMM_API gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t k,
                                         int64_t experts, const void *ids, int64_t ld_ids,
                                         int32_t id_bytes, int32_t *position, int32_t *offsets,
@@ -484,7 +484,8 @@ GEMM_API gemm_status_t gemm_expert_combine_backward(
  * are taken as clamped to that range, and an expert whose end lies before its start has no rows.
  * dtype: f16 or bf16 (GEMM_F32 is UNSUPPORTED). Operands TMA cannot address (a base, leading
  * dimension or stride that is no multiple of 16 bytes) are copied first. experts in [1, 1024].
- * GEMM_OPT_MAX_CTAS caps the CTAs; the other tile options have no effect. */
+ * GEMM_OPT_MAX_CTAS caps the CTAs and GEMM_OPT_STREAM_K says whether the last tiles' K is shared
+ * over clusters; the other options of products and gemm_set_kernel_events have no effect. */
 GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t rows, int64_t N,
                                        int64_t K, const void *X, int64_t ldx, const void *W,
                                        int64_t ldw, int64_t stride_w, const int32_t *offsets,
