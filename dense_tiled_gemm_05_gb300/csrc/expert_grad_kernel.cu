@@ -17,9 +17,10 @@
 // same rows from L2, each from another K-block on. Tiles of an expert with many rows run long: the experts come in the order of
 // their rows, most first, and every other round of clusters runs backwards, so that the shares even
 // out (16 experts of 46 to 4407 rows, 2048 x 4096: 184 us, 189 in their own order; 64 experts of 0
-// to 1781 rows, 1024 x 2048: 81 and 84). An expert without rows gets zeros. One accumulation a tile, in the rows'
-// order: the same call gives the same bits. Bound by the tensor cores for many rows an expert, by
-// the writing of D for few (256 rows of bf16: as long as its MMAs).
+// to 1781 rows, 1024 x 2048: 81 and 84). An expert without rows gets zeros. One accumulation a tile, in a
+// fixed order: the same call gives the same bits. Bound by the tensor cores for many rows an expert
+// (16384 rows, 4096 x 2048: one expert 1780 TFLOP/s, 16 of 1024 rows 1700), by the writing of D for
+// few (64 of 256 rows: 244 us for 1.07 GB written and 0.2 read).
 #include "activation.cuh"
 #include "expert_kernels.h"
 #include "expert_tiles.cuh"

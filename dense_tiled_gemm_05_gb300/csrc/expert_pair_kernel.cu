@@ -7,8 +7,7 @@
 // How many rows an expert has is known on the device only, from none to all of them, so tiles
 // have to fit any count. The weights are the MMA's M side, 256 output features on a pair of CTAs
 // (tcgen05.mma.cta_group::2), and the tokens its N side, whose width is set for every tile: an
-// expert's rows are shared evenly over tiles of at most 256 (gated: 128), each a multiple of 32
-// wide. 256-row tiles of tokens would waste half a tile an expert on average, an eighth of the
+// expert's rows are shared evenly over tiles of at most 256, each a multiple of 32 wide. 256-row tiles of tokens would waste half a tile an expert on average, an eighth of the
 // time at 1024 rows and a third at 256. The same layout serves few tokens: a 32-column MMA, and
 // the time is that of the weights' stream.
 //
@@ -27,8 +26,10 @@
 // and a shuffle brings them together: 128 features a tile, one MMA a K-step. Other weights (other
 // layouts, feature counts that are no multiple of 16) run as two MMAs a K-step against the same
 // 128 tokens, g and u in the same lanes of two column ranges: those narrower MMAs read a third more
-// shared memory an operation and reached 1340 TFLOP/s where 256 columns reach 1660 (16384 rows,
-// 2048 x 4096).
+// shared memory an operation (16384 rows of 16 experts, 2048 x 4096: 1751 TFLOP/s, interleaved 1830).
+//
+// Measured on one GB300: 16384 rows, 4096 x 2048, one expert 1900 TFLOP/s, 16 of 1024 rows 1820, 16 of
+// 46 to 4407 rows 1680; 256 rows of 32 experts, 4096 x 2048: 81 us for 540 MB.
 //
 // The epilogue has one feature a lane and tokens along its registers: a warp's store of one
 // token is 32 neighbouring features. Rows past the expert's last are not stored (they are the
@@ -186,22 +187,46 @@ __device__ __forceinline__ SkSchedule share_out(int tiles, int kb, int clusters,
     while (most < clusters && 4 * (most + 1) * (most + 1) <= kb) ++most;
     slots = min(clusters, tiles * most);
   }
-  const int rest = slots > 0 ? tiles % slots : 0;
-  // K-blocks of the last round that a cluster is spared
-  const int64_t shared = static_cast<int64_t>(tiles < slots ? tiles : rest) * kb;
-  const int64_t saved = slots > 0 ? kb - (shared + slots - 1) / slots : 0;
-  const bool split = mode != 1 && shared > 0 && kb > 1 && (mode == 2 || (saved > cost && !(narrow && 2 * tiles > clusters)));
-  if (!split) return sk_make(tiles, kb, clusters, tiles);
+  if (slots == 0) return sk_make(0, kb, clusters, 0);
+  const int part = tiles < slots ? tiles : tiles % slots;  // tiles of the last round
+  // K-blocks of it that a cluster is spared
+  const int shared = kb < (1 << 20) ? static_cast<int>((static_cast<uint32_t>(part * kb) + slots - 1) / slots)
+                                    : static_cast<int>((static_cast<int64_t>(part) * kb + slots - 1) / slots);
+  const bool pays = kb - shared > cost && !(narrow && 2 * tiles > clusters);
+  if (mode == 1 || part == 0 || kb < 2 || (mode != 2 && !pays)) return sk_make(tiles, kb, clusters, tiles);
   return sk_make(tiles, kb, slots, sk_dp_tiles(tiles, kb, slots, true));
 }
 
-// A cluster's pieces of work, in its order.
+// A cluster's pieces of work, in its order: tc::WorkIter for whole tiles as a rule, with the 64-bit
+// divisions of shared ones left until there are any.
 struct ExpertWork {
-  WorkIter it;
-  bool idle;
+  SkSchedule S;
+  int slot, tile;
+  int64_t lo, hi;
+  bool shares;
   __device__ __forceinline__ ExpertWork(const SkSchedule &s, int cluster)
-      : it(s, cluster < s.slots ? cluster : 0), idle(cluster >= s.slots) {}
-  __device__ __forceinline__ bool next(SkSegment &seg) { return !idle && it.next(seg); }
+      : S(s), slot(cluster), tile(cluster), lo(0), hi(0), shares(s.sk_units > 0 && cluster < s.slots) {
+    if (cluster >= s.slots) tile = s.dp_tiles;
+  }
+  __device__ __forceinline__ bool next(SkSegment &seg) {
+    if (tile < S.dp_tiles) {
+      seg.tile = tile;
+      seg.kb_begin = 0;
+      seg.kb_end = S.kb;
+      seg.role = kSegFull;
+      seg.first_src = seg.last_src = -1;
+      tile += S.slots;
+      return true;
+    }
+    if (shares) {
+      lo = sk_begin(S, slot);
+      hi = sk_begin(S, slot + 1);
+      shares = false;
+    }
+    if (hi <= lo) return false;
+    hi = sk_segment_at(S, slot, hi, &seg);  // the share, walked from its end to its start
+    return true;
+  }
 };
 
 template <int MODE, bool W_MN, bool NARROW>
@@ -255,14 +280,15 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * ACC);
     tmem_relinquish_pair();
   }
-  // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
-  grid_dependency_wait();
-  const int epoch = sk_epoch_begin(p.sk_epoch_word);
-  table.fill(p.offsets, p.rows, kExpertThreads);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  // Up to here only this CTA's own resources: the prologue may overlap the previous kernel.
+  grid_dependency_wait();
   grid_launch_dependents();
+  const int epoch = sk_epoch_begin(p.sk_epoch_word);
+  table.fill(p.offsets, p.rows, kExpertThreads);
+  __syncthreads();
   const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
   const uint32_t smem_base = smem_u32(smem);
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
@@ -272,8 +298,8 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
   const int width = tiles > 0 ? (table.offsets[p.experts] - table.offsets[0]) / max(tiles / table.across, 1) : 0;
   const SkSchedule sched = share_out(tiles, p.k_blocks, gridDim.x / 2, p.stream_k, 4 + width / 8, NARROW);
   const bool split = sched.dp_tiles < sched.tiles;
-  // Every CTA has read the epoch word before it arrives here, and the next launch reads it after
-  // this one: the last to arrive may advance it at once.
+  // All of this CTA has read the epoch word, and the next launch reads it after this one has ended:
+  // the last CTA to arrive may advance it at once.
   if (split && threadIdx.x == 32 + 1) sk_epoch_end(p.sk_epoch_word, epoch);
   ExpertWork work(sched, cluster_id);
   SkSegment seg;
