@@ -14,13 +14,14 @@
 // tells the issuer. All other blocks go from TMA to the MMAs as ever.
 //
 // The schedule is fixed, tile by tile through the experts, so that the clusters at work read the
-// same rows from L2, each from another K-block on. Tiles of an expert with many rows run long: the experts come in the order of
-// their rows, most first, and every other round of clusters runs backwards, so that the shares even
-// out (16 experts of 46 to 4407 rows, 2048 x 4096: 184 us, 189 in their own order; 64 experts of 0
-// to 1781 rows, 1024 x 2048: 81 and 84). An expert without rows gets zeros. One accumulation a tile, in a
-// fixed order: the same call gives the same bits. Bound by the tensor cores for many rows an expert
-// (16384 rows, 4096 x 2048: one expert 1780 TFLOP/s, 16 of 1024 rows 1700), by the writing of D for
-// few (64 of 256 rows: 244 us for 1.07 GB written and 0.2 read).
+// same rows from L2, each from another K-block on (all from the first: 4 to 9 % slower). Tiles of an
+// expert with many rows run long: the experts come in the order of their rows, most first, and every
+// other round of clusters runs backwards, so that the shares even out (16 experts of 46 to 4407
+// rows, 2048 x 4096: 184 us, 189 in their own order; 64 experts of 0 to 1781 rows, 1024 x 2048: 81
+// and 84). An expert without rows gets zeros. One accumulation a tile, in a fixed order: the same
+// call gives the same bits. Bound by the tensor cores for many rows an expert (16384 rows,
+// 4096 x 2048: one expert 1780 TFLOP/s, 16 of 1024 rows 1700), by the writing of D for few (64 of 256
+// rows: 244 us for 1.07 GB written and 0.2 read).
 #include "activation.cuh"
 #include "expert_kernels.h"
 #include "expert_tiles.cuh"
@@ -50,10 +51,10 @@ constexpr int ORDER_OFFSET = BAR_OFFSET + (4 * STAGES + 5) * 8 + (8 + 2 * STAGES
 constexpr int kOrdered = 256;                   // experts that are put in order, at most
 static_assert(ORDER_OFFSET + (kOrdered + 1) * 4 + kOrdered + 1024 <= SMEM_BYTES, "shared memory");
 
-// Experts by their rows, most first (equal ones by number), and their first rows, in shared memory:
-// read from there, a tile's place costs each role some hundred cycles, from global memory (there is
-// no room for an L1) 3700. More experts than kOrdered come in their own order, from global memory.
-// Offsets are kept inside [0, rows], and an expert whose end lies before its start has no rows.
+// Experts by their rows, most first (equal ones by number), and their first rows, in shared memory,
+// where a tile's place takes each role 400 cycles to find. More experts than kOrdered come in their
+// own order, from global memory. Offsets are kept inside [0, rows], and an expert whose end lies
+// before its start has no rows.
 struct ExpertOrder {
   int32_t *offsets;  // [kOrdered + 1]
   uint8_t *order;    // [kOrdered]

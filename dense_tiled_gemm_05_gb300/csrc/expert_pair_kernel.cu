@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
   // All of this CTA has read the epoch word, and the next launch reads it after this one has ended:
   // the last CTA to arrive may advance it at once.
   if (split && threadIdx.x == 32 + 1) sk_epoch_end(p.sk_epoch_word, epoch);
+  __syncwarp();
   ExpertWork work(sched, cluster_id);
   SkSegment seg;
 

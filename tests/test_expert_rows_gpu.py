@@ -315,6 +315,9 @@ def test_refusals(g, h):
         h.expert_sort(ids.view(-1), 4)
     with pytest.raises(g.GemmError, match="UNSUPPORTED"):
         h.expert_sort(ids, 1025)
+    many = g.lib().gemm_expert_sort(h.handle, 2 ** 26 + 1, 1, 4, ids.data_ptr(), 1, 8, position.data_ptr(),
+                                    rows.data_ptr(), None)
+    assert g.STATUS[many] == "GEMM_ERR_UNSUPPORTED"  # (nothing is read or written)
     with pytest.raises(TypeError):
         h.expert_gather(x, ids)
     with pytest.raises(ValueError):
