@@ -554,8 +554,8 @@ class Gemm:
     def expert_matmul(self, x, w, offsets, out=None, stream=None):
         """Each expert's rows against its weights: out[r] = x[r] @ w[e] for the rows r of e. x is
         rows x K in the order by expert, w is experts x K x N (each row- or column-major; weights
-        stored as [experts, N, K] are passed as ``w.transpose(1, 2)``), f16 or bf16. Rows from
-        offsets[experts] on are left as they were (``out``, when given) and not read."""
+        stored as [experts, N, K] are passed as ``w.transpose(1, 2)``); the 16-bit types run on the
+        tensor cores, f32 on the fp32 units, some forty times slower. Rows from offsets[experts] on are left as they were (``out``, when given) and not read."""
         return (_native_module or native()).expert_matmul(self._address, x, w, offsets, out, stream)
 
     def expert_matmul_backward(self, grad, x, w, offsets, need=(True, True), out=None, stream=None):

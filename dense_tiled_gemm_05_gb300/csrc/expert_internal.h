@@ -43,6 +43,11 @@ cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int gra
 cudaError_t expert_zero_launch(void *y, int64_t ldy, int es, const int32_t *offsets, int64_t experts,
                                int64_t rows, int64_t N, cudaStream_t s);
 
+// fp32: h = act(g) * u for the rows of all experts; h may be g.
+cudaError_t expert_gated_rows_launch(const float *g, int64_t ldg, const float *u, int64_t ldu, float *h,
+                                     int64_t ldh, int act, const int32_t *offsets, int64_t experts,
+                                     int64_t rows, int64_t F, cudaStream_t s);
+
 // Copies `count` matrices of `lines` lines of `len` 16-bit elements (lines ld apart, matrices stride
 // apart, of any alignment) to lines to_ld apart that follow one another from a 16-byte boundary
 // (to_ld: a multiple of 8, at least len).

@@ -84,5 +84,22 @@ struct ExpertGradMaps {
 cudaError_t expert_grad_launch(const ExpertGradMaps &maps, const ExpertGradParams &p, int grid,
                                cudaStream_t s);
 
+// fp32: C[r] (+)= A[r] B[e] for the rows of each expert (A: rows x K, B: K x N each), or, with grad,
+// C[e] = sum over e's rows of A[r]^T B[r] (M x N each). Element (i, k) of an operand is at
+// i * line + k * step, i being C's row or column and k the summed index; line or step is 1.
+struct ExpertF32Params {
+  const int32_t *offsets;
+  int32_t experts, rows;
+  int32_t M, N;            // M: grad only
+  int64_t K;               // not grad
+  const float *A, *B;
+  int64_t a_line, a_step, b_line, b_step;
+  int64_t stride_b;        // from expert to expert (not grad)
+  float *C;
+  int64_t ldc, stride_c;   // stride_c: grad only
+  int32_t add;
+};
+cudaError_t expert_f32_launch(bool grad, const ExpertF32Params &p, int sm_count, cudaStream_t s);
+
 }  // namespace ff
 }  // namespace gemm_gb300

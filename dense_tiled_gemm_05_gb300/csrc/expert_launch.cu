@@ -1,5 +1,5 @@
 // expert_launch.cu -- host side of the experts' products (expert_pair_kernel.cu,
-// expert_grad_kernel.cu): copies of operands TMA cannot address, tensor maps, launch.
+// expert_grad_kernel.cu, expert_f32_kernel.cu): copies of operands TMA cannot address, tensor maps, launch.
 #include <cstring>
 
 #include "expert_launch.h"
@@ -11,7 +11,7 @@ namespace ff {
 
 namespace {
 
-constexpr int ES = 2;  // bytes an element: 16-bit types only
+constexpr int ES = 2;  // bytes an element of the tensor cores' operands
 // Rows an expert with rows, on average, up to which its products run in narrow tiles.
 constexpr int64_t kNarrowRows = 32;
 
@@ -97,7 +97,7 @@ ExpertOperand expert_rows(const void *X, int64_t ld, int64_t rows, int64_t cols)
 }
 
 bool expert_tiles_fit(int64_t experts, int64_t rows, int64_t N, int64_t K) {
-  const int64_t n = (N + 127) / 128, k = (K + 127) / 128, t = rows / 128 + experts;
+  const int64_t n = (N + 63) / 64, k = (K + 63) / 64, t = rows / 64 + experts;
   const int64_t most = INT32_MAX / 4;
   return t <= most / n && t <= most / k && n <= most / k && experts <= most / (n * k);
 }
@@ -178,6 +178,36 @@ gemm_status_t run_expert_grad(gemm_handle_t h, const ExpertGrad &q, cudaStream_t
   const int64_t tiles = q.experts * p.tiles_m * p.tiles_n;
   const cudaError_t e = expert_grad_launch(maps, p, static_cast<int>(2 * clusters_of(h, tiles, false)), s);
   if (e != cudaSuccess) return cuda_fail(e, "expert gradient launch");
+  h->launches += 1;
+  return GEMM_OK;
+}
+
+gemm_status_t run_expert_f32(gemm_handle_t h, const ExpertProduct &q, bool add, cudaStream_t s) {
+  ExpertF32Params p{};
+  p.offsets = q.offsets;
+  p.experts = static_cast<int32_t>(q.experts), p.rows = static_cast<int32_t>(q.rows);
+  p.N = static_cast<int32_t>(q.N), p.K = q.K;
+  p.A = static_cast<const float *>(q.X.ptr), p.a_line = q.X.ld, p.a_step = 1;
+  p.B = static_cast<const float *>(q.W.ptr), p.stride_b = q.W.stride;
+  p.b_line = q.w_mn ? 1 : q.W.ld, p.b_step = q.w_mn ? q.W.ld : 1;
+  p.C = static_cast<float *>(q.C), p.ldc = q.ldc;
+  p.add = add;
+  const cudaError_t e = expert_f32_launch(false, p, h->sm_count, s);
+  if (e != cudaSuccess) return cuda_fail(e, "expert fp32 product launch");
+  h->launches += 1;
+  return GEMM_OK;
+}
+
+gemm_status_t run_expert_grad_f32(gemm_handle_t h, const ExpertGrad &q, cudaStream_t s) {
+  ExpertF32Params p{};
+  p.offsets = q.offsets;
+  p.experts = static_cast<int32_t>(q.experts), p.rows = static_cast<int32_t>(q.rows);
+  p.M = static_cast<int32_t>(q.A.len), p.N = static_cast<int32_t>(q.B.len);
+  p.A = static_cast<const float *>(q.A.ptr), p.a_line = 1, p.a_step = q.A.ld;
+  p.B = static_cast<const float *>(q.B.ptr), p.b_line = 1, p.b_step = q.B.ld;
+  p.C = static_cast<float *>(q.D), p.ldc = q.ldd, p.stride_c = q.stride_d;
+  const cudaError_t e = expert_f32_launch(true, p, h->sm_count, s);
+  if (e != cudaSuccess) return cuda_fail(e, "expert fp32 gradient launch");
   h->launches += 1;
   return GEMM_OK;
 }

@@ -55,6 +55,10 @@ struct ExpertGrad {
 };
 gemm_status_t run_expert_grad(gemm_handle_t h, const ExpertGrad &q, cudaStream_t s);
 
+// The same two products in fp32, operands as the caller stores them.
+gemm_status_t run_expert_f32(gemm_handle_t h, const ExpertProduct &q, bool add, cudaStream_t s);
+gemm_status_t run_expert_grad_f32(gemm_handle_t h, const ExpertGrad &q, cudaStream_t s);
+
 // Whether the tiles of a call can be numbered in 32 bits.
 bool expert_tiles_fit(int64_t experts, int64_t rows, int64_t N, int64_t K);
 

@@ -214,6 +214,27 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t r = lo + blockIdx.y; r < hi; r += gridDim.y) y[r * ldy + col] = from_f32<E>(0.0f);
 }
 
+// h = act(g) * u of the experts' rows in fp32; h may be g.
+__global__ void __launch_bounds__(kThreads)
+    gated_rows_kernel(const float *g, int64_t ldg, const float *__restrict__ u, int64_t ldu, float *h,
+                      int64_t ldh, int act, const int32_t *__restrict__ offsets, int experts, int64_t rows,
+                      int64_t F) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t lo = max(offsets[0], 0), hi = min(static_cast<int64_t>(offsets[experts]), rows);
+  const RowPiece<false> cols(static_cast<int64_t>(blockIdx.x) * kCols, F, threadIdx.x % 32);
+  for (int64_t r = lo + static_cast<int64_t>(blockIdx.y) * kWarps + threadIdx.x / 32; r < hi;
+       r += static_cast<int64_t>(gridDim.y) * kWarps) {
+    float a[VEC], b[VEC];
+    cols.load_f32(g + r * ldg, a);
+    cols.load_f32(u + r * ldu, b);
+    activate_all<false>(a, act);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) a[c] *= b[c];
+    cols.store(h + r * ldh, a);
+  }
+}
+
 // A warp copies 256 elements of a line, a lane eight: their 4-byte words, shifted by half a word
 // where the line starts on an odd element, as one 16-byte store. At a line's ends its own half of a
 // word is read. (32 matrices of 2048 x 1001, a
@@ -263,6 +284,14 @@ cudaError_t expert_stage_launch(const void *src, int64_t ld, int64_t stride, int
   const int64_t ctas = std::min<int64_t>((all * chunks + kWarps - 1) / kWarps, int64_t{1} << 20);
   launch_pdl(stage_kernel, dim3(static_cast<unsigned>(ctas)), kThreads, 0, s, static_cast<const uint16_t *>(src),
              ld, stride, lines, all, len, chunks, static_cast<uint16_t *>(dst), to_ld);
+  return cudaGetLastError();
+}
+
+cudaError_t expert_gated_rows_launch(const float *g, int64_t ldg, const float *u, int64_t ldu, float *h,
+                                     int64_t ldh, int act, const int32_t *offsets, int64_t experts,
+                                     int64_t rows, int64_t F, cudaStream_t s) {
+  launch_pdl(gated_rows_kernel, token_grid(rows, F), kThreads, 0, s, g, ldg, u, ldu, h, ldh, act, offsets,
+             static_cast<int>(experts), rows, F);
   return cudaGetLastError();
 }
 

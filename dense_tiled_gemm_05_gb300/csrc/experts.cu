@@ -48,16 +48,16 @@ gemm_status_t check_experts(gemm_handle_t h, int64_t experts, int64_t rows, int6
   if (!h || experts < 1 || rows < 0 || N < 0 || K < 0 || !offsets || !valid_dtype(dtype) ||
       !valid_layout(layout))
     return GEMM_ERR_INVALID_ARG;
-  if (dtype == GEMM_F32 || experts > ff::kMaxExperts || too_large(rows, 1, N, K) || 2 * N > INT32_MAX ||
+  if (experts > ff::kMaxExperts || too_large(rows, 1, N, K) || 2 * N > INT32_MAX ||
       !ff::expert_tiles_fit(experts, rows, N > 0 ? N : 1, K > 0 ? K : 1))
     return GEMM_ERR_UNSUPPORTED;
   return misaligned(offsets, 4) ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
-gemm_status_t zero_rows(gemm_handle_t h, void *Y, int64_t ld, int64_t rows, int64_t N,
+gemm_status_t zero_rows(gemm_handle_t h, void *Y, int64_t ld, int64_t rows, int64_t N, int es,
                         const int32_t *offsets, int64_t experts, cudaStream_t s) {
   if (!Y || rows == 0 || N == 0) return GEMM_OK;
-  return launched(h, ff::expert_zero_launch(Y, ld, 2, offsets, experts, rows, N, s), "expert zero launch");
+  return launched(h, ff::expert_zero_launch(Y, ld, es, offsets, experts, rows, N, s), "expert zero launch");
 }
 // The experts' weight gradients without any row.
 gemm_status_t zero_weights(gemm_handle_t h, void *D, int64_t experts, int64_t lines, int64_t len,
@@ -65,8 +65,8 @@ gemm_status_t zero_weights(gemm_handle_t h, void *D, int64_t experts, int64_t li
   const bool one = experts == 1 || stride == lines * ld;
   for (int64_t e = 0; e < (one ? 1 : experts); ++e) {
     const gemm_status_t st =
-        launched(h, zero_fill_launch(static_cast<char *>(D) + e * stride * 2, ld, one ? experts * lines : lines,
-                                     len, dtype, s), "zero fill");
+        launched(h, zero_fill_launch(static_cast<char *>(D) + e * stride * esize_of(dtype), ld,
+                                     one ? experts * lines : lines, len, dtype, s), "zero fill");
     if (st != GEMM_OK) return st;
   }
   return GEMM_OK;
@@ -84,7 +84,7 @@ gemm_status_t weight_gradient(gemm_handle_t h, const ff::ExpertOperand &X, const
   q.A = A, q.B = B;
   q.dtype = dtype;
   q.D = dW, q.ldd = ld, q.stride_d = stride;
-  return ff::run_expert_grad(h, q, s);
+  return dtype == GEMM_F32 ? ff::run_expert_grad_f32(h, q, s) : ff::run_expert_grad(h, q, s);
 }
 
 int flip(int layout) { return layout == GEMM_ROW_MAJOR ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR; }
@@ -232,7 +232,7 @@ GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t
   DeviceGuard g(h->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (K == 0) return zero_rows(h, Y, ldy, rows, N, offsets, experts, s);
+  if (K == 0) return zero_rows(h, Y, ldy, rows, N, es, offsets, experts, s);
   ff::ExpertProduct q;
   q.experts = experts, q.rows = rows, q.N = N, q.K = K, q.offsets = offsets;
   q.X = ff::expert_rows(X, ldx, rows, K);
@@ -240,6 +240,7 @@ GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t
   q.w_mn = w_layout == GEMM_ROW_MAJOR;
   q.dtype = dtype;
   q.C = Y, q.ldc = ldy;
+  if (dtype == GEMM_F32) return ff::run_expert_f32(h, q, false, s);
   Carve carve;
   q.X.plan(&carve), q.W.plan(&carve);
   st = reserve(h, h->ff, carve.bytes, s);
@@ -280,10 +281,11 @@ GEMM_API gemm_status_t gemm_run_expert_backward(
   const bool make_dx = dX && rows > 0 && K > 0 && N > 0;
   ff::ExpertOperand xs = ff::expert_rows(X, ldx, rows, K), ys = ff::expert_rows(dY, lddy, rows, N);
   ff::ExpertOperand ws = ff::expert_weights(W, ldw, stride_w, experts, K, N, w_layout);
+  const bool f32 = dtype == GEMM_F32;
   Carve carve;
-  ys.plan(&carve);
-  if (dW) xs.plan(&carve);
-  if (make_dx) ws.plan(&carve);
+  if (!f32) ys.plan(&carve);
+  if (!f32 && dW) xs.plan(&carve);
+  if (!f32 && make_dx) ws.plan(&carve);
   st = reserve(h, h->ff, carve.bytes, s);
   char *buf = static_cast<char *>(h->ff.ptr);
   if (st == GEMM_OK) st = ys.stage(h, buf, s);
@@ -297,9 +299,9 @@ GEMM_API gemm_status_t gemm_run_expert_backward(
     q.w_mn = flip(w_layout) == GEMM_ROW_MAJOR;
     q.dtype = dtype;
     q.C = dX, q.ldc = lddx;
-    st = ff::run_expert(h, q, s);
+    st = f32 ? ff::run_expert_f32(h, q, false, s) : ff::run_expert(h, q, s);
   } else if (dX) {
-    st = zero_rows(h, dX, lddx, rows, K, offsets, experts, s);
+    st = zero_rows(h, dX, lddx, rows, K, es, offsets, experts, s);
   }
   if (st != GEMM_OK) return st;
   return weight_gradient(h, xs, ys, experts, offsets, dW, lddw, stride_dw, dtype, w_layout, s);
@@ -335,9 +337,9 @@ GEMM_API gemm_status_t gemm_run_expert_gated(
   if (!g.ok) return GEMM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (K == 0) {  // g = u = 0, and so h
-    st = zero_rows(h, H, ldh, rows, F, offsets, experts, s);
-    if (st == GEMM_OK) st = zero_rows(h, gate, ld_gate, rows, F, offsets, experts, s);
-    return st == GEMM_OK ? zero_rows(h, up, ld_up, rows, F, offsets, experts, s) : st;
+    st = zero_rows(h, H, ldh, rows, F, es, offsets, experts, s);
+    if (st == GEMM_OK) st = zero_rows(h, gate, ld_gate, rows, F, es, offsets, experts, s);
+    return st == GEMM_OK ? zero_rows(h, up, ld_up, rows, F, es, offsets, experts, s) : st;
   }
   ff::ExpertProduct q;
   q.gated = true;
@@ -349,6 +351,24 @@ GEMM_API gemm_status_t gemm_run_expert_gated(
   q.dtype = dtype, q.act = activation;
   q.C = H, q.ldc = ldh;
   q.pre = gate, q.ld_pre = ld_gate, q.pre2 = up, q.ld_pre2 = ld_up;
+  if (dtype == GEMM_F32) {
+    // g goes to gate or, where that is not asked for, to H, and h = act(g) u takes its place; u goes to
+    // up or to the handle's buffer.
+    const int64_t ld_u = up ? ld_up : F, ld_g = gate ? ld_gate : ldh;
+    if (!up) st = reserve(h, h->ff, static_cast<size_t>(rows * F) * sizeof(float), s);
+    if (st != GEMM_OK) return st;
+    void *g32 = gate ? gate : H, *u32 = up ? up : h->ff.ptr;
+    q.C = g32, q.ldc = ld_g;
+    st = ff::run_expert_f32(h, q, false, s);
+    q.W = q.W2, q.C = u32, q.ldc = ld_u;
+    if (st == GEMM_OK) st = ff::run_expert_f32(h, q, false, s);
+    if (st != GEMM_OK) return st;
+    return launched(h, ff::expert_gated_rows_launch(static_cast<const float *>(g32), ld_g,
+                                                    static_cast<const float *>(u32), ld_u,
+                                                    static_cast<float *>(H), ldh, activation, offsets,
+                                                    experts, rows, F, s),
+                    "expert gated rows launch");
+  }
   Carve carve;
   q.X.plan(&carve), q.W.plan(&carve), q.W2.plan(&carve);
   st = reserve(h, h->ff, carve.bytes, s);
@@ -405,10 +425,11 @@ GEMM_API gemm_status_t gemm_run_expert_gated_backward(
   ff::ExpertOperand xs = ff::expert_rows(X, ldx, rows, K);
   ff::ExpertOperand wg = ff::expert_weights(Wg, ldwg, stride_wg, experts, K, F, w_layout);
   ff::ExpertOperand wu = ff::expert_weights(Wu, ldwu, stride_wu, experts, K, F, w_layout);
+  const bool f32 = dtype == GEMM_F32;
   Carve carve;
   const size_t d_off = carve.take(rows * ldd, es);
-  if (weights) xs.plan(&carve);
-  if (make_dx) wg.plan(&carve), wu.plan(&carve);
+  if (!f32 && weights) xs.plan(&carve);
+  if (!f32 && make_dx) wg.plan(&carve), wu.plan(&carve);
   st = reserve(h, h->ff, carve.bytes, s);
   if (st != GEMM_OK) return st;
   char *buf = static_cast<char *>(h->ff.ptr);
@@ -432,9 +453,15 @@ GEMM_API gemm_status_t gemm_run_expert_gated_backward(
     q.w_mn = flip(w_layout) == GEMM_ROW_MAJOR;
     q.dtype = dtype;
     q.C = dX, q.ldc = lddx;
-    st = ff::run_expert(h, q, s);
+    if (f32) {
+      st = ff::run_expert_f32(h, q, false, s);
+      q.X = us, q.W = wu;
+      if (st == GEMM_OK) st = ff::run_expert_f32(h, q, true, s);
+    } else {
+      st = ff::run_expert(h, q, s);
+    }
   } else if (dX) {
-    st = zero_rows(h, dX, lddx, rows, K, offsets, experts, s);
+    st = zero_rows(h, dX, lddx, rows, K, es, offsets, experts, s);
   }
   if (st == GEMM_OK)
     st = weight_gradient(h, xs, gs, experts, offsets, dWg, lddwg, stride_dwg, dtype, w_layout, s);

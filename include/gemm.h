@@ -480,12 +480,13 @@ GEMM_API gemm_status_t gemm_expert_combine_backward(
  * leading dimension ldw; stride_w is at least what one expert spans. For every row r of expert e
  *     Y[r] = X[r] @ W[e],
  * accumulated in fp32 and rounded once. Other rows of Y are left as they were, and other rows of X
- * add nothing, whatever they hold. Offsets are expected in increasing order inside [0, rows]; they
- * are taken as clamped to that range, and an expert whose end lies before its start has no rows.
- * dtype: f16 or bf16 (GEMM_F32 is UNSUPPORTED). Operands TMA cannot address (a base, leading
- * dimension or stride that is no multiple of 16 bytes) are copied first. experts in [1, 1024].
- * GEMM_OPT_MAX_CTAS caps the CTAs and GEMM_OPT_STREAM_K says whether the last tiles' K is shared
- * over clusters; the other options of products and gemm_set_kernel_events have no effect. */
+ * add nothing, whatever they hold. Offsets have to be in increasing order inside [0, rows]: others
+ * leave the results undefined, but nothing outside the matrices is read or written.
+ * 16-bit operands TMA cannot address (a base, leading dimension or stride that is no multiple of 16
+ * bytes) are copied first; f32 ones are multiplied on the fp32 units. experts in [1, 1024].
+ * For 16-bit types GEMM_OPT_MAX_CTAS caps the CTAs and GEMM_OPT_STREAM_K says whether the last
+ * tiles' K is shared over clusters; the other options of products and gemm_set_kernel_events have no
+ * effect. */
 GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t rows, int64_t N,
                                        int64_t K, const void *X, int64_t ldx, const void *W,
                                        int64_t ldw, int64_t stride_w, const int32_t *offsets,
@@ -505,8 +506,9 @@ GEMM_API gemm_status_t gemm_run_expert_backward(
 /* The gated pair of projections of every expert: for every row r of expert e, with
  * g = X[r] @ Wg[e] and u = X[r] @ Wu[e],
  *     H[r] = act(g) * u        (H: rows x F),
- * in one kernel that reads X once. `gate` and `up` (both or neither NULL) receive g and u for the
- * backward pass. Rows, offsets, types and weights as gemm_run_expert. */
+ * in one kernel that reads X once (f32: two products, then a pass over the rows). `gate` and `up`
+ * (both or neither NULL) receive g and u for the backward pass. Rows, offsets, types and weights as
+ * gemm_run_expert. */
 GEMM_API gemm_status_t gemm_run_expert_gated(
     gemm_handle_t h, int64_t experts, int64_t rows, int64_t F, int64_t K, const void *X,
     int64_t ldx, const void *Wg, int64_t ldwg, int64_t stride_wg, const void *Wu, int64_t ldwu,
@@ -516,7 +518,7 @@ GEMM_API gemm_status_t gemm_run_expert_gated(
 
 /* Backward pass of gemm_run_expert_gated from dH and the stored g and u (rows x F): with
  * dg = dH * u * act'(g) and du = dH * act(g), rounded to the dtype,
- *     dX[r] = dg[r] @ Wg[e]^T + du[r] @ Wu[e]^T   (one fp32 sum),
+ *     dX[r] = dg[r] @ Wg[e]^T + du[r] @ Wu[e]^T   (one fp32 sum; f32: the sum of two),
  *     dWg[e] = sum_r X[r]^T dg[r],  dWu[e] = sum_r X[r]^T du[r].
  * Any of dX, dWg, dWu may be NULL. Rows without an expert as in gemm_run_expert_backward. */
 GEMM_API gemm_status_t gemm_run_expert_gated_backward(

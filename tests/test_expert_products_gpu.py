@@ -60,6 +60,15 @@ def sentinel(rows, cols, t, pad=0, offset=0):
     return matrix(rows, cols, t, 99, pad=pad, offset=offset).fill_(7.0)
 
 
+def accumulation(t, K):
+    """Relative bound on a K-long sum: as the dense kernels' in the tensor cores; for fp32 chains of
+    128 fused multiply-adds, each added to a running total, so that no addend takes more than
+    min(K, 128) + ceil(K / 128) roundings of half a step."""
+    if t != torch.float32:
+        return acc_error(t, K)
+    return (min(K, 128) + -(-K // 128)) * 2.0 ** -24
+
+
 def untouched(y, bounds):
     assert (y[:bounds[0]] == 7).all() and (y[bounds[-1]:] == 7).all()
 
@@ -73,7 +82,7 @@ def check_product(h, x, w, offsets, bounds, out):
         xd, wd = x[a:b].double(), w[e].double()
         want = xd @ wd
         D = xd.abs() @ wd.abs()
-        assert_within(y[a:b], want, 1.01 * acc_error(t, K) * D + rounding(want, t), "y of %d" % e)
+        assert_within(y[a:b], want, 1.01 * accumulation(t, K) * D + rounding(want, t), "y of %d" % e)
     untouched(y, bounds)
 
 
@@ -85,11 +94,11 @@ def check_backward(h, dy, x, w, offsets, bounds, out, need=(True, True)):
         xd, wd, d = x[a:b].double(), w[e].double(), dy[a:b].double()
         if need[0]:
             want = d @ wd.t()
-            bound = acc_error(t, N) * (d.abs() @ wd.abs().t())
+            bound = accumulation(t, N) * (d.abs() @ wd.abs().t())
             assert_within(dx[a:b], want, bound * 1.01 + rounding(want, t), "dx of %d" % e)
         if need[1]:
             want = xd.t() @ d
-            bound = acc_error(t, b - a) * (xd.abs().t() @ d.abs())
+            bound = accumulation(t, b - a) * (xd.abs().t() @ d.abs())
             assert_within(dw[e], want, bound * 1.01 + rounding(want, t), "dw of %d" % e)
     if need[0]:
         untouched(dx, bounds)
@@ -101,7 +110,7 @@ def check_backward(h, dy, x, w, offsets, bounds, out, need=(True, True)):
 
 @pytest.mark.parametrize("counts", COUNTS, ids=str)
 @pytest.mark.parametrize("N,K", EXTENTS)
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_product(h, counts, N, K, dtype):
     t = TYPES[dtype]
     offsets, bounds = offsets_of(counts, 2)
@@ -117,8 +126,9 @@ def test_product(h, counts, N, K, dtype):
 @pytest.mark.parametrize("pad,offset,gap", [(0, 0, 0), (8, 8, 16), (3, 1, 0), (8, 0, 5)])
 @pytest.mark.parametrize("counts", [[5, 0, 300, 64], [40]], ids=str)
 @pytest.mark.parametrize("N,K", [(200, 136), (264, 72), (133, 65)])
-def test_product_layouts(h, counts, N, K, layout, pad, offset, gap):
-    t = torch.bfloat16
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_product_layouts(h, counts, N, K, layout, pad, offset, gap, dtype):
+    t = TYPES[dtype]
     offsets, bounds = offsets_of(counts, 1)
     rows = bounds[-1] + 2
     x = rows_with_gaps(rows, K, t, 1, bounds, pad, offset)
@@ -127,6 +137,18 @@ def test_product_layouts(h, counts, N, K, layout, pad, offset, gap):
     dy = rows_with_gaps(rows, N, t, 3, bounds, pad, offset)
     dx, dw = check_backward(h, dy, x, w, offsets, bounds, sentinel(rows, K, t, pad, offset))
     assert (dw.stride(1) == 1) == (layout == "col") or min(N, K) == 1
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+def test_long_f32_sums(h, layout):
+    """Addends of one sign, whose roundings grow with the running total."""
+    t = torch.float32
+    offsets, bounds = offsets_of([5000, 3, 2000])
+    x = matrix(bounds[-1], 3001, t, 1).abs_()
+    w = weights(3, 3001, 70, t, 2, layout).abs_()
+    check_product(h, x, w, offsets, bounds, sentinel(bounds[-1], 70, t))
+    dy = matrix(bounds[-1], 70, t, 3).abs_()
+    check_backward(h, dy, x, w, offsets, bounds, sentinel(bounds[-1], 3001, t))
 
 
 def test_parts(h):
@@ -146,7 +168,7 @@ def check_gated(h, x, wg, wu, offsets, bounds, act, save=True):
         a, b = bounds[e], bounds[e + 1]
         xd = x[a:b].double()
         gd, ud = xd @ wg[e].double(), xd @ wu[e].double()
-        err = acc_error(t, K)
+        err = accumulation(t, K)
         eg, eu = err * (xd.abs() @ wg[e].double().abs()), err * (xd.abs() @ wu[e].double().abs())
         if save:
             assert_within(gate[a:b], gd, eg + rounding(gd, t) * 1.01, "gate of %d" % e)
@@ -177,14 +199,14 @@ def check_gated_backward(h, dh, x, wg, wu, gate, up, offsets, bounds, act, need=
             wgd, wud = wg[e].double().t(), wu[e].double().t()
             want = dg @ wgd + du @ wud
             D = (dg.abs() + eg) @ wgd.abs() + (du.abs() + eu) @ wud.abs()
-            bound = eg @ wgd.abs() + eu @ wud.abs() + acc_error(t, 2 * F) * D
+            bound = eg @ wgd.abs() + eu @ wud.abs() + accumulation(t, 2 * F) * D
             assert_within(dx[a:b], want, bound * 1.01 + rounding(want, t), "dx of %d" % e)
         for dw, v, ev, needed, what in ((dwg, dg, eg, need[1], "dwg"), (dwu, du, eu, need[2], "dwu")):
             if not needed:
                 assert dw is None
                 continue
             want = xd.t() @ v
-            bound = xd.abs().t() @ ev + acc_error(t, b - a) * (xd.abs().t() @ (v.abs() + ev))
+            bound = xd.abs().t() @ ev + accumulation(t, b - a) * (xd.abs().t() @ (v.abs() + ev))
             assert_within(dw[e], want, bound * 1.01 + rounding(want, t), "%s of %d" % (what, e))
     if need[0]:
         untouched(dx, bounds)
@@ -192,7 +214,7 @@ def check_gated_backward(h, dh, x, wg, wu, gate, up, offsets, bounds, act, need=
 
 @pytest.mark.parametrize("counts", COUNTS, ids=str)
 @pytest.mark.parametrize("F,K", [(1, 1), (64, 64), (200, 136), (130, 1000), (1025, 127), (520, 72)])
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_gated(h, counts, F, K, dtype):
     t = TYPES[dtype]
     offsets, bounds = offsets_of(counts, 2)
@@ -205,12 +227,14 @@ def test_gated(h, counts, F, K, dtype):
 
 
 @pytest.mark.parametrize("act", ACTS)
-def test_gated_activations(h, act):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_activations(h, act, dtype):
+    t = TYPES[dtype]
     offsets, bounds = offsets_of([33, 0, 150])
-    x = matrix(183, 136, torch.bfloat16, 1, scale=3.0)
-    wg, wu = (weights(3, 136, 200, torch.bfloat16, s) for s in (2, 3))
+    x = matrix(183, 136, t, 1, scale=3.0)
+    wg, wu = (weights(3, 136, 200, t, s) for s in (2, 3))
     check_gated(h, x, wg, wu, offsets, bounds, act)
-    dh, gate, up = (matrix(183, 200, torch.bfloat16, s) for s in (4, 5, 6))
+    dh, gate, up = (matrix(183, 200, t, s) for s in (4, 5, 6))
     gate[0, :8] = 0
     check_gated_backward(h, dh, x, wg, wu, gate, up, offsets, bounds, act)
 
@@ -218,8 +242,9 @@ def test_gated_activations(h, act):
 @pytest.mark.parametrize("layout", ["row", "col"])
 @pytest.mark.parametrize("pad,offset,gap", [(0, 0, 0), (8, 8, 16), (3, 1, 0)])
 @pytest.mark.parametrize("F,K", [(200, 136), (133, 65)])
-def test_gated_layouts(h, F, K, layout, pad, offset, gap):
-    t = torch.float16
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_gated_layouts(h, F, K, layout, pad, offset, gap, dtype):
+    t = TYPES[dtype]
     offsets, bounds = offsets_of([5, 0, 200, 64], 1)
     rows = bounds[-1] + 2
     x = rows_with_gaps(rows, K, t, 1, bounds, pad, offset)
@@ -249,12 +274,14 @@ def test_gated_parts(h):
         check_gated_backward(h, dh, x, wg, wu, gate, up, offsets, bounds, "silu", need)
 
 
-def test_values_stay_with_their_expert(h):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_stay_with_their_expert(h, dtype):
     """NaN and infinities in one expert's rows or weights reach that expert's results alone."""
+    t = TYPES[dtype]
     counts = [33, 47, 21]
     offsets, bounds = offsets_of(counts)
-    x, dy = matrix(101, 72, torch.bfloat16, 1), matrix(101, 136, torch.bfloat16, 2)
-    w = weights(3, 72, 136, torch.bfloat16, 3)
+    x, dy = matrix(101, 72, t, 1), matrix(101, 136, t, 2)
+    w = weights(3, 72, 136, t, 3)
     clean = h.expert_matmul(x, w, offsets), *h.expert_matmul_backward(dy, x, w, offsets)
     x[bounds[1]:bounds[2]] = float("inf")
     dy[bounds[1]:bounds[2]] = float("nan")
@@ -269,10 +296,11 @@ def test_values_stay_with_their_expert(h):
     assert torch.isnan(dirty[2][1]).all()
 
 
-def test_bad_offsets_stay_inside(h):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_offsets_stay_inside(h, dtype):
     """Offsets outside the rows are taken as clamped, and an expert that would end before its start
     has no rows; nothing outside the matrices is written."""
-    t = torch.bfloat16
+    t = TYPES[dtype]
     store = torch.full((120, 72), 7.0, dtype=t, device="cuda")
     out = store[10:110]
     x, w = matrix(100, 64, t, 1), weights(4, 64, 72, t, 2)
@@ -291,8 +319,9 @@ def test_bad_offsets_stay_inside(h):
         assert torch.isfinite(dw).all()
 
 
-def test_empty(h):
-    t = torch.bfloat16
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_empty(h, dtype):
+    t = TYPES[dtype]
     e = lambda *s: torch.empty(*s, dtype=t, device="cuda")
     offsets, _ = offsets_of([0, 0])
     w = weights(2, 24, 40, t, 1)
@@ -314,15 +343,17 @@ def test_empty(h):
     assert (y[1:3] == 0).all() and (gate[1:3] == 0).all() and (up[1:3] == 0).all()
 
 
-def test_many_experts(h):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_experts(h, dtype):
     """1024 experts, most without rows."""
+    t = TYPES[dtype]
     counts = [0] * 1024
     for e in (0, 3, 500, 1023):
         counts[e] = e % 37 + 1
     offsets, bounds = offsets_of(counts)
-    x, w = matrix(bounds[-1], 72, torch.bfloat16, 1), weights(1024, 72, 80, torch.bfloat16, 2)
+    x, w = matrix(bounds[-1], 72, t, 1), weights(1024, 72, 80, t, 2)
     y = h.expert_matmul(x, w, offsets)
-    dy = matrix(bounds[-1], 80, torch.bfloat16, 3)
+    dy = matrix(bounds[-1], 80, t, 3)
     dx, dw = h.expert_matmul_backward(dy, x, w, offsets)
     for e in range(1024):
         a, b = bounds[e], bounds[e + 1]
@@ -333,7 +364,7 @@ def test_many_experts(h):
         for got, want, D, K in ((y[a:b], xd @ wd, xd.abs() @ wd.abs(), 72),
                                 (dx[a:b], d @ wd.t(), d.abs() @ wd.abs().t(), 80),
                                 (dw[e], xd.t() @ d, xd.abs().t() @ d.abs(), b - a)):
-            assert_within(got, want, 1.01 * acc_error(torch.bfloat16, K) * D + rounding(want, torch.bfloat16))
+            assert_within(got, want, 1.01 * acc_error(t, K) * D + rounding(want, t))
 
 
 def test_gradients_against_differences(h):
@@ -370,10 +401,11 @@ def test_gradients_against_differences(h):
         assert abs(got - slope) <= 2e-2 * size
 
 
-def test_captured_with_other_offsets(h):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_with_other_offsets(h, dtype):
     """One captured call serves every distribution of the rows; two graphs share the handle's
     buffers, which a larger call outgrows."""
-    t = torch.bfloat16
+    t = TYPES[dtype]
     x, dy = matrix(300, 133, t, 1), matrix(300, 72, t, 2)  # (rows TMA cannot address: copied first)
     w = weights(4, 133, 72, t, 3)
     offsets = torch.zeros(5, dtype=torch.int32, device="cuda")
@@ -454,8 +486,6 @@ def test_refusals(g, h):
     x, w = torch.zeros(6, 16, dtype=t, device="cuda"), torch.zeros(2, 16, 24, dtype=t, device="cuda")
     offsets = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
     dy = torch.zeros(6, 24, dtype=t, device="cuda")
-    with pytest.raises(g.GemmError, match="UNSUPPORTED"):
-        h.expert_matmul(x.float(), w.float(), offsets)
     with pytest.raises(TypeError):
         h.expert_matmul(x.half(), w, offsets)
     with pytest.raises(TypeError):
