@@ -30,7 +30,17 @@ cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *posi
 cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
                                   const void *w, int w_dtype, const void *residual, int64_t ldr,
                                   void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
-                                  int64_t rows, int64_t N, int sm_count, cudaStream_t s);
+                                  int64_t rows, int64_t N, int sm_count, int *status, uint64_t timeout_ns,
+                                  bool stall, cudaStream_t s);
+// The same by bulk copies: rows that start on 16-byte boundaries and are a multiple of eight long, of
+// sizes that fit. `stall`: no copy is issued, the waits (timeout_ns) end in the status.
+bool expert_combine_bulk_fits(int64_t tokens, int64_t k, int64_t N, int in_dtype, int out_dtype,
+                              bool residual, int sm_count);
+cudaError_t expert_combine_bulk_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
+                                       const void *w, int w_dtype, const void *residual, int64_t ldr,
+                                       void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
+                                       int64_t rows, int64_t N, int sm_count, int *status,
+                                       uint64_t timeout_ns, bool stall, cudaStream_t s);
 
 // dz[position[t, j]] = w[t, j] dy[t] (or null), dw[t, j] = dy[t] . z[position[t, j]] (or null).
 cudaError_t expert_combine_backward_launch(const void *dy, int64_t lddy, int grad_dtype,

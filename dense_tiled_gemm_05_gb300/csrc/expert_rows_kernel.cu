@@ -1,7 +1,8 @@
 // expert_rows_kernel.cu -- rows to their experts' order and back:
 //
 //   y[position[t, j]] = x[t]                                          (gather)
-//   y[t]  = sum_j w[t, j] z[position[t, j]] + residual[t]             (combine)
+//   y[t]  = sum_j w[t, j] z[position[t, j]] + residual[t]             (combine; see also
+//                                                                 expert_combine_kernel.cu)
 //   dz[position[t, j]] = w[t, j] dy[t],  dw[t, j] = dy[t] . z[position[t, j]]
 //
 // and the copies of operands that TMA cannot address.
@@ -41,8 +42,8 @@ dim3 token_grid(int64_t tokens, int64_t N) {
   const int64_t gx = (N + kCols - 1) / kCols, gy = (tokens + kWarps - 1) / kWarps;
   return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(gy, 65535)));
 }
-// Where they are mostly read, exactly as many CTAs as stay (16384 tokens of 4 x 4 KB and a residual:
-// 64 us; with two and a half times as many 72), whose warps walk tokens.
+// Where they are mostly read, exactly as many CTAs as stay (16384 tokens of 4 x 4 KB and a residual
+// through this file's kernel: 64 us; with two and a half times as many 72), whose warps walk tokens.
 dim3 walk_grid(int64_t tokens, int64_t N, int sm_count) {
   const int64_t all = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * kWalkers;
   const int64_t gx = (N + kCols - 1) / kCols, gy = (tokens + kWarps - 1) / kWarps;
@@ -328,9 +329,13 @@ cudaError_t expert_gather_launch(const void *x, int64_t ldx, const int32_t *posi
 cudaError_t expert_combine_launch(const void *z, int64_t ldz, int in_dtype, const int32_t *position,
                                   const void *w, int w_dtype, const void *residual, int64_t ldr,
                                   void *y, int64_t ldy, int out_dtype, int64_t tokens, int64_t k,
-                                  int64_t rows, int64_t N, int sm_count, cudaStream_t s) {
+                                  int64_t rows, int64_t N, int sm_count, int *status, uint64_t timeout_ns,
+                                  bool stall, cudaStream_t s) {
   const bool vector = aligned16(z, ldz, esize(in_dtype)) && aligned16(y, ldy, esize(out_dtype)) &&
                       aligned16(residual, ldr, esize(out_dtype)) && N % VEC == 0;
+  if (vector && expert_combine_bulk_fits(tokens, k, N, in_dtype, out_dtype, residual != nullptr, sm_count))
+    return expert_combine_bulk_launch(z, ldz, in_dtype, position, w, w_dtype, residual, ldr, y, ldy, out_dtype,
+                                      tokens, k, rows, N, sm_count, status, timeout_ns, stall, s);
   FF_TYPED(in_dtype, TI, {
     FF_TYPED(out_dtype, TO, {
       auto go = [&](auto kernel) {

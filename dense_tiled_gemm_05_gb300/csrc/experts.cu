@@ -173,7 +173,9 @@ GEMM_API gemm_status_t gemm_expert_combine(gemm_handle_t h, int64_t tokens, int6
   return launched(h, ff::expert_combine_launch(Z, ldz, in_dtype, position, weights,
                                                weights ? weight_dtype : GEMM_F32, residual,
                                                ld_residual, Y, ldy, out_dtype, tokens, k, rows, N,
-                                               h->sm_count, static_cast<cudaStream_t>(cuda_stream)),
+                                               h->sm_count, h->status, h->timeout_us * 1000ull,
+                                               (stall_flags(h->stall_producer) & kDebugStallProducer) != 0,
+                                               static_cast<cudaStream_t>(cuda_stream)),
                   "expert combine launch");
 }
 

@@ -158,6 +158,84 @@ def test_combine(h, tokens, k, experts, N, dtype, weights, out, pad, offset):
     assert_within(res, want, bound_res, "combine in place")
 
 
+# enough tokens and long enough rows for copies in bulk: one piece and more, the last one short, and
+# many rows a token
+LONG = [(7300, 1, 9, 776), (1700, 3, 17, 2056), (1250, 8, 40, 4096), (1300, 4, 64, 2048),
+        (3000, 2, 16, 1032), (2500, 5, 8, 3000)]
+
+
+@pytest.mark.parametrize("tokens,k,experts,N", LONG)
+@pytest.mark.parametrize("dtype,weights,out", [
+    ("f32", "f32", "f32"), ("f16", "f32", "f16"), ("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"),
+    ("f16", None, "f32"), ("bf16", None, "bf16"), ("f32", "f16", "bf16")])
+@pytest.mark.parametrize("pad", [0, 8])
+def test_combine_long(h, tokens, k, experts, N, dtype, weights, out, pad):
+    t = TYPES[out]
+    position, rows, w = pairs(tokens, k, experts, dtype, weights, 5, h, N, pad)
+    if w is not None:
+        w[position < 0] = float("nan")
+    position[5] = -1
+    position[position == 3] = 2 ** 31 - 1
+    res = matrix(tokens, N, t, 9, pad=pad)
+    store = torch.full((tokens + 2, N + pad), 7.0, dtype=t, device="cuda")
+    y = store[1:-1, :N]
+    h.expert_combine(rows, position, w, out=y)
+    onto = h.expert_combine(rows, position, w, residual=res, out_dtype=t)
+    place = res.clone()
+    h.expert_combine(rows, position, w, residual=place, out=place)
+    assert same_bits(onto, place)
+    assert (store[0] == 7).all() and (store[-1] == 7).all() and (store[:, N:] == 7).all()
+    assert (y[5] == 0).all() and torch.equal(onto[5], res[5])
+    bound = (k + 2) * 2.0 ** -24
+    for i in range(0, tokens, 100):  # few tokens: rows read by loads, in the same order
+        part = slice(i, min(i + 100, tokens))
+        p, f = position[part], None if w is None else w[part]
+        assert same_bits(y[part], h.expert_combine(rows, p, f, out_dtype=t))
+        assert same_bits(onto[part], h.expert_combine(rows, p, f, residual=res[part], out_dtype=t))
+        if i % 500 == 0:
+            has = (p >= 0) & (p < rows.shape[0])
+            z = gathered64(rows, torch.where(has, p, torch.full_like(p, -1)))
+            f = torch.where(has, f.double(), torch.zeros_like(z[..., 0])) if f is not None else has.double()
+            want, D = torch.einsum("tkn,tk->tn", z, f), torch.einsum("tkn,tk->tn", z.abs(), f.abs())
+            assert_within(y[part], want, bound * D + rounding(want, t) * (1 + bound), "combine")
+            want, D = want + res[part].double(), D + res[part].double().abs()
+            assert_within(onto[part], want, bound * D + rounding(want, t) * (1 + bound), "onto a residual")
+
+
+def test_combine_long_captured(h):
+    """A captured call reads positions and weights anew, also on a stream of its own."""
+    position, rows, w = pairs(1300, 4, 64, "bf16", "f32", 5, h, 2048)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            y = h.expert_combine(rows, position, w)
+    torch.cuda.synchronize()
+    for seed in (6, 7):
+        other, _, f = pairs(1300, 4, 64, "bf16", "f32", seed, h, 2048)
+        position.copy_(other)
+        w.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = rows.clone()
+        assert same_bits(y, h.expert_combine(kept, other, f))
+
+
+def test_combine_waits_are_bounded(g):
+    """Copies that never come end in a status, and the handle works on."""
+    hh = g.Gemm(0)
+    position, rows, w = pairs(1300, 4, 64, "bf16", "f32", 5, hh, 2048, none=0.0)
+    want = hh.expert_combine(rows, position, w)
+    hh.set_option("wait_timeout_us", 20000)
+    hh.set_option("fault_stall_producer", 1)
+    hh.expert_combine(rows, position, w)
+    assert hh.status() == 6
+    hh.set_option("fault_stall_producer", 0)
+    assert same_bits(hh.expert_combine(rows, position, w), want) and hh.status() == 0
+    hh.close()
+
+
 @pytest.mark.parametrize("tokens,k,experts,N", SHAPES + [(9, 2, 8, 8192), (2, 2, 4, 5001)])
 @pytest.mark.parametrize("dtype,weights,grad", [
     ("f32", "f32", "f32"), ("f16", "f32", "f16"), ("bf16", "bf16", "bf16"), ("bf16", "f32", "f32")])
