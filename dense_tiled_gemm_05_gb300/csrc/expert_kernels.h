@@ -28,6 +28,7 @@ struct ExpertParams {
   int64_t ldc;
   void *pre, *pre2;        // gated: receive the two products, or null
   int64_t ld_pre, ld_pre2;
+  int32_t wide;            // all rows stored start on 8-byte boundaries, and N is a multiple of four
   // sums of split tiles: [cluster][CTA][column][128], flags and epoch as in TcParams
   // (stream_k: GEMM_OPT_STREAM_K)
   int32_t stream_k;

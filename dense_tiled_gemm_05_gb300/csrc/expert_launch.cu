@@ -136,6 +136,11 @@ gemm_status_t run_expert(gemm_handle_t h, const ExpertProduct &q, cudaStream_t s
   p.dtype = q.dtype, p.act = q.act, p.panels = panels, p.up_first = apart < 0;
   p.C = q.C, p.ldc = q.ldc;
   p.pre = q.pre, p.ld_pre = q.ld_pre, p.pre2 = q.pre2, p.ld_pre2 = q.ld_pre2;
+  const auto eights = [](const void *rows, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(rows) % 8 == 0 && (ld * ES) % 8 == 0;
+  };
+  p.wide = q.N % 4 == 0 && eights(q.C, q.ldc) &&
+           (!q.pre || (eights(q.pre, q.ld_pre) && eights(q.pre2, q.ld_pre2)));
   p.status = h->status;
   p.timeout_ns = h->timeout_us * 1000ull;
   p.debug_flags = stall_flags(h->stall_producer);

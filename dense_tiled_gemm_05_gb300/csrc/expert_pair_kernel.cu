@@ -31,9 +31,9 @@
 // Measured on one GB300: 16384 rows, 4096 x 2048, one expert 1900 TFLOP/s, 16 of 1024 rows 1820, 16 of
 // 46 to 4407 rows 1680; 256 rows of 32 experts, 4096 x 2048: 81 us for 540 MB.
 //
-// The epilogue has one feature a lane and tokens along its registers: a warp's store of one
-// token is 32 neighbouring features. Rows past the expert's last are not stored (they are the
-// next expert's); bound: tensor cores for many rows an expert, HBM for few.
+// The epilogue has one feature a lane and tokens along its registers, which lanes exchange for wider
+// stores (store_tokens). Rows past the expert's last are not stored (they are the next expert's).
+// Bound: tensor cores for many rows an expert, HBM for few, the epilogue for K below some 1000.
 #include <atomic>
 
 #include "activation.cuh"
@@ -106,37 +106,70 @@ __device__ __forceinline__ void write_share(float *to, uint32_t t_acc, int c0) {
   for (int j = 0; j < 32; ++j) __stcg(to + (c0 + j) * BM, __uint_as_float(r[j]));
 }
 
+// COUNT tokens of a feature a lane, STEP rows apart from `to` (the lane's own feature) on, the rows below
+// `left` of them stored. `wide`: lanes exchange tokens for features by fours, so that each holds four
+// features of every fourth token and stores 8 bytes; else one by one, which takes the memory pipe 10
+// cycles a store (one GB300, 16384 rows of 16 experts, us, wide and not: 256 x 4096 46 and 78, 1024 x
+// 4096 88 and 92; gated with g and u kept 1024 x 2048 105 and 127; by twos 47, 88, 108, by eights 55,
+// 88, 110). By whole warps; `live`: the lane's feature exists.
+template <typename T, int COUNT, int STEP>
+__device__ __forceinline__ void store_tokens(T *to, int64_t ld, const float (&v)[COUNT], int left, bool live,
+                                             bool wide, int lane) {
+  if (!wide) {
+    if (!live) return;
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j)
+      if (STEP * j < left) to[STEP * j * ld] = from_f32<T>(v[j]);
+    return;
+  }
+  constexpr int OUT = std::is_same<T, __half>::value ? GEMM_F16 : GEMM_BF16;
+  const bool one = lane & 1, two = lane & 2;
+  const uint32_t pick = one ? 0x3276 : 0x5410;
+  // (all exchanges before the first store: the other way round 59 us for the 46 above)
+  uint32_t x[COUNT / 2];  // token 2 i + one of two features
+#pragma unroll
+  for (int i = 0; i < COUNT / 2; ++i) {
+    const uint32_t w = pack2<OUT>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+    x[i] = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick);
+  }
+  uint2 y[COUNT / 4];  // token 4 i + lane % 4 of four features
+#pragma unroll
+  for (int i = 0; i < COUNT / 4; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, two ? x[2 * i] : x[2 * i + 1], 2);
+    y[i] = two ? uint2{got, x[2 * i + 1]} : uint2{x[2 * i], got};
+  }
+  to -= lane & 3;
+#pragma unroll
+  for (int i = 0; i < COUNT / 4; ++i) {
+    const int row = STEP * (4 * i + (lane & 3));
+    if (live && row < left) *reinterpret_cast<uint2 *>(to + row * ld) = y[i];
+  }
+}
+
 // 32 tokens' columns from c0 on of this lane, the `left` first of them stored from `row` on: one
 // feature f, ...
 template <typename T, bool GATED, int ACC>
 __device__ __forceinline__ void finish(const ExpertParams &p, uint32_t t_acc, int c0, const Shares &sh,
-                                       int64_t row, int left, int64_t f) {
+                                       int64_t row, int left, int64_t f, int lane) {
   uint32_t r[32], q[32];
   read_sums(t_acc, c0, sh, r);
   if (GATED) read_sums(t_acc, ACC / 2 + c0, sh, q);
-  if (f >= p.N) return;
-  float a[32];
+  const bool live = f < p.N;
+  float a[32], u[32];
 #pragma unroll
   for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(r[j]);
   if (GATED) {
-    if (p.pre) {
-      T *g = static_cast<T *>(p.pre) + row * p.ld_pre + f;
-      T *u = static_cast<T *>(p.pre2) + row * p.ld_pre2 + f;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < left) {
-          g[j * p.ld_pre] = from_f32<T>(a[j]);
-          u[j * p.ld_pre2] = from_f32<T>(__uint_as_float(q[j]));
-        }
+    for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(q[j]);
+    if (p.pre) {
+      store_tokens<T, 32, 1>(static_cast<T *>(p.pre) + row * p.ld_pre + f, p.ld_pre, a, left, live, p.wide, lane);
+      store_tokens<T, 32, 1>(static_cast<T *>(p.pre2) + row * p.ld_pre2 + f, p.ld_pre2, u, left, live, p.wide, lane);
     }
     activate_all<true>(a, p.act);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) a[j] *= __uint_as_float(q[j]);
+    for (int j = 0; j < 32; ++j) a[j] *= u[j];
   }
-  T *y = static_cast<T *>(p.C) + row * p.ldc + f;
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < left) y[j * p.ldc] = from_f32<T>(a[j]);
+  store_tokens<T, 32, 1>(static_cast<T *>(p.C) + row * p.ldc + f, p.ldc, a, left, live, p.wide, lane);
 }
 
 // ... or g or u of one (the other 16 lanes have the other): the lower half of the warp finishes the
@@ -146,7 +179,7 @@ __device__ __forceinline__ void finish_mixed(const ExpertParams &p, uint32_t t_a
                                              int64_t row, int left, int64_t f, int lane) {
   uint32_t r[32];
   read_sums(t_acc, c0, sh, r);
-  const bool odd = lane >= 16, gate = odd == (p.up_first != 0);
+  const bool odd = lane >= 16, gate = odd == (p.up_first != 0), live = f < p.N;
   float a[16], u[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -156,24 +189,16 @@ __device__ __forceinline__ void finish_mixed(const ExpertParams &p, uint32_t t_a
     a[j] = gate ? mine : other;
     u[j] = gate ? other : mine;
   }
-  if (f >= p.N) return;
   row += odd;
   left -= odd;
   if (p.pre) {
-    T *g = static_cast<T *>(p.pre) + row * p.ld_pre + f;
-    T *v = static_cast<T *>(p.pre2) + row * p.ld_pre2 + f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (2 * j < left) {
-        g[2 * j * p.ld_pre] = from_f32<T>(a[j]);
-        v[2 * j * p.ld_pre2] = from_f32<T>(u[j]);
-      }
+    store_tokens<T, 16, 2>(static_cast<T *>(p.pre) + row * p.ld_pre + f, p.ld_pre, a, left, live, p.wide, lane);
+    store_tokens<T, 16, 2>(static_cast<T *>(p.pre2) + row * p.ld_pre2 + f, p.ld_pre2, u, left, live, p.wide, lane);
   }
   activate_all<true>(a, p.act);
-  T *y = static_cast<T *>(p.C) + row * p.ldc + f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (2 * j < left) y[2 * j * p.ldc] = from_f32<T>(a[j] * u[j]);
+  for (int j = 0; j < 16; ++j) a[j] *= u[j];
+  store_tokens<T, 16, 2>(static_cast<T *>(p.C) + row * p.ldc + f, p.ldc, a, left, live, p.wide, lane);
 }
 
 // How the tiles are shared: whole ones round-robin, or the last rounds by K-blocks. Sharing costs
@@ -461,9 +486,9 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
             else
               finish_mixed<__half>(p, t_row, c0, sh, row, left, f, lane);
           } else if (p.dtype == GEMM_BF16) {
-            finish<__nv_bfloat16, TWO, S::ACC>(p, t_row, c0, sh, row, left, f);
+            finish<__nv_bfloat16, TWO, S::ACC>(p, t_row, c0, sh, row, left, f, lane);
           } else {
-            finish<__half, TWO, S::ACC>(p, t_row, c0, sh, row, left, f);
+            finish<__half, TWO, S::ACC>(p, t_row, c0, sh, row, left, f, lane);
           }
         }
       }

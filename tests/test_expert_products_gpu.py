@@ -123,9 +123,9 @@ def test_product(h, counts, N, K, dtype):
 
 
 @pytest.mark.parametrize("layout", ["row", "col"])
-@pytest.mark.parametrize("pad,offset,gap", [(0, 0, 0), (8, 8, 16), (3, 1, 0), (8, 0, 5)])
+@pytest.mark.parametrize("pad,offset,gap", [(0, 0, 0), (8, 8, 16), (3, 1, 0), (8, 0, 5), (4, 4, 4), (2, 0, 0)])
 @pytest.mark.parametrize("counts", [[5, 0, 300, 64], [40]], ids=str)
-@pytest.mark.parametrize("N,K", [(200, 136), (264, 72), (133, 65)])
+@pytest.mark.parametrize("N,K", [(200, 136), (264, 72), (133, 65), (132, 68), (4, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_product_layouts(h, counts, N, K, layout, pad, offset, gap, dtype):
     t = TYPES[dtype]
@@ -240,8 +240,8 @@ def test_gated_activations(h, act, dtype):
 
 
 @pytest.mark.parametrize("layout", ["row", "col"])
-@pytest.mark.parametrize("pad,offset,gap", [(0, 0, 0), (8, 8, 16), (3, 1, 0)])
-@pytest.mark.parametrize("F,K", [(200, 136), (133, 65)])
+@pytest.mark.parametrize("pad,offset,gap", [(0, 0, 0), (8, 8, 16), (3, 1, 0), (4, 4, 4), (2, 2, 0)])
+@pytest.mark.parametrize("F,K", [(200, 136), (133, 65), (144, 64), (132, 68)])
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 def test_gated_layouts(h, F, K, layout, pad, offset, gap, dtype):
     t = TYPES[dtype]
