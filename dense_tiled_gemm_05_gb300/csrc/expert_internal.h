@@ -60,9 +60,9 @@ cudaError_t expert_gated_rows_launch(const float *g, int64_t ldg, const float *u
 
 // Copies `count` matrices of `lines` lines of `len` 16-bit elements (lines ld apart, matrices stride
 // apart, of any alignment) to lines to_ld apart that follow one another from a 16-byte boundary
-// (to_ld: a multiple of 8, at least len).
+// (to_ld: a multiple of 8, at least len); with offsets only those whose experts have rows.
 cudaError_t expert_stage_launch(const void *src, int64_t ld, int64_t stride, int64_t lines, int64_t count,
-                                int64_t len, void *dst, int64_t to_ld, cudaStream_t s);
+                                int64_t len, void *dst, int64_t to_ld, const int32_t *offsets, cudaStream_t s);
 
 // y = x * mask * scale + residual (null: 0); key: two 64-bit words on the device.
 cudaError_t dropout_launch(const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,

@@ -69,11 +69,11 @@ void ExpertOperand::plan(Carve *carve) {
   if (staged) offset = carve->take(count * lines * round_up(len, 8), ES);
 }
 
-gemm_status_t ExpertOperand::stage(gemm_handle_t h, char *buf, cudaStream_t s) {
+gemm_status_t ExpertOperand::stage(gemm_handle_t h, char *buf, cudaStream_t s, const int32_t *offsets) {
   if (!staged) return GEMM_OK;
   const int64_t to_ld = round_up(len, 8);
   char *to = buf + offset;
-  const cudaError_t err = expert_stage_launch(ptr, ld, stride, lines, count, len, to, to_ld, s);
+  const cudaError_t err = expert_stage_launch(ptr, ld, stride, lines, count, len, to, to_ld, offsets, s);
   if (err != cudaSuccess) return cuda_fail(err, "stage operand");
   h->launches += 1;
   ptr = to, ld = to_ld, stride = lines * to_ld;

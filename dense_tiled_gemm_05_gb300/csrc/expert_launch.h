@@ -20,8 +20,9 @@ struct ExpertOperand {
   size_t offset = 0;
   // Decides whether it is copied, and where.
   void plan(Carve *carve);
-  // Makes the copy in `buf`; ptr, ld and stride are then the copy's.
-  gemm_status_t stage(gemm_handle_t h, char *buf, cudaStream_t s);
+  // Makes the copy in `buf`; ptr, ld and stride are then the copy's. With offsets only matrices of
+  // experts that have rows are copied (the others are not read).
+  gemm_status_t stage(gemm_handle_t h, char *buf, cudaStream_t s, const int32_t *offsets = nullptr);
 };
 
 // The experts' weights as a call gives them: K x N of each expert in `layout`.

@@ -29,6 +29,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 32 * VEC;  // columns a warp covers at a time
 constexpr int kWalkers = 4;      // CTAs an SM of kernels whose warps walk tokens
+// CTAs of one of many matrices that are copied, at most. One that is passed over costs their starts:
+// products of 2001 x 4096 with 32 experts, us, one row of four of them and two rows of each: 53 and 295;
+// with 152 CTAs 62 and 303, with 608 50 and 295, but 54 against 34 for one row of 8 of 64, 1001 x 1408.
+constexpr int64_t kStageCtas = 304;
 
 bool aligned16(const void *p, int64_t ld, int es) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0);
@@ -238,20 +242,25 @@ __global__ void __launch_bounds__(kThreads)
 
 // A warp copies 256 elements of a line, a lane eight: their 4-byte words, shifted by half a word
 // where the line starts on an odd element, as one 16-byte store. At a line's ends its own half of a
-// word is read. (32 matrices of 2048 x 1001, a
-// quarter of a gigabyte read and written: about 60 us; with two-byte accesses 230.)
+// word is read. (32 matrices of 2048 x 1001, a quarter of a gigabyte read and written: about 60 us;
+// with two-byte accesses 230.) With offsets, matrices of experts without rows are passed over.
 __global__ void __launch_bounds__(kThreads)
-    stage_kernel(const uint16_t *__restrict__ src, int64_t ld, int64_t stride, int64_t lines, int64_t all,
-                 int64_t len, int64_t chunks, uint16_t *__restrict__ dst, int64_t to_ld) {
+    stage_kernel(const uint16_t *__restrict__ src, int64_t ld, int64_t stride, int64_t lines, int64_t len,
+                 int64_t chunks, uint16_t *__restrict__ dst, int64_t to_ld,
+                 const int32_t *__restrict__ offsets) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x % 32;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; i < all * chunks;
+  const int64_t e = blockIdx.y;
+  if (offsets && offsets[e + 1] <= offsets[e]) return;
+  src += e * stride;
+  dst += e * lines * to_ld;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; i < lines * chunks;
        i += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t line = i / chunks, e = line / lines;
+    const int64_t line = i / chunks;
     const int64_t j0 = (i - line * chunks) * kCols + lane * VEC;
     if (j0 >= len) continue;
-    const uint16_t *from = src + e * stride + (line - e * lines) * ld + j0;
+    const uint16_t *from = src + line * ld + j0;
     const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(from) / 2 % 2);
     const uint32_t *words = reinterpret_cast<const uint32_t *>(from - odd);
     const uint16_t *halves = from - odd;
@@ -280,11 +289,13 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t expert_stage_launch(const void *src, int64_t ld, int64_t stride, int64_t lines, int64_t count,
-                                int64_t len, void *dst, int64_t to_ld, cudaStream_t s) {
-  const int64_t chunks = (len + kCols - 1) / kCols, all = lines * count;
-  const int64_t ctas = std::min<int64_t>((all * chunks + kWarps - 1) / kWarps, int64_t{1} << 20);
-  launch_pdl(stage_kernel, dim3(static_cast<unsigned>(ctas)), kThreads, 0, s, static_cast<const uint16_t *>(src),
-             ld, stride, lines, all, len, chunks, static_cast<uint16_t *>(dst), to_ld);
+                                int64_t len, void *dst, int64_t to_ld, const int32_t *offsets, cudaStream_t s) {
+  const int64_t chunks = (len + kCols - 1) / kCols;
+  const int64_t ctas =
+      std::min<int64_t>((lines * chunks + kWarps - 1) / kWarps, count == 1 ? 1 << 20 : kStageCtas);
+  launch_pdl(stage_kernel, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(count)), kThreads, 0, s,
+             static_cast<const uint16_t *>(src), ld, stride, lines, len, chunks, static_cast<uint16_t *>(dst),
+             to_ld, offsets);
   return cudaGetLastError();
 }
 

@@ -248,7 +248,7 @@ GEMM_API gemm_status_t gemm_run_expert(gemm_handle_t h, int64_t experts, int64_t
   st = reserve(h, h->ff, carve.bytes, s);
   char *buf = static_cast<char *>(h->ff.ptr);
   if (st == GEMM_OK) st = q.X.stage(h, buf, s);
-  if (st == GEMM_OK) st = q.W.stage(h, buf, s);
+  if (st == GEMM_OK) st = q.W.stage(h, buf, s, offsets);
   return st == GEMM_OK ? ff::run_expert(h, q, s) : st;
 }
 
@@ -292,7 +292,7 @@ GEMM_API gemm_status_t gemm_run_expert_backward(
   char *buf = static_cast<char *>(h->ff.ptr);
   if (st == GEMM_OK) st = ys.stage(h, buf, s);
   if (st == GEMM_OK) st = xs.stage(h, buf, s);
-  if (st == GEMM_OK) st = ws.stage(h, buf, s);
+  if (st == GEMM_OK) st = ws.stage(h, buf, s, offsets);
   if (st != GEMM_OK) return st;
   if (make_dx) {
     ff::ExpertProduct q;
@@ -376,8 +376,8 @@ GEMM_API gemm_status_t gemm_run_expert_gated(
   st = reserve(h, h->ff, carve.bytes, s);
   char *buf = static_cast<char *>(h->ff.ptr);
   if (st == GEMM_OK) st = q.X.stage(h, buf, s);
-  if (st == GEMM_OK) st = q.W.stage(h, buf, s);
-  if (st == GEMM_OK) st = q.W2.stage(h, buf, s);
+  if (st == GEMM_OK) st = q.W.stage(h, buf, s, offsets);
+  if (st == GEMM_OK) st = q.W2.stage(h, buf, s, offsets);
   return st == GEMM_OK ? ff::run_expert(h, q, s) : st;
 }
 
@@ -443,8 +443,8 @@ GEMM_API gemm_status_t gemm_run_expert_gated_backward(
     if (st != GEMM_OK) return st;
   }
   st = xs.stage(h, buf, s);
-  if (st == GEMM_OK) st = wg.stage(h, buf, s);
-  if (st == GEMM_OK) st = wu.stage(h, buf, s);
+  if (st == GEMM_OK) st = wg.stage(h, buf, s, offsets);
+  if (st == GEMM_OK) st = wu.stage(h, buf, s, offsets);
   if (st != GEMM_OK) return st;
   const ff::ExpertOperand gs = ff::expert_rows(dg, ldd, rows, F), us = ff::expert_rows(du, ldd, rows, F);
   if (make_dx) {

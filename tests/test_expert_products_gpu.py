@@ -522,3 +522,21 @@ def test_refusals(g, h):
     many = torch.zeros(1025, 8, 8, dtype=t, device="cuda")
     with pytest.raises(g.GemmError, match="UNSUPPORTED"):
         h.expert_matmul(x[:, :8], many, torch.zeros(1026, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("counts", [[0, 3, 0, 0, 1, 0], [0] * 5 + [40], [7] + [0] * 200], ids=str)
+def test_copied_weights_of_few_experts(h, counts):
+    """Rows that TMA cannot address: only the weights of experts that have rows are copied, call by
+    call, and others' may hold anything."""
+    t = torch.bfloat16
+    w = weights(len(counts), 1001, 75, t, 2)
+    for e, n in enumerate(counts):
+        if n == 0:
+            w[e] = float("nan")
+    for turn in (counts, counts[::-1]):
+        offsets, bounds = offsets_of(turn)
+        x, dy = matrix(bounds[-1], 1001, t, 1), matrix(bounds[-1], 75, t, 3)
+        here = w if turn is counts else w.flip(0)
+        check_product(h, x, here, offsets, bounds, sentinel(bounds[-1], 75, t))
+        check_backward(h, dy, x, here, offsets, bounds, sentinel(bounds[-1], 1001, t))
+        check_gated(h, x, here, here.clone(), offsets, bounds, "silu")
