@@ -13,6 +13,9 @@ namespace ff {
 
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxSorted = int64_t{1} << 26;  // ids of a call (the work grows with their square)
+// Rows and features of the products: the kernels round them up to whole tiles and boxes (256 at most,
+// and 256 past a tile's start) in 32 bits.
+constexpr int64_t kMaxProductSize = INT32_MAX - 511;
 
 // Workspace of expert_sort_launch (0 when one CTA takes all ids).
 size_t expert_sort_bytes(int64_t n, int64_t experts);

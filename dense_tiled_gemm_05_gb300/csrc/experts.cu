@@ -48,7 +48,8 @@ gemm_status_t check_experts(gemm_handle_t h, int64_t experts, int64_t rows, int6
   if (!h || experts < 1 || rows < 0 || N < 0 || K < 0 || !offsets || !valid_dtype(dtype) ||
       !valid_layout(layout))
     return GEMM_ERR_INVALID_ARG;
-  if (experts > ff::kMaxExperts || too_large(rows, 1, N, K) || 2 * N > INT32_MAX ||
+  if (experts > ff::kMaxExperts || rows > ff::kMaxProductSize || N > ff::kMaxProductSize ||
+      K > ff::kMaxProductSize || 2 * N > INT32_MAX ||
       !ff::expert_tiles_fit(experts, rows, N > 0 ? N : 1, K > 0 ? K : 1))
     return GEMM_ERR_UNSUPPORTED;
   return misaligned(offsets, 4) ? GEMM_ERR_ALIGNMENT : GEMM_OK;

@@ -483,7 +483,8 @@ GEMM_API gemm_status_t gemm_expert_combine_backward(
  * add nothing, whatever they hold. Offsets have to be in increasing order inside [0, rows]: others
  * leave the results undefined, but nothing outside the matrices is read or written.
  * 16-bit operands TMA cannot address (a base, leading dimension or stride that is no multiple of 16
- * bytes) are copied first; f32 ones are multiplied on the fp32 units. experts in [1, 1024].
+ * bytes) are copied first; f32 ones are multiplied on the fp32 units. experts in [1, 1024]; rows and K
+ * up to INT32_MAX - 511 and N up to INT32_MAX / 2 (more: UNSUPPORTED; so in the calls below).
  * For 16-bit types GEMM_OPT_MAX_CTAS caps the CTAs and GEMM_OPT_STREAM_K says whether the last
  * tiles' K is shared over clusters; the other options of products and gemm_set_kernel_events have no
  * effect. */
