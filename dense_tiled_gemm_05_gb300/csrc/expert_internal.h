@@ -13,6 +13,8 @@ namespace ff {
 
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxSorted = int64_t{1} << 26;  // ids of a call (the work grows with their square)
+// A token's choices: the row kernels step through them by warps, 32 at a time, in 32 bits.
+constexpr int64_t kMaxChoices = INT32_MAX - 31;
 // Rows and features of the products: the kernels round them up to whole tiles and boxes (256 at most,
 // and 256 past a tile's start) in 32 bits.
 constexpr int64_t kMaxProductSize = INT32_MAX - 511;

@@ -21,7 +21,7 @@ using ff::vector_span;
 namespace {
 
 bool too_large(int64_t tokens, int64_t k, int64_t rows, int64_t N) {
-  return tokens > INT32_MAX || k > INT32_MAX || rows > INT32_MAX || N > INT32_MAX ||
+  return tokens > INT32_MAX || k > ff::kMaxChoices || rows > INT32_MAX || N > INT32_MAX ||
          tokens * k > INT32_MAX;
 }
 

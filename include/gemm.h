@@ -423,10 +423,11 @@ GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_handle_t h, int64_t M, int6
 /* --------------------------------------------------------- operators of experts
  *
  * The parts of a feed-forward block that is split over experts: the order of its tokens by
- * expert, rows into that order and back, the experts' products, and dropout. Each of `tokens` tokens chooses `k` of
- * `experts` experts; pair (t, j) is token t's j-th choice. Rows, types, alignment, streams,
- * overlaps and errors are those of the feed-forward operators; sizes are at most INT32_MAX, and
- * so is tokens * k (else GEMM_ERR_UNSUPPORTED). */
+ * expert, rows into that order and back, the experts' products, and dropout. Each of `tokens`
+ * tokens chooses `k` of `experts` experts; pair (t, j) is token t's j-th choice. Rows, types,
+ * alignment, streams, overlaps and errors are those of the feed-forward operators; sizes are at
+ * most INT32_MAX, k at most INT32_MAX - 31, and tokens * k at most INT32_MAX (else
+ * GEMM_ERR_UNSUPPORTED). */
 
 /* The stable order of the pairs by expert: with ids[t, j] at ids + t * ld_ids + j (ld_ids >= k, in
  * elements; integers of id_bytes bytes, 4 or 8),

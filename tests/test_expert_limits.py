@@ -46,3 +46,27 @@ def test_products(call, dtype):
         assert call(size, 8, 8, dtype) == UNSUPPORTED
         assert call(1, 8, size, dtype) == UNSUPPORTED
         assert call(1, size, 8, dtype) == UNSUPPORTED
+
+
+def gather(tokens, k):
+    return g.lib().gemm_expert_gather(HANDLE, tokens, k, 8, P, 8, ODD, 4, P, 8, BF16, None)
+
+
+def combine(tokens, k):
+    return g.lib().gemm_expert_combine(HANDLE, tokens, k, 8, P, 8, 4, ODD, None, F32, None, 0, P, 8, BF16,
+                                       BF16, None)
+
+
+def combine_backward(tokens, k):
+    return g.lib().gemm_expert_combine_backward(HANDLE, tokens, k, 8, P, 8, P, 8, 4, ODD, None, F32, P, 8, None,
+                                                BF16, BF16, None)
+
+
+@pytest.mark.parametrize("call", [gather, combine, combine_backward])
+def test_choices(call):
+    """A warp takes a token's pairs 32 at a time, in 32 bits: a last step past INT32_MAX is refused."""
+    assert call(1, INT32_MAX - 31) == ALIGNMENT
+    assert call(INT32_MAX, 1) == ALIGNMENT
+    for k in (INT32_MAX - 30, INT32_MAX, INT32_MAX + 1):
+        assert call(1, k) == UNSUPPORTED
+    assert call(2 ** 16, 2 ** 15) == UNSUPPORTED
