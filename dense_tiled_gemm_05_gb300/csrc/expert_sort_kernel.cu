@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const SortPa
   int32_t *total = smem;            // [E]: entries of each expert, then their first rows
   int32_t *before = total + E;      // [E]: those in earlier chunks
   int32_t *cursor = before + E;     // [warps][E]
-  __shared__ int32_t warp_sum[kSortWarps];
+  int32_t *warp_sum = cursor + kSortWarps * E;  // [warps]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int i = threadIdx.x; i < (2 + kSortWarps) * E; i += kSortThreads) smem[i] = 0;
   __syncthreads();
@@ -179,12 +179,17 @@ int items_of(int64_t n) {
   return items;
 }
 
+// All of expert_place_kernel's shared memory (none is static: 48 KB is the limit of both together).
+constexpr size_t place_bytes(int64_t experts) {
+  return static_cast<size_t>((2 + kSortWarps) * experts + kSortWarps) * sizeof(int32_t);
+}
+
 template <int ITEMS>
 cudaError_t place_launch(const SortParams &p, dim3 grid, size_t smem, cudaStream_t s) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         expert_place_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        static_cast<int>((2 + kSortWarps) * kMaxExperts * sizeof(int32_t)));
+        static_cast<int>(place_bytes(kMaxExperts)));
     if (e != cudaSuccess) return e;
   }
   launch_pdl(expert_place_kernel<ITEMS>, grid, kSortThreads, smem, s, p);
@@ -216,7 +221,7 @@ cudaError_t expert_sort_launch(const void *ids, int64_t ld_ids, bool wide, int64
   const dim3 grid(static_cast<unsigned>(chunks));
   *launches = chunks > 1 ? 2 : 1;
   if (chunks > 1) launch_pdl(expert_count_kernel, grid, kSortThreads, experts * sizeof(int32_t), s, p);
-  const size_t smem = static_cast<size_t>(2 + kSortWarps) * experts * sizeof(int32_t);
+  const size_t smem = place_bytes(experts);
   switch (items) {
     case 4: return place_launch<4>(p, grid, smem, s);
     case 8: return place_launch<8>(p, grid, smem, s);
