@@ -376,14 +376,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncwarp();
   } else if (warp == kMaskWarp) {
     // ------------------------- rows past an expert's last: zeros (both CTAs)
+    // (a wait spans all tiles since the last ragged one, and so has their limits together: should one
+    // of them stop, the role that waits for it raises the abort flag, which ends this wait too)
     uint32_t fills = 0, phases = 0;
-    while (rounds.next(t)) {
+    Watchdog patient = wd;
+    for (patient.timeout_ns = 0; rounds.next(t);) {
       const Tile tile(p, order, t);
       const uint32_t before = fills;
       fills += static_cast<uint32_t>(tile.blocks);
+      if (patient.timeout_ns >> 62 == 0) patient.timeout_ns += wd.timeout_ns;
       if (!tile.ragged()) continue;
       const uint32_t stage = (before + static_cast<uint32_t>(tile.blocks - 1 - tile.start)) % STAGES;
-      bool ok = mbar_wait(&tail[stage], phases >> stage & 1, wd);
+      bool ok = mbar_wait(&tail[stage], phases >> stage & 1, patient);
+      patient.timeout_ns = 0;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       phases ^= 1u << stage;
