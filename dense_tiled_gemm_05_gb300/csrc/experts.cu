@@ -34,12 +34,18 @@ bool bad_weights(const void *W, int64_t experts, int64_t K, int64_t N, int64_t l
   if (K == 0 || N == 0) return false;
   return bad_matrix(W, K, N, ld, layout) || (experts > 1 && stride < weight_span(K, N, ld, layout));
 }
-// All experts' weights. (Two sets may be parts of one buffer, expert by expert.)
+// All experts' weights. Two sets may be parts of one buffer: column ranges of the same lines (where
+// experts are whole lines apart, so that all lines are multiples of ld from the first), or blocks of
+// lines, expert by expert.
 Span weights_span(const void *W, int64_t experts, int64_t K, int64_t N, int64_t ld, int64_t stride,
                   int layout, int es) {
-  if (K == 0 || N == 0) return Span{};
-  const int64_t one = weight_span(K, N, ld, layout);
-  return matrix_span(W, experts, one, experts > 1 ? stride : one, GEMM_ROW_MAJOR, es);
+  if (!W || K == 0 || N == 0) return Span{};
+  Span s = matrix_span(W, K, N, ld, layout, es);  // the first expert's
+  if (experts == 1) return s;
+  s.block = s.hi - s.lo, s.block_pitch = static_cast<uintptr_t>(stride * es);
+  s.hi += static_cast<uintptr_t>((experts - 1) * stride * es);
+  if (stride % ld != 0) s.pitch = 0;
+  return s;
 }
 
 // What the experts' products share: sizes and offsets.

@@ -11,16 +11,27 @@ namespace ff {
 inline bool valid_act(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SIGMOID; }
 
 // A buffer of a call: the bytes it spans and, for a matrix, its line pitch and the bytes of a
-// line, to keep outputs off inputs and each other.
+// line, to keep outputs off inputs and each other. Several matrices also have the pitch from one to
+// the next and the bytes of one (block_pitch 0: one matrix).
 struct Span {
   uintptr_t lo = 0, hi = 0;  // empty: lo == hi
   uintptr_t pitch = 0, line = 0;
+  uintptr_t block_pitch = 0, block = 0;
   bool meets(const Span &o) const {
     if (!(lo < o.hi && o.lo < hi)) return false;
-    // column ranges of one wider matrix share a span, but no element
-    if (pitch == 0 || pitch != o.pitch) return true;
-    const uintptr_t d = (lo < o.lo ? o.lo - lo : pitch - (lo - o.lo) % pitch) % pitch;
-    return d < line || d + o.line > pitch;
+    // column ranges of one wider matrix, or parts of matrices that follow one another at one pitch,
+    // share a span, but no element
+    return !(apart(o, pitch, line, o.pitch, o.line) || apart(o, pitch, line, o.block_pitch, o.block) ||
+             apart(o, block_pitch, block, o.pitch, o.line) ||
+             apart(o, block_pitch, block, o.block_pitch, o.block));
+  }
+
+ private:
+  // Whether `len` bytes at lo + i * step and `len_o` bytes at o.lo + j * step are apart for all i, j.
+  bool apart(const Span &o, uintptr_t step, uintptr_t len, uintptr_t step_o, uintptr_t len_o) const {
+    if (step == 0 || step != step_o) return false;
+    const uintptr_t d = (lo < o.lo ? o.lo - lo : step - (lo - o.lo) % step) % step;
+    return d >= len && d + len_o <= step;
   }
 };
 

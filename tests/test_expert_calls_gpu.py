@@ -4,7 +4,7 @@ import torch
 
 from expert_util import make_ids, sort_reference
 from ff_util import acc_error, assert_within, matrix, rounding
-from test_expert_products_gpu import offsets_of
+from test_expert_products_gpu import offsets_of, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,56 @@ def test_surplus_rows_after_many_whole_blocks(g):
     ref, D = xd.t() @ d, xd.abs().t() @ d.abs()
     assert_within(got[1][:300, -300:], ref, 1.01 * acc_error(BF16, b - a) * D + rounding(ref, BF16), "dw")
     hh.close()
+
+
+def backward_into(g, h, counts, layout, place):
+    """gemm_run_expert_gated_backward with both weight gradients in one buffer of NaN; place(F, K, E)
+    gives (elements, ld, stride, dWu's first element)."""
+    offsets, bounds = offsets_of(counts)
+    E, K, F, rows = len(counts), 72, 40, bounds[-1]
+    x, (dh, gate, up) = matrix(rows, K, BF16, 1), (matrix(rows, F, BF16, s) for s in (2, 3, 4))
+    wg, wu = (weights(E, K, F, BF16, s, layout) for s in (5, 6))
+    size, ld, stride, second = place(F, K, E)
+    buf = torch.full((size,), float("nan"), dtype=BF16, device="cuda")
+    lw, sw = (K, F * K) if layout == "col" else (F, F * K)
+    p = lambda t: t.data_ptr()
+    status = g.lib().gemm_run_expert_gated_backward(
+        h.handle, E, rows, F, K, p(dh), F, p(gate), F, p(up), F, p(x), K, p(wg), lw, sw, p(wu), lw, sw,
+        p(offsets), None, 0, p(buf), ld, stride, p(buf) + 2 * second, ld, stride, 2,
+        1 if layout == "col" else 0, 4, torch.cuda.current_stream().cuda_stream)
+    want = h.expert_gated_backward(dh, x, wg, wu, gate, up, offsets, need=(False, True, True))[1:]
+    shape = (E, F, K) if layout == "col" else (E, K, F)
+    got = [buf[o:].as_strided(shape, (stride, ld, 1)) for o in (0, second)]
+    return g.STATUS[status], buf, [v.transpose(1, 2) if layout == "col" else v for v in got], want
+
+
+# the gradients as column ranges of wider lines (of every expert, or all experts' lines on end), and as
+# parts of each expert's block of lines
+PLACES = {"columns": lambda F, K, E: (E * K * 2 * F, 2 * F, K * 2 * F, F),
+          "columns, gap": lambda F, K, E: (E * (K + 3) * (2 * F + 8), 2 * F + 8, (K + 3) * (2 * F + 8), F + 8),
+          "blocks": lambda F, K, E: (E * 2 * K * F, F, 2 * K * F, K * F)}
+
+
+@pytest.mark.parametrize("place", list(PLACES))
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("counts", [[90], [5, 0, 70]], ids=str)
+def test_weight_gradients_in_one_buffer(g, h, counts, layout, place):
+    def at(F, K, E):
+        return PLACES[place](F, K, E) if layout == "row" else PLACES[place](K, F, E)
+    status, buf, got, want = backward_into(g, h, counts, layout, at)
+    assert status == "GEMM_OK"
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    written = sum(v.numel() for v in got)
+    assert int(torch.isnan(buf).sum()) == buf.numel() - written
+
+
+@pytest.mark.parametrize("counts", [[90], [5, 0, 70]], ids=str)
+@pytest.mark.parametrize("second", [0, 1, 8, 39])
+def test_overlapping_weight_gradients_are_refused(g, h, counts, second):
+    """Gradients 40 wide in lines of 80 that start less than 40 apart, and across a line's end."""
+    for first in (second, 80 - second):
+        status, buf, *_ = backward_into(
+            g, h, counts, "row", lambda F, K, E: (E * K * 2 * F + 80, 2 * F, K * 2 * F, first))
+        assert status == "GEMM_ERR_INVALID_ARG"
+        assert torch.isnan(buf).all()
