@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from expert_util import make_ids, sort_reference
-from ff_util import acc_error, assert_within, matrix, rounding
+from ff_util import TYPES, acc_error, assert_within, matrix, rounding
 from test_expert_products_gpu import offsets_of, weights
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +110,38 @@ def test_overlapping_weight_gradients_are_refused(g, h, counts, second):
             g, h, counts, "row", lambda F, K, E: (E * K * 2 * F + 80, 2 * F, K * 2 * F, first))
         assert status == "GEMM_ERR_INVALID_ARG"
         assert torch.isnan(buf).all()
+
+
+# rows of a piece and more, the last piece short, for 16-bit and fp32 rows; one choice and many
+PIECES = [(1, 776), (2, 1032), (3, 2056), (5, 3000), (8, 1544)]
+
+
+@pytest.mark.parametrize("k,N", PIECES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("onto", [False, True])
+def test_combine_by_bulk_copies(g, k, N, dtype, out, onto):
+    """Long rows of many tokens come by bulk copies, and have the bits of a few tokens' rows, which come
+    by loads. Which of the two a call takes shows when no copy is issued: the waits end in a status."""
+    hh = g.Gemm(0)
+    tokens = 60 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    position, _ = hh.expert_sort(make_ids(tokens, k, 9, 3, none=0.1), 9)
+    rows = matrix(tokens * k, N, TYPES[dtype], 4)
+    w = matrix(tokens, k, torch.float32, 5).contiguous()
+    t = TYPES[out]
+    residual = matrix(tokens, N, t, 6) if onto else None
+    y = hh.expert_combine(rows, position, w, residual=residual, out_dtype=t)
+    parts = [slice(i, i + 100) for i in range(0, tokens, 100)]
+
+    def few(p):
+        return hh.expert_combine(rows, position[p], w[p], residual=residual[p] if onto else None, out_dtype=t)
+
+    for p in parts:
+        assert torch.equal(y[p], few(p))
+    assert hh.status() == 0
+    hh.set_option("wait_timeout_us", 2000)
+    hh.set_option("fault_stall_producer", 1)
+    few(parts[0])
+    assert hh.status() == 0
+    hh.expert_combine(rows, position, w, residual=residual, out_dtype=t)
+    assert hh.status() == 6
+    hh.close()
