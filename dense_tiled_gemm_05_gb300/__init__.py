@@ -526,7 +526,8 @@ class Gemm:
 
     def expert_gather(self, x, position, out=None, stream=None):
         """Rows in the order by expert: out[position[t, j]] = x[t]. out has tokens * k rows (or,
-        when given, as many as it has); those without a pair are left as they were."""
+        when given, as many as it has); those without a pair are left as they were. Every pair has
+        a row of its own, as :meth:`expert_sort` gives them."""
         return (_native_module or native()).expert_gather(self._address, x, position, out, stream)
 
     def expert_gather_backward(self, grad, position, stream=None):
@@ -555,7 +556,8 @@ class Gemm:
         """Each expert's rows against its weights: out[r] = x[r] @ w[e] for the rows r of e. x is
         rows x K in the order by expert, w is experts x K x N (each row- or column-major; weights
         stored as [experts, N, K] are passed as ``w.transpose(1, 2)``); the 16-bit types run on the
-        tensor cores, f32 on the fp32 units, some forty times slower. Rows from offsets[experts] on are left as they were (``out``, when given) and not read."""
+        tensor cores, f32 on the fp32 units, some forty times slower. Rows from offsets[experts] on
+        are left as they were (``out``, when given) and not read."""
         return (_native_module or native()).expert_matmul(self._address, x, w, offsets, out, stream)
 
     def expert_matmul_backward(self, grad, x, w, offsets, need=(True, True), out=None, stream=None):

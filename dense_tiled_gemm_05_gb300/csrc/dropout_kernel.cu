@@ -4,8 +4,8 @@
 // 2, 3", SC 2011) maps the counter (column / 8, row, offset) under the key (seed) to four 32-bit
 // words, which are eight 16-bit numbers, the low half of a word first. Element (row, column)
 // takes number column % 8 and is kept where that is not below round(65536 p). The kept share of
-// the 65536 numbers is exact, and the scale is its inverse, so the expectation is exact for the
-// p that is used. The same key gives the same mask whatever the strides, so the backward pass
+// the 65536 numbers is exact; the scale is its inverse rounded to fp32 (2^-24 of it at most). The
+// same key gives the same mask whatever the strides, so the backward pass
 // makes it again and nothing is stored.
 //
 // Bound by the bytes of x, residual and y: sixteen bits an element cost one generator call (20

@@ -20,8 +20,9 @@
 // rows, 2048 x 4096: 184 us, 189 in their own order; 64 experts of 0 to 1781 rows, 1024 x 2048: 81
 // and 84). An expert without rows gets zeros. One accumulation a tile, in a fixed order: the same
 // call gives the same bits. Bound by the tensor cores for many rows an expert (16384 rows,
-// 4096 x 2048: one expert 1780 TFLOP/s, 16 of 1024 rows 1700), by the writing of D for few (64 of 256
-// rows: 244 us for 1.07 GB written and 0.2 read).
+// 4096 x 2048: one expert 1730 TFLOP/s, 16 of 1024 rows 1690 to 1730), by the writing of D for few (64
+// of 256 rows: 244 us for 1.07 GB written and 0.2 read). A tile's rows are not shared over clusters:
+// fewer tiles than those leave them idle (5 experts of 4564 rows, 488 x 112: ten tiles, 29 us).
 #include "activation.cuh"
 #include "expert_kernels.h"
 #include "expert_tiles.cuh"

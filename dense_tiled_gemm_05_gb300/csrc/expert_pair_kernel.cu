@@ -7,9 +7,10 @@
 // How many rows an expert has is known on the device only, from none to all of them, so tiles
 // have to fit any count. The weights are the MMA's M side, 256 output features on a pair of CTAs
 // (tcgen05.mma.cta_group::2), and the tokens its N side, whose width is set for every tile: an
-// expert's rows are shared evenly over tiles of at most 256, each a multiple of 32 wide. 256-row tiles of tokens would waste half a tile an expert on average, an eighth of the
-// time at 1024 rows and a third at 256. The same layout serves few tokens: a 32-column MMA, and
-// the time is that of the weights' stream.
+// expert's rows are shared evenly over tiles of at most 256, each a multiple of 32 wide. 256-row
+// tiles of tokens would waste half a tile an expert on average, an eighth of the time at 1024 rows
+// and a third at 256. The same layout serves few tokens: a 32-column MMA, and the time is that of
+// the weights' stream.
 //
 // Grid: one cluster of two CTAs for every two SMs, which walk the tiles of all experts; every CTA
 // makes the table of tiles in its shared memory from the offsets, so that no count goes to the host
@@ -26,10 +27,12 @@
 // and a shuffle brings them together: 128 features a tile, one MMA a K-step. Other weights (other
 // layouts, feature counts that are no multiple of 16) run as two MMAs a K-step against the same
 // 128 tokens, g and u in the same lanes of two column ranges: those narrower MMAs read a third more
-// shared memory an operation (16384 rows of 16 experts, 2048 x 4096: 1751 TFLOP/s, interleaved 1830).
+// shared memory an operation (16 experts of 1024 rows, 2048 x 4096: 1840 TFLOP/s, interleaved 1940;
+// with g and u kept 1695 and 1825).
 //
-// Measured on one GB300: 16384 rows, 4096 x 2048, one expert 1900 TFLOP/s, 16 of 1024 rows 1820, 16 of
-// 46 to 4407 rows 1680; 256 rows of 32 experts, 4096 x 2048: 81 us for 540 MB.
+// Measured on one GB300, short runs: 16384 rows, 4096 x 2048, one expert 1900 to 1945 TFLOP/s, 16 of
+// 1024 rows 1800 to 1830, 16 of 46 to 4407 rows 1690 (back to back, at the power cap: 1650, 1550 and
+// 1450); 256 rows of 32 experts, 4096 x 2048: 80 us for 540 MB.
 //
 // The epilogue has one feature a lane and tokens along its registers, which lanes exchange for wider
 // stores (store_tokens). Rows past the expert's last are not stored (they are the next expert's).
@@ -345,8 +348,8 @@ __global__ void __launch_bounds__(kExpertThreads, NARROW ? 2 : 1)
       const int f0 = uniform(2 * tile.column + static_cast<int>(rank)) * S::FEATURES;
       const int half = uniform((tile.rows + 31) / 32 * 16);  // a CTA's tokens
       const int x_row = uniform(tile.row0) + static_cast<int>(rank) * half;
-      // the smallest box that holds them: one copy a stage (a copy's issue takes the loader some
-      // 50 cycles, and its loop ran as long as four MMAs with five 32-token ones)
+      // the smallest box that holds them: one copy a stage (with five 32-token ones the loader's loop
+      // ran as long as four MMAs)
       const int box = NARROW ? 0 : (half - 1) / 32;
       const uint32_t bytes = static_cast<uint32_t>(S::W_ALL + kRowBytes * 32 * (box + 1));
       const int kb_end = uniform(seg.kb_end);

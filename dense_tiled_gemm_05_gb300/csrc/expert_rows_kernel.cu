@@ -12,7 +12,8 @@
 // lane j the j-th, and hands them round by shuffles, so that all of a token's rows are on the
 // way at once. Each row is read and written once; every output element belongs to one lane,
 // which adds in the order of j in fp32 and rounds once. Positions outside [0, rows) are passed
-// over: nothing is read or written for them.
+// over: nothing is read or written for them. Pairs with one position write its row both, each
+// element at some time.
 #include <algorithm>
 
 #include "activation.cuh"

@@ -443,8 +443,8 @@ GEMM_API gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t
                                         void *cuda_stream);
 
 /* Y[position[t, j]] = X[t], bit for bit, for every pair whose position is in [0, rows): X is
- * tokens x N, Y rows x N. Other rows of Y are left as they were. Two pairs with one position leave
- * one of their tokens there. Its gradient is gemm_expert_combine without weights. */
+ * tokens x N, Y rows x N. Other rows of Y are left as they were. Two pairs with one position (none
+ * of gemm_expert_sort's have) leave either token's value in each element there. Its gradient is gemm_expert_combine without weights. */
 GEMM_API gemm_status_t gemm_expert_gather(gemm_handle_t h, int64_t tokens, int64_t k, int64_t N,
                                           const void *X, int64_t ldx, const int32_t *position,
                                           int64_t rows, void *Y, int64_t ldy, gemm_dtype_t dtype,
@@ -467,7 +467,8 @@ GEMM_API gemm_status_t gemm_expert_combine(gemm_handle_t h, int64_t tokens, int6
  *     dZ[position[t, j]] = weights[t, j] dY[t]                (rows x N of in_dtype),
  *     dweights[t, j] = sum_n dY[t, n] Z[position[t, j], n]    (tokens x k of weight_dtype),
  * 0 for a pair without a row; the residual's gradient is dY itself. Rows of dZ that no pair has
- * are left as they were. Either of dZ and dweights may be NULL; Z is read for dweights only. The
+ * are left as they were, and one that several pairs have gets either's value in each element, not
+ * their sum: positions are those of gemm_expert_sort, a row each. Either of dZ and dweights may be NULL; Z is read for dweights only. The
  * sums run in a fixed order: the same call gives the same bits. */
 GEMM_API gemm_status_t gemm_expert_combine_backward(
     gemm_handle_t h, int64_t tokens, int64_t k, int64_t N, const void *dY, int64_t lddy,
