@@ -145,3 +145,49 @@ def test_combine_by_bulk_copies(g, k, N, dtype, out, onto):
     hh.expert_combine(rows, position, w, residual=residual, out_dtype=t)
     assert hh.status() == 6
     hh.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_first_calls_are_captured(g, dtype):
+    """A handle's first calls, captured: its buffers are made, and cleared, outside the graph, and grow
+    from one captured call to the next. Replayed twice, with other work between, then called eagerly."""
+    t = TYPES[dtype]
+    eager, hh = g.Gemm(0), g.Gemm(0)
+    ids = make_ids(1500, 2, 6, 7, none=0.1)
+    tokens = matrix(1500, 133, t, 1)  # (rows TMA cannot address: copied first)
+    wg, wu = (weights(6, 133, 72, t, s) for s in (2, 3))
+    w = weights(1, 4096, 256, t, 4)  # few tiles with long K: shared
+    x, whole = matrix(5, 4096, t, 5), offsets_of([5])[0]
+    dh = matrix(3000, 72, t, 6)
+    key = torch.tensor([3, 4], device="cuda")
+
+    def calls(h):
+        position, offsets = h.expert_sort(ids, 6)
+        rows = h.expert_gather(tokens, position, out=torch.zeros(3000, 133, dtype=t, device="cuda"))
+        blank = lambda n: torch.zeros(3000, n, dtype=t, device="cuda")
+        y, gate, up = h.expert_gated(rows, wg, wu, offsets, save=True, out=blank(72))
+        live = (torch.arange(3000, device="cuda") < offsets[-1]).unsqueeze(1)
+        gate, up = (torch.where(live, v, torch.zeros_like(v)) for v in (gate, up))
+        return [h.expert_matmul(x, w, whole), position, offsets, rows, y, gate, up,
+                *h.expert_gated_backward(dh, rows, wg, wu, gate, up, offsets, out=blank(133)),
+                h.dropout(tokens, 0.3, key, residual=tokens)]
+
+    want = calls(eager)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        got = calls(hh)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+            a.zero_()
+    for a, b in zip(calls(hh), want):
+        assert torch.equal(a, b)
+    assert hh.status() == 0 and eager.status() == 0
+    del graph
+    hh.close()
+    eager.close()
